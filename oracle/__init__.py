@@ -37,3 +37,4 @@ from .quant import (  # noqa: F401
     quantize_experts,
     dequantize_experts,
 )
+from . import attention  # noqa: F401

@@ -1,4 +1,5 @@
-"""Python binding of the GB300 MoE layer library (``include/colibri_moe.h``).
+"""Python binding of the GB300 MoE layer library (``include/colibri_moe.h``; the
+attention operators of ``include/colibri_attn.h`` are in ``attention``).
 
 Argument marshalling only: every step of the layer runs in the CUDA library
 ``libcolibri_moe.so`` built in-tree by ``sparse_expert_ffn_gb300.build``.
@@ -38,6 +39,24 @@ class ColibriInt8Weights(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zp", ctypes.c_void_p)]
 
 
+class ColibriKVPages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class ColibriSeqs(ctypes.Structure):
+    _fields_ = [("seq_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("n_seqs", ctypes.c_int32),
+                ("n_rows", ctypes.c_int32), ("table_stride", ctypes.c_int32)]
+
+
+class ColibriRope(ctypes.Structure):
+    _fields_ = [("freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("style", ctypes.c_int32),
+                ("mscale", ctypes.c_float)]
+
+
 class ColibriError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -51,6 +70,8 @@ def _load():
             "(or __graft_entry__.build()); the layer has no non-CUDA implementation")
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, U64P = ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(ctypes.c_uint64)
+    I64, F32, F64, SZ = ctypes.c_int64, ctypes.c_float, ctypes.c_double, ctypes.c_size_t
+    KV, SQ, RP, SZP = (ctypes.POINTER(t) for t in (ColibriKVPages, ColibriSeqs, ColibriRope, SZ))
     sig = {
         "colibri_init": ([ctypes.POINTER(ColibriConfig), P, P, P, P, P, ctypes.c_int,
                           ctypes.POINTER(P)], I32),
@@ -75,6 +96,14 @@ def _load():
         "colibri_forward_routed": ([P, P, I32, I32, P, P, P, P], I32),
         "colibri_gather_rows": ([P, I32, P, I32, I32, I32, I32, P, P], I32),
         "colibri_combine_rows": ([P, I32, P, P, I32, I32, I32, I32, P, P, P], I32),
+        "colibri_rope_frequencies": ([I32, F64, I32, F64, I32, F64, F64, P, ctypes.POINTER(F32)], I32),
+        "colibri_append_qkv": ([KV, SQ, RP, I32, P, I64, P, I64, P, I64, P, P, F32, P, I64, P], I32),
+        "colibri_qk_norm_rope": ([SQ, RP, I32, I32, I32, I32, P, I64, P, I64, P, P, F32, P, I64, P, I64,
+                                  P], I32),
+        "colibri_attention_prompt_workspace": ([KV, SQ, I32, SZP], I32),
+        "colibri_attention_prompt": ([KV, SQ, I32, P, I64, F32, I32, P, I64, P, P, SZ, P], I32),
+        "colibri_attention_decode_workspace": ([KV, SQ, I32, I32, SZP], I32),
+        "colibri_attention_decode": ([KV, SQ, I32, P, I64, F32, I32, P, P, I64, P, P, SZ, P], I32),
         "colibri_free": ([P], None),
         "colibri_status_str": ([I32], ctypes.c_char_p),
     }
@@ -93,6 +122,9 @@ _C_NAMES = ("colibri_init", "colibri_init_int8", "colibri_quantize_int8_block64"
             "colibri_check", "colibri_launch_count", "colibri_workspace_bytes",
             "colibri_profile_enable", "colibri_profile_read", "colibri_route_static",
             "colibri_forward_routed", "colibri_gather_rows", "colibri_combine_rows",
+            "colibri_rope_frequencies", "colibri_append_qkv", "colibri_qk_norm_rope",
+            "colibri_attention_prompt_workspace", "colibri_attention_prompt",
+            "colibri_attention_decode_workspace", "colibri_attention_decode",
             "colibri_free")
 
 

@@ -1,0 +1,358 @@
+"""Attention operators of a pre-norm decoder block (``include/colibri_attn.h``).
+
+Argument marshalling only: the work is done by the CUDA library.  What a
+program keeps between calls is described once, by :class:`PagedKVCache`,
+:class:`Sequences` and :class:`Rope` over the program's own tensors; the
+functions then take row tensors ``[rows, heads, head_dim]`` (any row stride)
+and run on the tensors' device and its current stream (or ``stream``):
+
+* :func:`append_qkv`, :func:`qk_norm_rope`: per-head norms, rotary positions
+  and the write into the cache in one pass;
+* :func:`attention_prompt`, :func:`attention_prompt_paged`: packed sequences of
+  different lengths, grouped heads, causal or full;
+* :func:`attention_decode`: one row per sequence, with a shared prefix.
+"""
+
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+import sparse_expert_ffn_gb300 as _sef
+
+_STYLE = {"half": 0, "interleaved": 1}
+_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+_DTYPE = {torch.float32: _sef.DTYPE_FP32, torch.bfloat16: _sef.DTYPE_BF16}
+
+KVPages, Seqs, RopeArgs = _sef.ColibriKVPages, _sef.ColibriSeqs, _sef.ColibriRope
+
+
+def _int32(t, name, dim, device=None):
+    if t.dtype != torch.int32 or t.dim() != dim or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA int32 tensor with {dim} dimension(s)")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+
+
+def rope_frequencies(rot_dim: int, theta: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     trained: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(freq [rot_dim / 2] float64 CPU tensor, mscale) of ``colibri_rope_frequencies``:
+    radians per position, for contexts ``factor`` times the trained one
+    ("linear", "ntk", "yarn")."""
+    if scaling not in _SCALING:
+        raise ValueError(f"scaling must be one of {sorted(_SCALING)}")
+    freq = torch.empty(max(int(rot_dim), 0) // 2, dtype=torch.float64)
+    mscale = ctypes.c_float()
+    _sef._check(_sef.library().colibri_rope_frequencies(
+        int(rot_dim), float(theta), _SCALING[scaling], float(factor), int(trained), float(beta_fast),
+        float(beta_slow), freq.data_ptr() or None, ctypes.byref(mscale)), "colibri_rope_frequencies")
+    return freq, mscale.value
+
+
+class Rope:
+    """Rotary positions: ``freq`` [rot_dim / 2] float64 on the GPU (radians per
+    position), pairing ``style`` "half" or "interleaved", ``mscale`` the factor
+    of cos and sin."""
+
+    def __init__(self, freq, style: str = "half", mscale: float = 1.0):
+        if freq.dtype != torch.float64 or freq.dim() != 1 or not freq.is_cuda or not freq.is_contiguous():
+            raise ValueError("freq must be a contiguous CUDA float64 vector")
+        self.freq, self.device = freq, freq.device
+        self._c = RopeArgs(freq.data_ptr(), 2 * freq.numel(), _STYLE[style], float(mscale))
+        self._ref = ctypes.byref(self._c)
+
+
+class PagedKVCache:
+    """Keys and values in pages: ``k`` and ``v`` [pages, kv_heads, page_size,
+    head_dim] with the same strides, the last dimension contiguous (a
+    ``transpose(1, 2)`` of [pages, page_size, kv_heads, head_dim] storage
+    serves as well).  The program owns the tensors and hands out the pages."""
+
+    def __init__(self, k, v):
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("k and v must be [pages, kv_heads, page_size, head_dim] with equal strides "
+                             "and a contiguous last dimension")
+        if k.dtype not in _DTYPE or v.dtype != k.dtype or not k.is_cuda or v.device != k.device:
+            raise ValueError("k and v must be float32 or bfloat16 tensors of one CUDA device")
+        self.k, self.v, self.dtype, self.device = k, v, k.dtype, k.device
+        self.num_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
+        self._c = KVPages(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), k.shape[0],
+                          k.shape[2], k.shape[1], k.shape[3], _DTYPE[k.dtype])
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, n_kv_heads: int, head_dim: int,
+              dtype=torch.bfloat16, device="cuda"):
+        shape = (num_pages, n_kv_heads, page_size, head_dim)
+        return cls(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device))
+
+
+class Sequences:
+    """The sequences of a call (int32 CUDA tensors, read on the device at every
+    call, so their contents may change between calls): ``seq_start`` [B + 1]
+    first rows (None: row b is sequence b), ``kv_len`` [B] keys including the
+    call's rows (None: the sequence's rows), ``page_table`` [B, width] page ids
+    (None: no cache)."""
+
+    def __init__(self, seq_start=None, kv_len=None, page_table=None):
+        given = [t for t in (seq_start, kv_len, page_table) if t is not None]
+        if not given or (seq_start is None and kv_len is None):
+            raise ValueError("seq_start or kv_len must be given")
+        self.device = given[0].device
+        for t, name, dim in ((seq_start, "seq_start", 1), (kv_len, "kv_len", 1)):
+            if t is not None:
+                _int32(t, name, dim, self.device)
+        if page_table is not None:
+            if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != self.device \
+                    or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+                raise ValueError("page_table must be an int32 CUDA matrix with contiguous rows")
+        n = kv_len.shape[0] if kv_len is not None else seq_start.shape[0] - 1
+        if n < 0 or (seq_start is not None and seq_start.shape[0] != n + 1) or \
+                (page_table is not None and page_table.shape[0] != n):
+            raise ValueError("seq_start [B + 1], kv_len [B] and page_table [B, width] must agree on B")
+        if page_table is not None and n > 1 and page_table.stride(0) != page_table.shape[1]:
+            page_table = page_table.contiguous()
+        self.n_seqs = n
+        self.seq_start, self.kv_len, self.page_table = seq_start, kv_len, page_table
+        self._one_each = seq_start is None
+        self._c = Seqs(_sef._ptr(seq_start), _sef._ptr(kv_len), _sef._ptr(page_table), n, 0,
+                       0 if page_table is None else page_table.shape[1])
+        self._ref = ctypes.byref(self._c)
+
+    def _rows(self, t):
+        if self._one_each and t.shape[0] != self.n_seqs:
+            raise ValueError("without seq_start there is one row per sequence")
+        self._c.n_rows = t.shape[0]
+        return self._ref
+
+
+def _same(t, name, heads, head_dim, dtype, device, rows):
+    """Checks a row tensor; returns its row stride."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or t.dtype != dtype or \
+            t.device != device or t.shape[0] != rows:
+        raise ValueError(f"{name} must be [{rows}, {heads}, {head_dim}], {dtype}, on {device}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != head_dim):
+        raise ValueError(f"{name}'s heads must be contiguous")
+    return s0 if rows > 1 else heads * head_dim
+
+
+def _norm(w, name, head_dim, dtype, device):
+    if w is None:
+        return None
+    if tuple(w.shape) != (head_dim,) or w.dtype != dtype or w.device != device or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{head_dim}] {dtype} vector on {device}")
+    return w.data_ptr()
+
+
+class _On:
+    """The call's device made current, and the stream to run on."""
+
+    __slots__ = ("idx", "prev")
+
+    def __init__(self, device):
+        self.idx = device.index
+
+    def __enter__(self):
+        self.prev = torch.cuda.current_device()
+        if self.prev != self.idx:
+            torch.cuda.set_device(self.idx)
+
+    def __exit__(self, *exc):
+        if self.prev != self.idx:
+            torch.cuda.set_device(self.prev)
+
+
+def _stream(stream, device):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _rope_ref(rope, device):
+    if rope is None:
+        return None
+    if rope.device != device:
+        raise ValueError(f"rope.freq must be on {device}")
+    return rope._ref
+
+
+def _rows3(q):
+    if q.dim() != 3 or q.dtype not in _DTYPE or not q.is_cuda:
+        raise ValueError("q must be a [rows, heads, head_dim] float32 or bfloat16 CUDA tensor")
+
+
+def append_qkv(cache: PagedKVCache, seqs: Sequences, q, k, v, *, rope: Optional[Rope] = None, q_norm=None,
+               k_norm=None, eps: float = 1e-6, q_out=None, stream=None):
+    """Normalise (q_norm / k_norm given) and rotate (rope given) the rows' query
+    and key heads; keys and values go to their places in the cache, the queries
+    to ``q_out`` (a new tensor by default, may be ``q``), which is returned."""
+    _rows3(q)
+    dev, dt, D, rows = cache.device, cache.dtype, cache.head_dim, q.shape[0]
+    hq, hkv = q.shape[1], cache.n_kv_heads
+    if seqs.device != dev:
+        raise ValueError(f"seqs must be on {dev}")
+    if q_out is None:
+        q_out = torch.empty((rows, hq, D), dtype=dt, device=dev)
+    args = (_rope_ref(rope, dev), hq, q.data_ptr(), _same(q, "q", hq, D, dt, dev, rows),
+            k.data_ptr(), _same(k, "k", hkv, D, dt, dev, rows), v.data_ptr(), _same(v, "v", hkv, D, dt, dev, rows),
+            _norm(q_norm, "q_norm", D, dt, dev), _norm(k_norm, "k_norm", D, dt, dev), float(eps),
+            q_out.data_ptr(), _same(q_out, "q_out", hq, D, dt, dev, rows))
+    if rows == 0:
+        return q_out
+    with _On(dev):
+        _sef._check(_sef.library().colibri_append_qkv(cache._ref, seqs._rows(q), *args, _stream(stream, dev)),
+                    "colibri_append_qkv")
+    return q_out
+
+
+def qk_norm_rope(seqs: Sequences, q, k, *, rope: Optional[Rope] = None, q_norm=None, k_norm=None,
+                 eps: float = 1e-6, q_out=None, k_out=None, stream=None):
+    """:func:`append_qkv` for rows that go to no cache; returns (q_out, k_out)."""
+    _rows3(q)
+    dev, dt, D, rows, hq, hkv = q.device, q.dtype, q.shape[2], q.shape[0], q.shape[1], k.shape[1]
+    if seqs.device != dev:
+        raise ValueError(f"seqs must be on {dev}")
+    if q_out is None:
+        q_out = torch.empty((rows, hq, D), dtype=dt, device=dev)
+    if k_out is None:
+        k_out = torch.empty((rows, hkv, D), dtype=dt, device=dev)
+    args = (_rope_ref(rope, dev), hq, hkv, D, _DTYPE[dt], q.data_ptr(), _same(q, "q", hq, D, dt, dev, rows),
+            k.data_ptr(), _same(k, "k", hkv, D, dt, dev, rows),
+            _norm(q_norm, "q_norm", D, dt, dev), _norm(k_norm, "k_norm", D, dt, dev), float(eps),
+            q_out.data_ptr(), _same(q_out, "q_out", hq, D, dt, dev, rows),
+            k_out.data_ptr(), _same(k_out, "k_out", hkv, D, dt, dev, rows))
+    if rows == 0:
+        return q_out, k_out
+    with _On(dev):
+        _sef._check(_sef.library().colibri_qk_norm_rope(seqs._rows(q), *args, _stream(stream, dev)),
+                    "colibri_qk_norm_rope")
+    return q_out, k_out
+
+
+def _outputs(q, out, lse):
+    rows, hq, D = q.shape
+    if out is None:
+        out = torch.empty((rows, hq, D), dtype=q.dtype, device=q.device)
+    if lse is not None and (tuple(lse.shape) != (rows, hq) or lse.dtype != torch.float32 or
+                            lse.device != q.device or not lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous [{rows}, {hq}] float32 tensor on {q.device}")
+    return out, (None if lse is None else lse.data_ptr()), _same(out, "out", hq, D, q.dtype, q.device, rows)
+
+
+def _workspace(nbytes, device):
+    """A call's workspace, from the caching allocator: ordered on the current
+    stream like any tensor, a graph's own while a graph is captured."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _prompt(kv, kv_ref, seqs, q, scale, causal, out, lse, stream):
+    _rows3(q)
+    dev, rows, hq, D = q.device, q.shape[0], q.shape[1], q.shape[2]
+    if seqs.device != dev or kv.device != dev:
+        raise ValueError(f"keys and seqs must be on {dev}")
+    if q.dtype != kv.dtype or D != kv.head_dim:
+        raise ValueError("q and the keys must share dtype and head_dim")
+    stride = _same(q, "q", hq, D, q.dtype, dev, rows)
+    out, lse_ptr, o_stride = _outputs(q, out, lse)
+    if rows == 0:
+        return out
+    ref, lib, need = seqs._rows(q), _sef.library(), ctypes.c_size_t()
+    _sef._check(lib.colibri_attention_prompt_workspace(kv_ref, ref, hq, ctypes.byref(need)),
+                "colibri_attention_prompt_workspace")
+    with _On(dev), _ambient(stream):
+        ws = _workspace(need.value, dev)
+        _sef._check(lib.colibri_attention_prompt(
+            kv_ref, ref, hq, q.data_ptr(), stride, D ** -0.5 if scale is None else float(scale), int(causal),
+            out.data_ptr(), o_stride, lse_ptr, None if ws is None else ws.data_ptr(), need.value,
+            _stream(stream, dev)), "colibri_attention_prompt")
+    return out
+
+
+class _Nothing:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_NOTHING = _Nothing()
+
+
+def _ambient(stream):
+    """The workspace is allocated on the stream that the kernels run on."""
+    return _NOTHING if stream is None else torch.cuda.stream(stream)
+
+
+class _Packed:
+    """k and v rows [rows, kv_heads, head_dim] as one page."""
+
+    def __init__(self, k, v):
+        rows, hkv, D = k.shape
+        sk = _same(k, "k", hkv, D, k.dtype, k.device, rows)
+        if _same(v, "v", hkv, D, k.dtype, k.device, rows) != sk:
+            raise ValueError("k and v must have the same row stride")
+        self.dtype, self.device, self.head_dim = k.dtype, k.device, D
+        self._c = KVPages(k.data_ptr(), v.data_ptr(), max(rows, 1) * sk, D, sk, 1, max(rows, 1), hkv, D,
+                          _DTYPE.get(k.dtype, -1))
+
+
+def attention_prompt(seqs: Sequences, q, k, v, *, scale: Optional[float] = None, causal: bool = True, out=None,
+                     lse=None, stream=None):
+    """Attention of packed sequences over their own rows: q [rows, heads,
+    head_dim], k and v [rows, kv_heads, head_dim], sequence b at rows
+    seq_start[b] .. seq_start[b + 1] - 1 (seqs without kv_len and page_table).
+    scale defaults to head_dim ** -0.5; lse [rows, heads] float32 receives the
+    logarithms of the softmax sums.  Rows of no sequence are left as they were."""
+    if seqs.page_table is not None or seqs.kv_len is not None:
+        raise ValueError("packed keys take Sequences(seq_start); use attention_prompt_paged with a cache")
+    if k.dim() != 3 or v.dim() != 3 or k.shape[0] != q.shape[0]:
+        raise ValueError("k and v must be [rows, kv_heads, head_dim] with q's rows")
+    kv = _Packed(k, v)
+    return _prompt(kv, ctypes.byref(kv._c), seqs, q, scale, causal, out, lse, stream)
+
+
+def attention_prompt_paged(cache: PagedKVCache, seqs: Sequences, q, *, scale: Optional[float] = None,
+                           causal: bool = True, out=None, lse=None, stream=None):
+    """:func:`attention_prompt` over a cache's pages (seqs with kv_len and
+    page_table): row i of n of sequence b stands at position kv_len[b] - n + i."""
+    if seqs.page_table is None or seqs.kv_len is None:
+        raise ValueError("seqs needs kv_len and page_table")
+    return _prompt(cache, cache._ref, seqs, q, scale, causal, out, lse, stream)
+
+
+def attention_decode(cache: PagedKVCache, seqs: Sequences, q, *, prefix_len: int = 0, prefix_table=None,
+                     scale: Optional[float] = None, out=None, lse=None, stream=None):
+    """Attention of one row per sequence (q [B, heads, head_dim]) over its
+    kv_len[b] keys.  The first prefix_len keys (a multiple of the page size) of
+    every sequence are those of prefix_table [prefix_len / page_size], read once
+    for the batch."""
+    _rows3(q)
+    dev, rows, hq, D = q.device, q.shape[0], q.shape[1], q.shape[2]
+    if seqs.page_table is None or seqs.kv_len is None or seqs.seq_start is not None:
+        raise ValueError("seqs needs kv_len and page_table, and no seq_start")
+    if seqs.device != dev or cache.device != dev:
+        raise ValueError(f"the cache and seqs must be on {dev}")
+    if q.dtype != cache.dtype or D != cache.head_dim:
+        raise ValueError("q and the cache must share dtype and head_dim")
+    table = None
+    if prefix_table is not None:
+        _int32(prefix_table, "prefix_table", 1, dev)
+        if prefix_table.shape[0] * cache.page_size < prefix_len:
+            raise ValueError("prefix_table is shorter than the prefix")
+        table = prefix_table.data_ptr() if prefix_len else None
+    stride = _same(q, "q", hq, D, q.dtype, dev, rows)
+    out, lse_ptr, o_stride = _outputs(q, out, lse)
+    if rows == 0:
+        return out
+    ref, lib, need = seqs._rows(q), _sef.library(), ctypes.c_size_t()
+    _sef._check(lib.colibri_attention_decode_workspace(cache._ref, ref, hq, int(prefix_len), ctypes.byref(need)),
+                "colibri_attention_decode_workspace")
+    with _On(dev), _ambient(stream):
+        ws = _workspace(need.value, dev)
+        _sef._check(lib.colibri_attention_decode(
+            cache._ref, ref, hq, q.data_ptr(), stride, D ** -0.5 if scale is None else float(scale),
+            int(prefix_len), table, out.data_ptr(), o_stride, lse_ptr, None if ws is None else ws.data_ptr(),
+            need.value, _stream(stream, dev)), "colibri_attention_decode")
+    return out

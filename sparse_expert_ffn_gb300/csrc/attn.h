@@ -1,0 +1,79 @@
+// Attention operators: kernel arguments and launchers (internal to the library).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace colibri {
+
+enum class DType : int;
+
+// What the rows and keys of a launch are.
+enum AttnMode : int {
+    kAttnPrompt = 0,   // rows of seq_start, keys 0 .. kv_len[b] - 1
+    kAttnPrefix = 1,   // all n_seqs rows as one sequence over the shared prefix;
+                       // row i sees its first min(kv_len[i], prefix_len) keys
+    kAttnSuffix = 2    // row b over keys prefix_len .. kv_len[b] - 1
+};
+
+struct AttnArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* o;
+    float* lse;                  // [n_rows, hq] or null
+    const int32_t* seq_start;    // prompt
+    const int32_t* kv_len;       // null: the sequence's row count
+    const int32_t* table;        // null: packed keys
+    int64_t q_stride, o_stride;
+    int64_t page_stride, head_stride, row_stride;
+    int mode;
+    int n_seqs, n_rows;
+    int hq, hkv, group;
+    int table_stride;            // entries per sequence
+    int num_pages, page_size, page_shift;
+    int prefix_len;
+    int causal;
+    float scale_log2;            // scale * log2(e)
+    // work split over the keys: `splits` ranges per row tile.  part_o null:
+    // one range, the kernel writes o and lse; otherwise range s of this launch
+    // writes its normalised rows and log2-sums to slot part_slot + s
+    int splits;
+    int part_slot;
+    float* part_o;               // [slots][n_rows * hq][d]
+    float* part_lse;             // [slots][n_rows * hq]
+    uint64_t wait_limit_ns;      // bound of every mbarrier wait
+    int stall_tma;               // failure-detection tests only: issue no copy
+};
+
+// CUDA-core attention, float32 arithmetic throughout (float32 layers).
+int attn_simt_rows(const AttnArgs& a);       // rows per tile that the launch will use
+cudaError_t launch_attn_simt(DType dt, int d, const AttnArgs& a, cudaStream_t s);
+
+// o, lse from the partial rows of `slots` key ranges (slot order).
+cudaError_t launch_attn_join(DType dt, int d, const AttnArgs& a, int slots, cudaStream_t s);
+
+// Norm, rotation and placement of q, k, v rows.
+struct AppendArgs {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const void *q_norm, *k_norm;     // or null
+    float eps;
+    const double* freq;              // null: no rotation
+    int rot_dim, interleaved;
+    float mscale;
+    const int32_t *seq_start, *kv_len, *table;
+    int n_seqs, n_rows, table_stride;
+    int hq, hkv;
+    void* q_out;
+    int64_t q_out_stride;
+    // paged keys and values, or (v_out null) rows of k_out
+    void *k_out, *v_out;
+    int64_t page_stride, head_stride, row_stride;
+    int num_pages, page_shift;
+};
+cudaError_t launch_append(DType dt, int d, const AppendArgs& a, cudaStream_t s);
+
+}  // namespace colibri

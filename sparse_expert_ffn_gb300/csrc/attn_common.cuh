@@ -1,0 +1,112 @@
+// Device helpers of the attention kernels: which rows and keys a work item
+// covers.  Every value that comes from a device array is cut to the bounds the
+// launch knows, so whatever the arrays hold, every access stays in bounds.
+#pragma once
+
+#include "attn.h"
+#include "common.cuh"
+
+namespace colibri {
+
+// One sequence of a launch: rows row0 .. row0 + n - 1, keys kv0 .. kv - 1.
+struct AttnSeq {
+    int row0, n, kv0, kv, raw;
+};
+
+__device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
+    AttnSeq s;
+    if (a.mode == kAttnPrefix) {
+        s.row0 = 0, s.n = a.n_seqs, s.kv0 = 0, s.kv = s.raw = a.prefix_len;
+        return s;
+    }
+    if (a.mode == kAttnSuffix) {
+        s.row0 = b, s.n = 1, s.kv0 = a.prefix_len;
+    } else {
+        s.row0 = min(max(__ldg(a.seq_start + b), 0), a.n_rows);
+        s.n = min(max(__ldg(a.seq_start + b + 1), s.row0), a.n_rows) - s.row0;
+        s.kv0 = 0;
+    }
+    s.raw = a.kv_len ? max(__ldg(a.kv_len + b), 0) : s.n;
+    const int64_t cap = a.table ? (int64_t)a.table_stride << a.page_shift : (int64_t)s.n;
+    s.kv = (int)min((int64_t)s.raw, cap);
+    return s;
+}
+
+// Keys that row i of the sequence sees: kv0 .. attn_limit - 1.
+__device__ __forceinline__ int attn_limit(const AttnArgs& a, const AttnSeq& s, int i) {
+    if (a.mode == kAttnPrefix) return min(max(__ldg(a.kv_len + i), 0), s.kv);
+    if (!a.causal) return s.kv;
+    return min(max(s.raw - (s.n - 1 - i), 0), s.kv);
+}
+
+// Largest limit of rows i0 .. i1 - 1 (i0 < i1); for the prefix, the prefix.
+__device__ __forceinline__ int attn_limit_max(const AttnArgs& a, const AttnSeq& s, int i1) {
+    return a.mode == kAttnPrefix ? s.kv : attn_limit(a, s, i1 - 1);
+}
+
+// Page id of keys at page index `p` of sequence b, -1 where there is none.
+__device__ __forceinline__ int attn_page(const AttnArgs& a, int b, int p) {
+    const int64_t at = a.mode == kAttnPrefix ? (int64_t)p : (int64_t)b * a.table_stride + p;
+    const int id = __ldg(a.table + at);
+    return (unsigned)id < (unsigned)a.num_pages ? id : -1;
+}
+
+// Work item `item` of the launch as (sequence, tile), tiles of `per` rows of a
+// sequence's n * mul; called by a whole warp.  The last tiles of a sequence,
+// which see the most keys, come first.  False: no such item.
+__device__ __forceinline__ bool attn_item(const AttnArgs& a, int item, int mul, int per, int* b,
+                                          int* tile) {
+    const int lane = threadIdx.x & 31;
+    const int count = a.mode == kAttnPrefix ? 1 : a.n_seqs;
+    if (a.mode != kAttnPrompt) {
+        const int tiles = ((a.mode == kAttnPrefix ? a.n_seqs : 1) * mul + per - 1) / per;
+        *b = item / tiles;
+        *tile = item % tiles;
+        return *b < count;
+    }
+    int done = 0;
+    for (int base = 0; base < count; base += 32) {
+        int mine = 0;
+        if (base + lane < count) {
+            const int s0 = min(max(__ldg(a.seq_start + base + lane), 0), a.n_rows);
+            const int s1 = min(max(__ldg(a.seq_start + base + lane + 1), s0), a.n_rows);
+            mine = (int)(((int64_t)(s1 - s0) * mul + per - 1) / per);
+        }
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const unsigned holds = __ballot_sync(0xffffffffu, item - done < upto);
+        if (holds) {
+            const int src = __ffs(holds) - 1;
+            *b = base + src;
+            const int first = done + __shfl_sync(0xffffffffu, upto - mine, src);
+            *tile = __shfl_sync(0xffffffffu, mine, src) - 1 - (item - first);
+            return true;
+        }
+        done += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return false;
+}
+
+// Keys of split `sp` of the tile range kv0 .. end: whole tiles of `kt` keys,
+// the same number for every split but the last ones.
+__device__ __forceinline__ void attn_split(const AttnArgs& a, int sp, int kt, int kv0, int end,
+                                           int* lo, int* hi) {
+    const int tiles = end > kv0 ? (end - kv0 + kt - 1) / kt : 0;
+    const int per = (tiles + a.splits - 1) / a.splits;
+    *lo = min(end, kv0 + min(tiles, sp * per) * kt);
+    *hi = min(end, kv0 + min(tiles, (sp + 1) * per) * kt);
+}
+
+constexpr float kLn2 = 0.69314718055994530942f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+}  // namespace colibri

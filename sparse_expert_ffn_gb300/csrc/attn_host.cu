@@ -1,0 +1,408 @@
+// Host side of the attention operators (include/colibri_attn.h): argument
+// checks, the split of the keys, the launches.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <cstdlib>
+
+#include "attn.h"
+#include "colibri_attn.h"
+#include "common.cuh"
+#include "kernels.h"
+
+using namespace colibri;
+
+namespace {
+
+// The grids are sized for the GPU this library is built for, so that a
+// workspace's size does not depend on the machine that asks for it.
+constexpr int kSms = 152;
+constexpr int kMaxSplits = 64;
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+int elem_size(int dtype) { return dtype == COLIBRI_DTYPE_BF16 ? 2 : 4; }
+DType dtype_of(int dtype) { return dtype == COLIBRI_DTYPE_BF16 ? DType::BF16 : DType::F32; }
+
+// A row tensor [rows, heads, d] with `stride` elements from row to row.
+bool rows_ok(const void* p, int64_t stride, int heads, int d, int esz) {
+    return p && aligned16(p) && stride >= (int64_t)heads * d && (stride * esz) % 16 == 0 &&
+           stride * esz < ((int64_t)1 << 40);
+}
+
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+    const uintptr_t pa = (uintptr_t)a, pb = (uintptr_t)b;
+    return pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
+}
+
+colibri_status_t check_heads(int n_q_heads, int n_kv_heads, int head_dim, int dtype) {
+    if (dtype != COLIBRI_DTYPE_FP32 && dtype != COLIBRI_DTYPE_BF16) return COLIBRI_ERR_INVALID_ARG;
+    if (n_q_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || n_q_heads % n_kv_heads)
+        return COLIBRI_ERR_INVALID_ARG;
+    if ((head_dim != 64 && head_dim != 128) || n_q_heads / n_kv_heads > 128 || n_kv_heads > 65535 ||
+        n_q_heads > 65535)
+        return COLIBRI_ERR_UNSUPPORTED;
+    return COLIBRI_OK;
+}
+
+colibri_status_t check_kv(const colibri_kv_pages_t* kv, bool paged) {
+    if (!kv || !kv->k || !kv->v || !aligned16(kv->k) || !aligned16(kv->v)) return COLIBRI_ERR_INVALID_ARG;
+    if (kv->num_pages <= 0 || kv->page_size <= 0) return COLIBRI_ERR_INVALID_ARG;
+    const int esz = elem_size(kv->dtype);
+    for (const int64_t s : {kv->page_stride, kv->head_stride, kv->row_stride})
+        if (s < 0 || (s * esz) % 16 || s >= ((int64_t)1 << 37)) return COLIBRI_ERR_INVALID_ARG;
+    if (kv->row_stride < kv->head_dim || (kv->n_kv_heads > 1 && kv->head_stride < kv->head_dim) ||
+        (kv->num_pages > 1 && kv->page_stride < kv->head_dim))
+        return COLIBRI_ERR_INVALID_ARG;
+    if (paged) {
+        if (kv->page_size < 8 || kv->page_size > 65536 || (kv->page_size & (kv->page_size - 1)))
+            return COLIBRI_ERR_UNSUPPORTED;
+    } else if (kv->num_pages != 1) {
+        return COLIBRI_ERR_INVALID_ARG;
+    }
+    return COLIBRI_OK;
+}
+
+// Bytes from the first to behind the last element of k (or v).
+int64_t kv_extent(const colibri_kv_pages_t* kv) {
+    return ((int64_t)(kv->num_pages - 1) * kv->page_stride +
+            (int64_t)(kv->n_kv_heads - 1) * kv->head_stride +
+            (int64_t)(kv->page_size - 1) * kv->row_stride + kv->head_dim) * elem_size(kv->dtype);
+}
+
+colibri_status_t check_seqs(const colibri_seqs_t* s, int n_q_heads) {
+    if (!s || s->n_seqs < 0 || s->n_rows < 0 || s->table_stride < 0) return COLIBRI_ERR_INVALID_ARG;
+    if (!s->seq_start && s->n_rows != s->n_seqs) return COLIBRI_ERR_INVALID_ARG;
+    if (s->page_table && (!s->kv_len || s->table_stride <= 0)) return COLIBRI_ERR_INVALID_ARG;
+    for (const int32_t* p : {s->seq_start, s->kv_len, s->page_table})
+        if ((uintptr_t)p & 3) return COLIBRI_ERR_INVALID_ARG;
+    if ((int64_t)s->n_rows * n_q_heads > INT32_MAX || (int64_t)s->n_seqs * 128 > INT32_MAX)
+        return COLIBRI_ERR_INVALID_ARG;
+    return COLIBRI_OK;
+}
+
+colibri_status_t check_rope(const colibri_rope_t* r, int head_dim) {
+    if (!r) return COLIBRI_OK;
+    if (!r->freq || ((uintptr_t)r->freq & 7) || r->rot_dim <= 0 || r->rot_dim > head_dim ||
+        r->rot_dim % 16 || !(std::isfinite(r->mscale)))
+        return COLIBRI_ERR_INVALID_ARG;
+    if (r->style != COLIBRI_ROPE_HALF && r->style != COLIBRI_ROPE_INTERLEAVED)
+        return COLIBRI_ERR_INVALID_ARG;
+    return COLIBRI_OK;
+}
+
+// How a call's keys are split: ranges of the shared prefix and of the
+// sequences' own keys, each leaving a partial row per (row, head).
+struct Plan {
+    int prefix = 0;      // ranges of the prefix (0: no prefix launch)
+    int own = 1;         // ranges of the sequences' own keys
+    bool direct() const { return prefix == 0 && own == 1; }
+    int slots() const { return prefix + own; }
+    size_t bytes(const colibri_seqs_t* s, int hq, int d) const {
+        if (direct()) return 0;
+        const size_t rows = (size_t)slots() * s->n_rows * hq;
+        return ((rows * 4 + 255) & ~(size_t)255) + rows * d * 4;
+    }
+};
+
+// Ranges for `items` tiles over up to `keys` keys: enough for two CTAs per SM,
+// none under 256 keys.
+int choose_splits(int64_t items, int64_t keys) {
+    const int64_t want = (2 * kSms + items - 1) / std::max<int64_t>(items, 1);
+    return (int)std::max<int64_t>(1, std::min({want, (keys + 255) / 256, (int64_t)kMaxSplits}));
+}
+
+Plan make_plan(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq, int mode, int prefix_len) {
+    const int group = hq / kv->n_kv_heads;
+    const int64_t keys = s->page_table ? (int64_t)s->table_stride * kv->page_size : s->n_rows;
+    AttnArgs a{};
+    a.group = group;
+    a.mode = mode;
+    const int rows = attn_simt_rows(a);
+    Plan p;
+    const int64_t tiles = mode == kAttnSuffix ? (int64_t)s->n_seqs * ((group + rows - 1) / rows)
+                                              : (int64_t)s->n_rows * group / rows + s->n_seqs;
+    p.own = choose_splits(tiles * kv->n_kv_heads, std::max<int64_t>(keys - prefix_len, 1));
+    if (prefix_len > 0) {
+        a.mode = kAttnPrefix;
+        const int pr = attn_simt_rows(a);
+        p.prefix = choose_splits(((int64_t)s->n_rows * group + pr - 1) / pr * kv->n_kv_heads, prefix_len);
+    }
+    return p;
+}
+
+AttnArgs make_args(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq, const void* q,
+                   int64_t q_stride, float scale, void* o, int64_t o_stride, float* lse) {
+    AttnArgs a{};
+    a.q = q, a.k = kv->k, a.v = kv->v, a.o = o, a.lse = lse;
+    a.seq_start = s->seq_start, a.kv_len = s->kv_len, a.table = s->page_table;
+    a.q_stride = q_stride, a.o_stride = o_stride;
+    a.page_stride = kv->page_stride, a.head_stride = kv->head_stride, a.row_stride = kv->row_stride;
+    a.mode = s->seq_start ? kAttnPrompt : kAttnSuffix;
+    a.n_seqs = s->n_seqs, a.n_rows = s->n_rows;
+    a.hq = hq, a.hkv = kv->n_kv_heads, a.group = hq / kv->n_kv_heads;
+    a.table_stride = s->table_stride;
+    a.num_pages = kv->num_pages, a.page_size = kv->page_size;
+    a.page_shift = 0;
+    while ((1 << a.page_shift) < kv->page_size) ++a.page_shift;
+    a.scale_log2 = scale * 1.44269504088896340736f;
+    a.splits = 1;
+    return a;
+}
+
+colibri_status_t check_attention(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq,
+                                 const void* q, int64_t q_stride, float scale, const void* o,
+                                 int64_t o_stride, const float* lse) {
+    const int esz = elem_size(kv->dtype), d = kv->head_dim;
+    if (!rows_ok(q, q_stride, hq, d, esz) || !rows_ok(o, o_stride, hq, d, esz) || ((uintptr_t)lse & 3))
+        return COLIBRI_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return COLIBRI_ERR_INVALID_ARG;
+    if (s->n_rows == 0) return COLIBRI_OK;
+    const int64_t nq = ((int64_t)(s->n_rows - 1) * q_stride + (int64_t)hq * d) * esz;
+    const int64_t no = ((int64_t)(s->n_rows - 1) * o_stride + (int64_t)hq * d) * esz;
+    if (overlap(q, nq, o, no) || overlap(kv->k, kv_extent(kv), o, no) || overlap(kv->v, kv_extent(kv), o, no))
+        return COLIBRI_ERR_INVALID_ARG;
+    return COLIBRI_OK;
+}
+
+void place_workspace(AttnArgs& a, const Plan& p, void* ws) {
+    if (p.direct()) return;
+    const size_t rows = (size_t)p.slots() * a.n_rows * a.hq;
+    a.part_lse = static_cast<float*>(ws);
+    a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ((rows * 4 + 255) & ~(size_t)255));
+}
+
+colibri_status_t run_attention(AttnArgs a, const Plan& p, int dtype, int d, int prefix_len,
+                               const int32_t* prefix_table, void* ws, cudaStream_t s) {
+    const DType dt = dtype_of(dtype);
+    place_workspace(a, p, ws);
+    a.prefix_len = prefix_len;
+    cudaError_t e = cudaSuccess;
+    if (p.prefix > 0) {
+        AttnArgs f = a;
+        f.mode = kAttnPrefix;
+        f.causal = 0;
+        f.table = prefix_table;
+        f.splits = p.prefix;
+        f.part_slot = 0;
+        e = launch_attn_simt(dt, d, f, s);
+    }
+    a.splits = p.own;
+    a.part_slot = p.prefix;
+    if (e == cudaSuccess) e = launch_attn_simt(dt, d, a, s);
+    if (e == cudaSuccess && !p.direct()) e = launch_attn_join(dt, d, a, p.slots(), s);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
+}
+
+colibri_status_t check_prompt(const colibri_kv_pages_t* kv, const colibri_seqs_t* seqs, int n_q_heads) {
+    if (!kv || !seqs) return COLIBRI_ERR_INVALID_ARG;
+    colibri_status_t st = check_heads(n_q_heads, kv->n_kv_heads, kv->head_dim, kv->dtype);
+    if (st == COLIBRI_OK) st = check_seqs(seqs, n_q_heads);
+    if (st == COLIBRI_OK) st = check_kv(kv, seqs->page_table != nullptr);
+    if (st != COLIBRI_OK) return st;
+    // packed keys: the call's own rows
+    if (!seqs->page_table && (seqs->kv_len || (seqs->n_rows > 0 && kv->page_size != seqs->n_rows)))
+        return COLIBRI_ERR_INVALID_ARG;
+    return COLIBRI_OK;
+}
+
+colibri_status_t check_decode(const colibri_kv_pages_t* kv, const colibri_seqs_t* seqs, int n_q_heads,
+                              int prefix_len) {
+    if (!kv || !seqs || !seqs->page_table || !seqs->kv_len || seqs->seq_start)
+        return COLIBRI_ERR_INVALID_ARG;
+    colibri_status_t st = check_heads(n_q_heads, kv->n_kv_heads, kv->head_dim, kv->dtype);
+    if (st == COLIBRI_OK) st = check_seqs(seqs, n_q_heads);
+    if (st == COLIBRI_OK) st = check_kv(kv, true);
+    if (st != COLIBRI_OK) return st;
+    if (prefix_len < 0 || prefix_len % kv->page_size) return COLIBRI_ERR_INVALID_ARG;
+    return COLIBRI_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+colibri_status_t colibri_rope_frequencies(int32_t rot_dim, double theta, int32_t scaling, double factor,
+                                          int32_t trained, double beta_fast, double beta_slow,
+                                          double* freq, float* mscale) {
+    if (!freq || !mscale || rot_dim <= 0 || rot_dim % 16 || !(theta > 1.0) || !std::isfinite(theta))
+        return COLIBRI_ERR_INVALID_ARG;
+    if (scaling < COLIBRI_ROPE_SCALE_NONE || scaling > COLIBRI_ROPE_SCALE_YARN)
+        return COLIBRI_ERR_INVALID_ARG;
+    if (scaling != COLIBRI_ROPE_SCALE_NONE && (!(factor >= 1.0) || !std::isfinite(factor)))
+        return COLIBRI_ERR_INVALID_ARG;
+    const bool yarn = scaling == COLIBRI_ROPE_SCALE_YARN;
+    if (yarn && (trained <= 0 || !(beta_slow > 0.0) || !(beta_fast > beta_slow)))
+        return COLIBRI_ERR_INVALID_ARG;
+    const int half = rot_dim / 2;
+    if (scaling == COLIBRI_ROPE_SCALE_NTK)
+        theta *= std::pow(factor, (double)rot_dim / (double)(rot_dim - 2));
+    double lo = 0.0, hi = 0.0;
+    if (yarn) {
+        // the pair that turns `turns` times in the trained context
+        const auto at = [&](double turns) {
+            return rot_dim * std::log(trained / (turns * 2.0 * 3.14159265358979323846)) /
+                   (2.0 * std::log(theta));
+        };
+        lo = std::max(std::floor(at(beta_fast)), 0.0);
+        hi = std::min(std::ceil(at(beta_slow)), (double)(rot_dim - 1));
+    }
+    for (int i = 0; i < half; ++i) {
+        double f = std::pow(theta, -2.0 * i / rot_dim);
+        if (scaling == COLIBRI_ROPE_SCALE_LINEAR) {
+            f /= factor;
+        } else if (yarn) {
+            const double ramp = std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 1e-3)));
+            f = f / factor * ramp + f * (1.0 - ramp);
+        }
+        freq[i] = f;
+    }
+    *mscale = yarn ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return COLIBRI_OK;
+}
+
+colibri_status_t colibri_append_qkv(const colibri_kv_pages_t* cache, const colibri_seqs_t* seqs,
+                                    const colibri_rope_t* rope, int32_t n_q_heads, const void* q,
+                                    int64_t q_stride, const void* k, int64_t k_stride,
+                                    const void* v, int64_t v_stride, const void* q_norm,
+                                    const void* k_norm, float eps, void* q_out,
+                                    int64_t q_out_stride, void* stream) {
+    if (!cache || !seqs || !seqs->page_table || !seqs->kv_len) return COLIBRI_ERR_INVALID_ARG;
+    colibri_status_t st = check_heads(n_q_heads, cache->n_kv_heads, cache->head_dim, cache->dtype);
+    if (st == COLIBRI_OK) st = check_seqs(seqs, n_q_heads);
+    if (st == COLIBRI_OK) st = check_kv(cache, true);
+    if (st == COLIBRI_OK) st = check_rope(rope, cache->head_dim);
+    if (st != COLIBRI_OK) return st;
+    const int d = cache->head_dim, esz = elem_size(cache->dtype), hkv = cache->n_kv_heads;
+    if (!rows_ok(q, q_stride, n_q_heads, d, esz) || !rows_ok(k, k_stride, hkv, d, esz) ||
+        !rows_ok(v, v_stride, hkv, d, esz) || !rows_ok(q_out, q_out_stride, n_q_heads, d, esz) ||
+        !aligned16(q_norm) || !aligned16(k_norm) || !(eps >= 0.f))
+        return COLIBRI_ERR_INVALID_ARG;
+    if (q_out == q && q_out_stride != q_stride) return COLIBRI_ERR_INVALID_ARG;
+    if (seqs->n_rows == 0 || seqs->n_seqs == 0) return COLIBRI_OK;
+    AppendArgs a{};
+    a.q = q, a.k = k, a.v = v;
+    a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+    a.q_norm = q_norm, a.k_norm = k_norm, a.eps = eps;
+    if (rope) {
+        a.freq = rope->freq, a.rot_dim = rope->rot_dim, a.mscale = rope->mscale;
+        a.interleaved = rope->style == COLIBRI_ROPE_INTERLEAVED;
+    }
+    a.seq_start = seqs->seq_start, a.kv_len = seqs->kv_len, a.table = seqs->page_table;
+    a.n_seqs = seqs->n_seqs, a.n_rows = seqs->n_rows, a.table_stride = seqs->table_stride;
+    a.hq = n_q_heads, a.hkv = hkv;
+    a.q_out = q_out, a.q_out_stride = q_out_stride;
+    a.k_out = cache->k, a.v_out = cache->v;
+    a.page_stride = cache->page_stride, a.head_stride = cache->head_stride;
+    a.row_stride = cache->row_stride, a.num_pages = cache->num_pages;
+    while ((1 << a.page_shift) < cache->page_size) ++a.page_shift;
+    const cudaError_t e = launch_append(dtype_of(cache->dtype), d, a, (cudaStream_t)stream);
+    return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
+}
+
+colibri_status_t colibri_qk_norm_rope(const colibri_seqs_t* seqs, const colibri_rope_t* rope,
+                                      int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                      int32_t dtype, const void* q, int64_t q_stride,
+                                      const void* k, int64_t k_stride, const void* q_norm,
+                                      const void* k_norm, float eps, void* q_out,
+                                      int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                                      void* stream) {
+    if (!seqs) return COLIBRI_ERR_INVALID_ARG;
+    colibri_status_t st = check_heads(n_q_heads, n_kv_heads, head_dim, dtype);
+    if (st == COLIBRI_OK) st = check_seqs(seqs, n_q_heads);
+    if (st == COLIBRI_OK) st = check_rope(rope, head_dim);
+    if (st != COLIBRI_OK) return st;
+    const int d = head_dim, esz = elem_size(dtype);
+    if (!rows_ok(q, q_stride, n_q_heads, d, esz) || !rows_ok(k, k_stride, n_kv_heads, d, esz) ||
+        !rows_ok(q_out, q_out_stride, n_q_heads, d, esz) ||
+        !rows_ok(k_out, k_out_stride, n_kv_heads, d, esz) || !aligned16(q_norm) ||
+        !aligned16(k_norm) || !(eps >= 0.f))
+        return COLIBRI_ERR_INVALID_ARG;
+    if ((q_out == q && q_out_stride != q_stride) || (k_out == k && k_out_stride != k_stride))
+        return COLIBRI_ERR_INVALID_ARG;
+    if (seqs->n_rows == 0 || seqs->n_seqs == 0) return COLIBRI_OK;
+    AppendArgs a{};
+    a.q = q, a.k = k;
+    a.q_stride = q_stride, a.k_stride = k_stride;
+    a.q_norm = q_norm, a.k_norm = k_norm, a.eps = eps;
+    if (rope) {
+        a.freq = rope->freq, a.rot_dim = rope->rot_dim, a.mscale = rope->mscale;
+        a.interleaved = rope->style == COLIBRI_ROPE_INTERLEAVED;
+    }
+    a.seq_start = seqs->seq_start, a.kv_len = seqs->kv_len;
+    a.n_seqs = seqs->n_seqs, a.n_rows = seqs->n_rows;
+    a.hq = n_q_heads, a.hkv = n_kv_heads;
+    a.q_out = q_out, a.q_out_stride = q_out_stride;
+    a.k_out = k_out, a.row_stride = k_out_stride, a.head_stride = d;
+    const cudaError_t e = launch_append(dtype_of(dtype), d, a, (cudaStream_t)stream);
+    return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
+}
+
+colibri_status_t colibri_attention_prompt_workspace(const colibri_kv_pages_t* kv,
+                                                    const colibri_seqs_t* seqs, int32_t n_q_heads,
+                                                    size_t* bytes) {
+    if (!bytes) return COLIBRI_ERR_INVALID_ARG;
+    const colibri_status_t st = check_prompt(kv, seqs, n_q_heads);
+    if (st != COLIBRI_OK) return st;
+    const int mode = seqs->seq_start ? kAttnPrompt : kAttnSuffix;
+    *bytes = make_plan(kv, seqs, n_q_heads, mode, 0).bytes(seqs, n_q_heads, kv->head_dim);
+    return COLIBRI_OK;
+}
+
+colibri_status_t colibri_attention_prompt(const colibri_kv_pages_t* kv, const colibri_seqs_t* seqs,
+                                          int32_t n_q_heads, const void* q, int64_t q_stride,
+                                          float scale, int32_t causal, void* o, int64_t o_stride,
+                                          float* lse, void* workspace, size_t workspace_bytes,
+                                          void* stream) {
+    colibri_status_t st = check_prompt(kv, seqs, n_q_heads);
+    if (st == COLIBRI_OK) st = check_attention(kv, seqs, n_q_heads, q, q_stride, scale, o, o_stride, lse);
+    if (st != COLIBRI_OK) return st;
+    const int mode = seqs->seq_start ? kAttnPrompt : kAttnSuffix;
+    const Plan p = make_plan(kv, seqs, n_q_heads, mode, 0);
+    const size_t need = p.bytes(seqs, n_q_heads, kv->head_dim);
+    if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255)))
+        return COLIBRI_ERR_INVALID_ARG;
+    if (seqs->n_rows == 0 || seqs->n_seqs == 0) return COLIBRI_OK;
+    AttnArgs a = make_args(kv, seqs, n_q_heads, q, q_stride, scale, o, o_stride, lse);
+    a.causal = causal != 0;
+    return run_attention(a, p, kv->dtype, kv->head_dim, 0, nullptr, workspace, (cudaStream_t)stream);
+}
+
+colibri_status_t colibri_attention_decode_workspace(const colibri_kv_pages_t* cache,
+                                                    const colibri_seqs_t* seqs, int32_t n_q_heads,
+                                                    int32_t prefix_len, size_t* bytes) {
+    if (!bytes) return COLIBRI_ERR_INVALID_ARG;
+    const colibri_status_t st = check_decode(cache, seqs, n_q_heads, prefix_len);
+    if (st != COLIBRI_OK) return st;
+    *bytes = make_plan(cache, seqs, n_q_heads, kAttnSuffix, prefix_len)
+                 .bytes(seqs, n_q_heads, cache->head_dim);
+    return COLIBRI_OK;
+}
+
+colibri_status_t colibri_attention_decode(const colibri_kv_pages_t* cache, const colibri_seqs_t* seqs,
+                                          int32_t n_q_heads, const void* q, int64_t q_stride,
+                                          float scale, int32_t prefix_len,
+                                          const int32_t* prefix_table, void* o, int64_t o_stride,
+                                          float* lse, void* workspace, size_t workspace_bytes,
+                                          void* stream) {
+    colibri_status_t st = check_decode(cache, seqs, n_q_heads, prefix_len);
+    if (st == COLIBRI_OK)
+        st = check_attention(cache, seqs, n_q_heads, q, q_stride, scale, o, o_stride, lse);
+    if (st != COLIBRI_OK) return st;
+    if ((prefix_len > 0) != (prefix_table != nullptr) || ((uintptr_t)prefix_table & 3))
+        return COLIBRI_ERR_INVALID_ARG;
+    const Plan p = make_plan(cache, seqs, n_q_heads, kAttnSuffix, prefix_len);
+    const size_t need = p.bytes(seqs, n_q_heads, cache->head_dim);
+    if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255)))
+        return COLIBRI_ERR_INVALID_ARG;
+    if (seqs->n_rows == 0) return COLIBRI_OK;
+    AttnArgs a = make_args(cache, seqs, n_q_heads, q, q_stride, scale, o, o_stride, lse);
+    return run_attention(a, p, cache->dtype, cache->head_dim, prefix_len, prefix_table, workspace,
+                         (cudaStream_t)stream);
+}
+
+}  // extern "C"
