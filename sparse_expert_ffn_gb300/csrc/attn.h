@@ -52,6 +52,11 @@ struct AttnArgs {
 int attn_simt_rows(const AttnArgs& a);       // rows per tile that the launch will use
 cudaError_t launch_attn_simt(DType dt, int d, const AttnArgs& a, cudaStream_t s);
 
+// Tensor-core attention of bf16 rows (prompt and prefix modes): row tiles of
+// 2 * (128 / group) tokens of one sequence.
+int64_t attn_tc_items(const AttnArgs& a);    // row tiles of the launch, per key head
+cudaError_t launch_attn_tc(int d, const AttnArgs& a, cudaStream_t s);
+
 // o, lse from the partial rows of `slots` key ranges (slot order).
 cudaError_t launch_attn_join(DType dt, int d, const AttnArgs& a, int slots, cudaStream_t s);
 

@@ -115,23 +115,35 @@ int choose_splits(int64_t items, int64_t keys) {
     return (int)std::max<int64_t>(1, std::min({want, (keys + 255) / 256, (int64_t)kMaxSplits}));
 }
 
+// Row tiles of a launch and key head.
+int64_t row_tiles(const AttnArgs& a, bool tensor_cores) {
+    if (tensor_cores) return attn_tc_items(a);
+    const int rows = attn_simt_rows(a);
+    if (a.mode == kAttnSuffix) return (int64_t)a.n_seqs * ((a.group + rows - 1) / rows);
+    if (a.mode == kAttnPrefix) return ((int64_t)a.n_seqs * a.group + rows - 1) / rows;
+    return (int64_t)a.n_rows * a.group / rows + a.n_seqs;
+}
+
+// bf16 prompts and prefixes run on the tensor cores.
+bool on_tensor_cores(int dtype, int mode) { return dtype == COLIBRI_DTYPE_BF16 && mode != kAttnSuffix; }
+
 Plan make_plan(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq, int mode, int prefix_len) {
-    const int group = hq / kv->n_kv_heads;
     const int64_t keys = s->page_table ? (int64_t)s->table_stride * kv->page_size : s->n_rows;
     AttnArgs a{};
-    a.group = group;
-    a.mode = mode;
-    const int rows = attn_simt_rows(a);
+    a.n_rows = s->n_rows, a.n_seqs = s->n_seqs, a.group = hq / kv->n_kv_heads, a.mode = mode;
     Plan p;
-    const int64_t tiles = mode == kAttnSuffix ? (int64_t)s->n_seqs * ((group + rows - 1) / rows)
-                                              : (int64_t)s->n_rows * group / rows + s->n_seqs;
-    p.own = choose_splits(tiles * kv->n_kv_heads, std::max<int64_t>(keys - prefix_len, 1));
+    p.own = choose_splits(row_tiles(a, on_tensor_cores(kv->dtype, mode)) * kv->n_kv_heads,
+                          std::max<int64_t>(keys - prefix_len, 1));
     if (prefix_len > 0) {
         a.mode = kAttnPrefix;
-        const int pr = attn_simt_rows(a);
-        p.prefix = choose_splits(((int64_t)s->n_rows * group + pr - 1) / pr * kv->n_kv_heads, prefix_len);
+        p.prefix = choose_splits(row_tiles(a, on_tensor_cores(kv->dtype, a.mode)) * kv->n_kv_heads, prefix_len);
     }
     return p;
+}
+
+cudaError_t launch_attention(int dtype, int d, const AttnArgs& a, cudaStream_t s) {
+    if (on_tensor_cores(dtype, a.mode)) return launch_attn_tc(d, a, s);
+    return launch_attn_simt(dtype_of(dtype), d, a, s);
 }
 
 AttnArgs make_args(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq, const void* q,
@@ -150,6 +162,11 @@ AttnArgs make_args(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq
     while ((1 << a.page_shift) < kv->page_size) ++a.page_shift;
     a.scale_log2 = scale * 1.44269504088896340736f;
     a.splits = 1;
+    // the bound of the tensor-core kernel's waits, and the producer that copies
+    // nothing of the failure-detection tests
+    a.wait_limit_ns = 2000000000ull;
+    if (const char* e = std::getenv("COLIBRI_WAIT_LIMIT_NS")) a.wait_limit_ns = std::strtoull(e, nullptr, 10);
+    if (const char* e = std::getenv("COLIBRI_TEST_STALL_TMA")) a.stall_tma = std::atoi(e);
     return a;
 }
 
@@ -177,7 +194,6 @@ void place_workspace(AttnArgs& a, const Plan& p, void* ws) {
 
 colibri_status_t run_attention(AttnArgs a, const Plan& p, int dtype, int d, int prefix_len,
                                const int32_t* prefix_table, void* ws, cudaStream_t s) {
-    const DType dt = dtype_of(dtype);
     place_workspace(a, p, ws);
     a.prefix_len = prefix_len;
     cudaError_t e = cudaSuccess;
@@ -188,12 +204,12 @@ colibri_status_t run_attention(AttnArgs a, const Plan& p, int dtype, int d, int 
         f.table = prefix_table;
         f.splits = p.prefix;
         f.part_slot = 0;
-        e = launch_attn_simt(dt, d, f, s);
+        e = launch_attention(dtype, d, f, s);
     }
     a.splits = p.own;
     a.part_slot = p.prefix;
-    if (e == cudaSuccess) e = launch_attn_simt(dt, d, a, s);
-    if (e == cudaSuccess && !p.direct()) e = launch_attn_join(dt, d, a, p.slots(), s);
+    if (e == cudaSuccess) e = launch_attention(dtype, d, a, s);
+    if (e == cudaSuccess && !p.direct()) e = launch_attn_join(dtype_of(dtype), d, a, p.slots(), s);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
 }

@@ -1,0 +1,480 @@
+// Attention on the tensor cores (tcgen05, TMEM, TMA) for bf16: prompts, and
+// the shared prefix of a decode batch.
+//
+// One CTA takes two tiles of up to 128 rows of one sequence and key head and
+// walks its keys 128 at a time.  A tile's rows are (token, head of the group)
+// pairs, tokens * group of them, so the heads that share a key head share its
+// keys in shared memory, and a decode batch over a shared prefix is the same
+// kernel with the batch as the tokens.  Per tile and 128 keys:
+//   S = Q K^T   (128 x 128 x d, f32 in tensor memory)
+//   m' = max(m, max S),  P = 2^(c S - c m')  (bf16, written over S),  l += sum P
+//   O += P V    (128 x d x 128, P read from tensor memory)
+// with c = scale * log2(e).  O stays in tensor memory: it is multiplied by
+// 2^(c m - c m') only when a row's maximum has grown by more than 2^8 since it
+// was last taken as the reference (the weights are then below 2^8, which bf16
+// and f32 hold as exactly as those below 1), so that the softmax warps rarely
+// touch it.
+//
+// Roles: warps 0-3 and 4-7 the softmax of the two tiles (one row per thread,
+// no shuffles), warp 8 issues the MMAs, warp 9 the TMA copies (K and V tiles
+// alternate in a ring; with pages, one box per page).  The MMAs of one tile run
+// while the other tile is in its softmax.  A commit after S(j + 1) also covers
+// the O += P V of step j issued before it, so the one barrier per tile tells the
+// softmax warps both that S is there and that O may be rescaled.
+//
+// P is rounded to bf16 because the MMA takes both operands in one 16-bit type;
+// l adds the unrounded f32 values.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "attn_common.cuh"
+#include "kernels.h"
+#include "tc_common.cuh"
+
+namespace colibri {
+namespace {
+
+using namespace tc;
+
+constexpr int kTcThreads = 320;
+constexpr int kTileKeys = 128;
+constexpr uint32_t kHalfBytes = 128 * 128;      // 128 rows of one 128-byte swizzle atom
+
+// Ring slots of 128 keys: 4 of 32 KB, 8 of 16 KB (d = 64).
+template <int D> constexpr int kSlots = D == 128 ? 4 : 8;
+template <int D> constexpr uint32_t kTileBytes = (D / 64) * kHalfBytes;
+
+struct TcBars {
+    uint64_t q_full[2];
+    uint64_t s_full[2];       // S of the tile's next step is there, its O is up to date
+    uint64_t p_ready[2];      // P written, O rescaled
+    uint64_t o_done[2];       // the tile's last product is done
+    uint64_t kv_full[8];
+    uint64_t kv_empty[8];
+    uint64_t drain;
+    uint32_t tmem;
+    int item[2];
+    int abort;
+    int status;
+};
+
+template <int D>
+constexpr size_t tc_smem_bytes() {
+    return 1024 + 2 * kTileBytes<D> + kSlots<D> * kTileBytes<D> + sizeof(TcBars);
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                            int c3, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+
+// 16 consecutive 32-bit TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+
+// B operand with the MN index contiguous (V: rows are keys, the MMA's K; the
+// 64-column halves are kHalfBytes apart, 8-key groups 1024 bytes).
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(kHalfBytes >> 4) << 16;   // leading offset: next 64 columns
+    d |= (uint64_t)(1024 >> 4) << 32;         // stride offset: next 8 keys
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;                   // 128-byte swizzle
+    return d;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, AttnArgs a, int tokens, int box) {
+    extern __shared__ uint8_t raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t* sq = smem;
+    uint8_t* skv = smem + 2 * kTileBytes<D>;
+    TcBars& bars = *reinterpret_cast<TcBars*>(skv + kSlots<D> * kTileBytes<D>);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_u32(&bars.q_full[t]), 1);
+            mbar_init(smem_u32(&bars.s_full[t]), 1);
+            mbar_init(smem_u32(&bars.p_ready[t]), 4);
+            mbar_init(smem_u32(&bars.o_done[t]), 1);
+        }
+        for (int s = 0; s < kSlots<D>; ++s) {
+            mbar_init(smem_u32(&bars.kv_full[s]), 1);
+            mbar_init(smem_u32(&bars.kv_empty[s]), 1);
+        }
+        mbar_init(smem_u32(&bars.drain), 1);
+        bars.abort = 0;
+        bars.status = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    pdl_enter();
+    const int h = blockIdx.x % a.hkv;
+    if (warp == 9) {
+        int b = 0, tile = 0;
+        const bool ok = attn_item(a, blockIdx.x / a.hkv, 1, 2 * tokens, &b, &tile);
+        if (lane == 0) bars.item[0] = ok ? b : -1, bars.item[1] = tile;
+    }
+    __syncthreads();
+    const int b = bars.item[0];
+    if (b < 0) return;
+    if (warp == 8) tmem_alloc<false>(smem_u32(&bars.tmem), 512);
+    const AttnSeq seq = attn_seq(a, b);
+    const int tok0 = bars.item[1] * 2 * tokens;                 // first token of tile 0
+    // keys lo .. hi - 1 of this CTA; steps of each tile (tile 1's rows are later)
+    int lo, hi, steps[2];
+    attn_split(a, blockIdx.y, kTileKeys, seq.kv0, attn_limit_max(a, seq, min(tok0 + 2 * tokens, seq.n)), &lo, &hi);
+    for (int t = 0; t < 2; ++t) {
+        const int first = tok0 + t * tokens, last = min(first + tokens, seq.n);
+        const int end = first < seq.n ? min(hi, attn_limit_max(a, seq, last)) : lo;
+        steps[t] = end > lo ? (end - lo + kTileKeys - 1) / kTileKeys : 0;
+    }
+    const int nsteps = max(steps[0], steps[1]);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem;
+    volatile int* abort_flag = &bars.abort;
+    int* status = &bars.status;
+    const uint64_t limit = a.wait_limit_ns;
+    constexpr uint32_t kColO = 256;                             // S0 0, S1 128, O0 256, O1 256 + D
+    // one outcome for the whole warp, so that no collective runs without its lanes
+    const auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag, status, limit)) != 0;
+    };
+
+    if (warp < 8) {
+        // ------------------------------------------------ softmax, one row per thread
+        const int t = warp >> 2, r = tid & 127;
+        const int i = tok0 + t * tokens + r / a.group, g = r % a.group;
+        const bool live = r < tokens * a.group && i < seq.n;
+        const int lim = live ? min(hi, attn_limit(a, seq, i)) : 0;
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t ts = lane_base + t * 128, to = lane_base + kColO + t * D;
+        const float c = a.scale_log2;
+        float m = -INFINITY, l = 0.f;      // reference maximum (times c), sum of the weights
+        bool ok = true;
+        for (int j = 0; j < steps[t]; ++j) {
+            ok = warp_wait(&bars.s_full[t], j & 1);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) tmem_ld32(ts + 32 * x, s[x]);
+            tmem_ld_wait();
+            const int left = lim - (lo + j * kTileKeys);       // keys of this step that the row sees
+            if (left < kTileKeys) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int y = 0; y < 32; ++y)
+                        if (x * 32 + y >= left) s[x][y] = 0xff800000u;   // -infinity
+            }
+            float top[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                top[x] = __uint_as_float(s[x][0]);
+#pragma unroll
+                for (int y = 1; y < 32; ++y) top[x] = fmaxf(top[x], __uint_as_float(s[x][y]));
+            }
+            const float mn = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+            const bool grow = mn > m + 8.f;
+            if (__any_sync(0xffffffffu, grow)) {
+                const float keep = grow ? ex2(m - mn) : 1.f;
+                if (grow) m = mn;
+                l *= keep;
+                if (j > 0) {
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x) {
+                        uint32_t o[16];
+                        tmem_ld16(to + 16 * x, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * keep);
+                        tmem_st16(to + 16 * x, o);
+                    }
+                }
+            }
+            const float ref = m == -INFINITY ? 0.f : m;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                uint32_t p[16];
+#pragma unroll
+                for (int y = 0; y < 16; ++y) {
+                    const float p0 = ex2(fmaf(__uint_as_float(s[x][2 * y]), c, -ref));
+                    const float p1 = ex2(fmaf(__uint_as_float(s[x][2 * y + 1]), c, -ref));
+                    sum[(2 * y) & 3] += p0;
+                    sum[(2 * y + 1) & 3] += p1;
+                    p[y] = pack_h2<false>(p0, p1);
+                }
+                tmem_st16(ts + 16 * x, p);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars.p_ready[t]));
+        }
+        if (ok && steps[t] > 0) {
+            ok = warp_wait(&bars.o_done[t], 0);
+            tc_fence_after();
+        }
+        // o / l; a row without keys has l = 0
+        const float inv = !ok ? __int_as_float(0x7fc00000) : l > 0.f ? 1.f / l : l;
+        const int row = seq.row0 + i;
+        const int64_t flat = (int64_t)row * a.hq + h * a.group + g;
+        const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+        const int64_t at = (int64_t)(a.part_slot + blockIdx.y) * a.n_rows * a.hq + flat;
+        if (live) {
+            if (a.part_o) a.part_lse[at] = ok ? lse2 : inv;
+            else if (a.lse) a.lse[flat] = ok ? lse2 * kLn2 : inv;
+        }
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+            uint32_t o[32];
+            if (steps[t] > 0) {
+                tmem_ld32(to + 32 * x, o);
+                tmem_ld_wait();
+            } else {
+#pragma unroll
+                for (int y = 0; y < 32; ++y) o[y] = 0;
+            }
+            if (!live) continue;
+            // (a row that saw no key may stand in a tile that did)
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = l == 0.f && ok ? 0 : __float_as_uint(__uint_as_float(o[y]) * inv);
+            if (a.part_o) {
+                uint4* dst = reinterpret_cast<uint4*>(a.part_o + at * D + 32 * x);
+#pragma unroll
+                for (int y = 0; y < 8; ++y) dst[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+            } else {
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + (int64_t)row * a.o_stride +
+                                                      (int64_t)(h * a.group + g) * D + 32 * x);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        w[z] = pack_h2<false>(__uint_as_float(o[8 * y + 2 * z]), __uint_as_float(o[8 * y + 2 * z + 1]));
+                    dst[y] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
+    } else if (warp == 8) {
+        // ------------------------------------------------ MMA issue
+        const uint32_t q0 = smem_u32(sq), kv0 = smem_u32(skv);
+        constexpr uint32_t kIdS = idesc_bf16(128, kTileKeys);
+        constexpr uint32_t kIdO = idesc_bf16(128, D) | (1u << 16);   // V: MN-major
+        const auto scores = [&](int t, int j) {
+            const uint32_t k = kv0 + ((2 * j) % kSlots<D>) * kTileBytes<D>;
+            if (lane == 0) {
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    const uint32_t off = (x / 4) * kHalfBytes + (x % 4) * 32;
+                    mma_bf16<false>(tmem + t * 128, smem_desc_sw128(q0 + t * kTileBytes<D> + off),
+                                    smem_desc_sw128(k + off), kIdS, x > 0);
+                }
+                mma_commit<false>(smem_u32(&bars.s_full[t]));
+            }
+            __syncwarp();
+        };
+        const auto full = [&](int slot) { return warp_wait(&bars.kv_full[slot % kSlots<D>], (slot / kSlots<D>) & 1); };
+        bool ok = true;
+        if (nsteps > 0) {
+            ok = full(0);
+            for (int t = 0; t < 2 && ok; ++t) {
+                if (steps[t] == 0) continue;
+                ok = warp_wait(&bars.q_full[t], 0);
+                if (ok) scores(t, 0);
+            }
+            if (ok && lane == 0) mma_commit<false>(smem_u32(&bars.kv_empty[0]));
+            __syncwarp();
+        }
+        for (int j = 0; j < nsteps && ok; ++j) {
+            ok = full(2 * j + 1);
+            if (!ok) break;
+            const uint32_t v = kv0 + ((2 * j + 1) % kSlots<D>) * kTileBytes<D>;
+            const int have = hi - (lo + j * kTileKeys);
+            if (have < kTileKeys) {
+                // rows behind the last key: their weights are 0, and 0 times
+                // whatever lies there has to be 0
+                for (int e = lane; e < (kTileKeys - have) * (D / 64) * 8; e += 32) {
+                    const int row = have + (e >> 3) % (kTileKeys - have), half = (e >> 3) / (kTileKeys - have);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + half * kHalfBytes + row * 128 +
+                                                                                (e & 7) * 16),
+                                 "r"(0)
+                                 : "memory");
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+            }
+            for (int t = 0; t < 2 && ok; ++t) {
+                if (j >= steps[t]) continue;
+                ok = warp_wait(&bars.p_ready[t], j & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+#pragma unroll
+                    for (int x = 0; x < kTileKeys / 16; ++x)
+                        mma_f16_ta(tmem + kColO + t * D, tmem + t * 128 + x * 8, smem_desc_mn(v + x * 2048), kIdO,
+                                   j > 0 || x > 0);
+                    if (j + 1 == steps[t]) mma_commit<false>(smem_u32(&bars.o_done[t]));
+                }
+                __syncwarp();
+                if (j + 1 < steps[t]) {
+                    ok = full(2 * j + 2);
+                    if (ok) scores(t, j + 1);
+                }
+            }
+            if (!ok) break;
+            // (no commit is left to arrive when the last product's has)
+            if (lane == 0 && j + 1 < nsteps) {
+                mma_commit<false>(smem_u32(&bars.kv_empty[(2 * j + 1) % kSlots<D>]));
+                mma_commit<false>(smem_u32(&bars.kv_empty[(2 * j + 2) % kSlots<D>]));
+            }
+            __syncwarp();
+        }
+        if (!ok) {
+            // wait, bounded, for the products in flight
+            if (lane == 0) {
+                mma_commit<false>(smem_u32(&bars.drain));
+                mbar_wait_drain(smem_u32(&bars.drain), 0, kDrainLimitNs);
+            }
+            __syncwarp();
+        }
+    } else {
+        // ------------------------------------------------ TMA copies
+        const uint32_t q0 = smem_u32(sq), kv0 = smem_u32(skv);
+        int loaded = 0;                                         // slots filled so far
+        int q_loaded = 0;
+        if (!a.stall_tma) {
+            for (int t = 0; t < 2; ++t) {
+                if (steps[t] == 0) continue;
+                if (lane == 0) {
+                    const uint32_t bar = smem_u32(&bars.q_full[t]);
+                    mbar_expect_tx(bar, tokens * a.group * 128 * (D / 64));
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x)
+                        tma_load_4d(q0 + t * kTileBytes<D> + x * kHalfBytes, &tm_q, 64 * x, 0,
+                                    seq.row0 + tok0 + t * tokens, h, bar);
+                }
+                q_loaded |= 1 << t;
+            }
+            for (int n = 0; n < 2 * nsteps; ++n) {
+                const int slot = n % kSlots<D>, base = lo + (n >> 1) * kTileKeys;
+                if (n >= kSlots<D> &&
+                    !warp_wait(&bars.kv_empty[slot], (n / kSlots<D> - 1) & 1))
+                    break;
+                const uint32_t bar = smem_u32(&bars.kv_full[slot]);
+                const CUtensorMap* map = n & 1 ? &tm_v : &tm_k;
+                const int boxes = a.table ? (min(kTileKeys, hi - base) + box - 1) / box : 1;
+                if (lane == 0) mbar_expect_tx(bar, boxes * box * 128 * (D / 64));
+                __syncwarp();
+                for (int e = lane; e < boxes * (D / 64); e += 32) {
+                    const int at = e % boxes, x = e / boxes;
+                    int page = 0, row = seq.row0 + base;
+                    if (a.table) {
+                        const int key = base + at * box;
+                        page = attn_page(a, b, key >> a.page_shift);
+                        if (page < 0) page = a.num_pages;       // outside the tensor: zeros
+                        row = key & (a.page_size - 1);
+                    }
+                    tma_load_4d(kv0 + slot * kTileBytes<D> + x * kHalfBytes + at * box * 128, map, 64 * x, row, h, page,
+                                bar);
+                }
+                __syncwarp();
+                ++loaded;
+            }
+        }
+        // a CTA that gave up leaves none of its copies in flight
+        if (*abort_flag && lane == 0) {
+            for (int t = 0; t < 2; ++t)
+                if (q_loaded >> t & 1) mbar_wait_drain(smem_u32(&bars.q_full[t]), 0, kDrainLimitNs);
+            for (int n = max(0, loaded - kSlots<D>); n < loaded; ++n)
+                mbar_wait_drain(smem_u32(&bars.kv_full[n % kSlots<D>]), (n / kSlots<D>) & 1, kDrainLimitNs);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) tmem_dealloc<false>(tmem, 512);
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static EncodeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+// bf16 [n3][n2][n1][d] with the given strides (elements), boxes of
+// 64 x b1 x b2 elements, 128-byte swizzle, zeros outside.
+bool encode(CUtensorMap* m, const void* p, int d, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t n3,
+            int64_t s3, int b1, int b2) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    // (the stride of a dimension of one entry is never used, but has to be valid)
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)n1, (cuuint64_t)n2, (cuuint64_t)n3};
+    const cuuint64_t strides[3] = {(cuuint64_t)(n1 > 1 ? s1 : d) * 2, (cuuint64_t)(n2 > 1 ? s2 : d) * 2,
+                                   (cuuint64_t)(n3 > 1 ? s3 : d) * 2};
+    const cuuint32_t boxes[4] = {64, (cuuint32_t)b1, (cuuint32_t)b2, 1}, ones[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p), dims, strides, boxes, ones,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
+    const int tokens = 128 / a.group;
+    const int box = a.table ? (a.page_size < kTileKeys ? a.page_size : kTileKeys) : kTileKeys;
+    CUtensorMap tq, tk, tv;
+    if (!encode(&tq, a.q, D, a.group, D, a.n_rows, a.q_stride, a.hkv, (int64_t)a.group * D, a.group, tokens) ||
+        !encode(&tk, a.k, D, a.page_size, a.row_stride, a.hkv, a.head_stride, a.num_pages, a.page_stride, box, 1) ||
+        !encode(&tv, a.v, D, a.page_size, a.row_stride, a.hkv, a.head_stride, a.num_pages, a.page_stride, box, 1))
+        return cudaErrorInvalidValue;
+    auto kern = attn_tc_kernel<D>;
+    const int bytes = (int)tc_smem_bytes<D>();
+    cudaError_t e = smem_attr((const void*)kern, bytes);
+    if (e != cudaSuccess) return e;
+    const int64_t items = attn_tc_items(a);
+    return launch_pdl(kern, dim3((unsigned)(items * a.hkv), a.splits), dim3(kTcThreads), bytes, s, tq, tk, tv, a, tokens,
+                      box);
+}
+
+}  // namespace
+
+int64_t attn_tc_items(const AttnArgs& a) {
+    const int per = 2 * (128 / a.group);
+    if (a.mode == kAttnPrompt) return a.n_rows / per + a.n_seqs;
+    if (a.mode == kAttnPrefix) return (a.n_seqs + per - 1) / per;
+    return a.n_seqs;
+}
+
+cudaError_t launch_attn_tc(int d, const AttnArgs& a, cudaStream_t s) {
+    return d == 64 ? launch<64>(a, s) : launch<128>(a, s);
+}
+
+}  // namespace colibri
