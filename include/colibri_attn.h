@@ -69,7 +69,7 @@ typedef struct {
  * call; whatever they hold, every access stays in bounds: seq_start is cut to
  * 0 .. n_rows, rows at or behind seq_start[n_seqs] belong to no sequence and
  * their outputs are left as they were, a kv_len beyond the page table is cut
- * to it and a negative one is 0, a page id outside 0 .. num_pages - 1 is
+ * to it (and to 2^31 - 2^20) and a negative one is 0, a page id outside 0 .. num_pages - 1 is
  * never written and reads as rows of zeros.
  */
 typedef struct {

@@ -44,6 +44,9 @@ struct AttnArgs {
     int part_slot;
     float* part_o;               // [slots][n_rows * hq][d]
     float* part_lse;             // [slots][n_rows * hq]
+    // launch_attn_decode: the cut rows' pieces (attn_decode_pieces() rows)
+    float* piece_o;
+    float* piece_lse;
     uint64_t wait_limit_ns;      // bound of every mbarrier wait
     int stall_tma;               // failure-detection tests only: issue no copy
 };
@@ -56,6 +59,12 @@ cudaError_t launch_attn_simt(DType dt, int d, const AttnArgs& a, cudaStream_t s)
 // 2 * (128 / group) tokens of one sequence.
 int64_t attn_tc_items(const AttnArgs& a);    // row tiles of the launch, per key head
 cudaError_t launch_attn_tc(int d, const AttnArgs& a, cudaStream_t s);
+
+// bf16 rows of suffix mode, equal shares of the key list per CTA, join
+// included.  part_o null: no prefix; otherwise the prefix left its rows in slots
+// 0 .. part_slot - 1, and slot part_slot is used for rows written in one piece.
+size_t attn_decode_pieces(int group);
+cudaError_t launch_attn_decode(int d, const AttnArgs& a, cudaStream_t s);
 
 // o, lse from the partial rows of `slots` key ranges (slot order).
 cudaError_t launch_attn_join(DType dt, int d, const AttnArgs& a, int slots, cudaStream_t s);

@@ -8,6 +8,10 @@
 
 namespace colibri {
 
+// Keys of a sequence at most, so that a tile behind the last one still has
+// int32 positions.
+constexpr int kMaxKeys = 0x7ff00000;
+
 // One sequence of a launch: rows row0 .. row0 + n - 1, keys kv0 .. kv - 1.
 struct AttnSeq {
     int row0, n, kv0, kv, raw;
@@ -28,7 +32,7 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
     }
     s.raw = a.kv_len ? max(__ldg(a.kv_len + b), 0) : s.n;
     const int64_t cap = a.table ? (int64_t)a.table_stride << a.page_shift : (int64_t)s.n;
-    s.kv = (int)min((int64_t)s.raw, cap);
+    s.kv = (int)min(min((int64_t)s.raw, cap), (int64_t)kMaxKeys);
     return s;
 }
 

@@ -95,17 +95,17 @@ colibri_status_t check_rope(const colibri_rope_t* r, int head_dim) {
 }
 
 // How a call's keys are split: ranges of the shared prefix and of the
-// sequences' own keys, each leaving a partial row per (row, head).
+// sequences' own keys, each leaving a partial row per (row, head).  shares: the
+// own keys run in equal shares per CTA (launch_attn_decode), which leaves at
+// most one partial row per (row, head) and the pieces of the cut ones.
 struct Plan {
     int prefix = 0;      // ranges of the prefix (0: no prefix launch)
     int own = 1;         // ranges of the sequences' own keys
-    bool direct() const { return prefix == 0 && own == 1; }
-    int slots() const { return prefix + own; }
-    size_t bytes(const colibri_seqs_t* s, int hq, int d) const {
-        if (direct()) return 0;
-        const size_t rows = (size_t)slots() * s->n_rows * hq;
-        return ((rows * 4 + 255) & ~(size_t)255) + rows * d * 4;
-    }
+    bool shares = false;
+    size_t rows = 0, pieces = 0;     // partial rows of a slot; piece rows
+    int slots() const { return prefix == 0 && own == 1 ? 0 : prefix + own; }
+    size_t lse_bytes() const { return ((slots() * rows + pieces) * 4 + 255) & ~(size_t)255; }
+    size_t bytes(int d) const { return lse_bytes() + (slots() * rows + pieces) * d * 4; }
 };
 
 // Ranges for `items` tiles over up to `keys` keys: enough for two CTAs per SM,
@@ -132,8 +132,14 @@ Plan make_plan(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq, in
     AttnArgs a{};
     a.n_rows = s->n_rows, a.n_seqs = s->n_seqs, a.group = hq / kv->n_kv_heads, a.mode = mode;
     Plan p;
-    p.own = choose_splits(row_tiles(a, on_tensor_cores(kv->dtype, mode)) * kv->n_kv_heads,
-                          std::max<int64_t>(keys - prefix_len, 1));
+    p.rows = (size_t)s->n_rows * hq;
+    if (kv->dtype == COLIBRI_DTYPE_BF16 && mode == kAttnSuffix) {
+        p.shares = true;
+        p.pieces = attn_decode_pieces(a.group);
+    } else {
+        p.own = choose_splits(row_tiles(a, on_tensor_cores(kv->dtype, mode)) * kv->n_kv_heads,
+                              std::max<int64_t>(keys - prefix_len, 1));
+    }
     if (prefix_len > 0) {
         a.mode = kAttnPrefix;
         p.prefix = choose_splits(row_tiles(a, on_tensor_cores(kv->dtype, a.mode)) * kv->n_kv_heads, prefix_len);
@@ -185,16 +191,18 @@ colibri_status_t check_attention(const colibri_kv_pages_t* kv, const colibri_seq
     return COLIBRI_OK;
 }
 
-void place_workspace(AttnArgs& a, const Plan& p, void* ws) {
-    if (p.direct()) return;
-    const size_t rows = (size_t)p.slots() * a.n_rows * a.hq;
-    a.part_lse = static_cast<float*>(ws);
-    a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ((rows * 4 + 255) & ~(size_t)255));
+void place_workspace(AttnArgs& a, const Plan& p, int d, void* ws) {
+    if (p.slots() + p.pieces == 0) return;
+    float* lse = static_cast<float*>(ws);
+    float* o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.lse_bytes());
+    a.piece_lse = lse + p.slots() * p.rows;
+    a.piece_o = o + p.slots() * p.rows * d;
+    if (p.slots() > 0) a.part_lse = lse, a.part_o = o;
 }
 
 colibri_status_t run_attention(AttnArgs a, const Plan& p, int dtype, int d, int prefix_len,
                                const int32_t* prefix_table, void* ws, cudaStream_t s) {
-    place_workspace(a, p, ws);
+    place_workspace(a, p, d, ws);
     a.prefix_len = prefix_len;
     cudaError_t e = cudaSuccess;
     if (p.prefix > 0) {
@@ -208,10 +216,19 @@ colibri_status_t run_attention(AttnArgs a, const Plan& p, int dtype, int d, int 
     }
     a.splits = p.own;
     a.part_slot = p.prefix;
-    if (e == cudaSuccess) e = launch_attention(dtype, d, a, s);
-    if (e == cudaSuccess && !p.direct()) e = launch_attn_join(dtype_of(dtype), d, a, p.slots(), s);
+    if (e == cudaSuccess && p.shares) {
+        e = launch_attn_decode(d, a, s);
+    } else {
+        if (e == cudaSuccess) e = launch_attention(dtype, d, a, s);
+        if (e == cudaSuccess && p.slots() > 0) e = launch_attn_join(dtype_of(dtype), d, a, p.slots(), s);
+    }
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
+}
+
+// The list of all keys of all heads is counted in 64 bits, times the CTAs.
+bool countable(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int n_q_heads) {
+    return (double)s->n_seqs * s->table_stride * kv->page_size * n_q_heads <= 1e15;
 }
 
 colibri_status_t check_prompt(const colibri_kv_pages_t* kv, const colibri_seqs_t* seqs, int n_q_heads) {
@@ -220,6 +237,7 @@ colibri_status_t check_prompt(const colibri_kv_pages_t* kv, const colibri_seqs_t
     if (st == COLIBRI_OK) st = check_seqs(seqs, n_q_heads);
     if (st == COLIBRI_OK) st = check_kv(kv, seqs->page_table != nullptr);
     if (st != COLIBRI_OK) return st;
+    if (seqs->page_table && !countable(kv, seqs, n_q_heads)) return COLIBRI_ERR_UNSUPPORTED;
     // packed keys: the call's own rows
     if (!seqs->page_table && (seqs->kv_len || (seqs->n_rows > 0 && kv->page_size != seqs->n_rows)))
         return COLIBRI_ERR_INVALID_ARG;
@@ -235,6 +253,7 @@ colibri_status_t check_decode(const colibri_kv_pages_t* kv, const colibri_seqs_t
     if (st == COLIBRI_OK) st = check_kv(kv, true);
     if (st != COLIBRI_OK) return st;
     if (prefix_len < 0 || prefix_len % kv->page_size) return COLIBRI_ERR_INVALID_ARG;
+    if (!countable(kv, seqs, n_q_heads)) return COLIBRI_ERR_UNSUPPORTED;
     return COLIBRI_OK;
 }
 
@@ -365,7 +384,7 @@ colibri_status_t colibri_attention_prompt_workspace(const colibri_kv_pages_t* kv
     const colibri_status_t st = check_prompt(kv, seqs, n_q_heads);
     if (st != COLIBRI_OK) return st;
     const int mode = seqs->seq_start ? kAttnPrompt : kAttnSuffix;
-    *bytes = make_plan(kv, seqs, n_q_heads, mode, 0).bytes(seqs, n_q_heads, kv->head_dim);
+    *bytes = make_plan(kv, seqs, n_q_heads, mode, 0).bytes(kv->head_dim);
     return COLIBRI_OK;
 }
 
@@ -379,7 +398,7 @@ colibri_status_t colibri_attention_prompt(const colibri_kv_pages_t* kv, const co
     if (st != COLIBRI_OK) return st;
     const int mode = seqs->seq_start ? kAttnPrompt : kAttnSuffix;
     const Plan p = make_plan(kv, seqs, n_q_heads, mode, 0);
-    const size_t need = p.bytes(seqs, n_q_heads, kv->head_dim);
+    const size_t need = p.bytes(kv->head_dim);
     if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255)))
         return COLIBRI_ERR_INVALID_ARG;
     if (seqs->n_rows == 0 || seqs->n_seqs == 0) return COLIBRI_OK;
@@ -395,7 +414,7 @@ colibri_status_t colibri_attention_decode_workspace(const colibri_kv_pages_t* ca
     const colibri_status_t st = check_decode(cache, seqs, n_q_heads, prefix_len);
     if (st != COLIBRI_OK) return st;
     *bytes = make_plan(cache, seqs, n_q_heads, kAttnSuffix, prefix_len)
-                 .bytes(seqs, n_q_heads, cache->head_dim);
+                 .bytes(cache->head_dim);
     return COLIBRI_OK;
 }
 
@@ -412,7 +431,7 @@ colibri_status_t colibri_attention_decode(const colibri_kv_pages_t* cache, const
     if ((prefix_len > 0) != (prefix_table != nullptr) || ((uintptr_t)prefix_table & 3))
         return COLIBRI_ERR_INVALID_ARG;
     const Plan p = make_plan(cache, seqs, n_q_heads, kAttnSuffix, prefix_len);
-    const size_t need = p.bytes(seqs, n_q_heads, cache->head_dim);
+    const size_t need = p.bytes(cache->head_dim);
     if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255)))
         return COLIBRI_ERR_INVALID_ARG;
     if (seqs->n_rows == 0) return COLIBRI_OK;
