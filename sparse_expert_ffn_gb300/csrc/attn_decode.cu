@@ -111,11 +111,29 @@ __device__ __forceinline__ uint32_t bf16x2(float x, float y) {
 // page ids of up to 32 page parts ahead lie one per lane.
 template <int D>
 struct Stream {
-    int b, h, lo, hi;          // sequence, key head, keys of the piece
+    static constexpr int kChunks = D / 8;                          // 16-byte chunks of a row
+    static constexpr int kRowsPer = 32 / kChunks;                  // rows that a pass of the warp covers
+    static constexpr int kPasses = kStepKeys<D> / kRowsPer;
+    int b, lo, hi;             // sequence, keys of the piece
     int parts;                 // pages that a step touches
     int window;                // first step whose page parts the lanes hold
     int id;
+    const __nv_bfloat16* k;    // this lane's chunk of row 0 of the head in page 0 (packed: key 0)
+    const __nv_bfloat16* v;
+    uint32_t dst;              // this lane's place in a stage, pass 0
 
+    __device__ __forceinline__ void begin(const AttnArgs& a, int seq, int h, int first, int end) {
+        const int lane = threadIdx.x & 31, chunk = lane % kChunks, row = lane / kChunks;
+        b = seq, lo = first, hi = end;
+        int64_t at = (int64_t)h * a.head_stride + chunk * 8;
+        if (!a.table) at += (int64_t)b * a.row_stride;             // packed rows: the row's own key
+        k = static_cast<const __nv_bfloat16*>(a.k) + at;
+        v = static_cast<const __nv_bfloat16*>(a.v) + at;
+        // (the chunk's swizzled place: the row's low bits of later passes are xored in copy())
+        dst = row * (D * 2) + ((chunk ^ row) << 4);
+        parts = a.page_size < kStepKeys<D> ? kStepKeys<D> / a.page_size : 1;
+        if (a.table) fill(a, 0);
+    }
     __device__ __forceinline__ int first_key(int step) const {
         return lo + (step * kWarps + (int)(threadIdx.x >> 5)) * kStepKeys<D>;
     }
@@ -126,29 +144,51 @@ struct Stream {
         id = key < hi ? attn_page(a, b, key >> a.page_shift) : -1;
     }
     __device__ __forceinline__ void copy(const AttnArgs& a, int step, uint32_t stage) {
-        constexpr int kChunks = D / 8;                             // 16-byte chunks of a row
-        constexpr int kRowsPer = 32 / kChunks;                     // rows that a pass of the warp covers
-        const int lane = threadIdx.x & 31, key0 = first_key(step);
+        const int lane = threadIdx.x & 31, key0 = first_key(step), row0 = lane / kChunks;
         if (a.table && step >= window + 32 / parts) fill(a, step);
-        const int chunk = lane % kChunks;
-        const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + (int64_t)h * a.head_stride + chunk * 8;
-        const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + (int64_t)h * a.head_stride + chunk * 8;
+        // rows of one pass lie kRowsPer apart: their swizzle differs by that in
+        // the row's low three bits
+        const auto place = [&](int i) {
+            return stage + ((dst + i * kRowsPer * (D * 2)) ^ (((i * kRowsPer) & 7) << 4));
+        };
+        if (a.table && parts > 1) {
 #pragma unroll
-        for (int i = 0; i < kStepKeys<D> / kRowsPer; ++i) {
-            const int row = i * kRowsPer + lane / kChunks, key = key0 + row;
-            int64_t at;
-            bool there = key < hi;
-            if (a.table) {
+            for (int i = 0; i < kPasses; ++i) {
+                const int row = i * kRowsPer + row0, key = key0 + row;
                 const int page = __shfl_sync(0xffffffffu, id, (step - window) * parts + row / (kStepKeys<D> / parts));
-                there = there && page >= 0;
-                at = (int64_t)page * a.page_stride + (int64_t)(key & (a.page_size - 1)) * a.row_stride;
-            } else {
-                at = (int64_t)(b + key) * a.row_stride;           // packed rows: one key, the row's own
+                const bool there = key < hi && page >= 0;
+                const int64_t at = there ? (int64_t)page * a.page_stride +
+                                               (int64_t)(key & (a.page_size - 1)) * a.row_stride : 0;
+                cp16(place(i), k + at, there);
+                cp16(place(i) + kStageBytes / 2, v + at, there);
             }
-            if (!there) at = 0;
-            const uint32_t dst = stage + row * (D * 2) + ((chunk ^ (row & 7)) << 4);
-            cp16(dst, k + at, there);
-            cp16(dst + kStageBytes / 2, v + at, there);
+            return;
+        }
+        // the whole step lies in one page (or in packed rows)
+        int64_t at = (int64_t)row0 * a.row_stride;
+        bool page_there = true;
+        if (a.table) {
+            const int page = __shfl_sync(0xffffffffu, id, step - window);
+            page_there = page >= 0;
+            at += (int64_t)max(page, 0) * a.page_stride + (int64_t)(key0 & (a.page_size - 1)) * a.row_stride;
+        }
+        const int64_t pass = (int64_t)kRowsPer * a.row_stride;
+        if (page_there && key0 + kStepKeys<D> <= hi) {
+            const __nv_bfloat16 *kp = k + at, *vp = v + at;
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                cp16(place(i), kp, true);
+                cp16(place(i) + kStageBytes / 2, vp, true);
+                kp += pass, vp += pass;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const bool there = page_there && key0 + i * kRowsPer + row0 < hi;
+                const int64_t off = there ? at + i * pass : 0;
+                cp16(place(i), k + off, there);
+                cp16(place(i) + kStageBytes / 2, v + off, there);
+            }
         }
     }
 };
@@ -215,12 +255,8 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(AttnArgs a,
         const int h = item / tiles, r0 = (item % tiles) * ROWS;
         const int count = (int)min((int64_t)(units - step0), u1 - u);   // units of this piece
         Stream<D> st;
-        st.b = b, st.h = h;
-        st.lo = sq.kv0 + step0 * kUnitKeys<D>;
-        st.hi = min(sq.kv, st.lo + count * kUnitKeys<D>);
-        st.parts = a.page_size < KS ? KS / a.page_size : 1;
-        st.id = -1, st.window = 0;
-        if (a.table) st.fill(a, 0);
+        st.begin(a, b, h, sq.kv0 + step0 * kUnitKeys<D>,
+                 min(sq.kv, sq.kv0 + (step0 + count) * kUnitKeys<D>));
 #pragma unroll
         for (int s = 0; s < kStages - 1; ++s) {
             if (s < count) st.copy(a, s, ring + s * kStageBytes);
@@ -279,24 +315,31 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(AttnArgs a,
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 float top[2] = {-INFINITY, -INFINITY};
+                if (left < KS) {
+#pragma unroll
+                    for (int n = 0; n < KS / 8; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (n * 8 + 2 * (lane & 3) + (e & 1) >= left) s[t][n][e] = -INFINITY;
+                }
 #pragma unroll
                 for (int n = 0; n < KS / 8; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        s[t][n][e] = n * 8 + 2 * (lane & 3) + (e & 1) < left ? s[t][n][e] * a.scale_log2 : -INFINITY;
-                        top[e >> 1] = fmaxf(top[e >> 1], s[t][n][e]);
-                    }
+                    for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[t][n][e]);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
                     top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-                    top[r] = fmaxf(top[r], m[t][r]);
+                    top[r] *= a.scale_log2;
                 }
-                if (__any_sync(0xffffffffu, top[0] > m[t][0] || top[1] > m[t][1])) {
+                // the reference maximum moves only when a row's has grown by
+                // more than 2^8 (weights below 2^8 are held as exactly)
+                if (__any_sync(0xffffffffu, top[0] > m[t][0] + 8.f || top[1] > m[t][1] + 8.f)) {
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const float keep = top[r] == -INFINITY ? 1.f : ex2(m[t][r] - top[r]);
-                        m[t][r] = top[r];
+                        const bool grow = top[r] > m[t][r];
+                        const float keep = grow ? ex2(m[t][r] - top[r]) : 1.f;
+                        if (grow) m[t][r] = top[r];
                         l[t][r] *= keep;
 #pragma unroll
                         for (int x = 0; x < D / 8; ++x) o[t][x][2 * r] *= keep, o[t][x][2 * r + 1] *= keep;
@@ -307,7 +350,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(AttnArgs a,
                 for (int n = 0; n < KS / 8; ++n) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        s[t][n][e] = ex2(s[t][n][e] - ref[e >> 1]);
+                        s[t][n][e] = ex2(fmaf(s[t][n][e], a.scale_log2, -ref[e >> 1]));
                         l[t][e >> 1] += s[t][n][e];
                     }
                     pf[t][n / 2][(n & 1) * 2] = bf16x2(s[t][n][0], s[t][n][1]);
