@@ -60,14 +60,15 @@ cudaError_t launch_attn_simt(DType dt, int d, const AttnArgs& a, cudaStream_t s)
 int64_t attn_tc_items(const AttnArgs& a);    // row tiles of the launch, per key head
 cudaError_t launch_attn_tc(int d, const AttnArgs& a, cudaStream_t s);
 
-// bf16 rows of suffix mode, equal shares of the key list per CTA, join
-// included.  part_o null: no prefix; otherwise the prefix left its rows in slots
-// 0 .. part_slot - 1, and slot part_slot is used for rows written in one piece.
+// bf16 rows of suffix mode, equal shares of the key list per CTA.  part_o null:
+// no prefix; otherwise slot part_slot takes the rows written in one piece.
 size_t attn_decode_pieces(int group);
 cudaError_t launch_attn_decode(int d, const AttnArgs& a, cudaStream_t s);
 
-// o, lse from the partial rows of `slots` key ranges (slot order).
-cudaError_t launch_attn_join(DType dt, int d, const AttnArgs& a, int slots, cudaStream_t s);
+// o, lse from the partial rows of `slots` slots, and of the pieces that
+// launch_attn_decode left (shares; slot part_slot then holds the rows it wrote
+// whole, and without a prefix those are not touched).
+cudaError_t launch_attn_join(DType dt, int d, const AttnArgs& a, int slots, bool shares, cudaStream_t s);
 
 // Norm, rotation and placement of q, k, v rows.
 struct AppendArgs {

@@ -105,6 +105,53 @@ __device__ __forceinline__ void attn_split(const AttnArgs& a, int sp, int kt, in
     *hi = min(end, kv0 + min(tiles, (sp + 1) * per) * kt);
 }
 
+// Equal shares of the key list (attn_decode.cu): rows of a group's row tile,
+// keys of a unit, CTAs that share the list (2 per SM), units of a share at least.
+__host__ __device__ constexpr int row_tile(int group) { return group <= 16 ? 16 : 32; }
+__host__ __device__ constexpr int row_tiles(int group) { return (group + row_tile(group) - 1) / row_tile(group); }
+
+template <int D> constexpr int kUnitKeys = 8192 / D;
+constexpr int kShareCtas = 304;
+constexpr int kMinUnits = 2;
+
+// Units of sequence b per (head, row tile).
+template <int D>
+__device__ __forceinline__ int seq_units(const AttnArgs& a, int b) {
+    const AttnSeq s = attn_seq(a, b);
+    return s.kv > s.kv0 ? (s.kv - s.kv0 + kUnitKeys<D> - 1) / kUnitKeys<D> : 0;
+}
+
+// The whole list: its length, and the units before sequence `upto`.  Called by
+// a whole warp.
+template <int D>
+__device__ __forceinline__ void count_units(const AttnArgs& a, int per_seq, int upto, int64_t* total,
+                                            int64_t* before) {
+    int64_t all = 0, part = 0;
+    for (int b = threadIdx.x & 31; b < a.n_seqs; b += 32) {
+        const int64_t u = (int64_t)seq_units<D>(a, b) * per_seq;
+        all += u;
+        if (b < upto) part += u;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        part += __shfl_xor_sync(0xffffffffu, part, o);
+    }
+    *total = all;
+    *before = part;
+}
+
+// CTAs that share the list, share c's first unit, and the share that unit u
+// falls into.
+__device__ __forceinline__ int share_count(int64_t total, int ctas) {
+    const int64_t most = (total + kMinUnits - 1) / kMinUnits;
+    return most < ctas ? (int)most : ctas;
+}
+__device__ __forceinline__ int64_t share_begin(int64_t total, int shares, int c) { return total * c / shares; }
+__device__ __forceinline__ int share_of(int64_t total, int shares, int64_t u) {
+    return (int)(((u + 1) * shares - 1) / total);
+}
+
 constexpr float kLn2 = 0.69314718055994530942f;
 
 __device__ __forceinline__ float ex2(float x) {

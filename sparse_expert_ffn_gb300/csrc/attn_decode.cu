@@ -33,53 +33,9 @@ constexpr int kWarps = 4;
 constexpr int kDecThreads = 32 * kWarps;
 constexpr int kStages = 3;
 template <int D> constexpr int kStepKeys = 2048 / D;              // keys of a warp's step
-template <int D> constexpr int kUnitKeys = kWarps * kStepKeys<D>;
+static_assert(kUnitKeys<64> == kWarps * kStepKeys<64> && kUnitKeys<128> == kWarps * kStepKeys<128>, "a unit is a step of every warp");
 constexpr int kStageBytes = 8192;                                 // K then V of one step
 constexpr int kRingBytes = kStages * kStageBytes;
-constexpr int kCtas = 304;                                        // 2 per SM
-constexpr int kMinUnits = 2;                                      // units of a CTA's share at least
-
-__host__ __device__ constexpr int row_tile(int group) { return group <= 16 ? 16 : 32; }
-__host__ __device__ constexpr int row_tiles(int group) { return (group + row_tile(group) - 1) / row_tile(group); }
-
-// Units of sequence b per (head, row tile).
-template <int D>
-__device__ __forceinline__ int seq_units(const AttnArgs& a, int b) {
-    const AttnSeq s = attn_seq(a, b);
-    return s.kv > s.kv0 ? (s.kv - s.kv0 + kUnitKeys<D> - 1) / kUnitKeys<D> : 0;
-}
-
-// The whole list: its length, and the units before sequence `upto`.  Called by
-// a whole warp.
-template <int D>
-__device__ __forceinline__ void count_units(const AttnArgs& a, int per_seq, int upto, int64_t* total,
-                                            int64_t* before) {
-    int64_t all = 0, part = 0;
-    for (int b = threadIdx.x & 31; b < a.n_seqs; b += 32) {
-        const int64_t u = (int64_t)seq_units<D>(a, b) * per_seq;
-        all += u;
-        if (b < upto) part += u;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        all += __shfl_xor_sync(0xffffffffu, all, o);
-        part += __shfl_xor_sync(0xffffffffu, part, o);
-    }
-    *total = all;
-    *before = part;
-}
-
-// CTAs that share the list, share c's first unit, and the share that unit u
-// falls into.
-__device__ __forceinline__ int share_count(int64_t total, int ctas) {
-    const int64_t most = (total + kMinUnits - 1) / kMinUnits;
-    return most < ctas ? (int)most : ctas;
-}
-__device__ __forceinline__ int64_t share_begin(int64_t total, int shares, int c) { return total * c / shares; }
-__device__ __forceinline__ int share_of(int64_t total, int shares, int64_t u) {
-    return (int)(((u + 1) * shares - 1) / total);
-}
-
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) {
     const int n = there ? 16 : 0;                                  // 0: the 16 bytes become zeros
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
@@ -432,78 +388,17 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(AttnArgs a,
     }
 }
 
-// One warp per (row, head): the prefix's slots, then the row's own keys (one
-// whole result, or pieces in key order).  Rows that one CTA wrote directly
-// (no prefix, one piece) are left alone.
-template <int D>
-__global__ void attn_decode_join_kernel(AttnArgs a, int per_seq, int ctas) {
-    pdl_enter();
-    const int lane = threadIdx.x & 31;
-    const int64_t total_rows = (int64_t)a.n_rows * a.hq;
-    const int64_t flat = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    if (flat >= total_rows) return;
-    const int b = (int)(flat / a.hq), head = (int)(flat % a.hq);
-    const int h = head / a.group, g = head % a.group, ROWS = row_tile(a.group);
-    const int item = h * row_tiles(a.group) + g / ROWS;
-    int64_t total, first;
-    count_units<D>(a, per_seq, b, &total, &first);
-    const int units = seq_units<D>(a, b);
-    int c0 = 0, c1 = -1, shares = 0;
-    if (units > 0) {
-        shares = share_count(total, ctas);
-        first += (int64_t)item * units;
-        c0 = share_of(total, shares, first);
-        c1 = share_of(total, shares, first + units - 1);
-    }
-    const int prefix = a.part_slot;                                // slots of the prefix
-    if (c0 == c1 && prefix == 0) return;
-    constexpr int V = D / 32;
-    float acc[V] = {};
-    float top = -INFINITY, sum = 0.f;
-    const auto add = [&](const float* lse, const float* rows) {
-        const float w2 = *lse;
-        if (w2 == -INFINITY) return;                               // rows of no key are not written
-        const float mn = fmaxf(top, w2), keep = ex2(top - mn), w = ex2(w2 - mn);
-        top = mn;
-        sum = sum * keep + w;
-#pragma unroll
-        for (int c = 0; c < V; ++c) acc[c] = fmaf(w, rows[lane * V + c], acc[c] * keep);
-    };
-    for (int s = 0; s < prefix; ++s) {
-        const int64_t at = s * total_rows + flat;
-        add(a.part_lse + at, a.part_o + at * D);
-    }
-    if (c0 == c1) {
-        const int64_t at = prefix * total_rows + flat;
-        add(a.part_lse + at, a.part_o + at * D);
-    } else {
-        for (int c = c0; c <= c1; ++c) {
-            const int last = c == c0 && share_begin(total, shares, c) < first;
-            const int64_t at = ((int64_t)c * 2 + last) * ROWS + g % ROWS;
-            add(a.piece_lse + at, a.piece_o + at * D);
-        }
-    }
-    const float inv = sum > 0.f ? 1.f / sum : sum;
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + (int64_t)b * a.o_stride + (int64_t)head * D + lane * V;
-#pragma unroll
-    for (int c = 0; c < V; ++c) out[c] = __float2bfloat16_rn(acc[c] * inv);
-    if (lane == 0 && a.lse) a.lse[flat] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
-}
-
 template <int D, int MT>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     auto kern = attn_decode_kernel<D, MT>;
     const int bytes = kWarps * kRingBytes, per_seq = a.hkv * row_tiles(a.group);
     cudaError_t e = smem_attr((const void*)kern, bytes);
-    if (e == cudaSuccess) e = launch_pdl(kern, dim3(kCtas), dim3(kDecThreads), bytes, s, a, per_seq);
-    if (e != cudaSuccess) return e;
-    const int64_t rows = (int64_t)a.n_rows * a.hq;
-    return launch_pdl(attn_decode_join_kernel<D>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, a, per_seq, kCtas);
+    return e != cudaSuccess ? e : launch_pdl(kern, dim3(kShareCtas), dim3(kDecThreads), bytes, s, a, per_seq);
 }
 
 }  // namespace
 
-size_t attn_decode_pieces(int group) { return (size_t)kCtas * 2 * row_tile(group); }
+size_t attn_decode_pieces(int group) { return (size_t)kShareCtas * 2 * row_tile(group); }
 
 cudaError_t launch_attn_decode(int d, const AttnArgs& a, cudaStream_t s) {
     if (d == 64) return a.group <= 16 ? launch<64, 1>(a, s) : launch<64, 2>(a, s);

@@ -108,11 +108,15 @@ struct Plan {
     size_t bytes(int d) const { return lse_bytes() + (slots() * rows + pieces) * d * 4; }
 };
 
-// Ranges for `items` tiles over up to `keys` keys: enough for two CTAs per SM,
-// none under 256 keys.
-int choose_splits(int64_t items, int64_t keys) {
-    const int64_t want = (2 * kSms + items - 1) / std::max<int64_t>(items, 1);
-    return (int)std::max<int64_t>(1, std::min({want, (keys + 255) / 256, (int64_t)kMaxSplits}));
+// Key ranges per row tile of a launch with `items` tiles over up to `keys`
+// keys, of which the GPU holds `slots` at a time: as many as one wave takes, of
+// at least two 128-key steps each.  More tiles than that are not split: the
+// partial rows' way through memory costs more than an even last wave gives
+// (2560 rows in 3 chunks over up to 9000 keys: 233 us in one range, 355 us in
+// the number that evened the waves).
+int choose_splits(int64_t items, int64_t keys, int slots) {
+    const int64_t most = std::max<int64_t>(1, keys / 256);
+    return (int)std::max<int64_t>(1, std::min({slots / std::max<int64_t>(items, 1), most, (int64_t)kMaxSplits}));
 }
 
 // Row tiles of a launch and key head.
@@ -127,6 +131,12 @@ int64_t row_tiles(const AttnArgs& a, bool tensor_cores) {
 // bf16 prompts and prefixes run on the tensor cores.
 bool on_tensor_cores(int dtype, int mode) { return dtype == COLIBRI_DTYPE_BF16 && mode != kAttnSuffix; }
 
+// (one tensor-core CTA per SM, two of the CUDA-core kernel)
+int splits_for(const AttnArgs& a, const colibri_kv_pages_t* kv, int64_t keys) {
+    const bool tc = on_tensor_cores(kv->dtype, a.mode);
+    return choose_splits(row_tiles(a, tc) * kv->n_kv_heads, keys, tc ? kSms : 2 * kSms);
+}
+
 Plan make_plan(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq, int mode, int prefix_len) {
     const int64_t keys = s->page_table ? (int64_t)s->table_stride * kv->page_size : s->n_rows;
     AttnArgs a{};
@@ -137,12 +147,11 @@ Plan make_plan(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq, in
         p.shares = true;
         p.pieces = attn_decode_pieces(a.group);
     } else {
-        p.own = choose_splits(row_tiles(a, on_tensor_cores(kv->dtype, mode)) * kv->n_kv_heads,
-                              std::max<int64_t>(keys - prefix_len, 1));
+        p.own = splits_for(a, kv, std::max<int64_t>(keys - prefix_len, 1));
     }
     if (prefix_len > 0) {
         a.mode = kAttnPrefix;
-        p.prefix = choose_splits(row_tiles(a, on_tensor_cores(kv->dtype, a.mode)) * kv->n_kv_heads, prefix_len);
+        p.prefix = splits_for(a, kv, prefix_len);
     }
     return p;
 }
@@ -216,12 +225,9 @@ colibri_status_t run_attention(AttnArgs a, const Plan& p, int dtype, int d, int 
     }
     a.splits = p.own;
     a.part_slot = p.prefix;
-    if (e == cudaSuccess && p.shares) {
-        e = launch_attn_decode(d, a, s);
-    } else {
-        if (e == cudaSuccess) e = launch_attention(dtype, d, a, s);
-        if (e == cudaSuccess && p.slots() > 0) e = launch_attn_join(dtype_of(dtype), d, a, p.slots(), s);
-    }
+    if (e == cudaSuccess) e = p.shares ? launch_attn_decode(d, a, s) : launch_attention(dtype, d, a, s);
+    if (e == cudaSuccess && (p.shares || p.slots() > 0))
+        e = launch_attn_join(dtype_of(dtype), d, a, p.shares ? p.prefix : p.slots(), p.shares, s);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
 }

@@ -1,5 +1,4 @@
-// Attention on CUDA cores, float32 arithmetic throughout: float32 layers, and
-// the joining of key ranges for every kernel.
+// Attention on CUDA cores, float32 arithmetic throughout: float32 layers.
 //
 // One CTA takes a tile of ROWS (row, head of the group) rows of one sequence
 // and key head and walks its keys 64 at a time:
@@ -234,61 +233,6 @@ cudaError_t launch_simt(const AttnArgs& a, cudaStream_t s) {
     return launch_pdl(kern, dim3((unsigned)items, a.hkv, a.splits), dim3(kThreads), bytes, s, a);
 }
 
-// One warp per (row, head): the slots' log2-sums give each slot's weight, the
-// weighted rows add up in slot order.  A slot whose range held no key has
-// log2-sum -infinity and its rows, never written, are not read.
-template <typename T, int D>
-__global__ void attn_join_kernel(AttnArgs a, int slots) {
-    pdl_enter();
-    const int lane = threadIdx.x & 31;
-    const int64_t total = (int64_t)a.n_rows * a.hq;
-    const int64_t flat = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    if (flat >= total) return;
-    const int row = (int)(flat / a.hq), head = (int)(flat % a.hq);
-    if (a.mode == kAttnPrompt) {
-        // rows of no sequence have no partial rows and keep their output
-        bool live = false;
-        for (int b = lane; b < a.n_seqs; b += 32)
-            live |= row >= max(__ldg(a.seq_start + b), 0) && row < __ldg(a.seq_start + b + 1);
-        if (!__any_sync(0xffffffffu, live)) return;
-    }
-    float top = -INFINITY;
-    for (int s = lane; s < slots; s += 32) top = fmaxf(top, a.part_lse[s * total + flat]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    constexpr int V = D / 32;
-    float acc[V] = {};
-    float sum = 0.f;
-    if (top != -INFINITY) {
-#pragma unroll 4
-        for (int s = 0; s < slots; ++s) {
-            const float w2 = a.part_lse[s * total + flat];
-            if (w2 == -INFINITY) continue;
-            const float w = ex2(w2 - top);
-            sum += w;
-            const float* p = a.part_o + (s * total + flat) * D + lane * V;
-#pragma unroll
-            for (int c = 0; c < V; c += 2) {
-                const float2 v = *reinterpret_cast<const float2*>(p + c);
-                acc[c] = fmaf(w, v.x, acc[c]);
-                acc[c + 1] = fmaf(w, v.y, acc[c + 1]);
-            }
-        }
-    }
-    const float inv = sum > 0.f ? 1.f / sum : sum;
-    T* out = static_cast<T*>(a.o) + (int64_t)row * a.o_stride + (int64_t)head * D + lane * V;
-#pragma unroll
-    for (int c = 0; c < V; ++c) out[c] = from_f32<T>(acc[c] * inv);
-    if (lane == 0 && a.lse) a.lse[flat] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
-}
-
-template <typename T, int D>
-cudaError_t launch_join(const AttnArgs& a, int slots, cudaStream_t s) {
-    const int64_t total = (int64_t)a.n_rows * a.hq;
-    if (total == 0) return cudaSuccess;
-    return launch_pdl(attn_join_kernel<T, D>, dim3((unsigned)((total + 3) / 4)), dim3(128), 0, s, a, slots);
-}
-
 }  // namespace
 
 // Tiles of 16 rows for single tokens (a group of at most 16 heads), 64 rows
@@ -304,13 +248,6 @@ cudaError_t launch_attn_simt(DType dt, int d, const AttnArgs& a, cudaStream_t s)
     if (d == 64)
         return few ? launch_simt<__nv_bfloat16, 16, 64>(a, s) : launch_simt<__nv_bfloat16, 64, 64>(a, s);
     return few ? launch_simt<__nv_bfloat16, 16, 128>(a, s) : launch_simt<__nv_bfloat16, 64, 128>(a, s);
-}
-
-cudaError_t launch_attn_join(DType dt, int d, const AttnArgs& a, int slots, cudaStream_t s) {
-    if (dt == DType::F32)
-        return d == 64 ? launch_join<float, 64>(a, slots, s) : launch_join<float, 128>(a, slots, s);
-    return d == 64 ? launch_join<__nv_bfloat16, 64>(a, slots, s)
-                   : launch_join<__nv_bfloat16, 128>(a, slots, s);
 }
 
 }  // namespace colibri

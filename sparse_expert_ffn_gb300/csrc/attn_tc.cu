@@ -16,7 +16,8 @@
 // touch it.
 //
 // Roles: warps 0-3 and 4-7 the softmax of the two tiles (one row per thread,
-// no shuffles), warp 8 issues the MMAs, warp 9 the TMA copies (K and V tiles
+// no shuffles; they take over registers of the others, since a row's 128
+// scores stay in registers), warp 8 issues the MMAs, warp 9 the TMA copies (K and V tiles
 // alternate in a ring; with pages, one box per page).  The MMAs of one tile run
 // while the other tile is in its softmax.  A commit after S(j + 1) also covers
 // the O += P V of step j issued before it, so the one barrier per tile tells the
@@ -36,7 +37,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kTcThreads = 320;
+constexpr int kTcThreads = 384;               // 2 softmax warpgroups, 1 of MMA issue and copies
 constexpr int kTileKeys = 128;
 constexpr uint32_t kHalfBytes = 128 * 128;      // 128 rows of one 128-byte swizzle atom
 
@@ -55,7 +56,6 @@ struct TcBars {
     uint32_t tmem;
     int item[2];
     int abort;
-    int status;
 };
 
 template <int D>
@@ -82,6 +82,48 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
         : "r"(taddr));
 }
 
+// One lane of the (whole) warp; the form that lets the compiler keep what the
+// lane issues in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+// A value that every lane holds, as a uniform one.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// Two f32 operations per instruction.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    return v;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // B operand with the MN index contiguous (V: rows are keys, the MMA's K; the
 // 64-column halves are kHalfBytes apart, 8-key groups 1024 bytes).
 __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
@@ -94,6 +136,24 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
     return d;
 }
 
+// mbar_wait for a chain of short waits: the clock and the abort flag are looked
+// at once in 64 tries (reading the global timer takes longer than most waits).
+__device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                             uint64_t limit_ns) {
+    uint64_t t0 = 0;
+    for (int i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (i & 63) continue;
+        if (*abort_flag) return false;
+        const uint64_t now = globaltimer();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > limit_ns) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -103,7 +163,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint8_t* sq = smem;
     uint8_t* skv = smem + 2 * kTileBytes<D>;
     TcBars& bars = *reinterpret_cast<TcBars*>(skv + kSlots<D> * kTileBytes<D>);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
     if (tid == 0) {
         for (int t = 0; t < 2; ++t) {
@@ -118,7 +178,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         mbar_init(smem_u32(&bars.drain), 1);
         bars.abort = 0;
-        bars.status = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     pdl_enter();
@@ -142,22 +201,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int end = first < seq.n ? min(hi, attn_limit_max(a, seq, last)) : lo;
         steps[t] = end > lo ? (end - lo + kTileKeys - 1) / kTileKeys : 0;
     }
+    lo = uniform(lo), hi = uniform(hi), steps[0] = uniform(steps[0]), steps[1] = uniform(steps[1]);
     const int nsteps = max(steps[0], steps[1]);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = bars.tmem;
+    const uint32_t tmem = uniform(bars.tmem);
     volatile int* abort_flag = &bars.abort;
-    int* status = &bars.status;
     const uint64_t limit = a.wait_limit_ns;
     constexpr uint32_t kColO = 256;                             // S0 0, S1 128, O0 256, O1 256 + D
     // one outcome for the whole warp, so that no collective runs without its lanes
     const auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag, status, limit)) != 0;
+        return __all_sync(0xffffffffu, bounded_wait(smem_u32(bar), parity, abort_flag, limit)) != 0;
     };
 
     if (warp < 8) {
         // ------------------------------------------------ softmax, one row per thread
+        // (384 x 168 registers at launch = 256 x 208 + 128 x 88)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int t = warp >> 2, r = tid & 127;
         const int i = tok0 + t * tokens + r / a.group, g = r % a.group;
         const bool live = r < tokens * a.group && i < seq.n;
@@ -186,9 +247,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float top[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                top[x] = __uint_as_float(s[x][0]);
+                top[x] = fmaxf(__uint_as_float(s[x][0]), __uint_as_float(s[x][1]));
 #pragma unroll
-                for (int y = 1; y < 32; ++y) top[x] = fmaxf(top[x], __uint_as_float(s[x][y]));
+                for (int y = 2; y < 32; y += 2)
+                    top[x] = max3(top[x], __uint_as_float(s[x][y]), __uint_as_float(s[x][y + 1]));
             }
             const float mn = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
             const bool grow = mn > m + 8.f;
@@ -209,21 +271,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             }
             const float ref = m == -INFINITY ? 0.f : m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint64_t c2 = pack2(c, c), ref2 = pack2(-ref, -ref);
+            uint64_t sum[2] = {0, 0};
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 uint32_t p[16];
 #pragma unroll
                 for (int y = 0; y < 16; ++y) {
-                    const float p0 = ex2(fmaf(__uint_as_float(s[x][2 * y]), c, -ref));
-                    const float p1 = ex2(fmaf(__uint_as_float(s[x][2 * y + 1]), c, -ref));
-                    sum[(2 * y) & 3] += p0;
-                    sum[(2 * y + 1) & 3] += p1;
+                    const float2 e = unpack2(fma2(pack2(__uint_as_float(s[x][2 * y]), __uint_as_float(s[x][2 * y + 1])),
+                                                  c2, ref2));
+                    const float p0 = ex2(e.x), p1 = ex2(e.y);
+                    sum[y & 1] = add2(sum[y & 1], pack2(p0, p1));
                     p[y] = pack_h2<false>(p0, p1);
                 }
                 tmem_st16(ts + 16 * x, p);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            const float2 sums = unpack2(add2(sum[0], sum[1]));
+            l += sums.x + sums.y;
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -274,14 +338,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             }
         }
-    } else if (warp == 8) {
+    } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 8) {
         // ------------------------------------------------ MMA issue
         const uint32_t q0 = smem_u32(sq), kv0 = smem_u32(skv);
         constexpr uint32_t kIdS = idesc_bf16(128, kTileKeys);
         constexpr uint32_t kIdO = idesc_bf16(128, D) | (1u << 16);   // V: MN-major
+        const bool leader = elect_one();
         const auto scores = [&](int t, int j) {
             const uint32_t k = kv0 + ((2 * j) % kSlots<D>) * kTileBytes<D>;
-            if (lane == 0) {
+            if (leader) {
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
                     const uint32_t off = (x / 4) * kHalfBytes + (x % 4) * 32;
@@ -301,7 +368,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ok = warp_wait(&bars.q_full[t], 0);
                 if (ok) scores(t, 0);
             }
-            if (ok && lane == 0) mma_commit<false>(smem_u32(&bars.kv_empty[0]));
+            if (ok && leader) mma_commit<false>(smem_u32(&bars.kv_empty[0]));
             __syncwarp();
         }
         for (int j = 0; j < nsteps && ok; ++j) {
@@ -327,7 +394,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ok = warp_wait(&bars.p_ready[t], j & 1);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
+                if (leader) {
 #pragma unroll
                     for (int x = 0; x < kTileKeys / 16; ++x)
                         mma_f16_ta(tmem + kColO + t * D, tmem + t * 128 + x * 8, smem_desc_mn(v + x * 2048), kIdO,
@@ -342,7 +409,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             if (!ok) break;
             // (no commit is left to arrive when the last product's has)
-            if (lane == 0 && j + 1 < nsteps) {
+            if (leader && j + 1 < nsteps) {
                 mma_commit<false>(smem_u32(&bars.kv_empty[(2 * j + 1) % kSlots<D>]));
                 mma_commit<false>(smem_u32(&bars.kv_empty[(2 * j + 2) % kSlots<D>]));
             }
@@ -350,13 +417,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         if (!ok) {
             // wait, bounded, for the products in flight
-            if (lane == 0) {
+            if (leader) {
                 mma_commit<false>(smem_u32(&bars.drain));
                 mbar_wait_drain(smem_u32(&bars.drain), 0, kDrainLimitNs);
             }
             __syncwarp();
         }
-    } else {
+    } else if (warp == 9) {
         // ------------------------------------------------ TMA copies
         const uint32_t q0 = smem_u32(sq), kv0 = smem_u32(skv);
         int loaded = 0;                                         // slots filled so far
@@ -374,27 +441,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 q_loaded |= 1 << t;
             }
+            // the page of this lane's box of a step; read a step ahead
+            const auto look = [&](int j) {
+                const int key = lo + j * kTileKeys + lane % (kTileKeys / box) * box;
+                return a.table && j < nsteps && key < hi ? attn_page(a, b, key >> a.page_shift) : -1;
+            };
+            int ahead = look(0), page = -1;
             for (int n = 0; n < 2 * nsteps; ++n) {
                 const int slot = n % kSlots<D>, base = lo + (n >> 1) * kTileKeys;
-                if (n >= kSlots<D> &&
-                    !warp_wait(&bars.kv_empty[slot], (n / kSlots<D> - 1) & 1))
-                    break;
+                if (!(n & 1)) page = ahead, ahead = look((n >> 1) + 1);
+                if (n >= kSlots<D> && !warp_wait(&bars.kv_empty[slot], (n / kSlots<D> - 1) & 1)) break;
                 const uint32_t bar = smem_u32(&bars.kv_full[slot]);
                 const CUtensorMap* map = n & 1 ? &tm_v : &tm_k;
-                const int boxes = a.table ? (min(kTileKeys, hi - base) + box - 1) / box : 1;
-                if (lane == 0) mbar_expect_tx(bar, boxes * box * 128 * (D / 64));
-                __syncwarp();
-                for (int e = lane; e < boxes * (D / 64); e += 32) {
-                    const int at = e % boxes, x = e / boxes;
-                    int page = 0, row = seq.row0 + base;
-                    if (a.table) {
-                        const int key = base + at * box;
-                        page = attn_page(a, b, key >> a.page_shift);
-                        if (page < 0) page = a.num_pages;       // outside the tensor: zeros
-                        row = key & (a.page_size - 1);
-                    }
-                    tma_load_4d(kv0 + slot * kTileBytes<D> + x * kHalfBytes + at * box * 128, map, 64 * x, row, h, page,
-                                bar);
+                const uint32_t dst = kv0 + slot * kTileBytes<D>;
+                if (a.table) {
+                    // one box per page and 64-column half; lane l has box l mod 128 / box
+                    const int boxes = (min(kTileKeys, hi - base) + box - 1) / box, at = lane % (kTileKeys / box);
+                    if (lane == 0) mbar_expect_tx(bar, boxes * box * 128 * (D / 64));
+                    __syncwarp();
+                    for (int x = lane / (kTileKeys / box); x < D / 64; x += 32 / (kTileKeys / box))
+                        if (at < boxes)                             // (no such page: zeros)
+                            tma_load_4d(dst + x * kHalfBytes + at * box * 128, map, 64 * x,
+                                        (base + at * box) & (a.page_size - 1), h, page < 0 ? a.num_pages : page, bar);
+                } else if (lane == 0) {
+                    mbar_expect_tx(bar, kTileBytes<D>);
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x)
+                        tma_load_4d(dst + x * kHalfBytes, map, 64 * x, seq.row0 + base, h, 0, bar);
                 }
                 __syncwarp();
                 ++loaded;
@@ -408,6 +481,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 mbar_wait_drain(smem_u32(&bars.kv_full[n % kSlots<D>]), (n / kSlots<D>) & 1, kDrainLimitNs);
         }
         __syncwarp();
+    }
     }
     tc_fence_before();
     __syncthreads();
