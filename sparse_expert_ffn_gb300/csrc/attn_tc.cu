@@ -41,14 +41,15 @@ constexpr int kTcThreads = 384;               // 2 softmax warpgroups, 1 of MMA 
 constexpr int kTileKeys = 128;
 constexpr uint32_t kHalfBytes = 128 * 128;      // 128 rows of one 128-byte swizzle atom
 
-// Ring slots of 128 keys: 4 of 32 KB, 8 of 16 KB (d = 64).
-template <int D> constexpr int kSlots = D == 128 ? 4 : 8;
+// Ring slots of 128 keys: 5 of 32 KB, 8 of 16 KB (d = 64).
+template <int D> constexpr int kSlots = D == 128 ? 5 : 8;
 template <int D> constexpr uint32_t kTileBytes = (D / 64) * kHalfBytes;
 
 struct TcBars {
     uint64_t q_full[2];
     uint64_t s_full[2];       // S of the tile's next step is there, its O is up to date
-    uint64_t p_ready[2];      // P written, O rescaled
+    uint64_t p_most[2];       // O rescaled, P's first 96 keys written
+    uint64_t p_ready[2];      // P's last 32 keys written
     uint64_t o_done[2];       // the tile's last product is done
     uint64_t kv_full[8];
     uint64_t kv_empty[8];
@@ -169,6 +170,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_u32(&bars.q_full[t]), 1);
             mbar_init(smem_u32(&bars.s_full[t]), 1);
+            mbar_init(smem_u32(&bars.p_most[t]), 4);
             mbar_init(smem_u32(&bars.p_ready[t]), 4);
             mbar_init(smem_u32(&bars.o_done[t]), 1);
         }
@@ -227,6 +229,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t ts = lane_base + t * 128, to = lane_base + kColO + t * D;
         const float c = a.scale_log2;
         float m = -INFINITY, l = 0.f;      // reference maximum (times c), sum of the weights
+        const auto hand_over = [&](uint64_t* bar) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(bar));
+        };
         bool ok = true;
         for (int j = 0; j < steps[t]; ++j) {
             ok = warp_wait(&bars.s_full[t], j & 1);
@@ -244,15 +252,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int y = 0; y < 32; ++y)
                         if (x * 32 + y >= left) s[x][y] = 0xff800000u;   // -infinity
             }
-            float top[4];
+            float top[8];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                top[x] = fmaxf(__uint_as_float(s[x][0]), __uint_as_float(s[x][1]));
+            for (int x = 0; x < 8; ++x)
+                top[x] = fmaxf(__uint_as_float(s[x / 2][x % 2 * 16]), __uint_as_float(s[x / 2][x % 2 * 16 + 1]));
 #pragma unroll
-                for (int y = 2; y < 32; y += 2)
-                    top[x] = max3(top[x], __uint_as_float(s[x][y]), __uint_as_float(s[x][y + 1]));
-            }
-            const float mn = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+            for (int y = 2; y < 16; y += 2)
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    top[x] = max3(top[x], __uint_as_float(s[x / 2][x % 2 * 16 + y]),
+                                  __uint_as_float(s[x / 2][x % 2 * 16 + y + 1]));
+            const float mn = max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7])) * c;
             const bool grow = mn > m + 8.f;
             if (__any_sync(0xffffffffu, grow)) {
                 const float keep = grow ? ex2(m - mn) : 1.f;
@@ -272,7 +282,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             const float ref = m == -INFINITY ? 0.f : m;
             const uint64_t c2 = pack2(c, c), ref2 = pack2(-ref, -ref);
-            uint64_t sum[2] = {0, 0};
+            uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 uint32_t p[16];
@@ -281,17 +291,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const float2 e = unpack2(fma2(pack2(__uint_as_float(s[x][2 * y]), __uint_as_float(s[x][2 * y + 1])),
                                                   c2, ref2));
                     const float p0 = ex2(e.x), p1 = ex2(e.y);
-                    sum[y & 1] = add2(sum[y & 1], pack2(p0, p1));
+                    sum[y & 3] = add2(sum[y & 3], pack2(p0, p1));
                     p[y] = pack_h2<false>(p0, p1);
                 }
                 tmem_st16(ts + 16 * x, p);
+                if (x == 2) hand_over(&bars.p_most[t]);   // the product with V starts on these
             }
-            const float2 sums = unpack2(add2(sum[0], sum[1]));
+            hand_over(&bars.p_ready[t]);
+            const float2 sums = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
             l += sums.x + sums.y;
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars.p_ready[t]));
         }
         if (ok && steps[t] > 0) {
             ok = warp_wait(&bars.o_done[t], 0);
@@ -346,35 +354,48 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         constexpr uint32_t kIdS = idesc_bf16(128, kTileKeys);
         constexpr uint32_t kIdO = idesc_bf16(128, D) | (1u << 16);   // V: MN-major
         const bool leader = elect_one();
-        const auto scores = [&](int t, int j) {
-            const uint32_t k = kv0 + ((2 * j) % kSlots<D>) * kTileBytes<D>;
-            if (leader) {
-#pragma unroll
-                for (int x = 0; x < D / 16; ++x) {
-                    const uint32_t off = (x / 4) * kHalfBytes + (x % 4) * 32;
-                    mma_bf16<false>(tmem + t * 128, smem_desc_sw128(q0 + t * kTileBytes<D> + off),
-                                    smem_desc_sw128(k + off), kIdS, x > 0);
-                }
-                mma_commit<false>(smem_u32(&bars.s_full[t]));
-            }
+        // The warp stays together whatever a wait says: a lane whose wait gave
+        // up goes on without waiting, and the leader issues nothing more.
+        bool ok = true;
+        const auto wait = [&](uint64_t* bar, uint32_t parity) {
+            if (ok) ok = bounded_wait(smem_u32(bar), parity, abort_flag, limit);
             __syncwarp();
         };
-        const auto full = [&](int slot) { return warp_wait(&bars.kv_full[slot % kSlots<D>], (slot / kSlots<D>) & 1); };
-        bool ok = true;
-        if (nsteps > 0) {
-            ok = full(0);
-            for (int t = 0; t < 2 && ok; ++t) {
-                if (steps[t] == 0) continue;
-                ok = warp_wait(&bars.q_full[t], 0);
-                if (ok) scores(t, 0);
+        const auto scores = [&](int t, int slot) {
+            const uint32_t k = kv0 + slot * kTileBytes<D>;
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+                const uint32_t off = (x / 4) * kHalfBytes + (x % 4) * 32;
+                mma_bf16<false>(tmem + t * 128, smem_desc_sw128(q0 + t * kTileBytes<D> + off), smem_desc_sw128(k + off),
+                                kIdS, x > 0);
             }
-            if (ok && leader) mma_commit<false>(smem_u32(&bars.kv_empty[0]));
+            mma_commit<false>(smem_u32(&bars.s_full[t]));
+        };
+        // slots in the order K(0), V(0), K(1), ...; `next` waits for the one after the last
+        int slot = -1;
+        uint32_t lap = 0;
+        const auto next = [&]() {
+            if (++slot == kSlots<D>) slot = 0, lap ^= 1;
+            wait(&bars.kv_full[slot], lap);
+            return slot;
+        };
+        int kslot = 0, vslot = 0;
+        if (nsteps > 0) {
+            kslot = next();
+            for (int t = 0; t < 2; ++t) {
+                if (steps[t] == 0) continue;
+                wait(&bars.q_full[t], 0);
+                if (leader && ok) scores(t, kslot);
+                __syncwarp();
+            }
+            if (leader && ok) mma_commit<false>(smem_u32(&bars.kv_empty[kslot]));
             __syncwarp();
+            vslot = next();
+            if (nsteps > 1) kslot = next();
         }
-        for (int j = 0; j < nsteps && ok; ++j) {
-            ok = full(2 * j + 1);
-            if (!ok) break;
-            const uint32_t v = kv0 + ((2 * j + 1) % kSlots<D>) * kTileBytes<D>;
+        for (int j = 0; j < nsteps; ++j) {
+            // V(j) and K(j + 1) are there
+            const uint32_t v = kv0 + vslot * kTileBytes<D>;
             const int have = hi - (lo + j * kTileKeys);
             if (have < kTileKeys) {
                 // rows behind the last key: their weights are 0, and 0 times
@@ -389,32 +410,46 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
             }
-            for (int t = 0; t < 2 && ok; ++t) {
-                if (j >= steps[t]) continue;
-                ok = warp_wait(&bars.p_ready[t], j & 1);
-                if (!ok) break;
-                tc_fence_after();
-                if (leader) {
+            const bool more = j + 1 < nsteps;
+            int vnext = 0, knext = 0;
 #pragma unroll
-                    for (int x = 0; x < kTileKeys / 16; ++x)
+            for (int t = 0; t < 2; ++t) {
+                if (j < steps[t]) {
+                    const auto product = [&](int x) {
                         mma_f16_ta(tmem + kColO + t * D, tmem + t * 128 + x * 8, smem_desc_mn(v + x * 2048), kIdO,
                                    j > 0 || x > 0);
-                    if (j + 1 == steps[t]) mma_commit<false>(smem_u32(&bars.o_done[t]));
+                    };
+                    wait(&bars.p_most[t], j & 1);
+                    tc_fence_after();
+                    if (leader && ok) {
+#pragma unroll
+                        for (int x = 0; x < 6; ++x) product(x);
+                    }
+                    __syncwarp();
+                    wait(&bars.p_ready[t], j & 1);
+                    tc_fence_after();
+                    if (leader && ok) {
+                        product(6);
+                        product(7);
+                        // (nothing is committed that nobody waits for: no arrival
+                        // is outstanding when the CTA ends)
+                        if (j + 1 == steps[t]) mma_commit<false>(smem_u32(&bars.o_done[t]));
+                        if (more && (t == 1 || steps[1] <= j)) mma_commit<false>(smem_u32(&bars.kv_empty[vslot]));
+                        if (j + 1 < steps[t]) scores(t, kslot);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-                if (j + 1 < steps[t]) {
-                    ok = full(2 * j + 2);
-                    if (ok) scores(t, j + 1);
+                if (t == 0 && more) {
+                    // the next step's tiles, while the other tile is in its softmax
+                    vnext = next();
+                    if (j + 2 < nsteps) knext = next();
                 }
             }
-            if (!ok) break;
-            // (no commit is left to arrive when the last product's has)
-            if (leader && j + 1 < nsteps) {
-                mma_commit<false>(smem_u32(&bars.kv_empty[(2 * j + 1) % kSlots<D>]));
-                mma_commit<false>(smem_u32(&bars.kv_empty[(2 * j + 2) % kSlots<D>]));
-            }
+            if (leader && ok && more) mma_commit<false>(smem_u32(&bars.kv_empty[kslot]));
             __syncwarp();
+            vslot = vnext, kslot = knext;
         }
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
             // wait, bounded, for the products in flight
             if (leader) {
