@@ -7,21 +7,31 @@
 // keys in shared memory, and a decode batch over a shared prefix is the same
 // kernel with the batch as the tokens.  Per tile and 128 keys:
 //   S = Q K^T   (128 x 128 x d, f32 in tensor memory)
-//   m' = max(m, max S),  P = 2^(c S - c m')  (bf16, written over S),  l += sum P
+//   P = 2^(c S - m')  (bf16, written over S),  l += sum P
 //   O += P V    (128 x d x 128, P read from tensor memory)
-// with c = scale * log2(e).  O stays in tensor memory: it is multiplied by
-// 2^(c m - c m') only when a row's maximum has grown by more than 2^8 since it
-// was last taken as the reference (the weights are then below 2^8, which bf16
-// and f32 hold as exactly as those below 1), so that the softmax warps rarely
-// touch it.
+// with c = scale * log2(e), and instead of the running maximum a reference m'
+// that stands as long as the row's maximum is not more than 24 above it (nor
+// more than 64 below it while the row has no weight): bf16 and f32 hold weights
+// up to 2^24 as exactly as those up to 1.  So the weights are formed
+// without waiting for the maximum, and S is read again, and O, which stays in
+// tensor memory, multiplied by 2^(m - m'), only in the few steps that move
+// the reference.
 //
 // Roles: warps 0-3 and 4-7 the softmax of the two tiles (one row per thread,
 // no shuffles; they take over registers of the others, since a row's 128
-// scores stay in registers), warp 8 issues the MMAs, warp 9 the TMA copies (K and V tiles
-// alternate in a ring; with pages, one box per page).  The MMAs of one tile run
-// while the other tile is in its softmax.  A commit after S(j + 1) also covers
+// scores stay in registers), warps 8 and 10 issue the MMAs of one tile each
+// (a wait costs about 150 cycles even when it is over; one warp for both tiles
+// held the tensor pipe up between them), warp 9 the TMA copies (K and V tiles
+// alternate in a ring; with pages, one box per page) and the work list.  The MMAs
+// of one tile run while the other tile is in its softmax.  A commit after S(j + 1) also covers
 // the O += P V of step j issued before it, so the one barrier per tile tells the
 // softmax warps both that S is there and that O may be rescaled.
+//
+// The grid has a CTA per work item, those that see the most keys first; a
+// running CTA takes over the next CTA that has not started (cluster launch
+// control) while it works on its own item, so that the next item's copies and
+// first scores overlap the end of the last one, and the tensor memory and
+// barriers are set up once.
 //
 // P is rounded to bf16 because the MMA takes both operands in one 16-bit type;
 // l adds the unrounded f32 values.
@@ -45,24 +55,43 @@ constexpr uint32_t kHalfBytes = 128 * 128;      // 128 rows of one 128-byte swiz
 template <int D> constexpr int kSlots = D == 128 ? 5 : 8;
 template <int D> constexpr uint32_t kTileBytes = (D / 64) * kHalfBytes;
 
+// A work item, as every role needs it.
+struct Item {
+    int b;                    // sequence, < 0: no more items
+    int h, split, tok0;       // key head, key range, first token of tile 0
+    int lo, hi;               // keys
+    int steps[2];             // 128-key steps of each tile
+    AttnSeq seq;
+};
+
 struct TcBars {
+    alignas(16) uint8_t taken[16];   // the hardware's answer: which CTA was taken over
     uint64_t q_full[2];
+    uint64_t q_empty[2];      // the item's last scores of the tile are done
     uint64_t s_full[2];       // S of the tile's next step is there, its O is up to date
     uint64_t p_most[2];       // O rescaled, P's first 96 keys written
     uint64_t p_ready[2];      // P's last 32 keys written
-    uint64_t o_done[2];       // the tile's last product is done
+    uint64_t o_done[2];       // the item's last product of the tile is done
     uint64_t kv_full[8];
-    uint64_t kv_empty[8];
-    uint64_t drain;
+    uint64_t kv_empty[8];     // both tiles are done with the slot
+    uint64_t tail[2];         // item n & 1's last value tile is cleared behind its last row
+    uint64_t turn[2];         // the other tile's batch of MMAs has been issued
+    uint64_t item_full[2];
+    uint64_t item_empty[2];
+    uint64_t taken_full;
+    uint64_t drain[2];
     uint32_t tmem;
-    int item[2];
     int abort;
+    int announced;            // items that the copying warp has handed out
+    int orphan;               // item[2] was taken over and not handed out
+    Item item[3];
 };
 
 template <int D>
 constexpr size_t tc_smem_bytes() {
     return 1024 + 2 * kTileBytes<D> + kSlots<D> * kTileBytes<D> + sizeof(TcBars);
 }
+static_assert(tc_smem_bytes<128>() <= 232448 && tc_smem_bytes<64>() <= 232448, "fits an SM");
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
                                             int c3, uint32_t bar) {
@@ -155,56 +184,93 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, vola
     }
 }
 
+// Asks for the next CTA that has not started; the answer arrives on `bar`.
+__device__ __forceinline__ void take_over(uint32_t answer, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     answer),
+                 "r"(bar)
+                 : "memory");
+}
+// The answer: true and the CTA's index, or false when none was left.
+__device__ __forceinline__ bool taken_over(uint32_t answer, int* x, int* y) {
+    uint32_t got, cx, cy;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 r, [%3];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, _, _}, r;\n\t}"
+        : "=&r"(got), "=&r"(cx), "=&r"(cy)
+        : "r"(answer)
+        : "memory");
+    *x = (int)cx, *y = (int)cy;
+    return got != 0;
+}
+
+// CTA (x, y) of the grid as a work item; called by a whole warp.
+__device__ __forceinline__ Item work_item(const AttnArgs& a, int x, int y, int tokens) {
+    Item it;
+    int tile = 0;
+    it.b = -1;
+    it.h = x % a.hkv, it.split = y;
+    if (!attn_item(a, x / a.hkv, 1, 2 * tokens, &it.b, &tile)) {
+        it.b = -1;
+        return it;
+    }
+    it.seq = attn_seq(a, it.b);
+    it.tok0 = tile * 2 * tokens;
+    attn_split(a, y, kTileKeys, it.seq.kv0, attn_limit_max(a, it.seq, min(it.tok0 + 2 * tokens, it.seq.n)), &it.lo, &it.hi);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int first = it.tok0 + t * tokens, last = min(first + tokens, it.seq.n);
+        const int end = first < it.seq.n ? min(it.hi, attn_limit_max(a, it.seq, last)) : it.lo;
+        it.steps[t] = end > it.lo ? (end - it.lo + kTileKeys - 1) / kTileKeys : 0;
+    }
+    return it;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, AttnArgs a, int tokens, int box) {
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t* sq = smem;
     uint8_t* skv = smem + 2 * kTileBytes<D>;
     TcBars& bars = *reinterpret_cast<TcBars*>(skv + kSlots<D> * kTileBytes<D>);
+    const uint32_t q0 = smem_u32(smem), kv0 = smem_u32(skv);
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
     if (tid == 0) {
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_u32(&bars.q_full[t]), 1);
+            mbar_init(smem_u32(&bars.q_empty[t]), 1);
             mbar_init(smem_u32(&bars.s_full[t]), 1);
             mbar_init(smem_u32(&bars.p_most[t]), 4);
             mbar_init(smem_u32(&bars.p_ready[t]), 4);
             mbar_init(smem_u32(&bars.o_done[t]), 1);
+            mbar_init(smem_u32(&bars.item_full[t]), 1);
+            mbar_init(smem_u32(&bars.item_empty[t]), 10);       // softmax and MMA warps
+            mbar_init(smem_u32(&bars.drain[t]), 1);
+            mbar_init(smem_u32(&bars.tail[t]), 2);
+            mbar_init(smem_u32(&bars.turn[t]), 1);
         }
         for (int s = 0; s < kSlots<D>; ++s) {
             mbar_init(smem_u32(&bars.kv_full[s]), 1);
-            mbar_init(smem_u32(&bars.kv_empty[s]), 1);
+            mbar_init(smem_u32(&bars.kv_empty[s]), 2);
         }
-        mbar_init(smem_u32(&bars.drain), 1);
-        bars.abort = 0;
+        mbar_init(smem_u32(&bars.taken_full), 1);
+        bars.abort = bars.announced = bars.orphan = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     pdl_enter();
-    const int h = blockIdx.x % a.hkv;
     if (warp == 9) {
-        int b = 0, tile = 0;
-        const bool ok = attn_item(a, blockIdx.x / a.hkv, 1, 2 * tokens, &b, &tile);
-        if (lane == 0) bars.item[0] = ok ? b : -1, bars.item[1] = tile;
+        const Item it = work_item(a, blockIdx.x, blockIdx.y, tokens);
+        if (lane == 0) bars.item[0] = it;
     }
     __syncthreads();
-    const int b = bars.item[0];
-    if (b < 0) return;
+    if (bars.item[0].b < 0) return;                             // (and so are all later CTAs)
     if (warp == 8) tmem_alloc<false>(smem_u32(&bars.tmem), 512);
-    const AttnSeq seq = attn_seq(a, b);
-    const int tok0 = bars.item[1] * 2 * tokens;                 // first token of tile 0
-    // keys lo .. hi - 1 of this CTA; steps of each tile (tile 1's rows are later)
-    int lo, hi, steps[2];
-    attn_split(a, blockIdx.y, kTileKeys, seq.kv0, attn_limit_max(a, seq, min(tok0 + 2 * tokens, seq.n)), &lo, &hi);
-    for (int t = 0; t < 2; ++t) {
-        const int first = tok0 + t * tokens, last = min(first + tokens, seq.n);
-        const int end = first < seq.n ? min(hi, attn_limit_max(a, seq, last)) : lo;
-        steps[t] = end > lo ? (end - lo + kTileKeys - 1) / kTileKeys : 0;
-    }
-    lo = uniform(lo), hi = uniform(hi), steps[0] = uniform(steps[0]), steps[1] = uniform(steps[1]);
-    const int nsteps = max(steps[0], steps[1]);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -216,101 +282,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, bounded_wait(smem_u32(bar), parity, abort_flag, limit)) != 0;
     };
+    // item n of this CTA (the first one is there from the start)
+    const auto item_there = [&](int n) { return n == 0 || warp_wait(&bars.item_full[n & 1], ((n >> 1) - !(n & 1)) & 1); };
+    const auto item_left = [&](int n) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.item_empty[n & 1]));
+    };
+    int item_no = 0;                                            // items that this warp is done with
 
-    if (warp < 8) {
-        // ------------------------------------------------ softmax, one row per thread
-        // (384 x 168 registers at launch = 256 x 208 + 128 x 88)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        const int t = warp >> 2, r = tid & 127;
-        const int i = tok0 + t * tokens + r / a.group, g = r % a.group;
-        const bool live = r < tokens * a.group && i < seq.n;
-        const int lim = live ? min(hi, attn_limit(a, seq, i)) : 0;
-        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t ts = lane_base + t * 128, to = lane_base + kColO + t * D;
-        const float c = a.scale_log2;
-        float m = -INFINITY, l = 0.f;      // reference maximum (times c), sum of the weights
-        const auto hand_over = [&](uint64_t* bar) {
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(bar));
-        };
-        bool ok = true;
-        for (int j = 0; j < steps[t]; ++j) {
-            ok = warp_wait(&bars.s_full[t], j & 1);
-            if (!ok) break;
-            tc_fence_after();
-            uint32_t s[4][32];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) tmem_ld32(ts + 32 * x, s[x]);
-            tmem_ld_wait();
-            const int left = lim - (lo + j * kTileKeys);       // keys of this step that the row sees
-            if (left < kTileKeys) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-#pragma unroll
-                    for (int y = 0; y < 32; ++y)
-                        if (x * 32 + y >= left) s[x][y] = 0xff800000u;   // -infinity
-            }
-            float top[8];
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-                top[x] = fmaxf(__uint_as_float(s[x / 2][x % 2 * 16]), __uint_as_float(s[x / 2][x % 2 * 16 + 1]));
-#pragma unroll
-            for (int y = 2; y < 16; y += 2)
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    top[x] = max3(top[x], __uint_as_float(s[x / 2][x % 2 * 16 + y]),
-                                  __uint_as_float(s[x / 2][x % 2 * 16 + y + 1]));
-            const float mn = max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7])) * c;
-            const bool grow = mn > m + 8.f;
-            if (__any_sync(0xffffffffu, grow)) {
-                const float keep = grow ? ex2(m - mn) : 1.f;
-                if (grow) m = mn;
-                l *= keep;
-                if (j > 0) {
-#pragma unroll
-                    for (int x = 0; x < D / 16; ++x) {
-                        uint32_t o[16];
-                        tmem_ld16(to + 16 * x, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * keep);
-                        tmem_st16(to + 16 * x, o);
-                    }
-                }
-            }
-            const float ref = m == -INFINITY ? 0.f : m;
-            const uint64_t c2 = pack2(c, c), ref2 = pack2(-ref, -ref);
-            uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                uint32_t p[16];
-#pragma unroll
-                for (int y = 0; y < 16; ++y) {
-                    const float2 e = unpack2(fma2(pack2(__uint_as_float(s[x][2 * y]), __uint_as_float(s[x][2 * y + 1])),
-                                                  c2, ref2));
-                    const float p0 = ex2(e.x), p1 = ex2(e.y);
-                    sum[y & 3] = add2(sum[y & 3], pack2(p0, p1));
-                    p[y] = pack_h2<false>(p0, p1);
-                }
-                tmem_st16(ts + 16 * x, p);
-                if (x == 2) hand_over(&bars.p_most[t]);   // the product with V starts on these
-            }
-            hand_over(&bars.p_ready[t]);
-            const float2 sums = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
-            l += sums.x + sums.y;
-        }
-        if (ok && steps[t] > 0) {
-            ok = warp_wait(&bars.o_done[t], 0);
-            tc_fence_after();
-        }
+    // Output rows of an item's tile t: this thread's row times inv, or NaN.
+    const auto write_row = [&](const Item& it, int t, bool ok, bool keys, float l, float m, uint32_t to) {
+        const int r = tid & 127, i = it.tok0 + t * tokens + r / a.group, g = r % a.group;
+        const bool live = r < tokens * a.group && i < it.seq.n;
         // o / l; a row without keys has l = 0
         const float inv = !ok ? __int_as_float(0x7fc00000) : l > 0.f ? 1.f / l : l;
-        const int row = seq.row0 + i;
-        const int64_t flat = (int64_t)row * a.hq + h * a.group + g;
+        const int row = it.seq.row0 + i;
+        const int64_t flat = (int64_t)row * a.hq + it.h * a.group + g;
         const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
-        const int64_t at = (int64_t)(a.part_slot + blockIdx.y) * a.n_rows * a.hq + flat;
+        const int64_t at = (int64_t)(a.part_slot + it.split) * a.n_rows * a.hq + flat;
         if (live) {
             if (a.part_o) a.part_lse[at] = ok ? lse2 : inv;
             else if (a.lse) a.lse[flat] = ok ? lse2 * kLn2 : inv;
@@ -318,7 +307,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int x = 0; x < D / 32; ++x) {
             uint32_t o[32];
-            if (steps[t] > 0) {
+            if (keys) {
                 tmem_ld32(to + 32 * x, o);
                 tmem_ld_wait();
             } else {
@@ -335,7 +324,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int y = 0; y < 8; ++y) dst[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
             } else {
                 uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + (int64_t)row * a.o_stride +
-                                                      (int64_t)(h * a.group + g) * D + 32 * x);
+                                                      (int64_t)(it.h * a.group + g) * D + 32 * x);
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                     uint32_t w[4];
@@ -346,180 +335,366 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             }
         }
-    } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 8) {
-        // ------------------------------------------------ MMA issue
-        const uint32_t q0 = smem_u32(sq), kv0 = smem_u32(skv);
-        constexpr uint32_t kIdS = idesc_bf16(128, kTileKeys);
-        constexpr uint32_t kIdO = idesc_bf16(128, D) | (1u << 16);   // V: MN-major
-        const bool leader = elect_one();
-        // The warp stays together whatever a wait says: a lane whose wait gave
-        // up goes on without waiting, and the leader issues nothing more.
+    };
+
+    if (warp < 8) {
+        // ------------------------------------------------ softmax, one row per thread
+        // (384 x 168 registers at launch = 256 x 208 + 128 x 88)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int t = warp >> 2, r = tid & 127;
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t ts = lane_base + t * 128, to = lane_base + kColO + t * D;
+        const float c = a.scale_log2;
+        const auto hand_over = [&](uint64_t* bar) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(bar));
+        };
+        uint32_t step_no = 0, done_no = 0;                      // of this tile, over all items
         bool ok = true;
-        const auto wait = [&](uint64_t* bar, uint32_t parity) {
-            if (ok) ok = bounded_wait(smem_u32(bar), parity, abort_flag, limit);
-            __syncwarp();
-        };
-        const auto scores = [&](int t, int slot) {
-            const uint32_t k = kv0 + slot * kTileBytes<D>;
+        while (ok) {
+            ok = item_there(item_no);
+            if (!ok) break;
+            const Item& it = bars.item[item_no & 1];
+            if (it.b < 0) break;
+            const int i = it.tok0 + t * tokens + r / a.group;
+            const bool live = r < tokens * a.group && i < it.seq.n;
+            const int steps = uniform(it.steps[t]), lo = uniform(it.lo);
+            const int lim = live ? min(it.hi, attn_limit(a, it.seq, i)) : 0;
+            float m = 0.f, l = 0.f;            // reference (in units of log2), sum of the weights
+            for (int j = 0; j < steps; ++j, ++step_no) {
+                ok = warp_wait(&bars.s_full[t], step_no & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const int left = lim - (lo + j * kTileKeys);       // keys of this step that the row sees
+                uint32_t s[4][32], p[3][16];
+                uint64_t sum[4], c2 = pack2(c, c), ref2;
+                const auto weights = [&](const uint32_t (&sx)[32], uint32_t (&px)[16]) {
 #pragma unroll
-            for (int x = 0; x < D / 16; ++x) {
-                const uint32_t off = (x / 4) * kHalfBytes + (x % 4) * 32;
-                mma_bf16<false>(tmem + t * 128, smem_desc_sw128(q0 + t * kTileBytes<D> + off), smem_desc_sw128(k + off),
-                                kIdS, x > 0);
-            }
-            mma_commit<false>(smem_u32(&bars.s_full[t]));
-        };
-        // slots in the order K(0), V(0), K(1), ...; `next` waits for the one after the last
-        int slot = -1;
-        uint32_t lap = 0;
-        const auto next = [&]() {
-            if (++slot == kSlots<D>) slot = 0, lap ^= 1;
-            wait(&bars.kv_full[slot], lap);
-            return slot;
-        };
-        int kslot = 0, vslot = 0;
-        if (nsteps > 0) {
-            kslot = next();
-            for (int t = 0; t < 2; ++t) {
-                if (steps[t] == 0) continue;
-                wait(&bars.q_full[t], 0);
-                if (leader && ok) scores(t, kslot);
-                __syncwarp();
-            }
-            if (leader && ok) mma_commit<false>(smem_u32(&bars.kv_empty[kslot]));
-            __syncwarp();
-            vslot = next();
-            if (nsteps > 1) kslot = next();
-        }
-        for (int j = 0; j < nsteps; ++j) {
-            // V(j) and K(j + 1) are there
-            const uint32_t v = kv0 + vslot * kTileBytes<D>;
-            const int have = hi - (lo + j * kTileKeys);
-            if (have < kTileKeys) {
-                // rows behind the last key: their weights are 0, and 0 times
-                // whatever lies there has to be 0
-                for (int e = lane; e < (kTileKeys - have) * (D / 64) * 8; e += 32) {
-                    const int row = have + (e >> 3) % (kTileKeys - have), half = (e >> 3) / (kTileKeys - have);
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + half * kHalfBytes + row * 128 +
-                                                                                (e & 7) * 16),
-                                 "r"(0)
-                                 : "memory");
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-            }
-            const bool more = j + 1 < nsteps;
-            int vnext = 0, knext = 0;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (j < steps[t]) {
-                    const auto product = [&](int x) {
-                        mma_f16_ta(tmem + kColO + t * D, tmem + t * 128 + x * 8, smem_desc_mn(v + x * 2048), kIdO,
-                                   j > 0 || x > 0);
-                    };
-                    wait(&bars.p_most[t], j & 1);
-                    tc_fence_after();
-                    if (leader && ok) {
-#pragma unroll
-                        for (int x = 0; x < 6; ++x) product(x);
+                    for (int y = 0; y < 16; ++y) {
+                        const float2 e =
+                            unpack2(fma2(pack2(__uint_as_float(sx[2 * y]), __uint_as_float(sx[2 * y + 1])), c2, ref2));
+                        const float p0 = ex2(e.x), p1 = ex2(e.y);
+                        sum[y & 3] = add2(sum[y & 3], pack2(p0, p1));
+                        px[y] = pack_h2<false>(p0, p1);
                     }
-                    __syncwarp();
-                    wait(&bars.p_ready[t], j & 1);
-                    tc_fence_after();
-                    if (leader && ok) {
-                        product(6);
-                        product(7);
-                        // (nothing is committed that nobody waits for: no arrival
-                        // is outstanding when the CTA ends)
-                        if (j + 1 == steps[t]) mma_commit<false>(smem_u32(&bars.o_done[t]));
-                        if (more && (t == 1 || steps[1] <= j)) mma_commit<false>(smem_u32(&bars.kv_empty[vslot]));
-                        if (j + 1 < steps[t]) scores(t, kslot);
-                    }
-                    __syncwarp();
-                }
-                if (t == 0 && more) {
-                    // the next step's tiles, while the other tile is in its softmax
-                    vnext = next();
-                    if (j + 2 < nsteps) knext = next();
-                }
-            }
-            if (leader && ok && more) mma_commit<false>(smem_u32(&bars.kv_empty[kslot]));
-            __syncwarp();
-            vslot = vnext, kslot = knext;
-        }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
-            // wait, bounded, for the products in flight
-            if (leader) {
-                mma_commit<false>(smem_u32(&bars.drain));
-                mbar_wait_drain(smem_u32(&bars.drain), 0, kDrainLimitNs);
-            }
-            __syncwarp();
-        }
-    } else if (warp == 9) {
-        // ------------------------------------------------ TMA copies
-        const uint32_t q0 = smem_u32(sq), kv0 = smem_u32(skv);
-        int loaded = 0;                                         // slots filled so far
-        int q_loaded = 0;
-        if (!a.stall_tma) {
-            for (int t = 0; t < 2; ++t) {
-                if (steps[t] == 0) continue;
-                if (lane == 0) {
-                    const uint32_t bar = smem_u32(&bars.q_full[t]);
-                    mbar_expect_tx(bar, tokens * a.group * 128 * (D / 64));
+                };
+#pragma unroll 1
+                while (true) {
 #pragma unroll
-                    for (int x = 0; x < D / 64; ++x)
-                        tma_load_4d(q0 + t * kTileBytes<D> + x * kHalfBytes, &tm_q, 64 * x, 0,
-                                    seq.row0 + tok0 + t * tokens, h, bar);
+                    for (int x = 0; x < 4; ++x) tmem_ld32(ts + 32 * x, s[x]);
+                    tmem_ld_wait();
+                    if (left < kTileKeys) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+#pragma unroll
+                            for (int y = 0; y < 32; ++y)
+                                if (x * 32 + y >= left) s[x][y] = 0xff800000u;   // -infinity
+                    }
+                    // the weights are formed on the reference as it is, beside the
+                    // maximum: it stands except for a few steps of a row
+                    ref2 = pack2(-m, -m);
+                    sum[0] = sum[1] = sum[2] = sum[3] = 0;
+                    float top[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        top[x] = fmaxf(__uint_as_float(s[x / 2][x % 2 * 16]), __uint_as_float(s[x / 2][x % 2 * 16 + 1]));
+#pragma unroll
+                    for (int y = 2; y < 16; y += 2)
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            top[x] = max3(top[x], __uint_as_float(s[x / 2][x % 2 * 16 + y]),
+                                          __uint_as_float(s[x / 2][x % 2 * 16 + y + 1]));
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) weights(s[x], p[x]);
+                    const float mn =
+                        max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7])) * c;
+                    const bool move = mn > m + 24.f || (l == 0.f && mn < m - 64.f && mn != -INFINITY);
+                    if (!__any_sync(0xffffffffu, move)) break;
+                    // (a row without weight yet has O = 0, or none before the first product)
+                    const float keep = move && l != 0.f ? ex2(m - mn) : 1.f;
+                    if (move) m = mn;
+                    l *= keep;
+                    if (j > 0) {
+#pragma unroll
+                        for (int x = 0; x < D / 16; ++x) {
+                            uint32_t o[16];
+                            tmem_ld16(to + 16 * x, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * keep);
+                            tmem_st16(to + 16 * x, o);
+                        }
+                    }
                 }
-                q_loaded |= 1 << t;
+#pragma unroll
+                for (int x = 0; x < 3; ++x) tmem_st16(ts + 16 * x, p[x]);
+                hand_over(&bars.p_most[t]);                        // the product with V starts on these
+                weights(s[3], p[0]);
+                tmem_st16(ts + 48, p[0]);
+                hand_over(&bars.p_ready[t]);
+                const float2 sums = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+                l += sums.x + sums.y;
             }
-            // the page of this lane's box of a step; read a step ahead
-            const auto look = [&](int j) {
-                const int key = lo + j * kTileKeys + lane % (kTileKeys / box) * box;
-                return a.table && j < nsteps && key < hi ? attn_page(a, b, key >> a.page_shift) : -1;
+            if (ok && steps > 0) {
+                ok = warp_wait(&bars.o_done[t], done_no++ & 1);
+                tc_fence_after();
+            }
+            write_row(it, t, ok, steps > 0, l, m, to);
+            item_left(item_no++);
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 8 || warp == 10) {
+            // ------------------------------------------------ MMA issue, one tile each
+            const int t = warp == 8 ? 0 : 1;
+            constexpr uint32_t kIdS = idesc_bf16(128, kTileKeys);
+            constexpr uint32_t kIdO = idesc_bf16(128, D) | (1u << 16);   // V: MN-major
+            const uint32_t ts = tmem + t * 128, to = tmem + kColO + t * D, qt = q0 + t * kTileBytes<D>;
+            const bool leader = elect_one();
+            // The warp stays together whatever a wait says: a lane whose wait gave
+            // up goes on without waiting, and the leader issues nothing more.
+            bool ok = true;
+            const auto wait = [&](uint64_t* bar, uint32_t parity) {
+                if (ok) ok = bounded_wait(smem_u32(bar), parity, abort_flag, limit);
+                __syncwarp();
             };
-            int ahead = look(0), page = -1;
-            for (int n = 0; n < 2 * nsteps; ++n) {
-                const int slot = n % kSlots<D>, base = lo + (n >> 1) * kTileKeys;
-                if (!(n & 1)) page = ahead, ahead = look((n >> 1) + 1);
-                if (n >= kSlots<D> && !warp_wait(&bars.kv_empty[slot], (n / kSlots<D> - 1) & 1)) break;
-                const uint32_t bar = smem_u32(&bars.kv_full[slot]);
-                const CUtensorMap* map = n & 1 ? &tm_v : &tm_k;
-                const uint32_t dst = kv0 + slot * kTileBytes<D>;
-                if (a.table) {
-                    // one box per page and 64-column half; lane l has box l mod 128 / box
-                    const int boxes = (min(kTileKeys, hi - base) + box - 1) / box, at = lane % (kTileKeys / box);
-                    if (lane == 0) mbar_expect_tx(bar, boxes * box * 128 * (D / 64));
-                    __syncwarp();
-                    for (int x = lane / (kTileKeys / box); x < D / 64; x += 32 / (kTileKeys / box))
-                        if (at < boxes)                             // (no such page: zeros)
-                            tma_load_4d(dst + x * kHalfBytes + at * box * 128, map, 64 * x,
-                                        (base + at * box) & (a.page_size - 1), h, page < 0 ? a.num_pages : page, bar);
-                } else if (lane == 0) {
-                    mbar_expect_tx(bar, kTileBytes<D>);
+            const auto scores = [&](int slot) {
+                const uint32_t k = kv0 + slot * kTileBytes<D>;
 #pragma unroll
-                    for (int x = 0; x < D / 64; ++x)
-                        tma_load_4d(dst + x * kHalfBytes, map, 64 * x, seq.row0 + base, h, 0, bar);
+                for (int x = 0; x < D / 16; ++x) {
+                    const uint32_t off = (x / 4) * kHalfBytes + (x % 4) * 32;
+                    mma_bf16<false>(ts, smem_desc_sw128(qt + off), smem_desc_sw128(k + off), kIdS, x > 0);
+                }
+                mma_commit<false>(smem_u32(&bars.s_full[t]));
+            };
+            // slots in the order K(0), V(0), K(1), ...; `next` waits for the one after the last
+            int slot = -1;
+            uint32_t lap = 0;
+            const auto next = [&]() {
+                if (++slot == kSlots<D>) slot = 0, lap ^= 1;
+                wait(&bars.kv_full[slot], lap);
+                return slot;
+            };
+            // The two tiles' batches (the product of a step and the next scores) go to
+            // the tensor pipe in turn.  Left alone, the pipe shares itself between
+            // them, both tiles then finish and start their softmax together, and the
+            // pipe waits for both (8192 tokens: 444 us).
+            uint32_t batch = 0;
+            const auto my_turn = [&]() {
+                if (t == 1) wait(&bars.turn[1], batch & 1);
+                else if (batch > 0) wait(&bars.turn[0], (batch - 1) & 1);
+                ++batch;
+            };
+            const auto pass_on = [&]() { mbar_arrive(smem_u32(&bars.turn[t ^ 1])); };
+            uint32_t step_no = 0, q_no = 0, tail_laps = 0;
+            while (__all_sync(0xffffffffu, ok)) {
+                if (!item_there(item_no)) {
+                    ok = false;
+                    break;
+                }
+                const Item& it = bars.item[item_no & 1];
+                if (uniform(it.b) < 0) break;
+                const int mine = uniform(it.steps[t]), nsteps = max(mine, uniform(it.steps[t ^ 1]));
+                const int have = uniform((it.hi - it.lo) % kTileKeys);      // keys of the last tile, 0: all
+                int kslot = 0, vslot = 0;
+                if (nsteps > 0) {
+                    kslot = next();
+                    if (mine > 0) wait(&bars.q_full[t], q_no++ & 1);
+                    my_turn();
+                    if (leader && ok) {
+                        if (mine > 0) {
+                            scores(kslot);
+                            if (mine == 1) mma_commit<false>(smem_u32(&bars.q_empty[t]));
+                        }
+                        pass_on();
+                        mma_commit<false>(smem_u32(&bars.kv_empty[kslot]));
+                    }
+                    __syncwarp();
+                }
+                for (int j = 0; j < nsteps; ++j) {
+                    vslot = next();
+                    if (j + 1 < nsteps) kslot = next();
+                    const uint32_t v = kv0 + vslot * kTileBytes<D>;
+                    if (j + 1 == nsteps && have > 0) {
+                        // rows behind the last key: their weights are 0, and 0
+                        // times whatever lies there has to be 0.  Each of the
+                        // two warps clears half of them.
+                        for (int e = lane + 32 * t; e < (kTileKeys - have) * (D / 64) * 8; e += 64) {
+                            const int row = have + (e >> 3) % (kTileKeys - have), half = (e >> 3) / (kTileKeys - have);
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                             v + half * kHalfBytes + row * 128 + (e & 7) * 16),
+                                         "r"(0)
+                                         : "memory");
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&bars.tail[item_no & 1]));
+                        wait(&bars.tail[item_no & 1], tail_laps >> (item_no & 1) & 1);
+                        tail_laps ^= 1u << (item_no & 1);
+                    }
+                    const auto product = [&](int x) {
+                        mma_f16_ta(to, ts + x * 8, smem_desc_mn(v + x * 2048), kIdO, j > 0 || x > 0);
+                    };
+                    my_turn();
+                    if (j < mine) {
+                        wait(&bars.p_most[t], step_no & 1);
+                        tc_fence_after();
+                        if (leader && ok) {
+#pragma unroll
+                            for (int x = 0; x < 6; ++x) product(x);
+                        }
+                        __syncwarp();
+                        wait(&bars.p_ready[t], step_no & 1);
+                        ++step_no;
+                        tc_fence_after();
+                    }
+                    if (leader && ok) {
+                        if (j < mine) {
+                            product(6);
+                            product(7);
+                            if (j + 1 == mine) mma_commit<false>(smem_u32(&bars.o_done[t]));
+                        }
+                        if (j + 1 < mine) {
+                            scores(kslot);
+                            if (j + 2 == mine) mma_commit<false>(smem_u32(&bars.q_empty[t]));
+                        }
+                        pass_on();
+                        mma_commit<false>(smem_u32(&bars.kv_empty[vslot]));
+                        if (j + 1 < nsteps) mma_commit<false>(smem_u32(&bars.kv_empty[kslot]));
+                    }
+                    __syncwarp();
+                }
+                item_left(item_no++);
+            }
+            // wait, bounded, for all that was issued: no arrival is outstanding
+            // when the CTA ends
+            if (leader) {
+                mma_commit<false>(smem_u32(&bars.drain[t]));
+                mbar_wait_drain(smem_u32(&bars.drain[t]), 0, kDrainLimitNs);
+            }
+            __syncwarp();
+        } else if (warp == 9) {
+            // ------------------------------------------------ TMA copies, work list
+            uint32_t loaded = 0;                                    // slots filled so far, over all items
+            uint32_t q_no[2] = {0, 0};
+            const uint32_t answer = smem_u32(bars.taken), answer_bar = smem_u32(&bars.taken_full);
+            bool ok = !a.stall_tma;
+            bool asked = false;
+            if (lane == 0) bars.announced = 1;
+            while (ok) {
+                const Item& it = bars.item[item_no & 1];
+                const int lo = uniform(it.lo), hi = uniform(it.hi), h = uniform(it.h);
+                const int nsteps = uniform(max(it.steps[0], it.steps[1]));
+                if (lane == 0) {
+                    mbar_expect_tx(answer_bar, 16);
+                    take_over(answer, answer_bar);
+                }
+                asked = true;
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (uniform(it.steps[t]) == 0) continue;
+                    if (q_no[t] > 0) ok = warp_wait(&bars.q_empty[t], (q_no[t] - 1) & 1);
+                    if (!ok) break;
+                    ++q_no[t];
+                    if (lane == 0) {
+                        const uint32_t bar = smem_u32(&bars.q_full[t]);
+                        mbar_expect_tx(bar, tokens * a.group * 128 * (D / 64));
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x)
+                            tma_load_4d(q0 + t * kTileBytes<D> + x * kHalfBytes, &tm_q, 64 * x, 0,
+                                        it.seq.row0 + it.tok0 + t * tokens, h, bar);
+                    }
+                    __syncwarp();
+                }
+                // the page of this lane's box of a step; read a step ahead
+                const auto look = [&](int j) {
+                    const int key = lo + j * kTileKeys + lane % (kTileKeys / box) * box;
+                    return a.table && j < nsteps && key < hi ? attn_page(a, it.b, key >> a.page_shift) : -1;
+                };
+                int ahead = look(0), page = -1;
+                for (int n = 0; n < 2 * nsteps && ok; ++n) {
+                    const int slot = loaded % kSlots<D>, base = lo + (n >> 1) * kTileKeys;
+                    if (!(n & 1)) page = ahead, ahead = look((n >> 1) + 1);
+                    if (loaded >= kSlots<D>) ok = warp_wait(&bars.kv_empty[slot], (loaded / kSlots<D> - 1) & 1);
+                    if (!ok) break;
+                    const uint32_t bar = smem_u32(&bars.kv_full[slot]);
+                    const CUtensorMap* map = n & 1 ? &tm_v : &tm_k;
+                    const uint32_t dst = kv0 + slot * kTileBytes<D>;
+                    if (a.table) {
+                        // one box per page and 64-column half; lane l has box l mod 128 / box
+                        const int boxes = (min(kTileKeys, hi - base) + box - 1) / box, at = lane % (kTileKeys / box);
+                        if (lane == 0) mbar_expect_tx(bar, boxes * box * 128 * (D / 64));
+                        __syncwarp();
+                        for (int x = lane / (kTileKeys / box); x < D / 64; x += 32 / (kTileKeys / box))
+                            if (at < boxes)                             // (no such page: zeros)
+                                tma_load_4d(dst + x * kHalfBytes + at * box * 128, map, 64 * x,
+                                            (base + at * box) & (a.page_size - 1), h, page < 0 ? a.num_pages : page, bar);
+                    } else if (lane == 0) {
+                        mbar_expect_tx(bar, kTileBytes<D>);
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x)
+                            tma_load_4d(dst + x * kHalfBytes, map, 64 * x, it.seq.row0 + base, h, 0, bar);
+                    }
+                    __syncwarp();
+                    ++loaded;
+                }
+                if (!ok) break;
+                // the next item
+                ok = warp_wait(&bars.taken_full, item_no & 1);
+                if (!ok) break;
+                asked = false;
+                int x, y;
+                Item nx;
+                nx.b = -1;
+                if (taken_over(answer, &x, &y)) nx = work_item(a, x, y, tokens);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (the answer is read before the next)
+                const int n = item_no + 1;
+                if (n >= 2) ok = warp_wait(&bars.item_empty[n & 1], ((n >> 1) - 1) & 1);
+                if (!ok) {
+                    if (nx.b >= 0 && lane == 0) bars.item[2] = nx, bars.orphan = 1;
+                    break;
+                }
+                if (lane == 0) {
+                    bars.item[n & 1] = nx;
+                    bars.announced = n + 1;
+                    mbar_arrive(smem_u32(&bars.item_full[n & 1]));
                 }
                 __syncwarp();
-                ++loaded;
+                item_no = n;
+                if (uniform(nx.b) < 0) break;
+            }
+            // a CTA that gave up leaves none of its copies in flight, and none of the
+            // work it took over unanswered
+            if (*abort_flag) {
+                if (asked) {
+                    mbar_wait_drain(answer_bar, item_no & 1, kDrainLimitNs);
+                    __syncwarp();
+                    int x, y;
+                    if (mbar_try_wait(answer_bar, item_no & 1) && taken_over(answer, &x, &y)) {
+                        const Item nx = work_item(a, x, y, tokens);
+                        if (lane == 0 && nx.b >= 0) bars.item[2] = nx, bars.orphan = 1;
+                    }
+                }
+                if (lane == 0) {
+                    for (int t = 0; t < 2; ++t)
+                        if (q_no[t] > 0) mbar_wait_drain(smem_u32(&bars.q_full[t]), (q_no[t] - 1) & 1, kDrainLimitNs);
+                    for (uint32_t n = loaded > kSlots<D> ? loaded - kSlots<D> : 0; n < loaded; ++n)
+                        mbar_wait_drain(smem_u32(&bars.kv_full[n % kSlots<D>]), (n / kSlots<D>) & 1, kDrainLimitNs);
+                }
+                __syncwarp();
             }
         }
-        // a CTA that gave up leaves none of its copies in flight
-        if (*abort_flag && lane == 0) {
-            for (int t = 0; t < 2; ++t)
-                if (q_loaded >> t & 1) mbar_wait_drain(smem_u32(&bars.q_full[t]), 0, kDrainLimitNs);
-            for (int n = max(0, loaded - kSlots<D>); n < loaded; ++n)
-                mbar_wait_drain(smem_u32(&bars.kv_full[n % kSlots<D>]), (n / kSlots<D>) & 1, kDrainLimitNs);
-        }
-        __syncwarp();
-    }
     }
     tc_fence_before();
     __syncthreads();
+    if (bars.abort && warp < 8) {
+        // rows of items that were handed out or taken over, and that this warp
+        // has not come to
+        for (int n = item_no; n < bars.announced; ++n)
+            if (bars.item[n & 1].b >= 0) write_row(bars.item[n & 1], warp >> 2, false, false, 0.f, 0.f, 0);
+        if (bars.orphan) write_row(bars.item[2], warp >> 2, false, false, 0.f, 0.f, 0);
+    }
     if (warp == 8) tmem_dealloc<false>(tmem, 512);
 }
 
