@@ -58,6 +58,8 @@ cudaError_t launch_attn_simt(DType dt, int d, const AttnArgs& a, cudaStream_t s)
 // Tensor-core attention of bf16 rows (prompt and prefix modes): row tiles of
 // 2 * (128 / group) tokens of one sequence.
 int64_t attn_tc_items(const AttnArgs& a);    // row tiles of the launch, per key head
+// Pages and heads as one dimension of a tensor map; false: more than 2^31 - 1 of them.
+bool attn_tc_units(const AttnArgs& a, int64_t* unit, int* per_page, int* per_head, int* count);
 cudaError_t launch_attn_tc(int d, const AttnArgs& a, cudaStream_t s);
 
 // bf16 rows of suffix mode, equal shares of the key list per CTA.  part_o null:

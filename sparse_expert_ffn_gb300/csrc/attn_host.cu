@@ -232,6 +232,16 @@ colibri_status_t run_attention(AttnArgs a, const Plan& p, int dtype, int d, int 
     return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
 }
 
+// The pages can be named by the tensor-core kernel's tensor map.
+bool mappable(const colibri_kv_pages_t* kv) {
+    AttnArgs a{};
+    a.hkv = kv->n_kv_heads, a.num_pages = kv->num_pages;
+    a.page_stride = kv->page_stride, a.head_stride = kv->head_stride;
+    int64_t unit;
+    int per_page, per_head, count;
+    return attn_tc_units(a, &unit, &per_page, &per_head, &count);
+}
+
 // The list of all keys of all heads is counted in 64 bits, times the CTAs.
 bool countable(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int n_q_heads) {
     return (double)s->n_seqs * s->table_stride * kv->page_size * n_q_heads <= 1e15;
@@ -243,7 +253,7 @@ colibri_status_t check_prompt(const colibri_kv_pages_t* kv, const colibri_seqs_t
     if (st == COLIBRI_OK) st = check_seqs(seqs, n_q_heads);
     if (st == COLIBRI_OK) st = check_kv(kv, seqs->page_table != nullptr);
     if (st != COLIBRI_OK) return st;
-    if (seqs->page_table && !countable(kv, seqs, n_q_heads)) return COLIBRI_ERR_UNSUPPORTED;
+    if (seqs->page_table && !(countable(kv, seqs, n_q_heads) && mappable(kv))) return COLIBRI_ERR_UNSUPPORTED;
     // packed keys: the call's own rows
     if (!seqs->page_table && (seqs->kv_len || (seqs->n_rows > 0 && kv->page_size != seqs->n_rows)))
         return COLIBRI_ERR_INVALID_ARG;
@@ -259,7 +269,7 @@ colibri_status_t check_decode(const colibri_kv_pages_t* kv, const colibri_seqs_t
     if (st == COLIBRI_OK) st = check_kv(kv, true);
     if (st != COLIBRI_OK) return st;
     if (prefix_len < 0 || prefix_len % kv->page_size) return COLIBRI_ERR_INVALID_ARG;
-    if (!countable(kv, seqs, n_q_heads)) return COLIBRI_ERR_UNSUPPORTED;
+    if (!countable(kv, seqs, n_q_heads) || !mappable(kv)) return COLIBRI_ERR_UNSUPPORTED;
     return COLIBRI_OK;
 }
 
