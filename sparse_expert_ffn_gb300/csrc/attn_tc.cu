@@ -245,13 +245,83 @@ __device__ __forceinline__ bool taken_over(uint32_t answer, int* x, int* y) {
     return got != 0;
 }
 
+// Item number `item` of a prompt launch with tiles of `per` rows, the tiles that
+// see the most keys first whatever sequence they are of, so that the last ones
+// to be taken over are short (in the order of the sequences, three chunks over
+// 9000, 4100 and 1024 keys took 181 us).  Tile r from the end of a sequence has
+// the key  top - r * per  (causal; else its kv length); the item is found by
+// bisection of the number of tiles whose key is at least c.  Called by a whole
+// warp, up to 32 * kKept sequences.
+constexpr int kKept = 4;
+__device__ __forceinline__ bool longest_first(const AttnArgs& a, int item, int per, int* b, int* tile) {
+    const int lane = threadIdx.x & 31;
+    int tiles[kKept], top[kKept], most = 0, sum = 0;
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+        const int q = lane + 32 * k;
+        tiles[k] = top[k] = 0;
+        if (q < a.n_seqs) {
+            const AttnSeq s = attn_seq(a, q);
+            tiles[k] = (s.n + per - 1) / per;
+            top[k] = a.causal ? max(s.raw - s.n + tiles[k] * per, 0) : s.kv;
+        }
+        if (tiles[k] > 0) most = max(most, top[k]);
+        sum += tiles[k];
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (item >= __reduce_add_sync(0xffffffffu, sum)) return false;
+    // (keys below 0 count as 0: the threshold 0 takes every tile)
+    const auto mine = [&](int k, int c) {
+        if (tiles[k] == 0) return 0;
+        if (c == 0) return tiles[k];
+        if (top[k] < c) return 0;
+        return a.causal ? min(tiles[k], (top[k] - c) / per + 1) : tiles[k];
+    };
+    const auto count = [&](int c) {
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < kKept; ++k) n += mine(k, c);
+        return __reduce_add_sync(0xffffffffu, n);
+    };
+    int lo = 0, hi = most + 1;                                  // count(lo) > item >= count(hi)
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (count(mid) > item) lo = mid;
+        else hi = mid;
+    }
+    // tiles of key lo exactly, in the order of the sequences
+    int left = item - count(hi);
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+        const int from = mine(k, hi), here = mine(k, lo) - from;
+        int upto = here;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const unsigned holds = __ballot_sync(0xffffffffu, left < upto);
+        if (holds) {
+            const int src = __ffs(holds) - 1;
+            *b = src + 32 * k;
+            *tile = __shfl_sync(0xffffffffu, tiles[k] - 1 - from - (left - (upto - here)), src);
+            return true;
+        }
+        left -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return false;                                               // (not reached)
+}
+
 // CTA (x, y) of the grid as a work item; called by a whole warp.
 __device__ __forceinline__ Item work_item(const AttnArgs& a, int x, int y, int tokens) {
     Item it;
     int tile = 0;
     it.b = -1;
     it.h = x % a.hkv, it.split = y;
-    if (!attn_item(a, x / a.hkv, 1, 2 * tokens, &it.b, &tile)) {
+    // (the order counts only where CTAs wait for their turn)
+    const bool sorted = a.mode == kAttnPrompt && a.n_seqs > 1 && a.n_seqs <= 32 * kKept && gridDim.x * gridDim.y > 152;
+    if (!(sorted ? longest_first(a, x / a.hkv, 2 * tokens, &it.b, &tile)
+                 : attn_item(a, x / a.hkv, 1, 2 * tokens, &it.b, &tile))) {
         it.b = -1;
         return it;
     }
@@ -398,7 +468,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int i = it.tok0 + t * tokens + r / a.group;
             const bool live = r < tokens * a.group && i < it.seq.n;
             const int steps = uniform(it.steps[t]), lo = uniform(it.lo);
-            const int lim = live ? min(it.hi, attn_limit(a, it.seq, i)) : 0;
+            // (a thread without a row computes what nobody reads; it masks nothing
+            // and never moves its reference)
+            const int lim = live ? min(it.hi, attn_limit(a, it.seq, i)) : it.hi;
             float m = 0.f, l = 0.f;            // reference (in units of log2), sum of the weights
             for (int j = 0; j < steps; ++j, ++step_no) {
                 ok = warp_wait(&bars.s_full[t], step_no & 1);
@@ -422,12 +494,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) tmem_ld32(ts + 32 * x, s[x]);
                     tmem_ld_wait();
-                    if (left < kTileKeys) {
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
+                    for (int x = 0; x < 4; ++x) {
+                        if (left >= 32 * x + 32) continue;         // (rows of a warp differ by few keys)
 #pragma unroll
-                            for (int y = 0; y < 32; ++y)
-                                if (x * 32 + y >= left) s[x][y] = 0xff800000u;   // -infinity
+                        for (int y = 0; y < 32; ++y)
+                            if (x * 32 + y >= left) s[x][y] = 0xff800000u;   // -infinity
                     }
                     // the weights are formed on the reference as it is, beside the
                     // maximum: it stands except for a few steps of a row
@@ -447,7 +519,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int x = 0; x < 3; ++x) weights(s[x], p[x]);
                     const float mn =
                         max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7])) * c;
-                    const bool move = mn > m + 24.f || (l == 0.f && mn < m - 64.f && mn != -INFINITY);
+                    const bool move = live && (mn > m + 24.f || (l == 0.f && mn < m - 64.f && mn != -INFINITY));
                     if (!__any_sync(0xffffffffu, move)) break;
                     // (a row without weight yet has O = 0, or none before the first product)
                     const float keep = move && l != 0.f ? ex2(m - mn) : 1.f;
@@ -625,11 +697,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const Item& it = bars.item[item_no & 1];
                 const int lo = uniform(it.lo), hi = uniform(it.hi), h = uniform(it.h);
                 const int nsteps = uniform(max(it.steps[0], it.steps[1]));
-                if (lane == 0) {
-                    mbar_expect_tx(answer_bar, 16);
-                    take_over(answer, answer_bar);
-                }
-                asked = true;
+                const auto ask = [&]() {
+                    if (lane == 0) {
+                        mbar_expect_tx(answer_bar, 16);
+                        take_over(answer, answer_bar);
+                    }
+                    asked = true;
+                };
                 for (int t = 0; t < 2 && ok; ++t) {
                     if (uniform(it.steps[t]) == 0) continue;
                     if (q_no[t] > 0) ok = warp_wait(&bars.q_empty[t], (q_no[t] - 1) & 1);
@@ -654,6 +728,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int n = 0; n < 2 * nsteps && ok; ++n) {
                     const int slot = loaded % kSlots<D>, base = lo + (n >> 1) * kTileKeys;
                     if (!(n & 1)) page = ahead, ahead = look((n >> 1) + 1);
+                    // the next item is taken as late as its copies can still follow
+                    // this one's: whoever is free first takes the longest left
+                    if (n == 2 * nsteps - 2) ask();
                     if (loaded >= kSlots<D>) ok = warp_wait(&bars.kv_empty[slot], (loaded / kSlots<D> - 1) & 1);
                     if (!ok) break;
                     const uint32_t bar = smem_u32(&bars.kv_full[slot]);
@@ -678,6 +755,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     ++loaded;
                 }
                 if (!ok) break;
+                if (nsteps == 0) ask();
                 // the next item
                 ok = warp_wait(&bars.taken_full, item_no & 1);
                 if (!ok) break;
