@@ -105,30 +105,33 @@ __device__ __forceinline__ void attn_split(const AttnArgs& a, int sp, int kt, in
     *hi = min(end, kv0 + min(tiles, (sp + 1) * per) * kt);
 }
 
-// Equal shares of the key list (attn_decode.cu): rows of a group's row tile,
-// keys of a unit, CTAs that share the list (2 per SM), units of a share at least.
+// Equal shares of the key list (attn_decode.cu).  The list is made of steps of
+// kStepKeys keys of one (sequence, key head, row tile), one after another; a
+// share goes to one warp.
 __host__ __device__ constexpr int row_tile(int group) { return group <= 16 ? 16 : 32; }
 __host__ __device__ constexpr int row_tiles(int group) { return (group + row_tile(group) - 1) / row_tile(group); }
+// rows of a piece in the workspace
+__host__ __device__ constexpr int piece_rows(int group) { return group < row_tile(group) ? group : row_tile(group); }
+template <int D> constexpr int kStepKeys = 2048 / D;
+constexpr int kShareWarps = 4;                    // per CTA
+constexpr int kShares = 2 * 152 * kShareWarps;    // 2 CTAs per SM
+constexpr int kMinSteps = 4;                      // steps of a share at least
 
-template <int D> constexpr int kUnitKeys = 8192 / D;
-constexpr int kShareCtas = 304;
-constexpr int kMinUnits = 2;
-
-// Units of sequence b per (head, row tile).
+// Steps of sequence b per (head, row tile).
 template <int D>
-__device__ __forceinline__ int seq_units(const AttnArgs& a, int b) {
+__device__ __forceinline__ int seq_steps(const AttnArgs& a, int b) {
     const AttnSeq s = attn_seq(a, b);
-    return s.kv > s.kv0 ? (s.kv - s.kv0 + kUnitKeys<D> - 1) / kUnitKeys<D> : 0;
+    return s.kv > s.kv0 ? (s.kv - s.kv0 + kStepKeys<D> - 1) / kStepKeys<D> : 0;
 }
 
-// The whole list: its length, and the units before sequence `upto`.  Called by
+// The whole list: its length, and the steps before sequence `upto`.  Called by
 // a whole warp.
 template <int D>
-__device__ __forceinline__ void count_units(const AttnArgs& a, int per_seq, int upto, int64_t* total,
+__device__ __forceinline__ void count_steps(const AttnArgs& a, int per_seq, int upto, int64_t* total,
                                             int64_t* before) {
     int64_t all = 0, part = 0;
     for (int b = threadIdx.x & 31; b < a.n_seqs; b += 32) {
-        const int64_t u = (int64_t)seq_units<D>(a, b) * per_seq;
+        const int64_t u = (int64_t)seq_steps<D>(a, b) * per_seq;
         all += u;
         if (b < upto) part += u;
     }
@@ -141,11 +144,10 @@ __device__ __forceinline__ void count_units(const AttnArgs& a, int per_seq, int 
     *before = part;
 }
 
-// CTAs that share the list, share c's first unit, and the share that unit u
-// falls into.
-__device__ __forceinline__ int share_count(int64_t total, int ctas) {
-    const int64_t most = (total + kMinUnits - 1) / kMinUnits;
-    return most < ctas ? (int)most : ctas;
+// Shares of the list, share c's first step, and the share that step u falls into.
+__device__ __forceinline__ int share_count(int64_t total) {
+    const int64_t most = (total + kMinSteps - 1) / kMinSteps;
+    return most < kShares ? (int)most : kShares;
 }
 __device__ __forceinline__ int64_t share_begin(int64_t total, int shares, int c) { return total * c / shares; }
 __device__ __forceinline__ int share_of(int64_t total, int shares, int64_t u) {

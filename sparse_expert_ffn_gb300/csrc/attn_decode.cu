@@ -5,22 +5,22 @@
 // its head group, so the products are few and what counts is that all SMs
 // stream all the time, whatever the lengths of the sequences are.
 //
-// Work is cut into units of kUnitKeys keys of one (sequence, key head, row
-// tile), laid out one after another, and every CTA takes an equal share of the
-// whole list: a CTA's share may end inside a sequence and begin inside another
-// one.  A (sequence, head) that falls to one CTA is written directly; the
-// pieces of one that is cut go to the workspace, at most two per CTA (its first
-// and its last), and the join adds them in key order.  Nothing depends on the
-// order in which CTAs run.
+// Work is cut into steps of 2048 / d keys (8 KB of K and V) of one (sequence,
+// key head, row tile), laid out one after another, and every warp of the grid
+// takes an equal share of the whole list: a share may end inside a sequence and
+// begin inside another one.  A (sequence, head) that falls to one warp is
+// written directly; the pieces of one that is cut go to the workspace, at most
+// two per warp (its first and its last), and attn_join.cu adds them in key
+// order.  Nothing depends on the order in which warps run, and no warp waits
+// for another: each streams its share through its own ring of 3 stages with
+// cp.async, two steps ahead of the products, across the ends of its pieces.
 //
-// Each of a CTA's 4 warps streams its own keys (2048 / d at a time, 8 KB of K
-// and V) through its own ring of 3 stages with cp.async, so no warp waits for
-// another until the end of a piece.  The rows of the group are the 16 rows of
-// mma.sync m16n8k16 (2 tiles up to 32 rows): tensor-memory MMAs would pad them
-// to 64 or 128 and spend most of the time of a 16-key step on that padding.
-// Scores stay in registers and become the A operand of the product with V as
-// they lie.  The running maximum and sum are f32 per row, P is rounded to bf16
-// for the product (its operands share one 16-bit type).
+// The rows of the group are the 16 rows of mma.sync m16n8k16 (2 tiles up to 32
+// rows): tensor-memory MMAs would pad them to 64 or 128 and spend most of the
+// time of a 16-key step on that padding.  Scores stay in registers and become
+// the A operand of the product with V as they lie.  The reference maximum and
+// the sum are f32 per row, P is rounded to bf16 for the product (its operands
+// share one 16-bit type).
 #include <cuda_runtime.h>
 
 #include "attn_common.cuh"
@@ -29,13 +29,11 @@
 namespace colibri {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kDecThreads = 32 * kWarps;
+constexpr int kDecThreads = 32 * kShareWarps;
 constexpr int kStages = 3;
-template <int D> constexpr int kStepKeys = 2048 / D;              // keys of a warp's step
-static_assert(kUnitKeys<64> == kWarps * kStepKeys<64> && kUnitKeys<128> == kWarps * kStepKeys<128>, "a unit is a step of every warp");
 constexpr int kStageBytes = 8192;                                 // K then V of one step
 constexpr int kRingBytes = kStages * kStageBytes;
+
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) {
     const int n = there ? 16 : 0;                                  // 0: the 16 bytes become zeros
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
@@ -63,8 +61,37 @@ __device__ __forceinline__ uint32_t bf16x2(float x, float y) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// One warp's stream over the keys of a piece: which step is copied next.  The
-// page ids of up to 32 page parts ahead lie one per lane.
+// A position in a warp's share: the piece it is in, step by step.
+template <int D>
+struct Walk {
+    int b, units;              // sequence, its steps per (head, row tile)
+    int64_t in_seq;            // steps of sequence b before the piece
+    int item;                  // (head, row tile) of the sequence
+    int lo, hi;                // keys of the piece
+    int step, count;           // steps of the piece: done, all
+    bool whole;                // the piece is all of the sequence's steps
+
+    // The piece at in_seq, of at most `left` steps.  False: nothing there.
+    __device__ __forceinline__ bool piece(const AttnArgs& a, int per_seq, int64_t left) {
+        if (in_seq == (int64_t)units * per_seq) {
+            in_seq = 0, units = 0;
+            while (++b < a.n_seqs && (units = seq_steps<D>(a, b)) == 0) {}
+            if (units == 0) return false;                          // (not reached: left > 0)
+        }
+        const AttnSeq s = attn_seq(a, b);
+        item = (int)(in_seq / units);
+        const int first = (int)(in_seq - (int64_t)item * units);
+        count = (int)min((int64_t)(units - first), left);
+        whole = count == units;
+        lo = s.kv0 + first * kStepKeys<D>;
+        hi = min(s.kv, lo + count * kStepKeys<D>);
+        step = 0;
+        in_seq += count;
+        return true;
+    }
+};
+
+// One warp's copies.  The page ids of up to 32 page parts ahead lie one per lane.
 template <int D>
 struct Stream {
     static constexpr int kChunks = D / 8;                          // 16-byte chunks of a row
@@ -90,9 +117,7 @@ struct Stream {
         parts = a.page_size < kStepKeys<D> ? kStepKeys<D> / a.page_size : 1;
         if (a.table) fill(a, 0);
     }
-    __device__ __forceinline__ int first_key(int step) const {
-        return lo + (step * kWarps + (int)(threadIdx.x >> 5)) * kStepKeys<D>;
-    }
+    __device__ __forceinline__ int first_key(int step) const { return lo + step * kStepKeys<D>; }
     __device__ __forceinline__ void fill(const AttnArgs& a, int step) {
         const int lane = threadIdx.x & 31;
         window = step;
@@ -150,74 +175,60 @@ struct Stream {
 };
 
 template <int D, int MT>
-__global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(AttnArgs a, int per_seq) {
-    constexpr int KS = kStepKeys<D>, ROWS = 16 * MT, kAcc = D + 4;
-    static_assert(ROWS * (kAcc + 2) * 4 <= kRingBytes, "a warp's rows fit its ring");
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t place[4];
-    pdl_enter();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__device__ __forceinline__ void decode_share(const AttnArgs& a, int per_seq, uint8_t* smem) {
+    constexpr int KS = kStepKeys<D>, ROWS = 16 * MT;
+    const int lane = threadIdx.x & 31, share = blockIdx.x * kShareWarps + (threadIdx.x >> 5);
     const int tiles = row_tiles(a.group);
-    // this CTA's share u0 .. u1 - 1, and the sequence that u0 lies in
-    if (warp == 0) {
-        int64_t total, unused;
-        count_units<D>(a, per_seq, 0, &total, &unused);
-        int64_t u0 = 0, u1 = 0, before = 0;
-        if (total > 0) {
-            const int shares = share_count(total, gridDim.x);
-            if ((int)blockIdx.x < shares) {
-                u0 = share_begin(total, shares, blockIdx.x);
-                u1 = share_begin(total, shares, blockIdx.x + 1);
-            }
-        }
-        int seq = 0;
-        if (u1 > u0) {
-            for (int base = 0;; base += 32) {
-                int64_t upto = base + lane < a.n_seqs ? (int64_t)seq_units<D>(a, base + lane) * per_seq : 0;
-                const int64_t mine = upto;
+    // this warp's share of the list, and the sequence that its first step lies in
+    int64_t total, left, before = 0, u0;
+    count_steps<D>(a, per_seq, 0, &total, &left);
+    if (total == 0) return;
+    const int shares = share_count(total);
+    if (share >= shares) return;
+    u0 = share_begin(total, shares, share);
+    left = share_begin(total, shares, share + 1) - u0;             // (at least one)
+    Walk<D> load;
+    for (int base = 0;; base += 32) {
+        const int mine = base + lane < a.n_seqs ? seq_steps<D>(a, base + lane) : 0;
+        int64_t upto = (int64_t)mine * per_seq;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-                    if (lane >= o) upto += v;
-                }
-                const unsigned holds = __ballot_sync(0xffffffffu, u0 < before + upto);
-                if (holds) {
-                    const int src = __ffs(holds) - 1;
-                    seq = base + src;
-                    before += __shfl_sync(0xffffffffu, upto - mine, src);
-                    break;
-                }
-                before += __shfl_sync(0xffffffffu, upto, 31);
-            }
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
         }
-        if (lane == 0) place[0] = u0, place[1] = u1, place[2] = seq, place[3] = u0 - before;
+        const unsigned holds = __ballot_sync(0xffffffffu, u0 - before < upto);
+        if (holds) {
+            const int src = __ffs(holds) - 1;
+            load.b = base + src;
+            load.units = __shfl_sync(0xffffffffu, mine, src);
+            load.in_seq = u0 - before - (__shfl_sync(0xffffffffu, upto, src) - (int64_t)load.units * per_seq);
+            break;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    __syncthreads();
-    const int64_t u1 = place[1];
-    int64_t u = place[0];
-    if (u >= u1) return;
-    int b = (int)place[2];
-    int64_t in_seq = place[3];                                     // units of sequence b before u
-    const int64_t begin = u;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * kRingBytes;
-    float* own = reinterpret_cast<float*>(smem + warp * kRingBytes);
-
-    while (u < u1) {
-        int units = 0;
-        while (b < a.n_seqs && (units = seq_units<D>(a, b)) == 0) ++b;
-        if (units == 0) return;                                    // (not reached: u < u1)
-        const AttnSeq sq = attn_seq(a, b);
-        const int item = (int)(in_seq / units), step0 = (int)(in_seq % units);
-        const int h = item / tiles, r0 = (item % tiles) * ROWS;
-        const int count = (int)min((int64_t)(units - step0), u1 - u);   // units of this piece
-        Stream<D> st;
-        st.begin(a, b, h, sq.kv0 + step0 * kUnitKeys<D>,
-                 min(sq.kv, sq.kv0 + (step0 + count) * kUnitKeys<D>));
-#pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) {
-            if (s < count) st.copy(a, s, ring + s * kStageBytes);
-            cp_commit();
+    Walk<D> at = load;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * kRingBytes;
+    int64_t to_load = left;
+    Stream<D> st;
+    int slot_in = 0, slot_out = 0;
+    load.step = load.count = 0;
+    const auto copy_next = [&]() {
+        if (to_load > 0) {
+            if (load.step == load.count) {
+                if (!load.piece(a, per_seq, to_load)) return;
+                st.begin(a, load.b, load.item / tiles, load.lo, load.hi);
+            }
+            st.copy(a, load.step++, ring + slot_in * kStageBytes);
+            --to_load;
         }
+        slot_in = slot_in == kStages - 1 ? 0 : slot_in + 1;
+    };
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) copy_next(), cp_commit();
+    bool first_piece = true;
+#pragma unroll 1
+    while (left > 0 && at.piece(a, per_seq, left)) {
+        const int b = at.b, h = at.item / tiles, r0 = (at.item % tiles) * ROWS;
         // the group's rows as A operands: row lane / 4 (+ 8), columns 2 (lane % 4) (+ 8)
         uint32_t qf[MT][D / 16][4];
 #pragma unroll
@@ -240,14 +251,15 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(AttnArgs a,
 #pragma unroll
             for (int x = 0; x < D / 8; ++x) o[t][x][0] = o[t][x][1] = o[t][x][2] = o[t][x][3] = 0.f;
         }
-        for (int step = 0; step < count; ++step) {
+#pragma unroll 1
+        for (int step = 0; step < at.count; ++step) {
             cp_wait<kStages - 2>();
             __syncwarp();
             // (the stage that this copy fills was read in the previous step)
-            if (step + kStages - 1 < count)
-                st.copy(a, step + kStages - 1, ring + (step + kStages - 1) % kStages * kStageBytes);
+            copy_next();
             cp_commit();
-            const uint32_t ks = ring + step % kStages * kStageBytes, vs = ks + kStageBytes / 2;
+            const uint32_t ks = ring + slot_out * kStageBytes, vs = ks + kStageBytes / 2;
+            slot_out = slot_out == kStages - 1 ? 0 : slot_out + 1;
             float s[MT][KS / 8][4];
 #pragma unroll
             for (int t = 0; t < MT; ++t)
@@ -266,17 +278,17 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(AttnArgs a,
                         mma16816(s[t][2 * n + 1], qf[t][x], kf[2], kf[3]);
                     }
                 }
-            const int left = st.hi - st.first_key(step);           // keys of this step
+            const int keys = at.hi - (at.lo + step * KS);          // of this step
             uint32_t pf[MT][KS / 16][4];
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 float top[2] = {-INFINITY, -INFINITY};
-                if (left < KS) {
+                if (keys < KS) {
 #pragma unroll
                     for (int n = 0; n < KS / 8; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (n * 8 + 2 * (lane & 3) + (e & 1) >= left) s[t][n][e] = -INFINITY;
+                            if (n * 8 + 2 * (lane & 3) + (e & 1) >= keys) s[t][n][e] = -INFINITY;
                 }
 #pragma unroll
                 for (int n = 0; n < KS / 8; ++n)
@@ -327,78 +339,66 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(AttnArgs a,
                     }
                 }
         }
-        cp_wait<0>();
-        __syncwarp();
-        // the warps' rows, added in warp order
+        left -= at.count;
+        // the piece's rows: the result, or a part of it
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                l[t][r] += __shfl_xor_sync(0xffffffffu, l[t][r], 1);
-                l[t][r] += __shfl_xor_sync(0xffffffffu, l[t][r], 2);
-                const int row = 16 * t + 8 * r + (lane >> 2);
+                float sum = l[t][r];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                const int row = 16 * t + 8 * r + (lane >> 2), g = r0 + row;
+                if (g >= a.group) continue;
+                const float inv = sum > 0.f ? 1.f / sum : sum;     // no key: 0; NaN stays
+                const float lse2 = sum == 0.f ? -INFINITY : m[t][r] + log2f(sum);
+                const int head = h * a.group + g, c = 2 * (lane & 3);
+                const int64_t flat = (int64_t)b * a.hq + head;
+                if (at.whole && !a.part_o) {
+                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + (int64_t)b * a.o_stride + (int64_t)head * D + c;
+#pragma unroll
+                    for (int x = 0; x < D / 8; ++x)
+                        *reinterpret_cast<uint32_t*>(out + x * 8) = bf16x2(o[t][x][2 * r] * inv, o[t][x][2 * r + 1] * inv);
+                    if (c == 0 && a.lse) a.lse[flat] = lse2 * kLn2;
+                    continue;
+                }
+                const int64_t to = at.whole ? (int64_t)a.part_slot * a.n_rows * a.hq + flat
+                                            : ((int64_t)share * 2 + (first_piece ? 0 : 1)) * piece_rows(a.group) + row;
+                float* out = (at.whole ? a.part_o : a.piece_o) + to * D + c;
 #pragma unroll
                 for (int x = 0; x < D / 8; ++x)
-                    *reinterpret_cast<float2*>(own + row * kAcc + x * 8 + 2 * (lane & 3)) =
-                        make_float2(o[t][x][2 * r], o[t][x][2 * r + 1]);
-                if ((lane & 3) == 0) own[ROWS * kAcc + row] = m[t][r], own[ROWS * (kAcc + 1) + row] = l[t][r];
+                    *reinterpret_cast<float2*>(out + x * 8) = make_float2(o[t][x][2 * r] * inv, o[t][x][2 * r + 1] * inv);
+                if (c == 0) (at.whole ? a.part_lse : a.piece_lse)[to] = lse2;
             }
-        __syncthreads();
-        const bool whole = step0 == 0 && count == units;           // the (sequence, head) is this CTA's alone
-        for (int e = threadIdx.x; e < ROWS * (D / 4); e += kDecThreads) {
-            const int row = e / (D / 4), c = (e % (D / 4)) * 4, g = r0 + row;
-            if (g >= a.group) continue;
-            float top = -INFINITY, sum = 0.f;
-            const float* all = reinterpret_cast<const float*>(smem);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, all[w * (kRingBytes / 4) + ROWS * kAcc + row]);
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float* p = all + w * (kRingBytes / 4);
-                const float mw = p[ROWS * kAcc + row], f = mw == -INFINITY ? 0.f : ex2(mw - top);
-                const float4 v = *reinterpret_cast<const float4*>(p + row * kAcc + c);
-                sum += f * p[ROWS * (kAcc + 1) + row];
-                acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y);
-                acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
-            }
-            const float inv = sum > 0.f ? 1.f / sum : sum;
-            acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-            const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
-            const int head = h * a.group + g;
-            const int64_t flat = (int64_t)b * a.hq + head;
-            if (whole && !a.part_o) {
-                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + (int64_t)b * a.o_stride + (int64_t)head * D + c;
-                *reinterpret_cast<uint2*>(out) = make_uint2(bf16x2(acc.x, acc.y), bf16x2(acc.z, acc.w));
-                if (c == 0 && a.lse) a.lse[flat] = lse2 * kLn2;
-            } else if (whole) {
-                const int64_t at = (int64_t)a.part_slot * a.n_rows * a.hq + flat;
-                *reinterpret_cast<float4*>(a.part_o + at * D + c) = acc;
-                if (c == 0) a.part_lse[at] = lse2;
-            } else {
-                const int64_t at = ((int64_t)blockIdx.x * 2 + (u == begin ? 0 : 1)) * ROWS + row;
-                *reinterpret_cast<float4*>(a.piece_o + at * D + c) = acc;
-                if (c == 0) a.piece_lse[at] = lse2;
-            }
-        }
-        __syncthreads();
-        u += count;
-        in_seq += count;
-        if (in_seq == (int64_t)units * per_seq) ++b, in_seq = 0;
+        first_piece = false;
     }
+    cp_wait<0>();
+}
+
+// Behind a prefix launch (beside_prefix) the kernel starts while that one is
+// running, on the SMs that it leaves: it needs nothing of it, and what came
+// before it is complete when its CTAs let this kernel start.  It waits for it at
+// the end, so that the join, which waits for this kernel, finds both done.
+template <int D, int MT>
+__global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __grid_constant__ AttnArgs a, int per_seq) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    if (!a.beside_prefix) pdl_wait();
+    pdl_launch_dependents();
+    decode_share<D, MT>(a, per_seq, smem);
+    if (a.beside_prefix) pdl_wait();
 }
 
 template <int D, int MT>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     auto kern = attn_decode_kernel<D, MT>;
-    const int bytes = kWarps * kRingBytes, per_seq = a.hkv * row_tiles(a.group);
+    const int bytes = kShareWarps * kRingBytes, per_seq = a.hkv * row_tiles(a.group);
     cudaError_t e = smem_attr((const void*)kern, bytes);
-    return e != cudaSuccess ? e : launch_pdl(kern, dim3(kShareCtas), dim3(kDecThreads), bytes, s, a, per_seq);
+    return e != cudaSuccess ? e : launch_pdl(kern, dim3(kShares / kShareWarps), dim3(kDecThreads), bytes, s, a, per_seq);
 }
 
 }  // namespace
 
-size_t attn_decode_pieces(int group) { return (size_t)kShareCtas * 2 * row_tile(group); }
+size_t attn_decode_pieces(int group) { return (size_t)kShares * 2 * piece_rows(group); }
 
 cudaError_t launch_attn_decode(int d, const AttnArgs& a, cudaStream_t s) {
     if (d == 64) return a.group <= 16 ? launch<64, 1>(a, s) : launch<64, 2>(a, s);

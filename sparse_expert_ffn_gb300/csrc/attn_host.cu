@@ -21,6 +21,7 @@ namespace {
 // workspace's size does not depend on the machine that asks for it.
 constexpr int kSms = 152;
 constexpr int kMaxSplits = 64;
+constexpr int kPrefixSms = 104;
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
@@ -131,10 +132,11 @@ int64_t row_tiles(const AttnArgs& a, bool tensor_cores) {
 // bf16 prompts and prefixes run on the tensor cores.
 bool on_tensor_cores(int dtype, int mode) { return dtype == COLIBRI_DTYPE_BF16 && mode != kAttnSuffix; }
 
-// (one tensor-core CTA per SM, two of the CUDA-core kernel)
+// (one tensor-core CTA per SM, two of the CUDA-core kernel; a prefix on the
+// tensor cores leaves SMs to the sequences' own keys, which run beside it)
 int splits_for(const AttnArgs& a, const colibri_kv_pages_t* kv, int64_t keys) {
     const bool tc = on_tensor_cores(kv->dtype, a.mode);
-    return choose_splits(row_tiles(a, tc) * kv->n_kv_heads, keys, tc ? kSms : 2 * kSms);
+    return choose_splits(row_tiles(a, tc) * kv->n_kv_heads, keys, !tc ? 2 * kSms : a.mode == kAttnPrefix ? kPrefixSms : kSms);
 }
 
 Plan make_plan(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq, int mode, int prefix_len) {
@@ -225,6 +227,7 @@ colibri_status_t run_attention(AttnArgs a, const Plan& p, int dtype, int d, int 
     }
     a.splits = p.own;
     a.part_slot = p.prefix;
+    a.beside_prefix = p.prefix > 0;
     if (e == cudaSuccess) e = p.shares ? launch_attn_decode(d, a, s) : launch_attention(dtype, d, a, s);
     if (e == cudaSuccess && (p.shares || p.slots() > 0))
         e = launch_attn_join(dtype_of(dtype), d, a, p.shares ? p.prefix : p.slots(), p.shares, s);

@@ -4,8 +4,8 @@
 //
 // One CTA per (row, head).  Bound by latency: the log2-sums are read all at
 // once, then every warp adds its own quarter of the rows with independent
-// loads, and the quarters are added at the end.  A range that held no key has
-// log2-sum -infinity and its rows, never written, are not read.
+// loads, and the quarters are added at the end.  A range that held no key of the
+// row has log2-sum -infinity, so weight 0, and left zeros.
 #include <cuda_runtime.h>
 
 #include "attn_common.cuh"
@@ -15,7 +15,7 @@ namespace colibri {
 namespace {
 
 constexpr int kJoinThreads = 128;
-constexpr int kMaxParts = 512;            // 64 + 1 slots and 304 pieces at most
+constexpr int kMaxParts = kShares + 72;   // 64 + 1 slots and a piece per share at most
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int slots, int shares_per_seq) {
@@ -32,10 +32,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int
         int live = 1, c0 = 0, c1 = -1, first_is_last = 0;
         if (shares_per_seq) {
             int64_t total, first;
-            count_units<D>(a, shares_per_seq, row, &total, &first);
-            const int units = seq_units<D>(a, row);
+            count_steps<D>(a, shares_per_seq, row, &total, &first);
+            const int units = seq_steps<D>(a, row);
             if (units > 0) {
-                const int shares = share_count(total, kShareCtas);
+                const int shares = share_count(total);
                 first += (int64_t)((head / a.group) * row_tiles(a.group) + g / ROWS) * units;
                 c0 = share_of(total, shares, first);
                 c1 = share_of(total, shares, first + units - 1);
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int
     // part i: its index among the slots' or the pieces' rows
     const auto piece = [&](int i) {
         const int c = c0 + i - in_slots;
-        return ((int64_t)c * 2 + (c == c0 && place[3])) * ROWS + g % ROWS;
+        return ((int64_t)c * 2 + (c == c0 && place[3])) * piece_rows(a.group) + g % ROWS;
     };
     float top = -INFINITY;
     bool bad = false;
@@ -78,11 +78,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
     if (top != -INFINITY) {
-#pragma unroll 4
+#pragma unroll 8
         for (int i = warp; i < parts; i += 4) {
-            const float w2 = weight[i];
-            if (w2 == -INFINITY) continue;
-            const float w = ex2(w2 - top);
+            const float w = ex2(weight[i] - top);
             sum += w;
             if (lane < D / 4) {
                 const float* p = i < in_slots ? a.part_o + (i * total_rows + flat) * D : a.piece_o + piece(i) * D;
