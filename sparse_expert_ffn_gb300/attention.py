@@ -130,8 +130,7 @@ class Sequences:
 
 def _same(t, name, heads, head_dim, dtype, device, rows):
     """Checks a row tensor; returns its row stride."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or t.dtype != dtype or \
-            t.device != device or t.shape[0] != rows:
+    if t.shape != (rows, heads, head_dim) or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name} must be [{rows}, {heads}, {head_dim}], {dtype}, on {device}")
     s0, s1, s2 = t.stride()
     if s2 != 1 or (heads > 1 and s1 != head_dim):
@@ -147,26 +146,29 @@ def _norm(w, name, head_dim, dtype, device):
     return w.data_ptr()
 
 
-class _On:
-    """The call's device made current, and the stream to run on."""
-
-    __slots__ = ("idx", "prev")
-
-    def __init__(self, device):
-        self.idx = device.index
-
-    def __enter__(self):
-        self.prev = torch.cuda.current_device()
-        if self.prev != self.idx:
-            torch.cuda.set_device(self.idx)
-
-    def __exit__(self, *exc):
-        if self.prev != self.idx:
-            torch.cuda.set_device(self.prev)
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _stream(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    """The stream to run on: the device's current one by default."""
+    return _raw_stream(device.index) if stream is None else stream.cuda_stream
+
+
+def _on(device, call, what, *args):
+    """The C call with the tensors' device current."""
+    prev = _current_device()
+    if prev == device.index:
+        status = call(*args)
+    else:
+        torch.cuda.set_device(device.index)
+        try:
+            status = call(*args)
+        finally:
+            torch.cuda.set_device(prev)
+    if status:
+        _sef._check(status, what)
 
 
 def _rope_ref(rope, device):
@@ -200,9 +202,8 @@ def append_qkv(cache: PagedKVCache, seqs: Sequences, q, k, v, *, rope: Optional[
             q_out.data_ptr(), _same(q_out, "q_out", hq, D, dt, dev, rows))
     if rows == 0:
         return q_out
-    with _On(dev):
-        _sef._check(_sef.library().colibri_append_qkv(cache._ref, seqs._rows(q), *args, _stream(stream, dev)),
-                    "colibri_append_qkv")
+    _on(dev, _sef.library().colibri_append_qkv, "colibri_append_qkv", cache._ref, seqs._rows(q), *args,
+        _stream(stream, dev))
     return q_out
 
 
@@ -224,9 +225,8 @@ def qk_norm_rope(seqs: Sequences, q, k, *, rope: Optional[Rope] = None, q_norm=N
             k_out.data_ptr(), _same(k_out, "k_out", hkv, D, dt, dev, rows))
     if rows == 0:
         return q_out, k_out
-    with _On(dev):
-        _sef._check(_sef.library().colibri_qk_norm_rope(seqs._rows(q), *args, _stream(stream, dev)),
-                    "colibri_qk_norm_rope")
+    _on(dev, _sef.library().colibri_qk_norm_rope, "colibri_qk_norm_rope", seqs._rows(q), *args,
+        _stream(stream, dev))
     return q_out, k_out
 
 
@@ -240,10 +240,15 @@ def _outputs(q, out, lse):
     return out, (None if lse is None else lse.data_ptr()), _same(out, "out", hq, D, q.dtype, q.device, rows)
 
 
-def _workspace(nbytes, device):
-    """A call's workspace, from the caching allocator: ordered on the current
+def _workspace(nbytes, device, stream):
+    """A call's workspace, from the caching allocator: ordered on the call's
     stream like any tensor, a graph's own while a graph is captured."""
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    if not nbytes:
+        return None
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def _prompt(kv, kv_ref, seqs, q, scale, causal, out, lse, stream):
@@ -260,29 +265,11 @@ def _prompt(kv, kv_ref, seqs, q, scale, causal, out, lse, stream):
     ref, lib, need = seqs._rows(q), _sef.library(), ctypes.c_size_t()
     _sef._check(lib.colibri_attention_prompt_workspace(kv_ref, ref, hq, ctypes.byref(need)),
                 "colibri_attention_prompt_workspace")
-    with _On(dev), _ambient(stream):
-        ws = _workspace(need.value, dev)
-        _sef._check(lib.colibri_attention_prompt(
-            kv_ref, ref, hq, q.data_ptr(), stride, D ** -0.5 if scale is None else float(scale), int(causal),
-            out.data_ptr(), o_stride, lse_ptr, None if ws is None else ws.data_ptr(), need.value,
-            _stream(stream, dev)), "colibri_attention_prompt")
+    ws = _workspace(need.value, dev, stream)
+    _on(dev, lib.colibri_attention_prompt, "colibri_attention_prompt", kv_ref, ref, hq, q.data_ptr(), stride,
+        D ** -0.5 if scale is None else float(scale), int(causal), out.data_ptr(), o_stride, lse_ptr,
+        None if ws is None else ws.data_ptr(), need.value, _stream(stream, dev))
     return out
-
-
-class _Nothing:
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *exc):
-        pass
-
-
-_NOTHING = _Nothing()
-
-
-def _ambient(stream):
-    """The workspace is allocated on the stream that the kernels run on."""
-    return _NOTHING if stream is None else torch.cuda.stream(stream)
 
 
 class _Packed:
@@ -349,10 +336,8 @@ def attention_decode(cache: PagedKVCache, seqs: Sequences, q, *, prefix_len: int
     ref, lib, need = seqs._rows(q), _sef.library(), ctypes.c_size_t()
     _sef._check(lib.colibri_attention_decode_workspace(cache._ref, ref, hq, int(prefix_len), ctypes.byref(need)),
                 "colibri_attention_decode_workspace")
-    with _On(dev), _ambient(stream):
-        ws = _workspace(need.value, dev)
-        _sef._check(lib.colibri_attention_decode(
-            cache._ref, ref, hq, q.data_ptr(), stride, D ** -0.5 if scale is None else float(scale),
-            int(prefix_len), table, out.data_ptr(), o_stride, lse_ptr, None if ws is None else ws.data_ptr(),
-            need.value, _stream(stream, dev)), "colibri_attention_decode")
+    ws = _workspace(need.value, dev, stream)
+    _on(dev, lib.colibri_attention_decode, "colibri_attention_decode", cache._ref, ref, hq, q.data_ptr(), stride,
+        D ** -0.5 if scale is None else float(scale), int(prefix_len), table, out.data_ptr(), o_stride, lse_ptr,
+        None if ws is None else ws.data_ptr(), need.value, _stream(stream, dev))
     return out

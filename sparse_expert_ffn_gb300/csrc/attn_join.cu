@@ -3,8 +3,8 @@
 // in a fixed order, so that results do not depend on timing.
 //
 // One CTA per (row, head).  Bound by latency: the log2-sums are read all at
-// once, then every warp adds its own quarter of the rows with independent
-// loads, and the quarters are added at the end.  A range that held no key of the
+// once, then every warp adds its own share of the rows with independent loads,
+// and the shares are added at the end.  A range that held no key of the
 // row has log2-sum -infinity, so weight 0, and left zeros.
 #include <cuda_runtime.h>
 
@@ -14,13 +14,13 @@
 namespace colibri {
 namespace {
 
-constexpr int kJoinThreads = 128;
 constexpr int kMaxParts = kShares + 72;   // 64 + 1 slots and a piece per share at most
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int slots, int shares_per_seq) {
+template <typename T, int D, int kThreads>
+__global__ void __launch_bounds__(kThreads) attn_join_kernel(AttnArgs a, int slots, int shares_per_seq) {
     __shared__ float weight[kMaxParts];
-    __shared__ float4 quarter[4][D / 4];
+    constexpr int kWarps = kThreads / 32;
+    __shared__ float4 share[kWarps][D / 4];
     __shared__ int place[5];
     pdl_enter();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -62,24 +62,29 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int
     };
     float top = -INFINITY;
     bool bad = false;
-    for (int i = tid; i < parts; i += kJoinThreads) {
+    for (int i = tid; i < parts; i += kThreads) {
         const float v = i < in_slots ? a.part_lse[i * total_rows + flat] : a.piece_lse[piece(i)];
         weight[i] = v;
         top = fmaxf(top, v);
         bad |= isnan(v);
     }
-    __shared__ float tops[4];
+    __shared__ float tops[kWarps], sums[kWarps];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) tops[warp] = top;
     // a NaN log2-sum (scores that are NaN, rows whose wait gave up) makes the row NaN
-    top = __syncthreads_or(bad) ? __int_as_float(0x7fc00000)
-                                : fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+    if (__syncthreads_or(bad)) {
+        top = __int_as_float(0x7fc00000);
+    } else {
+        top = tops[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, tops[w]);
+    }
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
     if (top != -INFINITY) {
 #pragma unroll 8
-        for (int i = warp; i < parts; i += 4) {
+        for (int i = warp; i < parts; i += kWarps) {
             const float w = ex2(weight[i] - top);
             sum += w;
             if (lane < D / 4) {
@@ -90,15 +95,17 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int
             }
         }
     }
-    __shared__ float sums[4];
-    if (lane < D / 4) quarter[warp][lane] = acc;
+    if (lane < D / 4) share[warp][lane] = acc;
     if (lane == 0) sums[warp] = sum;
     __syncthreads();
-    sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += sums[w];
     const float inv = sum > 0.f ? 1.f / sum : sum;                 // no key: 0; NaN stays
     if (tid < D) {
-        const float* q = reinterpret_cast<const float*>(quarter);
-        const float v = (q[tid] + q[D + tid]) + (q[2 * D + tid] + q[3 * D + tid]);
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v += reinterpret_cast<const float*>(share[w])[tid];
         static_cast<T*>(a.o)[(int64_t)row * a.o_stride + (int64_t)head * D + tid] = from_f32<T>(v * inv);
     }
     if (tid == 0 && a.lse) a.lse[flat] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
@@ -108,8 +115,11 @@ template <typename T, int D>
 cudaError_t launch(const AttnArgs& a, int slots, bool shares, cudaStream_t s) {
     const int64_t rows = (int64_t)a.n_rows * a.hq;
     if (rows == 0) return cudaSuccess;
-    return launch_pdl(attn_join_kernel<T, D>, dim3((unsigned)rows), dim3(kJoinThreads), 0, s, a, slots,
-                      shares ? a.hkv * row_tiles(a.group) : 0);
+    const int per_seq = shares ? a.hkv * row_tiles(a.group) : 0;
+    // few rows may have many pieces each (one sequence: 32 rows of 152), many rows few
+    if (rows <= 2 * 152)
+        return launch_pdl(attn_join_kernel<T, D, 512>, dim3((unsigned)rows), dim3(512), 0, s, a, slots, per_seq);
+    return launch_pdl(attn_join_kernel<T, D, 128>, dim3((unsigned)rows), dim3(128), 0, s, a, slots, per_seq);
 }
 
 }  // namespace
