@@ -719,15 +719,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     __syncwarp();
                 }
-                // the page of this lane's box of a step; read a step ahead
-                const auto look = [&](int j) {
-                    const int key = lo + j * kTileKeys + lane % (kTileKeys / box) * box;
-                    return kPaged && j < nsteps && key < hi ? attn_page(a, it.b, key >> a.page_shift) : -1;
+                // page ids of 32 boxes, one per lane, and of the 32 after them
+                const int per_step = kTileKeys / box;
+                const auto look = [&](int first) {
+                    const int key = lo + (first + lane) * box;
+                    return kPaged && key < hi ? attn_page(a, it.b, key >> a.page_shift) : -1;
                 };
-                int ahead = look(0), page = -1;
+                int ids = look(0), ids_ahead = look(32), page = -1;
                 for (int n = 0; n < 2 * nsteps && ok; ++n) {
                     const int slot = loaded % kSlots<D>, base = lo + (n >> 1) * kTileKeys;
-                    if (!(n & 1)) page = ahead, ahead = look((n >> 1) + 1);
+                    if (kPaged && !(n & 1)) {
+                        const int first = (n >> 1) * per_step;
+                        if (first > 0 && (first & 31) == 0) ids = ids_ahead, ids_ahead = look(first + 32);
+                        page = __shfl_sync(0xffffffffu, ids, (first + lane) & 31);
+                    }
                     // the next item is taken as late as its copies can still follow
                     // this one's: whoever is free first takes the longest left
                     if (n == 2 * nsteps - 2) ask();
