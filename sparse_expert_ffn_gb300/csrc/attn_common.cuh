@@ -149,9 +149,15 @@ __device__ __forceinline__ int share_count(int64_t total) {
     const int64_t most = (total + kMinSteps - 1) / kMinSteps;
     return most < kShares ? (int)most : kShares;
 }
-__device__ __forceinline__ int64_t share_begin(int64_t total, int shares, int c) { return total * c / shares; }
+// (in 32 bits where the products fit them: a 64-bit division is some 100 instructions)
+constexpr int64_t kSmallList = 1 << 21;
+static_assert(kSmallList * kShares < ((int64_t)1 << 32), "fits 32 bits");
+__device__ __forceinline__ int64_t share_begin(int64_t total, int shares, int c) {
+    return total < kSmallList ? (uint32_t)total * (uint32_t)c / (uint32_t)shares : total * c / shares;
+}
 __device__ __forceinline__ int share_of(int64_t total, int shares, int64_t u) {
-    return (int)(((u + 1) * shares - 1) / total);
+    return total < kSmallList ? (int)(((uint32_t)(u + 1) * (uint32_t)shares - 1u) / (uint32_t)total)
+                              : (int)(((u + 1) * shares - 1) / total);
 }
 
 constexpr float kLn2 = 0.69314718055994530942f;
