@@ -375,9 +375,9 @@ __device__ __forceinline__ void decode_share(const AttnArgs& a, int per_seq, uin
     cp_wait<0>();
 }
 
-// Behind a prefix launch (beside_prefix) the kernel starts while that one is
-// running, on the SMs that it leaves: it needs nothing of it, and what came
-// before it is complete when its CTAs let this kernel start.  It waits for it at
+// Behind a prefix launch (beside_prefix) the kernel starts on the SMs that this
+// one has left: it needs nothing of it, and what came before it is complete when
+// its CTAs let this kernel start.  It waits for it at
 // the end, so that the join, which waits for this kernel, finds both done.
 template <int D, int MT>
 __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __grid_constant__ AttnArgs a, int per_seq) {

@@ -21,7 +21,6 @@ namespace {
 // workspace's size does not depend on the machine that asks for it.
 constexpr int kSms = 152;
 constexpr int kMaxSplits = 64;
-constexpr int kPrefixSms = 104;
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
@@ -132,11 +131,10 @@ int64_t row_tiles(const AttnArgs& a, bool tensor_cores) {
 // bf16 prompts and prefixes run on the tensor cores.
 bool on_tensor_cores(int dtype, int mode) { return dtype == COLIBRI_DTYPE_BF16 && mode != kAttnSuffix; }
 
-// (one tensor-core CTA per SM, two of the CUDA-core kernel; a prefix on the
-// tensor cores leaves SMs to the sequences' own keys, which run beside it)
+// (one tensor-core CTA per SM, two of the CUDA-core kernel)
 int splits_for(const AttnArgs& a, const colibri_kv_pages_t* kv, int64_t keys) {
     const bool tc = on_tensor_cores(kv->dtype, a.mode);
-    return choose_splits(row_tiles(a, tc) * kv->n_kv_heads, keys, !tc ? 2 * kSms : a.mode == kAttnPrefix ? kPrefixSms : kSms);
+    return choose_splits(row_tiles(a, tc) * kv->n_kv_heads, keys, tc ? kSms : 2 * kSms);
 }
 
 Plan make_plan(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq, int mode, int prefix_len) {

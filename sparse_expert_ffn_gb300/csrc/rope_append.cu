@@ -13,10 +13,12 @@
 // of the top 32 bits are then good to float32 rounding.  One set of angles
 // serves every head of a row.
 //
-// Bound by HBM: each element is read once and written once.  A head is held by
-// head_dim / 8 lanes, 8 consecutive elements each (one 16-byte vector of bf16,
-// two of float32); its norm is a butterfly over those lanes, its rotation in
-// the half layout one shuffle from the lane that holds the partner elements.
+// Bound by HBM (each element is read once and written once), and close to it by
+// instruction issue, so the work per element is kept small: a head is held by
+// head_dim / 16 lanes, each with the first elements of eight pairs and their
+// second ones, so that the rotation needs no exchange; the norm is a butterfly
+// over those lanes; and a lane group takes several heads of one row, whose
+// cosines and sines, times the norm weights, stay in registers.
 #include <cuda_runtime.h>
 
 #include "attn.h"
@@ -28,28 +30,23 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 8 consecutive elements of a row (not read through the read-only path: q_out
-// may be q).
+// 8 consecutive elements (not read through the read-only path: q_out may be q).
 template <typename T>
 struct Vec8;
 template <>
 struct Vec8<float> {
     float4 a, b;
     __device__ __forceinline__ void load(const float* p) {
-        a = reinterpret_cast<const float4*>(p)[0];
-        b = reinterpret_cast<const float4*>(p)[1];
+        a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
     }
     __device__ __forceinline__ void store(float* p) const {
-        reinterpret_cast<float4*>(p)[0] = a;
-        reinterpret_cast<float4*>(p)[1] = b;
+        reinterpret_cast<float4*>(p)[0] = a, reinterpret_cast<float4*>(p)[1] = b;
     }
     __device__ __forceinline__ void get(float (&v)[8]) const {
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     }
     __device__ __forceinline__ void set(const float (&v)[8]) {
-        a = make_float4(v[0], v[1], v[2], v[3]);
-        b = make_float4(v[4], v[5], v[6], v[7]);
+        a = make_float4(v[0], v[1], v[2], v[3]), b = make_float4(v[4], v[5], v[6], v[7]);
     }
 };
 template <>
@@ -58,12 +55,9 @@ struct Vec8<__nv_bfloat16> {
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = a; }
     __device__ __forceinline__ void get(float (&v)[8]) const {
-        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&a);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __bfloat1622float2(h[i]);
-            v[2 * i] = f.x, v[2 * i + 1] = f.y;
-        }
+        for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
     __device__ __forceinline__ void set(const float (&v)[8]) {
         uint32_t w[4];
@@ -103,55 +97,131 @@ __device__ __forceinline__ void row_place(const AppendArgs& a, int row, int* seq
     }
 }
 
-// One CTA per (row, slice of the row's heads); heads are q's, then k's, then
-// v's.  The loads of a lane group's heads are issued before the row's place
-// and angles are known.
-template <typename T, int D, int HEADS>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
-    constexpr int kLanes = D / 8;                  // lanes of a head
-    constexpr int kGroups = kThreads / kLanes;     // heads in flight per pass
-    __shared__ float2 turn[D / 2];                 // mscale * (cos, sin)
-    __shared__ int place[2];
+constexpr int kBatch = 2;                          // heads of a lane group in flight
+
+// Heads h0, h0 + step, ... of one kind (query or key) of a row: loaded, normalised,
+// rotated and stored.  Element order in a lane: c0 .. c0 + 7, c1 .. c1 + 7.
+template <typename T, int D, bool kInterleaved>
+struct Heads {
+    static constexpr int kLanes = D / 16;
+    // (u, w) -> (u m[0] - w m[1], w m[2] + u m[3]): rotation and norm weights
+    float m[8][4];
+    bool norm;
+    float eps;
+
+    __device__ __forceinline__ void prepare(const T* weight, float e, const float2* turn, int lane, bool turns, int c0,
+                                            int c1) {
+        norm = weight != nullptr, eps = e;
+        float g[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) g[i] = 1.f;
+        if (norm) {
+            Vec8<T> v;
+            float f[8];
+            v.load(weight + c0);
+            v.get(f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = f[i];
+            v.load(weight + c1);
+            v.get(f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[8 + i] = f[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 t = turns ? turn[8 * lane + i] : make_float2(1.f, 0.f);
+            const float gu = g[kInterleaved ? 2 * i : i], gw = g[kInterleaved ? 2 * i + 1 : i + 8];
+            m[i][0] = gu * t.x, m[i][1] = gw * t.y, m[i][2] = gw * t.x, m[i][3] = gu * t.y;
+        }
+    }
+    __device__ __forceinline__ void apply(Vec8<T> (&x)[2]) const {
+        float p[16];
+        {
+            float f[8];
+            x[0].get(f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = f[i];
+            x[1].get(f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[8 + i] = f[i];
+        }
+        float inv = 1.f;
+        if (norm) {
+            float ss = 0.f, st = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(p[i], p[i], ss), st = fmaf(p[8 + i], p[8 + i], st);
+            ss += st;
+            // (the lanes of the head only: other groups of the warp may have fewer heads)
+            const uint32_t mine = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mine, ss, o);
+            inv = rsqrtf(fmaf(ss, 1.f / D, eps));
+        }
+        float y[2][8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float u = p[kInterleaved ? 2 * i : i] * inv, w = p[kInterleaved ? 2 * i + 1 : i + 8] * inv;
+            const float yu = u * m[i][0] - w * m[i][1], yw = w * m[i][2] + u * m[i][3];
+            if (kInterleaved) y[i / 4][i % 4 * 2] = yu, y[i / 4][i % 4 * 2 + 1] = yw;
+            else y[0][i] = yu, y[1][i] = yw;
+        }
+        x[0].set(y[0]);
+        x[1].set(y[1]);
+    }
+};
+
+// A CTA takes kGroups / per_row rows, `per_row` lane groups each (a power of two);
+// group `sub` of a row takes heads sub, sub + step, ... of q's, of k's and of v's
+// (step: per_row times the CTAs that share the row).
+template <typename T, int D, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_constant__ AppendArgs a, int per_row) {
+    constexpr int kLanes = D / 16;                 // lanes of a head
+    constexpr int kGroups = kThreads / kLanes;
+    __shared__ float2 turn[2 * kThreads];          // rows x pairs: mscale * (cos, sin)
+    __shared__ int place[16][2];
     pdl_enter();
     const int tid = threadIdx.x, lane = tid % kLanes, grp = tid / kLanes;
-    const int row = blockIdx.x;
-    const int heads = a.hq + (a.v_out ? 2 : 1) * a.hkv;
-    const int h0 = (blockIdx.y * HEADS) * kGroups + grp;
-
-    Vec8<T> x[HEADS];
-#pragma unroll
-    for (int c = 0; c < HEADS; ++c) {
-        const int h = h0 + c * kGroups;
-        if (h < a.hq)
-            x[c].load(static_cast<const T*>(a.q) + row * a.q_stride + (int64_t)h * D + lane * 8);
-        else if (h < a.hq + a.hkv)
-            x[c].load(static_cast<const T*>(a.k) + row * a.k_stride + (int64_t)(h - a.hq) * D + lane * 8);
-        else if (h < heads)
-            x[c].load(static_cast<const T*>(a.v) + row * a.v_stride + (int64_t)(h - a.hq - a.hkv) * D + lane * 8);
-    }
-    if (tid < 32) {
-        int seq, pos;
-        row_place(a, row, &seq, &pos);
-        if (tid == 0) place[0] = seq, place[1] = pos;
-    }
+    const int rows = kGroups / per_row, r = grp / per_row;
+    const int64_t row0 = (int64_t)blockIdx.x * rows, row = row0 + r;
+    const int sub = grp % per_row + per_row * blockIdx.y, step = per_row * gridDim.y;
     const int pairs = a.freq ? a.rot_dim >> 1 : 0;
-    // a frequency's fraction of a turn, 2^64 to the turn (formed in double:
-    // freq / 2 pi is rounded once, at 2^-53 of itself)
-    uint64_t step = 0;
-    if (tid < pairs) {
-        const double t = __ldg(a.freq + tid) * 0.15915494309189533577;
-        step = __double2ull_rd((t - floor(t)) * 18446744073709551616.0);
+    // this lane's elements.  Half layout: the first and second elements of eight
+    // pairs, then the elements that are not rotated; interleaved: sixteen neighbours.
+    int c0 = 16 * lane, c1 = 16 * lane + 8;
+    const bool turns = 16 * lane < 2 * pairs;
+    if (!kInterleaved && turns) c0 = 8 * lane, c1 = pairs + 8 * lane;
+
+    // the first heads are loaded before the row's place and angles are known
+    const T* q = static_cast<const T*>(a.q) + row * a.q_stride;
+    Vec8<T> x[kBatch][2];
+    const auto load = [&](const T* p, int h, int heads) {
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c)
+            if (h + c * step < heads) {
+                x[c][0].load(p + (int64_t)(h + c * step) * D + c0);
+                x[c][1].load(p + (int64_t)(h + c * step) * D + c1);
+            }
+    };
+    if (row < a.n_rows) load(q, sub, a.hq);
+    for (int w = tid >> 5; w < rows; w += kThreads / 32) {
+        int seq = -1, pos = 0;
+        if (row0 + w < a.n_rows) row_place(a, (int)(row0 + w), &seq, &pos);
+        if ((tid & 31) == 0) place[w][0] = seq, place[w][1] = pos;
     }
     __syncthreads();
-    const int seq = place[0], pos = place[1];
-    if (seq < 0) return;
-    if (tid < pairs) {
-        const int32_t top = (int32_t)((step * (uint64_t)(int64_t)pos) >> 32);
+    for (int e = tid; e < rows * pairs; e += kThreads) {
+        // a frequency's fraction of a turn, 2^64 to the turn (formed in double:
+        // freq / 2 pi is rounded once, at 2^-53 of itself)
+        const double t = __ldg(a.freq + e % pairs) * 0.15915494309189533577;
+        const uint64_t unit = __double2ull_rd((t - floor(t)) * 18446744073709551616.0);
+        const int32_t top = (int32_t)((unit * (uint64_t)(int64_t)place[e / pairs][1]) >> 32);
         float sn, cs;
         sincospif((float)top * 4.656612873077392578125e-10f, &sn, &cs);   // 2^-31: half turns
-        turn[tid] = make_float2(cs * a.mscale, sn * a.mscale);
+        turn[e] = make_float2(cs * a.mscale, sn * a.mscale);
     }
     __syncthreads();
+    const int seq = place[r][0], pos = place[r][1];
+    if (seq < 0) return;
 
     // the row's place in the cache
     int64_t at = -1;
@@ -162,96 +232,74 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
                 at = (int64_t)id * a.page_stride + (int64_t)(pos & ((1 << a.page_shift) - 1)) * a.row_stride;
         }
     } else {
-        at = (int64_t)row * a.row_stride;
+        at = row * a.row_stride;
     }
-    const int half = a.rot_dim >> 4;               // lanes of half the rotated part
+    Heads<T, D, kInterleaved> hd;
+    hd.prepare(static_cast<const T*>(a.q_norm), a.eps, turn + r * pairs, lane, turns, c0, c1);
+    T* q_out = static_cast<T*>(a.q_out) + row * a.q_out_stride;
+    for (int h = sub; h < a.hq; h += kBatch * step) {
+        if (h != sub) load(q, h, a.hq);
 #pragma unroll
-    for (int c = 0; c < HEADS; ++c) {
-        const int h = h0 + c * kGroups;
-        // (the lane groups of a warp may hold different kinds of heads: the
-        // shuffles below are over the whole warp, outside the branches)
-        const bool is_q = h < a.hq, is_k = !is_q && h < a.hq + a.hkv;
-        const void* w = is_q ? a.q_norm : is_k ? a.k_norm : nullptr;
-        float y[8];
-        x[c].get(y);
-        if (a.q_norm || a.k_norm) {
-            float ss = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (w) {
-                const float inv = 1.0f / sqrtf(ss / (float)D + a.eps);
-                Vec8<T> wv;
-                float g[8];
-                wv.load(static_cast<const T*>(w) + lane * 8);
-                wv.get(g);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * g[e];
-            }
+        for (int c = 0; c < kBatch; ++c) {
+            if (h + c * step >= a.hq) break;
+            hd.apply(x[c]);
+            x[c][0].store(q_out + (int64_t)(h + c * step) * D + c0);
+            x[c][1].store(q_out + (int64_t)(h + c * step) * D + c1);
         }
-        if (pairs) {
-            if (a.interleaved) {
-                if (lane * 8 < a.rot_dim && (is_q || is_k)) {
+    }
+    if (at < 0) return;
+    const T* k = static_cast<const T*>(a.k) + row * a.k_stride;
+    T* k_out = static_cast<T*>(a.k_out) + at;
+    if (sub < a.hkv) hd.prepare(static_cast<const T*>(a.k_norm), a.eps, turn + r * pairs, lane, turns, c0, c1);
+    for (int h = sub; h < a.hkv; h += kBatch * step) {
+        load(k, h, a.hkv);
 #pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        const float2 t = turn[lane * 4 + e / 2];
-                        const float p = y[e], r = y[e + 1];
-                        y[e] = p * t.x - r * t.y;
-                        y[e + 1] = r * t.x + p * t.y;
-                    }
-                }
-            } else {
-                const bool low = lane < half;
-                const int src = (tid & 31) - lane + (low ? lane + half : lane < 2 * half ? lane - half : lane);
-                float z[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) z[e] = __shfl_sync(0xffffffffu, y[e], src);
-                if (lane < 2 * half && (is_q || is_k)) {
-                    const float sign = low ? -1.f : 1.f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float2 t = turn[(low ? lane : lane - half) * 8 + e];
-                        y[e] = fmaf(y[e], t.x, sign * z[e] * t.y);
-                    }
-                }
-            }
+        for (int c = 0; c < kBatch; ++c) {
+            if (h + c * step >= a.hkv) break;
+            hd.apply(x[c]);
+            x[c][0].store(k_out + (int64_t)(h + c * step) * a.head_stride + c0);
+            x[c][1].store(k_out + (int64_t)(h + c * step) * a.head_stride + c1);
         }
-        if (h >= heads) continue;
-        if (is_q || is_k) x[c].set(y);            // v's bits are copied
-        if (is_q)
-            x[c].store(static_cast<T*>(a.q_out) + row * a.q_out_stride + (int64_t)h * D + lane * 8);
-        else if (at >= 0) {
-            const int hk = is_k ? h - a.hq : h - a.hq - a.hkv;
-            x[c].store(static_cast<T*>(is_k ? a.k_out : a.v_out) + at + (int64_t)hk * a.head_stride + lane * 8);
+    }
+    if (!a.v_out) return;
+    const T* v = static_cast<const T*>(a.v) + row * a.v_stride;
+    T* v_out = static_cast<T*>(a.v_out) + at;
+    for (int h = sub; h < a.hkv; h += kBatch * step) {
+        load(v, h, a.hkv);
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c) {
+            if (h + c * step >= a.hkv) break;
+            x[c][0].store(v_out + (int64_t)(h + c * step) * a.head_stride + c0);
+            x[c][1].store(v_out + (int64_t)(h + c * step) * a.head_stride + c1);
         }
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kInterleaved>
 cudaError_t launch(const AppendArgs& a, cudaStream_t s) {
-    constexpr int kGroups = kThreads / (D / 8);
-    const int heads = a.hq + (a.v_out ? 2 : 1) * a.hkv;
-    const int passes = (heads + kGroups - 1) / kGroups;
-    // a few rows are bound by latency: one pass per CTA; otherwise one CTA
-    // takes up to four passes of a row, so that their loads overlap and the
-    // angles are formed once
-    const int per = a.n_rows < 152 ? 1 : passes < 4 ? passes : 4;
-    const dim3 grid(a.n_rows, (passes + per - 1) / per), block(kThreads);
-    switch (per) {
-        case 1: return launch_pdl(append_kernel<T, D, 1>, grid, block, 0, s, a);
-        case 2: return launch_pdl(append_kernel<T, D, 2>, grid, block, 0, s, a);
-        case 3: return launch_pdl(append_kernel<T, D, 3>, grid, block, 0, s, a);
-        default: return launch_pdl(append_kernel<T, D, 4>, grid, block, 0, s, a);
-    }
+    constexpr int kGroups = kThreads / (D / 16);
+    auto kern = append_kernel<T, D, kInterleaved>;
+    // four groups per row while that gives three CTAs per SM; fewer rows are
+    // spread over more groups, and a few over as many CTAs as give every group
+    // one head (they are bound by latency)
+    int per_row = 4;
+    while (per_row < kGroups && (int64_t)a.n_rows * per_row < (int64_t)3 * 152 * kGroups) per_row *= 2;
+    const int rows = kGroups / per_row;
+    const int slices = rows == 1 && a.n_rows < 3 * 152 ? (a.hq + kGroups - 1) / kGroups : 1;
+    return launch_pdl(kern, dim3((unsigned)(((int64_t)a.n_rows + rows - 1) / rows), slices), dim3(kThreads), 0, s, a,
+                      per_row);
 }
 
 }  // namespace
 
 cudaError_t launch_append(DType dt, int d, const AppendArgs& a, cudaStream_t s) {
     if (a.n_rows <= 0) return cudaSuccess;
-    if (dt == DType::F32) return d == 64 ? launch<float, 64>(a, s) : launch<float, 128>(a, s);
-    return d == 64 ? launch<__nv_bfloat16, 64>(a, s) : launch<__nv_bfloat16, 128>(a, s);
+    const bool il = a.freq && a.interleaved;
+    if (dt == DType::F32)
+        return d == 64 ? (il ? launch<float, 64, true>(a, s) : launch<float, 64, false>(a, s))
+                       : (il ? launch<float, 128, true>(a, s) : launch<float, 128, false>(a, s));
+    return d == 64 ? (il ? launch<__nv_bfloat16, 64, true>(a, s) : launch<__nv_bfloat16, 64, false>(a, s))
+                   : (il ? launch<__nv_bfloat16, 128, true>(a, s) : launch<__nv_bfloat16, 128, false>(a, s));
 }
 
 }  // namespace colibri
