@@ -44,7 +44,7 @@ struct AttnArgs {
     int part_slot;
     float* part_o;               // [slots][n_rows * hq][d]
     float* part_lse;             // [slots][n_rows * hq]
-    int beside_prefix;           // launch_attn_decode: the launch before it is the prefix's
+    int beside_prefix;           // suffix mode: the launch before it is the prefix's
     // launch_attn_decode: the cut rows' pieces (attn_decode_pieces() rows)
     float* piece_o;
     float* piece_lse;
@@ -52,9 +52,9 @@ struct AttnArgs {
     int stall_tma;               // failure-detection tests only: issue no copy
 };
 
-// CUDA-core attention, float32 arithmetic throughout (float32 layers).
-int attn_simt_rows(const AttnArgs& a);       // rows per tile that the launch will use
-cudaError_t launch_attn_simt(DType dt, int d, const AttnArgs& a, cudaStream_t s);
+// CUDA-core attention of float32 rows (every mode).
+int64_t attn_simt_items(const AttnArgs& a);  // row tiles of the launch, per key head
+cudaError_t launch_attn_simt(int d, const AttnArgs& a, cudaStream_t s);
 
 // Tensor-core attention of bf16 rows (prompt and prefix modes): row tiles of
 // 2 * (128 / group) tokens of one sequence.

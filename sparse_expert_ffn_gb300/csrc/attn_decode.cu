@@ -34,14 +34,6 @@ constexpr int kStages = 3;
 constexpr int kStageBytes = 8192;                                 // K then V of one step
 constexpr int kRingBytes = kStages * kStageBytes;
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) {
-    const int n = there ? 16 : 0;                                  // 0: the 16 bytes become zeros
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 __device__ __forceinline__ void ldm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");

@@ -110,22 +110,13 @@ struct Plan {
 
 // Key ranges per row tile of a launch with `items` tiles over up to `keys`
 // keys, of which the GPU holds `slots` at a time: as many as one wave takes, of
-// at least two 128-key steps each.  More tiles than that are not split: the
+// at least two steps of `step` keys each.  More tiles than that are not split: the
 // partial rows' way through memory costs more than an even last wave gives
 // (2560 rows in 3 chunks over up to 9000 keys: 233 us in one range, 355 us in
 // the number that evened the waves).
-int choose_splits(int64_t items, int64_t keys, int slots) {
-    const int64_t most = std::max<int64_t>(1, keys / 256);
+int choose_splits(int64_t items, int64_t keys, int slots, int step) {
+    const int64_t most = std::max<int64_t>(1, keys / (2 * step));
     return (int)std::max<int64_t>(1, std::min({slots / std::max<int64_t>(items, 1), most, (int64_t)kMaxSplits}));
-}
-
-// Row tiles of a launch and key head.
-int64_t row_tiles(const AttnArgs& a, bool tensor_cores) {
-    if (tensor_cores) return attn_tc_items(a);
-    const int rows = attn_simt_rows(a);
-    if (a.mode == kAttnSuffix) return (int64_t)a.n_seqs * ((a.group + rows - 1) / rows);
-    if (a.mode == kAttnPrefix) return ((int64_t)a.n_seqs * a.group + rows - 1) / rows;
-    return (int64_t)a.n_rows * a.group / rows + a.n_seqs;
 }
 
 // bf16 prompts and prefixes run on the tensor cores.
@@ -134,7 +125,8 @@ bool on_tensor_cores(int dtype, int mode) { return dtype == COLIBRI_DTYPE_BF16 &
 // (one tensor-core CTA per SM, two of the CUDA-core kernel)
 int splits_for(const AttnArgs& a, const colibri_kv_pages_t* kv, int64_t keys) {
     const bool tc = on_tensor_cores(kv->dtype, a.mode);
-    return choose_splits(row_tiles(a, tc) * kv->n_kv_heads, keys, tc ? kSms : 2 * kSms);
+    return tc ? choose_splits(attn_tc_items(a) * kv->n_kv_heads, keys, kSms, 128)
+              : choose_splits(attn_simt_items(a) * kv->n_kv_heads, keys, 2 * kSms, 64);
 }
 
 Plan make_plan(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq, int mode, int prefix_len) {
@@ -158,7 +150,7 @@ Plan make_plan(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq, in
 
 cudaError_t launch_attention(int dtype, int d, const AttnArgs& a, cudaStream_t s) {
     if (on_tensor_cores(dtype, a.mode)) return launch_attn_tc(d, a, s);
-    return launch_attn_simt(dtype_of(dtype), d, a, s);
+    return launch_attn_simt(d, a, s);
 }
 
 AttnArgs make_args(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq, const void* q,
