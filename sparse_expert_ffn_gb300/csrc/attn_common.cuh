@@ -55,10 +55,80 @@ __device__ __forceinline__ int attn_page(const AttnArgs& a, int b, int p) {
     return (unsigned)id < (unsigned)a.num_pages ? id : -1;
 }
 
+// Item number `item` of a prompt launch with tiles of `per` of a sequence's
+// n * mul rows, the tiles that see the most keys first whatever sequence they are
+// of, so that the last ones to start are short (in the order of the sequences,
+// packed prompts of head_dim 64 took 56 us, so 49 us).  Tile r from the end of a
+// sequence has the key  top - r * per  (causal; else its kv length), in rows; the
+// item is found by bisection of the number of tiles whose key is at least c.
+// Called by a whole warp, up to 32 * kKept sequences.
+constexpr int kKept = 4;
+__device__ __forceinline__ bool longest_first(const AttnArgs& a, int item, int mul, int per, int* b, int* tile) {
+    const int lane = threadIdx.x & 31;
+    int tiles[kKept], top[kKept], most = 0, sum = 0;
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+        const int q = lane + 32 * k;
+        tiles[k] = top[k] = 0;
+        if (q < a.n_seqs) {
+            const AttnSeq s = attn_seq(a, q);
+            tiles[k] = (int)(((int64_t)s.n * mul + per - 1) / per);
+            // (an order only: lengths past 2^23 count as that)
+            const int past = min(max((a.causal ? s.raw - s.n : s.kv), 0), 1 << 23) * mul;
+            top[k] = a.causal ? past + tiles[k] * per : past;
+        }
+        if (tiles[k] > 0) most = max(most, top[k]);
+        sum += tiles[k];
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (item >= __reduce_add_sync(0xffffffffu, sum)) return false;
+    // (keys below 0 count as 0: the threshold 0 takes every tile)
+    const auto mine = [&](int k, int c) {
+        if (tiles[k] == 0) return 0;
+        if (c == 0) return tiles[k];
+        if (top[k] < c) return 0;
+        return a.causal ? min(tiles[k], (top[k] - c) / per + 1) : tiles[k];
+    };
+    const auto count = [&](int c) {
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < kKept; ++k) n += mine(k, c);
+        return __reduce_add_sync(0xffffffffu, n);
+    };
+    int lo = 0, hi = most + 1;                                  // count(lo) > item >= count(hi)
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (count(mid) > item) lo = mid;
+        else hi = mid;
+    }
+    // tiles of key lo exactly, in the order of the sequences
+    int left = item - count(hi);
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+        const int from = mine(k, hi), here = mine(k, lo) - from;
+        int upto = here;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const unsigned holds = __ballot_sync(0xffffffffu, left < upto);
+        if (holds) {
+            const int src = __ffs(holds) - 1;
+            *b = src + 32 * k;
+            *tile = __shfl_sync(0xffffffffu, tiles[k] - 1 - from - (left - (upto - here)), src);
+            return true;
+        }
+        left -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return false;                                               // (not reached)
+}
+
 // Work item `item` of the launch as (sequence, tile), tiles of `per` rows of a
 // sequence's n * mul; called by a whole warp.  The last tiles of a sequence,
-// which see the most keys, come first.  False: no such item.
-__device__ __forceinline__ bool attn_item(const AttnArgs& a, int item, int mul, int per, int* b,
+// which see the most keys, come first, or with `sorted` those of any sequence.
+// False: no such item.
+__device__ __forceinline__ bool attn_item(const AttnArgs& a, int item, int mul, int per, bool sorted, int* b,
                                           int* tile) {
     const int lane = threadIdx.x & 31;
     const int count = a.mode == kAttnPrefix ? 1 : a.n_seqs;
@@ -68,6 +138,7 @@ __device__ __forceinline__ bool attn_item(const AttnArgs& a, int item, int mul, 
         *tile = item % tiles;
         return *b < count;
     }
+    if (sorted && count > 1 && count <= 32 * kKept) return longest_first(a, item, mul, per, b, tile);
     int done = 0;
     for (int base = 0; base < count; base += 32) {
         int mine = 0;

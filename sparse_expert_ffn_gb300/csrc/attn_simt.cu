@@ -41,14 +41,14 @@ __device__ __forceinline__ void simt_tile(const AttnArgs& a, SimtSmem<ROWS, D>& 
     const int tid = threadIdx.x;
     if (tid < 32) {
         int b = 0, tile = 0;
-        const bool ok = attn_item(a, blockIdx.x, a.group, ROWS, &b, &tile);
+        const bool ok = attn_item(a, blockIdx.x / a.hkv, a.group, ROWS, gridDim.x * gridDim.y > 304, &b, &tile);
         if (tid == 0) sm.item[0] = ok ? b : -1, sm.item[1] = tile;
     }
     __syncthreads();
     const int b = sm.item[0];
     if (b < 0) return;
     const AttnSeq sq = attn_seq(a, b);
-    const int h = blockIdx.y, sp = blockIdx.z;
+    const int h = blockIdx.x % a.hkv, sp = blockIdx.y;
     const int r0 = sm.item[1] * ROWS, rows = min(ROWS, sq.n * a.group - r0);
     if (rows <= 0) return;
 
@@ -235,7 +235,7 @@ cudaError_t launch_simt(const AttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int64_t items = attn_simt_items(a);
     if (items <= 0) return cudaSuccess;
-    return launch_pdl(kern, dim3((unsigned)items, a.hkv, a.splits), dim3(kThreads), bytes, s, a);
+    return launch_pdl(kern, dim3((unsigned)(items * a.hkv), a.splits), dim3(kThreads), bytes, s, a);
 }
 
 // Tiles of 16 rows for single tokens (a group of at most 16 heads), 64 rows

@@ -224,83 +224,13 @@ __device__ __forceinline__ bool taken_over(uint32_t answer, int* x, int* y) {
     return got != 0;
 }
 
-// Item number `item` of a prompt launch with tiles of `per` rows, the tiles that
-// see the most keys first whatever sequence they are of, so that the last ones
-// to be taken over are short (in the order of the sequences, three chunks over
-// 9000, 4100 and 1024 keys took 181 us).  Tile r from the end of a sequence has
-// the key  top - r * per  (causal; else its kv length); the item is found by
-// bisection of the number of tiles whose key is at least c.  Called by a whole
-// warp, up to 32 * kKept sequences.
-constexpr int kKept = 4;
-__device__ __forceinline__ bool longest_first(const AttnArgs& a, int item, int per, int* b, int* tile) {
-    const int lane = threadIdx.x & 31;
-    int tiles[kKept], top[kKept], most = 0, sum = 0;
-#pragma unroll
-    for (int k = 0; k < kKept; ++k) {
-        const int q = lane + 32 * k;
-        tiles[k] = top[k] = 0;
-        if (q < a.n_seqs) {
-            const AttnSeq s = attn_seq(a, q);
-            tiles[k] = (s.n + per - 1) / per;
-            top[k] = a.causal ? max(s.raw - s.n + tiles[k] * per, 0) : s.kv;
-        }
-        if (tiles[k] > 0) most = max(most, top[k]);
-        sum += tiles[k];
-    }
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (item >= __reduce_add_sync(0xffffffffu, sum)) return false;
-    // (keys below 0 count as 0: the threshold 0 takes every tile)
-    const auto mine = [&](int k, int c) {
-        if (tiles[k] == 0) return 0;
-        if (c == 0) return tiles[k];
-        if (top[k] < c) return 0;
-        return a.causal ? min(tiles[k], (top[k] - c) / per + 1) : tiles[k];
-    };
-    const auto count = [&](int c) {
-        int n = 0;
-#pragma unroll
-        for (int k = 0; k < kKept; ++k) n += mine(k, c);
-        return __reduce_add_sync(0xffffffffu, n);
-    };
-    int lo = 0, hi = most + 1;                                  // count(lo) > item >= count(hi)
-    while (hi - lo > 1) {
-        const int mid = lo + (hi - lo) / 2;
-        if (count(mid) > item) lo = mid;
-        else hi = mid;
-    }
-    // tiles of key lo exactly, in the order of the sequences
-    int left = item - count(hi);
-#pragma unroll
-    for (int k = 0; k < kKept; ++k) {
-        const int from = mine(k, hi), here = mine(k, lo) - from;
-        int upto = here;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
-        }
-        const unsigned holds = __ballot_sync(0xffffffffu, left < upto);
-        if (holds) {
-            const int src = __ffs(holds) - 1;
-            *b = src + 32 * k;
-            *tile = __shfl_sync(0xffffffffu, tiles[k] - 1 - from - (left - (upto - here)), src);
-            return true;
-        }
-        left -= __shfl_sync(0xffffffffu, upto, 31);
-    }
-    return false;                                               // (not reached)
-}
-
 // CTA (x, y) of the grid as a work item; called by a whole warp.
 __device__ __forceinline__ Item work_item(const AttnArgs& a, int x, int y, int tokens) {
     Item it;
     int tile = 0;
     it.b = -1;
     it.h = x % a.hkv, it.split = y;
-    // (the order counts only where CTAs wait for their turn)
-    const bool sorted = a.mode == kAttnPrompt && a.n_seqs > 1 && a.n_seqs <= 32 * kKept && gridDim.x * gridDim.y > 152;
-    if (!(sorted ? longest_first(a, x / a.hkv, 2 * tokens, &it.b, &tile)
-                 : attn_item(a, x / a.hkv, 1, 2 * tokens, &it.b, &tile))) {
+    if (!attn_item(a, x / a.hkv, 1, 2 * tokens, gridDim.x * gridDim.y > 152, &it.b, &tile)) {
         it.b = -1;
         return it;
     }
