@@ -105,27 +105,27 @@ class Sequences:
             if t is not None:
                 _int32(t, name, dim, self.device)
         if page_table is not None:
-            if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != self.device \
-                    or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-                raise ValueError("page_table must be an int32 CUDA matrix with contiguous rows")
+            _int32(page_table, "page_table", 2, self.device)
         n = kv_len.shape[0] if kv_len is not None else seq_start.shape[0] - 1
         if n < 0 or (seq_start is not None and seq_start.shape[0] != n + 1) or \
                 (page_table is not None and page_table.shape[0] != n):
             raise ValueError("seq_start [B + 1], kv_len [B] and page_table [B, width] must agree on B")
-        if page_table is not None and n > 1 and page_table.stride(0) != page_table.shape[1]:
-            page_table = page_table.contiguous()
         self.n_seqs = n
         self.seq_start, self.kv_len, self.page_table = seq_start, kv_len, page_table
-        self._one_each = seq_start is None
-        self._c = Seqs(_sef._ptr(seq_start), _sef._ptr(kv_len), _sef._ptr(page_table), n, 0,
-                       0 if page_table is None else page_table.shape[1])
-        self._ref = ctypes.byref(self._c)
+        self._args = (_sef._ptr(seq_start), _sef._ptr(kv_len), _sef._ptr(page_table), n)
+        self._last = (None, None)
 
     def _rows(self, t):
-        if self._one_each and t.shape[0] != self.n_seqs:
-            raise ValueError("without seq_start there is one row per sequence")
-        self._c.n_rows = t.shape[0]
-        return self._ref
+        """The C description for a call with t's rows (never changed once made:
+        two threads may call with one object)."""
+        rows = t.shape[0]
+        last = self._last
+        if last[0] != rows:
+            if self.seq_start is None and rows != self.n_seqs:
+                raise ValueError("without seq_start there is one row per sequence")
+            width = 0 if self.page_table is None else self.page_table.shape[1]
+            last = self._last = (rows, ctypes.byref(Seqs(*self._args, rows, width)))
+        return last[1]
 
 
 def _same(t, name, heads, head_dim, dtype, device, rows):

@@ -49,7 +49,8 @@ struct AttnArgs {
     float* piece_o;
     float* piece_lse;
     uint64_t wait_limit_ns;      // bound of every mbarrier wait
-    int stall_tma;               // failure-detection tests only: issue no copy
+    int stall_tma;               // failure-detection tests only: a CTA's copies stop at
+                                 // this item of its work (1: the first), 0 never
 };
 
 // CUDA-core attention of float32 rows (every mode).

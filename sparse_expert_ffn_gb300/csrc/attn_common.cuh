@@ -138,8 +138,10 @@ __device__ __forceinline__ bool attn_item(const AttnArgs& a, int item, int mul, 
         *tile = item % tiles;
         return *b < count;
     }
-    if (sorted && count > 1 && count <= 32 * kKept) return longest_first(a, item, mul, per, b, tile);
-    int done = 0;
+    // (tiles of up to 128 sequences, whatever seq_start holds, add up in 32 bits)
+    if (sorted && count > 1 && count <= 32 * kKept && (int64_t)a.n_rows * mul / per < 1 << 23)
+        return longest_first(a, item, mul, per, b, tile);
+    int64_t done = 0;
     for (int base = 0; base < count; base += 32) {
         int mine = 0;
         if (base + lane < count) {
@@ -157,8 +159,8 @@ __device__ __forceinline__ bool attn_item(const AttnArgs& a, int item, int mul, 
         if (holds) {
             const int src = __ffs(holds) - 1;
             *b = base + src;
-            const int first = done + __shfl_sync(0xffffffffu, upto - mine, src);
-            *tile = __shfl_sync(0xffffffffu, mine, src) - 1 - (item - first);
+            const int into = (int)(item - done) - __shfl_sync(0xffffffffu, upto - mine, src);
+            *tile = __shfl_sync(0xffffffffu, mine, src) - 1 - into;
             return true;
         }
         done += __shfl_sync(0xffffffffu, upto, 31);

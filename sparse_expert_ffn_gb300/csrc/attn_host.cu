@@ -79,8 +79,7 @@ colibri_status_t check_seqs(const colibri_seqs_t* s, int n_q_heads) {
     if (s->page_table && (!s->kv_len || s->table_stride <= 0)) return COLIBRI_ERR_INVALID_ARG;
     for (const int32_t* p : {s->seq_start, s->kv_len, s->page_table})
         if ((uintptr_t)p & 3) return COLIBRI_ERR_INVALID_ARG;
-    if ((int64_t)s->n_rows * n_q_heads > INT32_MAX || (int64_t)s->n_seqs * 128 > INT32_MAX)
-        return COLIBRI_ERR_INVALID_ARG;
+    if (((int64_t)s->n_rows + s->n_seqs) * std::max(n_q_heads, 128) > INT32_MAX) return COLIBRI_ERR_INVALID_ARG;
     return COLIBRI_OK;
 }
 

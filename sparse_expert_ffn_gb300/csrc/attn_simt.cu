@@ -8,10 +8,11 @@
 // key and value read.  Each thread holds ROWS / 16 rows x 4 keys of s and
 // ROWS / 16 rows x d / 16 columns of o; products are packed two to an
 // instruction, along d in s and along the columns in o, because one product per
-// instruction leaves no issue slots for the shared-memory reads (64-row tiles,
-// 1721 rows of 16 heads: 142 us, packed and with the next keys copied during the
-// products 99 us).  Prompts are bound by the f32 pipes, the 16-row tiles of
-// single tokens by latency and shared-memory reads.
+// instruction leaves no issue slots for the shared-memory reads; the next keys
+// are copied during the products.  Prompts are bound by the f32 pipes and the
+// shared-memory reads that feed them (4 x 4 products per thread, 256 threads:
+// 1721 rows of 16 heads 123 us; 8 x 4, 128 threads, 132 us: too few warps), the
+// 16-row tiles of single tokens by latency.
 #include <cuda_runtime.h>
 
 #include "attn_common.cuh"

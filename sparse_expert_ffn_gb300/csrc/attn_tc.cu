@@ -82,6 +82,7 @@ struct TcBars {
     uint64_t item_empty[2];
     uint64_t taken_full;
     uint64_t drain[2];
+    uint64_t never;           // failure-detection tests: nothing arrives
     uint32_t tmem;
     int abort;
     int announced;            // items that the copying warp has handed out
@@ -276,6 +277,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(smem_u32(&bars.kv_empty[s]), 2);
         }
         mbar_init(smem_u32(&bars.taken_full), 1);
+        mbar_init(smem_u32(&bars.never), 1);
         bars.abort = bars.announced = bars.orphan = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -599,7 +601,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint32_t loaded = 0;                                    // slots filled so far, over all items
             uint32_t q_no[2] = {0, 0};
             const uint32_t answer = smem_u32(bars.taken), answer_bar = smem_u32(&bars.taken_full);
-            bool ok = !a.stall_tma;
+            // (failure-detection tests: nothing is copied from item stall_tma on)
+            bool ok = a.stall_tma != 1 || warp_wait(&bars.never, 0);
             bool asked = false;
             if (lane == 0) bars.announced = 1;
             while (ok) {
@@ -644,7 +647,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     // the next item is taken as late as its copies can still follow
                     // this one's: whoever is free first takes the longest left
-                    if (n == 2 * nsteps - 2) ask();
+                    if (n == 2 * nsteps - 2) {
+                        ask();
+                        if (a.stall_tma > 1 && item_no + 1 >= a.stall_tma) ok = warp_wait(&bars.never, 0);
+                        if (!ok) break;
+                    }
                     if (loaded >= kSlots<D>) ok = warp_wait(&bars.kv_empty[slot], (loaded / kSlots<D> - 1) & 1);
                     if (!ok) break;
                     const uint32_t bar = smem_u32(&bars.kv_full[slot]);
@@ -756,9 +763,16 @@ bool encode(CUtensorMap* m, const void* p, int rank, const int64_t* dims, const 
         // (the stride of a dimension of one entry is never used, but has to be valid)
         if (i > 0) s[i - 1] = (cuuint64_t)(dims[i] > 1 ? strides[i - 1] : dims[0]) * 2;
     }
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(p), d, s, b, ones,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const auto call = [&]() {
+        return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(p), d, s, b, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (call()) return true;
+    // a driver call needs the device's context current, which a thread that has
+    // not called the runtime yet does not have
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && call();
 }
 
 template <int D, bool kPaged>
