@@ -97,7 +97,13 @@ __device__ __forceinline__ void row_place(const AppendArgs& a, int row, int* seq
     }
 }
 
-constexpr int kBatch = 2;                          // heads of a lane group in flight
+// heads of a lane group in flight (64 bytes per lane)
+template <typename T> constexpr int kBatch = sizeof(T) == 2 ? 2 : 1;
+// float32: the first key and value heads are loaded during the kind before them
+// (1852 rows of 48 heads 17.3 -> 15.5 us); for bf16 the registers that this takes
+// cost more (15373 rows 71 -> 78 us)
+template <typename T> constexpr bool kAhead = sizeof(T) == 4;
+template <typename T> using Vecs = Vec8<T>[kBatch<T>][2];
 
 // Heads h0, h0 + step, ... of one kind (query or key) of a row: loaded, normalised,
 // rotated and stored.  Element order in a lane: c0 .. c0 + 7, c1 .. c1 + 7.
@@ -193,16 +199,17 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
 
     // the first heads are loaded before the row's place and angles are known
     const T* q = static_cast<const T*>(a.q) + row * a.q_stride;
-    Vec8<T> x[kBatch][2];
-    const auto load = [&](const T* p, int h, int heads) {
+    Vecs<T> x, ahead;
+    Vecs<T>& y = *(kAhead<T> ? &ahead : &x);
+    const auto load = [&](Vecs<T>& x, const T* p, int h, int heads) {
 #pragma unroll
-        for (int c = 0; c < kBatch; ++c)
+        for (int c = 0; c < kBatch<T>; ++c)
             if (h + c * step < heads) {
                 x[c][0].load(p + (int64_t)(h + c * step) * D + c0);
                 x[c][1].load(p + (int64_t)(h + c * step) * D + c1);
             }
     };
-    if (row < a.n_rows) load(q, sub, a.hq);
+    if (row < a.n_rows) load(x, q, sub, a.hq);
     for (int w = tid >> 5; w < rows; w += kThreads / 32) {
         int seq = -1, pos = 0;
         if (row0 + w < a.n_rows) row_place(a, (int)(row0 + w), &seq, &pos);
@@ -237,10 +244,12 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
     Heads<T, D, kInterleaved> hd;
     hd.prepare(static_cast<const T*>(a.q_norm), a.eps, turn + r * pairs, lane, turns, c0, c1);
     T* q_out = static_cast<T*>(a.q_out) + row * a.q_out_stride;
-    for (int h = sub; h < a.hq; h += kBatch * step) {
-        if (h != sub) load(q, h, a.hq);
+    const T* k = static_cast<const T*>(a.k) + row * a.k_stride;
+    if (kAhead<T> && at >= 0) load(y, k, sub, a.hkv);
+    for (int h = sub; h < a.hq; h += kBatch<T> * step) {
+        if (h != sub) load(x, q, h, a.hq);
 #pragma unroll
-        for (int c = 0; c < kBatch; ++c) {
+        for (int c = 0; c < kBatch<T>; ++c) {
             if (h + c * step >= a.hq) break;
             hd.apply(x[c]);
             x[c][0].store(q_out + (int64_t)(h + c * step) * D + c0);
@@ -248,26 +257,26 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
         }
     }
     if (at < 0) return;
-    const T* k = static_cast<const T*>(a.k) + row * a.k_stride;
+    const T* v = static_cast<const T*>(a.v) + row * a.v_stride;
+    if (kAhead<T> && a.v_out) load(x, v, sub, a.hkv);
     T* k_out = static_cast<T*>(a.k_out) + at;
     if (sub < a.hkv) hd.prepare(static_cast<const T*>(a.k_norm), a.eps, turn + r * pairs, lane, turns, c0, c1);
-    for (int h = sub; h < a.hkv; h += kBatch * step) {
-        load(k, h, a.hkv);
+    for (int h = sub; h < a.hkv; h += kBatch<T> * step) {
+        if (!kAhead<T> || h != sub) load(y, k, h, a.hkv);
 #pragma unroll
-        for (int c = 0; c < kBatch; ++c) {
+        for (int c = 0; c < kBatch<T>; ++c) {
             if (h + c * step >= a.hkv) break;
-            hd.apply(x[c]);
-            x[c][0].store(k_out + (int64_t)(h + c * step) * a.head_stride + c0);
-            x[c][1].store(k_out + (int64_t)(h + c * step) * a.head_stride + c1);
+            hd.apply(y[c]);
+            y[c][0].store(k_out + (int64_t)(h + c * step) * a.head_stride + c0);
+            y[c][1].store(k_out + (int64_t)(h + c * step) * a.head_stride + c1);
         }
     }
     if (!a.v_out) return;
-    const T* v = static_cast<const T*>(a.v) + row * a.v_stride;
     T* v_out = static_cast<T*>(a.v_out) + at;
-    for (int h = sub; h < a.hkv; h += kBatch * step) {
-        load(v, h, a.hkv);
+    for (int h = sub; h < a.hkv; h += kBatch<T> * step) {
+        if (!kAhead<T> || h != sub) load(x, v, h, a.hkv);
 #pragma unroll
-        for (int c = 0; c < kBatch; ++c) {
+        for (int c = 0; c < kBatch<T>; ++c) {
             if (h + c * step >= a.hkv) break;
             x[c][0].store(v_out + (int64_t)(h + c * step) * a.head_stride + c0);
             x[c][1].store(v_out + (int64_t)(h + c * step) * a.head_stride + c1);
