@@ -72,7 +72,7 @@ __device__ __forceinline__ bool longest_first(const AttnArgs& a, int item, int m
         tiles[k] = top[k] = 0;
         if (q < a.n_seqs) {
             const AttnSeq s = attn_seq(a, q);
-            tiles[k] = (int)(((int64_t)s.n * mul + per - 1) / per);
+            tiles[k] = (int)(((uint32_t)s.n * (uint32_t)mul + (uint32_t)per - 1u) / (uint32_t)per);
             // (an order only: lengths past 2^23 count as that)
             const int past = min(max((a.causal ? s.raw - s.n : s.kv), 0), 1 << 23) * mul;
             top[k] = a.causal ? past + tiles[k] * per : past;
@@ -147,7 +147,8 @@ __device__ __forceinline__ bool attn_item(const AttnArgs& a, int item, int mul, 
         if (base + lane < count) {
             const int s0 = min(max(__ldg(a.seq_start + base + lane), 0), a.n_rows);
             const int s1 = min(max(__ldg(a.seq_start + base + lane + 1), s0), a.n_rows);
-            mine = (int)(((int64_t)(s1 - s0) * mul + per - 1) / per);
+            mine = (int)(((uint32_t)(s1 - s0) * (uint32_t)mul + (uint32_t)per - 1u) / (uint32_t)per);
+            if (a.kv_len) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.kv_len + base + lane));   // for attn_seq
         }
         int upto = mine;
 #pragma unroll

@@ -115,6 +115,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
         : "r"(taddr));
 }
 
+// 32 bytes to a 32-byte boundary.
+__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // One lane of the (whole) warp; the form that lets the compiler keep what the
 // lane issues in uniform registers.
 __device__ __forceinline__ bool elect_one() {
@@ -277,6 +284,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(smem_u32(&bars.kv_empty[s]), 2);
         }
         mbar_init(smem_u32(&bars.taken_full), 1);
+        for (const CUtensorMap* m : {&tm_q, &tm_k, &tm_v})
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
         mbar_init(smem_u32(&bars.never), 1);
         bars.abort = bars.announced = bars.orphan = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -308,6 +317,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     };
     int item_no = 0;                                            // items that this warp is done with
 
+    const bool wide_rows = (reinterpret_cast<uintptr_t>(a.o) % 32 | (uint64_t)a.o_stride % 16) == 0;
     // Output rows of an item's tile t: this thread's row times inv, or NaN.
     const auto write_row = [&](const Item& it, int t, bool ok, bool keys, float l, float m, uint32_t to) {
         const int r = tid & 127, i = it.tok0 + t * tokens + r / a.group, g = r % a.group;
@@ -336,20 +346,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // (a row that saw no key may stand in a tile that did)
 #pragma unroll
             for (int y = 0; y < 32; ++y) o[y] = l == 0.f && ok ? 0 : __float_as_uint(__uint_as_float(o[y]) * inv);
+            // (a row per thread: every store of a warp touches 32 cache lines, so
+            // few wide ones; 16-byte stores took 3550 cycles per item, as many as 1.3
+            // steps)
             if (a.part_o) {
-                uint4* dst = reinterpret_cast<uint4*>(a.part_o + at * D + 32 * x);
 #pragma unroll
-                for (int y = 0; y < 8; ++y) dst[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                for (int y = 0; y < 4; ++y) store32(a.part_o + at * D + 32 * x + 8 * y, o + 8 * y);
             } else {
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + (int64_t)row * a.o_stride +
-                                                      (int64_t)(it.h * a.group + g) * D + 32 * x);
+                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.o) + (int64_t)row * a.o_stride +
+                                     (int64_t)(it.h * a.group + g) * D + 32 * x;
+                uint32_t w[16];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    uint32_t w[4];
+                for (int y = 0; y < 16; ++y) w[y] = pack_h2<false>(__uint_as_float(o[2 * y]), __uint_as_float(o[2 * y + 1]));
+                if (wide_rows) {
+                    store32(dst, w);
+                    store32(dst + 16, w + 8);
+                } else {
 #pragma unroll
-                    for (int z = 0; z < 4; ++z)
-                        w[z] = pack_h2<false>(__uint_as_float(o[8 * y + 2 * z]), __uint_as_float(o[8 * y + 2 * z + 1]));
-                    dst[y] = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int y = 0; y < 4; ++y)
+                        reinterpret_cast<uint4*>(dst)[y] = make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
                 }
             }
         }
