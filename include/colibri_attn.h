@@ -40,9 +40,9 @@ extern "C" {
  *   p * page_stride + h * head_stride + r * row_stride + c
  * of k and of v, so both [pages, heads, rows, dim] and [pages, rows, heads,
  * dim] storage (and views of larger tensors) are described by their strides.
- * page_size is a power of two from 8 to 65536 for a paged cache.  Packed keys without
- * pages (colibri_seqs_t.page_table NULL) are one page of page_size rows, the
- * keys of sequence b being rows seq_start[b] .. seq_start[b + 1] - 1.
+ * page_size is a power of two from 8 to 65536 for a paged cache.  Packed keys
+ * without pages (colibri_seqs_t.page_table NULL) are one page of page_size rows,
+ * the keys of sequence b being rows seq_start[b] .. seq_start[b + 1] - 1.
  */
 typedef struct {
     void* k;               /* device */
@@ -69,8 +69,9 @@ typedef struct {
  * call; whatever they hold, every access stays in bounds: seq_start is cut to
  * 0 .. n_rows, rows at or behind seq_start[n_seqs] belong to no sequence and
  * their outputs are left as they were, a kv_len beyond the page table is cut
- * to it (and to 2^31 - 2^20) and a negative one is 0, a page id outside 0 .. num_pages - 1 is
- * never written and reads as rows of zeros.
+ * to it (and to 2^31 - 2^20) and a negative one is 0, a page id outside
+ * 0 .. num_pages - 1 is never written and reads as rows of zeros.  They must
+ * not change while a call that reads them runs.
  */
 typedef struct {
     const int32_t* seq_start;    /* [n_seqs + 1] device, or NULL */
@@ -135,8 +136,8 @@ colibri_status_t colibri_rope_frequencies(int32_t rot_dim, double theta, int32_t
  *   k, v  [n_rows, n_kv_heads, head_dim]
  *   q_norm, k_norm [head_dim] dtype
  *   q_out [n_rows, n_q_heads, head_dim]; may be q (with the same stride),
- *         otherwise it must not overlap q, k or v
- * q, k and v may be column ranges of one projection's rows.  A row whose
+ *         otherwise it must not overlap q, k or v, and the cache none of them
+ * q, k, v and q_out may be column ranges of one tensor's rows (equal strides).  A row whose
  * position is negative or has no page is not stored in the cache (its q_out is
  * written).  Two rows of one call never name the same place of the cache
  * unless page_table names a page twice.
@@ -150,7 +151,8 @@ colibri_status_t colibri_append_qkv(const colibri_kv_pages_t* cache, const colib
 
 /*
  * colibri_qk_norm_rope - the same for rows that go to no cache: q' into q_out
- * and k' into k_out (each may be its input, with the same stride).
+ * and k' into k_out (each may be its input, with the same stride; other
+ * overlaps as above).
  * seqs->page_table is not read.
  */
 colibri_status_t colibri_qk_norm_rope(const colibri_seqs_t* seqs, const colibri_rope_t* rope,
@@ -169,14 +171,16 @@ colibri_status_t colibri_qk_norm_rope(const colibri_seqs_t* seqs, const colibri_
  *   kv    a paged cache (seqs->page_table and kv_len given), or the prompt's
  *         own packed keys (page_table and kv_len NULL, num_pages 1,
  *         page_size n_rows)
- *   q, o  [n_rows, n_q_heads, head_dim]; o must not overlap q, k or v
+ *   q, o  [n_rows, n_q_heads, head_dim]; o must not overlap q, k or v (column
+ *         ranges of one tensor's rows may lie between each other)
  *   lse   [n_rows, n_q_heads] float32 or NULL: ln sum_j exp(scale * q . k_j),
  *         -infinity for a row that sees no key
  *   scale positive and finite
  *   workspace  colibri_attention_prompt_workspace() bytes, 256-byte aligned;
  *         may be NULL where that is 0
- * Scores, maxima, sums and outputs are float32; for bf16 the weights are
- * rounded to bf16 for the product with v.  Key rows beyond a sequence's
+ * Scores, maxima and sums are float32; for bf16 the weights are rounded to bf16
+ * for the product with v, and sums are formed of weights up to 2^24, so
+ * |v| * keys * 2^24 has to stay in float32's range.  Key rows beyond a sequence's
  * length may hold anything (NaN included).  Inside a sequence a non-finite
  * value row may also reach rows that do not see it, through a weight of 0.
  * Waits of the tensor-core kernel are bounded; rows whose wait gave up are

@@ -153,7 +153,20 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 
 def _stream(stream, device):
     """The stream to run on: the device's current one by default."""
-    return _raw_stream(device.index) if stream is None else stream.cuda_stream
+    if stream is None:
+        return _raw_stream(device.index)
+    if stream.device != device:
+        raise ValueError(f"the stream must be on {device}")
+    return stream.cuda_stream
+
+
+def _empty(shape, dtype, device, stream):
+    """A tensor for a call on `stream`, allocated there: its memory may have
+    belonged to a tensor that work on another stream still uses."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _on(device, call, what, *args):
@@ -195,7 +208,7 @@ def append_qkv(cache: PagedKVCache, seqs: Sequences, q, k, v, *, rope: Optional[
     if seqs.device != dev:
         raise ValueError(f"seqs must be on {dev}")
     if q_out is None:
-        q_out = torch.empty((rows, hq, D), dtype=dt, device=dev)
+        q_out = _empty((rows, hq, D), dt, dev, stream)
     args = (_rope_ref(rope, dev), hq, q.data_ptr(), _same(q, "q", hq, D, dt, dev, rows),
             k.data_ptr(), _same(k, "k", hkv, D, dt, dev, rows), v.data_ptr(), _same(v, "v", hkv, D, dt, dev, rows),
             _norm(q_norm, "q_norm", D, dt, dev), _norm(k_norm, "k_norm", D, dt, dev), float(eps),
@@ -215,9 +228,9 @@ def qk_norm_rope(seqs: Sequences, q, k, *, rope: Optional[Rope] = None, q_norm=N
     if seqs.device != dev:
         raise ValueError(f"seqs must be on {dev}")
     if q_out is None:
-        q_out = torch.empty((rows, hq, D), dtype=dt, device=dev)
+        q_out = _empty((rows, hq, D), dt, dev, stream)
     if k_out is None:
-        k_out = torch.empty((rows, hkv, D), dtype=dt, device=dev)
+        k_out = _empty((rows, hkv, D), dt, dev, stream)
     args = (_rope_ref(rope, dev), hq, hkv, D, _DTYPE[dt], q.data_ptr(), _same(q, "q", hq, D, dt, dev, rows),
             k.data_ptr(), _same(k, "k", hkv, D, dt, dev, rows),
             _norm(q_norm, "q_norm", D, dt, dev), _norm(k_norm, "k_norm", D, dt, dev), float(eps),
@@ -230,10 +243,10 @@ def qk_norm_rope(seqs: Sequences, q, k, *, rope: Optional[Rope] = None, q_norm=N
     return q_out, k_out
 
 
-def _outputs(q, out, lse):
+def _outputs(q, out, lse, stream):
     rows, hq, D = q.shape
     if out is None:
-        out = torch.empty((rows, hq, D), dtype=q.dtype, device=q.device)
+        out = _empty((rows, hq, D), q.dtype, q.device, stream)
     if lse is not None and (tuple(lse.shape) != (rows, hq) or lse.dtype != torch.float32 or
                             lse.device != q.device or not lse.is_contiguous()):
         raise ValueError(f"lse must be a contiguous [{rows}, {hq}] float32 tensor on {q.device}")
@@ -243,12 +256,7 @@ def _outputs(q, out, lse):
 def _workspace(nbytes, device, stream):
     """A call's workspace, from the caching allocator: ordered on the call's
     stream like any tensor, a graph's own while a graph is captured."""
-    if not nbytes:
-        return None
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _empty(nbytes, torch.uint8, device, stream) if nbytes else None
 
 
 def _prompt(kv, kv_ref, seqs, q, scale, causal, out, lse, stream):
@@ -259,7 +267,7 @@ def _prompt(kv, kv_ref, seqs, q, scale, causal, out, lse, stream):
     if q.dtype != kv.dtype or D != kv.head_dim:
         raise ValueError("q and the keys must share dtype and head_dim")
     stride = _same(q, "q", hq, D, q.dtype, dev, rows)
-    out, lse_ptr, o_stride = _outputs(q, out, lse)
+    out, lse_ptr, o_stride = _outputs(q, out, lse, stream)
     if rows == 0:
         return out
     ref, lib, need = seqs._rows(q), _sef.library(), ctypes.c_size_t()
@@ -330,7 +338,7 @@ def attention_decode(cache: PagedKVCache, seqs: Sequences, q, *, prefix_len: int
             raise ValueError("prefix_table is shorter than the prefix")
         table = prefix_table.data_ptr() if prefix_len else None
     stride = _same(q, "q", hq, D, q.dtype, dev, rows)
-    out, lse_ptr, o_stride = _outputs(q, out, lse)
+    out, lse_ptr, o_stride = _outputs(q, out, lse, stream)
     if rows == 0:
         return out
     ref, lib, need = seqs._rows(q), _sef.library(), ctypes.c_size_t()

@@ -38,6 +38,25 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
     return pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
 }
 
+// Rows of a tensor: `rows` times `width` bytes, `stride` bytes apart.
+struct Rows {
+    const void* p;
+    int64_t stride, width;
+    int64_t extent(int64_t rows) const { return (rows - 1) * stride + width; }
+};
+Rows row_bytes(const void* p, int64_t stride, int heads, int d, int esz) {
+    return {p, stride * esz, (int64_t)heads * d * esz};
+}
+// They share a byte.  Column ranges of one tensor's rows (equal strides) may lie
+// between each other; other tensors may not.
+bool clash(const Rows& a, const Rows& b, int64_t rows) {
+    if (rows <= 0 || !overlap(a.p, a.extent(rows), b.p, b.extent(rows))) return false;
+    if (a.stride != b.stride) return true;
+    int64_t off = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p) % a.stride;
+    if (off < 0) off += a.stride;
+    return off < a.width || off + b.width > a.stride;
+}
+
 colibri_status_t check_heads(int n_q_heads, int n_kv_heads, int head_dim, int dtype) {
     if (dtype != COLIBRI_DTYPE_FP32 && dtype != COLIBRI_DTYPE_BF16) return COLIBRI_ERR_INVALID_ARG;
     if (n_q_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || n_q_heads % n_kv_heads)
@@ -184,10 +203,13 @@ colibri_status_t check_attention(const colibri_kv_pages_t* kv, const colibri_seq
         return COLIBRI_ERR_INVALID_ARG;
     if (!(scale > 0.f) || !std::isfinite(scale)) return COLIBRI_ERR_INVALID_ARG;
     if (s->n_rows == 0) return COLIBRI_OK;
-    const int64_t nq = ((int64_t)(s->n_rows - 1) * q_stride + (int64_t)hq * d) * esz;
-    const int64_t no = ((int64_t)(s->n_rows - 1) * o_stride + (int64_t)hq * d) * esz;
-    if (overlap(q, nq, o, no) || overlap(kv->k, kv_extent(kv), o, no) || overlap(kv->v, kv_extent(kv), o, no))
-        return COLIBRI_ERR_INVALID_ARG;
+    const Rows out = row_bytes(o, o_stride, hq, d, esz);
+    if (clash(row_bytes(q, q_stride, hq, d, esz), out, s->n_rows)) return COLIBRI_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)kv->k, (const void*)kv->v}) {
+        const Rows packed = {p, kv->row_stride * esz, ((int64_t)(kv->n_kv_heads - 1) * kv->head_stride + d) * esz};
+        if (s->page_table ? overlap(p, kv_extent(kv), o, out.extent(s->n_rows)) : clash(packed, out, s->n_rows))
+            return COLIBRI_ERR_INVALID_ARG;
+    }
     return COLIBRI_OK;
 }
 
@@ -326,6 +348,16 @@ colibri_status_t colibri_append_qkv(const colibri_kv_pages_t* cache, const colib
         !aligned16(q_norm) || !aligned16(k_norm) || !(eps >= 0.f))
         return COLIBRI_ERR_INVALID_ARG;
     if (q_out == q && q_out_stride != q_stride) return COLIBRI_ERR_INVALID_ARG;
+    const Rows out = row_bytes(q_out, q_out_stride, n_q_heads, d, esz);
+    if ((q_out != q && clash(row_bytes(q, q_stride, n_q_heads, d, esz), out, seqs->n_rows)) ||
+        clash(row_bytes(k, k_stride, hkv, d, esz), out, seqs->n_rows) ||
+        clash(row_bytes(v, v_stride, hkv, d, esz), out, seqs->n_rows))
+        return COLIBRI_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)cache->k, (const void*)cache->v})
+        for (const Rows& r : {row_bytes(q, q_stride, n_q_heads, d, esz), row_bytes(k, k_stride, hkv, d, esz),
+                              row_bytes(v, v_stride, hkv, d, esz), out})
+            if (seqs->n_rows > 0 && overlap(p, kv_extent(cache), r.p, r.extent(seqs->n_rows)))
+                return COLIBRI_ERR_INVALID_ARG;
     if (seqs->n_rows == 0 || seqs->n_seqs == 0) return COLIBRI_OK;
     AppendArgs a{};
     a.q = q, a.k = k, a.v = v;
@@ -366,6 +398,11 @@ colibri_status_t colibri_qk_norm_rope(const colibri_seqs_t* seqs, const colibri_
         !aligned16(k_norm) || !(eps >= 0.f))
         return COLIBRI_ERR_INVALID_ARG;
     if ((q_out == q && q_out_stride != q_stride) || (k_out == k && k_out_stride != k_stride))
+        return COLIBRI_ERR_INVALID_ARG;
+    const Rows qi = row_bytes(q, q_stride, n_q_heads, d, esz), ki = row_bytes(k, k_stride, n_kv_heads, d, esz);
+    const Rows qo = row_bytes(q_out, q_out_stride, n_q_heads, d, esz), ko = row_bytes(k_out, k_out_stride, n_kv_heads, d, esz);
+    if ((q_out != q && clash(qi, qo, seqs->n_rows)) || (k_out != k && clash(ki, ko, seqs->n_rows)) ||
+        clash(qi, ko, seqs->n_rows) || clash(ki, qo, seqs->n_rows) || clash(qo, ko, seqs->n_rows))
         return COLIBRI_ERR_INVALID_ARG;
     if (seqs->n_rows == 0 || seqs->n_seqs == 0) return COLIBRI_OK;
     AppendArgs a{};

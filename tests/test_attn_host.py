@@ -192,6 +192,29 @@ def test_decode_refusals(sef, bad, status):
     assert Args(sef, **{**base, **bad}).decode() == status
 
 
+def test_overlaps_are_refused_and_column_ranges_are_not(sef):
+    B = Args.BASE
+    row = 1024                                          # q 512, k 256, v 256 elements of one projection
+    fused = dict(q=5 * B, qs=row, ks=row, vs=row)
+    ok = dict(n_rows=0)                                 # nothing runs
+    def at(**kw):
+        a = Args(sef, **kw)
+        a.at.update(k=5 * B + 1024, v=5 * B + 1536)
+        return a
+    assert at(**fused, **ok, qo=5 * B, qos=row).append() == 0
+    for kw, status in [(dict(qo=5 * B + 1024, qos=row), 1), (dict(qo=5 * B + 16, qos=row), 1),
+                       (dict(qo=5 * B + 2048, qos=512), 1), (dict(qo=B), 1)]:
+        assert at(**fused, **kw).append() == status, kw
+    # o between the columns of q's tensor (checked before the workspace is)
+    wide = dict(qs=2048, os=2048, q=5 * B, table_stride=4096, ws=None)
+    assert Args(sef, **{**wide, "o": 5 * B + 512}).prompt() == 1
+    assert Args(sef, **{**wide, "o": 5 * B + 1024, "n_rows": 0, "ws": 16 * B}).prompt() == 0
+    for kw in (dict(ko=5 * B), dict(qo=6 * B), dict(qo=9 * B, ko=9 * B), dict(ko=6 * B + 16)):
+        a = Args(sef)
+        a.at.update(kw)
+        assert a.rotate() == 1, kw
+
+
 def test_workspace_is_checked(sef):
     # few rows over a long table: the keys are split, so a workspace is needed
     kw = dict(seq_start=None, n_seqs=2, n_rows=2, table_stride=4096)
