@@ -10,12 +10,11 @@
 //   P = 2^(c S - m')  (bf16, written over S),  l += sum P
 //   O += P V    (128 x d x 128, P read from tensor memory)
 // with c = scale * log2(e), and instead of the running maximum a reference m'
-// that stands as long as the row's maximum is not more than 24 above it (nor
-// more than 64 below it while the row has no weight): bf16 and f32 hold weights
-// up to 2^24 as exactly as those up to 1.  So the weights are formed
-// without waiting for the maximum, and S is read again, and O, which stays in
-// tensor memory, multiplied by 2^(m - m'), only in the few steps that move
-// the reference.
+// that stands as long as the weights are not above 2^24 (nor below 2^-64 while
+// the row has none): bf16 and f32 hold weights up to 2^24 as exactly as those up
+// to 1.  Whether it stands shows in the sum of the weights, so a maximum is taken,
+// S read again, and O, which stays in tensor memory, multiplied by 2^(m - m'),
+// only in the few steps that move the reference.
 //
 // Roles: warps 0-3 and 4-7 the softmax of the two tiles (one row per thread,
 // no shuffles; they take over registers of the others, since a row's 128
@@ -57,6 +56,11 @@ constexpr uint32_t kHalfBytes = 128 * 128;      // 128 rows of one 128-byte swiz
 template <int D> constexpr int kSlots = D == 128 ? 5 : 8;
 template <int D> constexpr uint32_t kTileBytes = (D / 64) * kHalfBytes;
 
+// d = 64 leaves tensor memory for P in columns of its own: S(j + 1) is then formed
+// as soon as S(j) is no longer needed, during the softmax of step j, and the order
+// of the two tiles is left to the pipe.
+template <int D> constexpr bool kOwnP = D == 64;
+
 // A work item, as every role needs it.
 struct Item {
     int b;                    // sequence, < 0: no more items
@@ -73,7 +77,8 @@ struct TcBars {
     uint64_t s_full[2];       // S of the tile's next step is there, its O is up to date
     uint64_t p_most[2];       // O rescaled, P's first 96 keys written
     uint64_t p_ready[2];      // P's last 32 keys written
-    uint64_t o_done[2];       // the item's last product of the tile is done
+    uint64_t o_done[2];       // the item's last product of the tile is done (kOwnP: a step's)
+    uint64_t s_read[2];       // kOwnP: the softmax is done with S
     uint64_t kv_full[8];
     uint64_t kv_empty[8];     // both tiles are done with the slot
     uint64_t tail[2];         // item n & 1's last value tile is cleared behind its last row
@@ -273,6 +278,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(smem_u32(&bars.p_most[t]), 4);
             mbar_init(smem_u32(&bars.p_ready[t]), 4);
             mbar_init(smem_u32(&bars.o_done[t]), 1);
+            mbar_init(smem_u32(&bars.s_read[t]), 4);
             mbar_init(smem_u32(&bars.item_full[t]), 1);
             mbar_init(smem_u32(&bars.item_empty[t]), 10);       // softmax and MMA warps
             mbar_init(smem_u32(&bars.drain[t]), 1);
@@ -304,7 +310,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t tmem = uniform(bars.tmem);
     volatile int* abort_flag = &bars.abort;
     const uint64_t limit = a.wait_limit_ns;
-    constexpr uint32_t kColO = 256;                             // S0 0, S1 128, O0 256, O1 256 + D
+    // S0 0, S1 128, O0 256, O1 256 + D; P over S, or P0 384, P1 448
+    constexpr uint32_t kColO = 256, kColP = kOwnP<D> ? 384 : 0, kStepP = kOwnP<D> ? 64 : 128;
     // one outcome for the whole warp, so that no collective runs without its lanes
     const auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, bounded_wait(smem_u32(bar), parity, abort_flag, limit)) != 0;
@@ -376,7 +383,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int t = warp >> 2, r = tid & 127;
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t ts = lane_base + t * 128, to = lane_base + kColO + t * D;
+        const uint32_t ts = lane_base + t * 128, to = lane_base + kColO + t * D, tp = lane_base + kColP + t * kStepP;
         const float c = a.scale_log2;
         const auto hand_over = [&](uint64_t* bar) {
             tmem_st_wait();
@@ -415,8 +422,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         px[y] = pack_h2<false>(p0, p1);
                     }
                 };
-#pragma unroll 1
-                while (true) {
+                // S of the step, -infinity where the row sees no key
+                const auto load_scores = [&]() {
 #pragma unroll
                     for (int x = 0; x < 4; ++x) tmem_ld32(ts + 32 * x, s[x]);
                     tmem_ld_wait();
@@ -425,33 +432,55 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (left >= 32 * x + 32) continue;         // (rows of a warp differ by few keys)
 #pragma unroll
                         for (int y = 0; y < 32; ++y)
-                            if (x * 32 + y >= left) s[x][y] = 0xff800000u;   // -infinity
+                            if (x * 32 + y >= left) s[x][y] = 0xff800000u;
                     }
-                    // the weights are formed on the reference as it is, beside the
-                    // maximum: it stands except for a few steps of a row
-                    ref2 = pack2(-m, -m);
-                    sum[0] = sum[1] = sum[2] = sum[3] = 0;
+                };
+                // largest of chunks from .. 3, times c
+                const auto largest = [&](int from) {
                     float top[8];
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        top[x] = fmaxf(__uint_as_float(s[x / 2][x % 2 * 16]), __uint_as_float(s[x / 2][x % 2 * 16 + 1]));
+                    for (int x = 0; x < 8; ++x) top[x] = -INFINITY;
 #pragma unroll
-                    for (int y = 2; y < 16; y += 2)
+                    for (int x = 0; x < 4; ++x)
+                        if (x >= from) {
 #pragma unroll
-                        for (int x = 0; x < 8; ++x)
-                            top[x] = max3(top[x], __uint_as_float(s[x / 2][x % 2 * 16 + y]),
-                                          __uint_as_float(s[x / 2][x % 2 * 16 + y + 1]));
+                            for (int y = 0; y < 32; y += 2)
+                                top[y / 2 % 8] = max3(top[y / 2 % 8], __uint_as_float(s[x][y]), __uint_as_float(s[x][y + 1]));
+                        }
+                    return max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7])) * c;
+                };
+                bool waited = false;                               // for the last step's product
+#pragma unroll 1
+                for (int pass = 0;; ++pass) {
+                    load_scores();
+                    // The weights are formed on the reference as it is.  Whether it
+                    // stands shows in their sum (of the first 96; of the last 32, not
+                    // formed yet, in the largest score): a maximum is taken only in
+                    // the few steps where it does not
+                    ref2 = pack2(-m, -m);
+                    sum[0] = sum[1] = sum[2] = sum[3] = 0;
 #pragma unroll
                     for (int x = 0; x < 3; ++x) weights(s[x], p[x]);
-                    const float mn =
-                        max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7])) * c;
-                    const bool move = live && (mn > m + 24.f || (l == 0.f && mn < m - 64.f && mn != -INFINITY));
+                    const float2 some = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+                    const float most = largest(3), weight = some.x + some.y;
+                    const bool high = !(weight <= 16777216.f) || most > m + 24.f;
+                    const bool low = l == 0.f && left > 0 && weight < 5.421010862427522e-20f && most < m - 64.f;   // 2^-64
+                    if (pass > 0 || !__any_sync(0xffffffffu, live && (high || low))) break;
+                    load_scores();
+                    const float mn = largest(0);
+                    // (a sum above 2^24 has a weight above 2^17)
+                    const bool move = live && (mn > m + 16.f || (l == 0.f && mn < m - 64.f && mn != -INFINITY));
                     if (!__any_sync(0xffffffffu, move)) break;
                     // (a row without weight yet has O = 0, or none before the first product)
                     const float keep = move && l != 0.f ? ex2(m - mn) : 1.f;
                     if (move) m = mn;
                     l *= keep;
                     if (j > 0) {
+                        if (kOwnP<D>) {
+                            ok = warp_wait(&bars.o_done[t], (step_no - 1) & 1);
+                            tc_fence_after();
+                            waited = true;
+                        }
 #pragma unroll
                         for (int x = 0; x < D / 16; ++x) {
                             uint32_t o[16];
@@ -463,17 +492,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                     }
                 }
+                if (kOwnP<D>) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bars.s_read[t]));
+                    // P's columns are free once the last step's product is done
+                    if (j > 0 && !waited) {
+                        ok = warp_wait(&bars.o_done[t], (step_no - 1) & 1);
+                        tc_fence_after();
+                    }
+                    if (!ok) break;
+                }
 #pragma unroll
-                for (int x = 0; x < 3; ++x) tmem_st16(ts + 16 * x, p[x]);
+                for (int x = 0; x < 3; ++x) tmem_st16(tp + 16 * x, p[x]);
                 hand_over(&bars.p_most[t]);                        // the product with V starts on these
                 weights(s[3], p[0]);
-                tmem_st16(ts + 48, p[0]);
+                tmem_st16(tp + 48, p[0]);
                 hand_over(&bars.p_ready[t]);
                 const float2 sums = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
                 l += sums.x + sums.y;
             }
             if (ok && steps > 0) {
-                ok = warp_wait(&bars.o_done[t], done_no++ & 1);
+                ok = warp_wait(&bars.o_done[t], (kOwnP<D> ? step_no - 1 : done_no++) & 1);
                 tc_fence_after();
             }
             write_row(it, t, ok, steps > 0, l, m, to);
@@ -486,7 +526,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int t = warp == 8 ? 0 : 1;
             constexpr uint32_t kIdS = idesc_bf16(128, kTileKeys);
             constexpr uint32_t kIdO = idesc_bf16(128, D) | (1u << 16);   // V: MN-major
-            const uint32_t ts = tmem + t * 128, to = tmem + kColO + t * D, qt = q0 + t * kTileBytes<D>;
+            const uint32_t ts = tmem + t * 128, to = tmem + kColO + t * D, tp = tmem + kColP + t * kStepP;
+            const uint32_t qt = q0 + t * kTileBytes<D>;
             const bool leader = elect_one();
             // The warp stays together whatever a wait says: a lane whose wait gave
             // up goes on without waiting, and the leader issues nothing more.
@@ -518,12 +559,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // pipe waits for both (8192 tokens: 444 us).
             uint32_t batch = 0;
             const auto my_turn = [&]() {
+                if (kOwnP<D>) return;
                 if (t == 1) wait(&bars.turn[1], batch & 1);
                 else if (batch > 0) wait(&bars.turn[0], (batch - 1) & 1);
                 ++batch;
             };
-            const auto pass_on = [&]() { mbar_arrive(smem_u32(&bars.turn[t ^ 1])); };
-            uint32_t step_no = 0, q_no = 0, tail_laps = 0;
+            const auto pass_on = [&]() {
+                if (!kOwnP<D>) mbar_arrive(smem_u32(&bars.turn[t ^ 1]));
+            };
+            uint32_t step_no = 0, q_no = 0, tail_laps = 0, s_no = 0;
+            // kOwnP: the scores before these are no longer needed
+            const auto s_free = [&]() {
+                if (!kOwnP<D>) return;
+                if (s_no > 0) {
+                    wait(&bars.s_read[t], (s_no - 1) & 1);
+                    tc_fence_after();
+                }
+                ++s_no;
+            };
             while (__all_sync(0xffffffffu, ok)) {
                 if (!item_there(item_no)) {
                     ok = false;
@@ -536,7 +589,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 int kslot = 0, vslot = 0;
                 if (nsteps > 0) {
                     kslot = next();
-                    if (mine > 0) wait(&bars.q_full[t], q_no++ & 1);
+                    if (mine > 0) {
+                        wait(&bars.q_full[t], q_no++ & 1);
+                        s_free();
+                    }
                     my_turn();
                     if (leader && ok) {
                         if (mine > 0) {
@@ -571,8 +627,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         tail_laps ^= 1u << (item_no & 1);
                     }
                     const auto product = [&](int x) {
-                        mma_f16_ta(to, ts + x * 8, smem_desc_v<D, kPaged>(v + x * 2 * kGroupBytes<D, kPaged>), kIdO, j > 0 || x > 0);
+                        mma_f16_ta(to, tp + x * 8, smem_desc_v<D, kPaged>(v + x * 2 * kGroupBytes<D, kPaged>), kIdO, j > 0 || x > 0);
                     };
+                    if (kOwnP<D> && j + 1 < mine) {
+                        s_free();
+                        if (leader && ok) {
+                            scores(kslot);
+                            if (j + 2 == mine) mma_commit<false>(smem_u32(&bars.q_empty[t]));
+                        }
+                        __syncwarp();
+                    }
                     my_turn();
                     if (j < mine) {
                         wait(&bars.p_most[t], step_no & 1);
@@ -590,9 +654,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (j < mine) {
                             product(6);
                             product(7);
-                            if (j + 1 == mine) mma_commit<false>(smem_u32(&bars.o_done[t]));
+                            if (kOwnP<D> || j + 1 == mine) mma_commit<false>(smem_u32(&bars.o_done[t]));
                         }
-                        if (j + 1 < mine) {
+                        if (!kOwnP<D> && j + 1 < mine) {
                             scores(kslot);
                             if (j + 2 == mine) mma_commit<false>(smem_u32(&bars.q_empty[t]));
                         }
