@@ -392,7 +392,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(bar));
         };
         uint32_t step_no = 0, done_no = 0;                      // of this tile, over all items
+        // The warp stays together whatever a wait says: a lane whose wait gave up
+        // goes on without waiting, to the end of the item, whose rows become NaN.
         bool ok = true;
+        const auto wait = [&](uint64_t* bar, uint32_t parity) {
+            if (ok) ok = bounded_wait(smem_u32(bar), parity, abort_flag, limit);
+            __syncwarp();
+            tc_fence_after();
+        };
         while (ok) {
             ok = item_there(item_no);
             if (!ok) break;
@@ -406,9 +413,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int lim = live ? min(it.hi, attn_limit(a, it.seq, i)) : it.hi;
             float m = 0.f, l = 0.f;            // reference (in units of log2), sum of the weights
             for (int j = 0; j < steps; ++j, ++step_no) {
-                ok = warp_wait(&bars.s_full[t], step_no & 1);
-                if (!ok) break;
-                tc_fence_after();
+                wait(&bars.s_full[t], step_no & 1);
                 const int left = lim - (lo + j * kTileKeys);       // keys of this step that the row sees
                 uint32_t s[4][32], p[3][16];
                 uint64_t sum[4], c2 = pack2(c, c), ref2;
@@ -477,8 +482,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     l *= keep;
                     if (j > 0) {
                         if (kOwnP<D>) {
-                            ok = warp_wait(&bars.o_done[t], (step_no - 1) & 1);
-                            tc_fence_after();
+                            wait(&bars.o_done[t], (step_no - 1) & 1);
                             waited = true;
                         }
 #pragma unroll
@@ -497,11 +501,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&bars.s_read[t]));
                     // P's columns are free once the last step's product is done
-                    if (j > 0 && !waited) {
-                        ok = warp_wait(&bars.o_done[t], (step_no - 1) & 1);
-                        tc_fence_after();
-                    }
-                    if (!ok) break;
+                    if (j > 0 && !waited) wait(&bars.o_done[t], (step_no - 1) & 1);
                 }
 #pragma unroll
                 for (int x = 0; x < 3; ++x) tmem_st16(tp + 16 * x, p[x]);
@@ -512,10 +512,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const float2 sums = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
                 l += sums.x + sums.y;
             }
-            if (ok && steps > 0) {
-                ok = warp_wait(&bars.o_done[t], (kOwnP<D> ? step_no - 1 : done_no++) & 1);
-                tc_fence_after();
-            }
+            if (steps > 0) wait(&bars.o_done[t], (kOwnP<D> ? step_no - 1 : done_no++) & 1);
+            ok = __all_sync(0xffffffffu, ok);
             write_row(it, t, ok, steps > 0, l, m, to);
             item_left(item_no++);
         }
