@@ -20,8 +20,11 @@
 // no shuffles; they take over registers of the others, since a row's 128
 // scores stay in registers), warps 8 and 10 issue the MMAs of one tile each
 // (a wait costs about 150 cycles even when it is over; one warp for both tiles
-// held the tensor pipe up between them), warp 9 the TMA copies (K and V tiles
-// alternate in a ring; with pages, one box per page) and the work list.  The MMAs
+// held the tensor pipe up between them), warps 9 and 11 the TMA copies (K and V
+// tiles alternate in a ring; with pages, one box per page) and the work list.  A
+// box costs the warp that issues it about 65 cycles, so that K and V of 16-key
+// pages, from one warp, took 2700 cycles of a step's 3000 (chunks of prompts over a
+// cache: 160 us, with a warp each 149).  The MMAs
 // of one tile run while the other tile is in its softmax.  A commit after S(j + 1) also covers
 // the O += P V of step j issued before it, so the one barrier per tile tells the
 // softmax warps both that S is there and that O may be rescaled.
@@ -91,6 +94,7 @@ struct TcBars {
     uint32_t tmem;
     int abort;
     int announced;            // items that the copying warp has handed out
+    uint32_t filled[2];       // K and V tiles copied
     int orphan;               // item[2] was taken over and not handed out
     Item item[3];
 };
@@ -280,7 +284,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(smem_u32(&bars.o_done[t]), 1);
             mbar_init(smem_u32(&bars.s_read[t]), 4);
             mbar_init(smem_u32(&bars.item_full[t]), 1);
-            mbar_init(smem_u32(&bars.item_empty[t]), 10);       // softmax and MMA warps
+            mbar_init(smem_u32(&bars.item_empty[t]), 11);       // softmax and MMA warps, V's copies
             mbar_init(smem_u32(&bars.drain[t]), 1);
             mbar_init(smem_u32(&bars.tail[t]), 2);
             mbar_init(smem_u32(&bars.turn[t]), 1);
@@ -294,6 +298,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
         mbar_init(smem_u32(&bars.never), 1);
         bars.abort = bars.announced = bars.orphan = 0;
+        bars.filled[0] = bars.filled[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     pdl_enter();
@@ -673,16 +678,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 mbar_wait_drain(smem_u32(&bars.drain[t]), 0, kDrainLimitNs);
             }
             __syncwarp();
-        } else if (warp == 9) {
-            // ------------------------------------------------ TMA copies, work list
-            uint32_t loaded = 0;                                    // slots filled so far, over all items
+        } else {
+            // ------------------------------------------------ TMA copies: warp 9 Q and K, and
+            // the work list; warp 11 V.  Tile i of K is number 2 i of the ring, of V
+            // 2 i + 1.  (One code for both warps: a kernel as short as a prefix's takes
+            // 2 us more with two, which have to be fetched.)
+            const int kind = warp == 11;
+            uint32_t filled = 0;                                    // tiles so far, over all items
             uint32_t q_no[2] = {0, 0};
             const uint32_t answer = smem_u32(bars.taken), answer_bar = smem_u32(&bars.taken_full);
-            // (failure-detection tests: nothing is copied from item stall_tma on)
-            bool ok = a.stall_tma != 1 || warp_wait(&bars.never, 0);
+            const CUtensorMap* map = kind ? &tm_v : &tm_k;
+            const bool leader = elect_one();
+            // (failure-detection tests: no Q and K are copied from item stall_tma on)
+            bool ok = kind || a.stall_tma != 1 || warp_wait(&bars.never, 0);
             bool asked = false;
-            if (lane == 0) bars.announced = 1;
+            if (!kind && lane == 0) bars.announced = 1;
             while (ok) {
+                if (kind) {
+                    ok = item_there(item_no);
+                    if (!ok || uniform(bars.item[item_no & 1].b) < 0) break;
+                }
                 const Item& it = bars.item[item_no & 1];
                 const int lo = uniform(it.lo), hi = uniform(it.hi), h = uniform(it.h);
                 const int nsteps = uniform(max(it.steps[0], it.steps[1]));
@@ -693,7 +708,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     asked = true;
                 };
-                for (int t = 0; t < 2 && ok; ++t) {
+                for (int t = 0; t < 2 && ok && !kind; ++t) {
                     if (uniform(it.steps[t]) == 0) continue;
                     if (q_no[t] > 0) ok = warp_wait(&bars.q_empty[t], (q_no[t] - 1) & 1);
                     if (!ok) break;
@@ -715,24 +730,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     return kPaged && key < hi ? attn_page(a, it.b, key >> a.page_shift) : -1;
                 };
                 int ids = look(0), ids_ahead = look(32), page = -1;
-                for (int n = 0; n < 2 * nsteps && ok; ++n) {
-                    const int slot = loaded % kSlots<D>, base = lo + (n >> 1) * kTileKeys;
-                    if (kPaged && !(n & 1)) {
-                        const int first = (n >> 1) * per_step;
+                for (int j = 0; j < nsteps && ok; ++j) {
+                    const uint32_t n = 2 * filled + kind, slot = n % kSlots<D>;
+                    const int base = lo + j * kTileKeys;
+                    if (kPaged) {
+                        const int first = j * per_step;
                         if (first > 0 && (first & 31) == 0) ids = ids_ahead, ids_ahead = look(first + 32);
                         page = __shfl_sync(0xffffffffu, ids, (first + lane) & 31);
                     }
                     // the next item is taken as late as its copies can still follow
                     // this one's: whoever is free first takes the longest left
-                    if (n == 2 * nsteps - 2) {
+                    if (!kind && j == nsteps - 1) {
                         ask();
                         if (a.stall_tma > 1 && item_no + 1 >= a.stall_tma) ok = warp_wait(&bars.never, 0);
                         if (!ok) break;
                     }
-                    if (loaded >= kSlots<D>) ok = warp_wait(&bars.kv_empty[slot], (loaded / kSlots<D> - 1) & 1);
+                    if (n >= kSlots<D>) ok = warp_wait(&bars.kv_empty[slot], (n / kSlots<D> - 1) & 1);
                     if (!ok) break;
                     const uint32_t bar = smem_u32(&bars.kv_full[slot]);
-                    const CUtensorMap* map = n & 1 ? &tm_v : &tm_k;
                     const uint32_t dst = kv0 + slot * kTileBytes<D>;
                     if (kPaged) {
                         // one box per page, lane l has box l; a page that does not
@@ -743,16 +758,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (lane < boxes)
                             tma_load_5d(dst + lane * box * D * 2, map, 0, 0, 0, ((base + lane * box) & (a.page_size - 1)) >> 3,
                                         page < 0 ? units.count : page * units.per_page + h * units.per_head, bar);
-                    } else if (lane == 0) {
+                    } else if (leader) {
                         mbar_expect_tx(bar, kTileBytes<D>);
 #pragma unroll
                         for (int x = 0; x < D / 64; ++x)
                             tma_load_4d(dst + x * kHalfBytes, map, 64 * x, it.seq.row0 + base, h, 0, bar);
                     }
                     __syncwarp();
-                    ++loaded;
+                    ++filled;
                 }
                 if (!ok) break;
+                if (kind) {
+                    item_left(item_no++);
+                    continue;
+                }
                 if (nsteps == 0) ask();
                 // the next item
                 ok = warp_wait(&bars.taken_full, item_no & 1);
@@ -780,7 +799,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             // a CTA that gave up leaves none of its copies in flight, and none of the
             // work it took over unanswered
-            if (*abort_flag) {
+            if (!kind && *abort_flag) {
                 if (asked) {
                     mbar_wait_drain(answer_bar, item_no & 1, kDrainLimitNs);
                     __syncwarp();
@@ -793,15 +812,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (lane == 0) {
                     for (int t = 0; t < 2; ++t)
                         if (q_no[t] > 0) mbar_wait_drain(smem_u32(&bars.q_full[t]), (q_no[t] - 1) & 1, kDrainLimitNs);
-                    for (uint32_t n = loaded > kSlots<D> ? loaded - kSlots<D> : 0; n < loaded; ++n)
-                        mbar_wait_drain(smem_u32(&bars.kv_full[n % kSlots<D>]), (n / kSlots<D>) & 1, kDrainLimitNs);
                 }
                 __syncwarp();
             }
+            if (lane == 0) bars.filled[kind] = filled;
         }
     }
     tc_fence_before();
     __syncthreads();
+    if (bars.abort && tid == 0) {
+        // none of the copies stays in flight: each slot's last one
+        for (uint32_t slot = 0; slot < kSlots<D>; ++slot) {
+            int last = -1;
+            for (int kind = 0; kind < 2; ++kind)
+                for (int i = max((int)bars.filled[kind] - kSlots<D>, 0); i < (int)bars.filled[kind]; ++i)
+                    if ((2 * i + kind) % kSlots<D> == (int)slot) last = max(last, 2 * i + kind);
+            if (last >= 0) mbar_wait_drain(smem_u32(&bars.kv_full[slot]), (last / kSlots<D>) & 1, kDrainLimitNs);
+        }
+    }
     if (bars.abort && warp < 8) {
         // rows of items that were handed out or taken over, and that this warp
         // has not come to
