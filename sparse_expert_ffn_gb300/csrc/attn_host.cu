@@ -150,7 +150,8 @@ int splits_for(const AttnArgs& a, const colibri_kv_pages_t* kv, int64_t keys) {
 Plan make_plan(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq, int mode, int prefix_len) {
     const int64_t keys = s->page_table ? (int64_t)s->table_stride * kv->page_size : s->n_rows;
     AttnArgs a{};
-    a.n_rows = s->n_rows, a.n_seqs = s->n_seqs, a.group = hq / kv->n_kv_heads, a.mode = mode;
+    a.n_rows = s->n_rows, a.n_seqs = s->n_seqs, a.hkv = kv->n_kv_heads, a.group = hq / a.hkv, a.mode = mode;
+    a.prefix_len = prefix_len;
     Plan p;
     p.rows = (size_t)s->n_rows * hq;
     if (kv->dtype == COLIBRI_DTYPE_BF16 && mode == kAttnSuffix) {
