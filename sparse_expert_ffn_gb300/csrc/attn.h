@@ -64,10 +64,12 @@ int64_t attn_tc_items(const AttnArgs& a);    // row tiles of the launch, per key
 bool attn_tc_units(const AttnArgs& a, int64_t* unit, int* per_page, int* per_head, int* count);
 cudaError_t launch_attn_tc(int d, const AttnArgs& a, cudaStream_t s);
 
-// bf16 rows of suffix mode, equal shares of the key list per CTA.  part_o null:
-// no prefix; otherwise slot part_slot takes the rows written in one piece.
-size_t attn_decode_pieces(int group);
-cudaError_t launch_attn_decode(int d, const AttnArgs& a, cudaStream_t s);
+// Rows of suffix mode, equal shares of the key list per warp (bf16, and float32
+// groups of up to 32 heads).  part_o null: no prefix; otherwise slot part_slot
+// takes the rows written in one piece.
+bool attn_decode_takes(DType dt, int group);
+size_t attn_decode_pieces(DType dt, int group);
+cudaError_t launch_attn_decode(DType dt, int d, const AttnArgs& a, cudaStream_t s);
 
 // o, lse from the partial rows of `slots` slots, and of the pieces that
 // launch_attn_decode left (shares; slot part_slot then holds the rows it wrote

@@ -180,32 +180,41 @@ __device__ __forceinline__ void attn_split(const AttnArgs& a, int sp, int kt, in
 }
 
 // Equal shares of the key list (attn_decode.cu).  The list is made of steps of
-// kStepKeys keys of one (sequence, key head, row tile), one after another; a
-// share goes to one warp.
-__host__ __device__ constexpr int row_tile(int group) { return group <= 16 ? 16 : 32; }
-__host__ __device__ constexpr int row_tiles(int group) { return (group + row_tile(group) - 1) / row_tile(group); }
+// 4 KB of keys of one (sequence, key head, row tile), one after another; a share
+// goes to one warp.
+template <typename T>
+__host__ __device__ constexpr int row_tile(int group) {
+    return sizeof(T) == 4 ? 4 : group <= 16 ? 16 : 32;
+}
+template <typename T>
+__host__ __device__ constexpr int row_tiles(int group) {
+    return (group + row_tile<T>(group) - 1) / row_tile<T>(group);
+}
 // rows of a piece in the workspace
-__host__ __device__ constexpr int piece_rows(int group) { return group < row_tile(group) ? group : row_tile(group); }
-template <int D> constexpr int kStepKeys = 2048 / D;
+template <typename T>
+__host__ __device__ constexpr int piece_rows(int group) {
+    return group < row_tile<T>(group) ? group : row_tile<T>(group);
+}
+template <typename T, int D> constexpr int kStepKeys = 4096 / (D * (int)sizeof(T));
 constexpr int kShareWarps = 4;                    // per CTA
 constexpr int kShares = 2 * 152 * kShareWarps;    // 2 CTAs per SM
 constexpr int kMinSteps = 4;                      // steps of a share at least
 
 // Steps of sequence b per (head, row tile).
-template <int D>
+template <typename T, int D>
 __device__ __forceinline__ int seq_steps(const AttnArgs& a, int b) {
     const AttnSeq s = attn_seq(a, b);
-    return s.kv > s.kv0 ? (s.kv - s.kv0 + kStepKeys<D> - 1) / kStepKeys<D> : 0;
+    return s.kv > s.kv0 ? (s.kv - s.kv0 + kStepKeys<T, D> - 1) / kStepKeys<T, D> : 0;
 }
 
 // The whole list: its length, and the steps before sequence `upto`.  Called by
 // a whole warp.
-template <int D>
+template <typename T, int D>
 __device__ __forceinline__ void count_steps(const AttnArgs& a, int per_seq, int upto, int64_t* total,
                                             int64_t* before) {
     int64_t all = 0, part = 0;
     for (int b = threadIdx.x & 31; b < a.n_seqs; b += 32) {
-        const int64_t u = (int64_t)seq_steps<D>(a, b) * per_seq;
+        const int64_t u = (int64_t)seq_steps<T, D>(a, b) * per_seq;
         all += u;
         if (b < upto) part += u;
     }

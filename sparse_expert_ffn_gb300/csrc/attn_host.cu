@@ -154,9 +154,9 @@ Plan make_plan(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq, in
     a.prefix_len = prefix_len;
     Plan p;
     p.rows = (size_t)s->n_rows * hq;
-    if (kv->dtype == COLIBRI_DTYPE_BF16 && mode == kAttnSuffix) {
+    if (mode == kAttnSuffix && attn_decode_takes(dtype_of(kv->dtype), a.group)) {
         p.shares = true;
-        p.pieces = attn_decode_pieces(a.group);
+        p.pieces = attn_decode_pieces(dtype_of(kv->dtype), a.group);
     } else {
         p.own = splits_for(a, kv, std::max<int64_t>(keys - prefix_len, 1));
     }
@@ -240,7 +240,7 @@ colibri_status_t run_attention(AttnArgs a, const Plan& p, int dtype, int d, int 
     a.splits = p.own;
     a.part_slot = p.prefix;
     a.beside_prefix = p.prefix > 0;
-    if (e == cudaSuccess) e = p.shares ? launch_attn_decode(d, a, s) : launch_attention(dtype, d, a, s);
+    if (e == cudaSuccess) e = p.shares ? launch_attn_decode(dtype_of(dtype), d, a, s) : launch_attention(dtype, d, a, s);
     if (e == cudaSuccess && (p.shares || p.slots() > 0))
         e = launch_attn_join(dtype_of(dtype), d, a, p.shares ? p.prefix : p.slots(), p.shares, s);
     if (e == cudaSuccess) e = cudaGetLastError();

@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const __grid_consta
     const uint32_t flat = blockIdx.x;
     const int64_t total_rows = (int64_t)a.n_rows * a.hq;
     const int row = (int)(flat / (uint32_t)a.hq), head = (int)(flat % (uint32_t)a.hq);
-    const int tile_row = (head % a.group) % row_tile(a.group);
+    const int tile_row = (head % a.group) % row_tile<T>(a.group);
     // (what is read before the wait was there before the launches that this one
     // waits for: those waited for it before they let this one start)
     if (warp == 0) {
@@ -36,11 +36,11 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const __grid_consta
         int live = 1, c0 = 0, c1 = -1, first_is_last = 0;
         if (shares_per_seq) {
             int64_t total, first;
-            count_steps<D>(a, shares_per_seq, row, &total, &first);
-            const int steps = seq_steps<D>(a, row);
+            count_steps<T, D>(a, shares_per_seq, row, &total, &first);
+            const int steps = seq_steps<T, D>(a, row);
             if (steps > 0) {
                 const int shares = share_count(total);
-                first += (int64_t)((head / a.group) * row_tiles(a.group) + (head % a.group) / row_tile(a.group)) * steps;
+                first += (int64_t)((head / a.group) * row_tiles<T>(a.group) + (head % a.group) / row_tile<T>(a.group)) * steps;
                 c0 = share_of(total, shares, first);
                 c1 = share_of(total, shares, first + steps - 1);
                 first_is_last = share_begin(total, shares, c0) < first;
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const __grid_consta
                 const int c = c0 + i - in_slots;
                 const bool slot = i < in_slots;
                 const int64_t at = slot ? i * total_rows + flat
-                                        : ((int64_t)c * 2 + (c == c0 && place[3])) * piece_rows(a.group) + tile_row;
+                                        : ((int64_t)c * 2 + (c == c0 && place[3])) * piece_rows<T>(a.group) + tile_row;
                 w[k] = (slot ? a.part_lse : a.piece_lse)[at];
                 if (lane < D / 4)
                     v[k] = *reinterpret_cast<const float4*>((slot ? a.part_o : a.piece_o) + at * D + lane * 4);
@@ -117,7 +117,7 @@ template <typename T, int D>
 cudaError_t launch(const AttnArgs& a, int slots, bool shares, cudaStream_t s) {
     const int64_t rows = (int64_t)a.n_rows * a.hq;
     if (rows == 0) return cudaSuccess;
-    const int per_seq = shares ? a.hkv * row_tiles(a.group) : 0;
+    const int per_seq = shares ? a.hkv * row_tiles<T>(a.group) : 0;
     // few rows may have many pieces each (one sequence: 32 rows of 152), many rows few
     if (rows <= 2 * 152)
         return launch_pdl(attn_join_kernel<T, D, 512>, dim3((unsigned)rows), dim3(512), 0, s, a, slots, per_seq);

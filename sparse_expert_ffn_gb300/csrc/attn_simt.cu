@@ -11,8 +11,7 @@
 // instruction leaves no issue slots for the shared-memory reads; the next keys
 // are copied during the products.  Prompts are bound by the f32 pipes and the
 // shared-memory reads that feed them (4 x 4 products per thread, 256 threads:
-// 1721 rows of 16 heads 123 us; 8 x 4, 128 threads, 132 us: too few warps), the
-// 16-row tiles of single tokens by latency.
+// 1721 rows of 16 heads 123 us; 8 x 4, 128 threads, 132 us: too few warps).
 #include <cuda_runtime.h>
 
 #include "attn_common.cuh"
@@ -239,18 +238,15 @@ cudaError_t launch_simt(const AttnArgs& a, cudaStream_t s) {
     return launch_pdl(kern, dim3((unsigned)(items * a.hkv), a.splits), dim3(kThreads), bytes, s, a);
 }
 
-// Tiles of 16 rows for single tokens (a group of at most 16 heads), 64 rows
-// otherwise: a 64-row tile of 4 live rows spends 16 times the products.  A batch's
-// rows over a prefix are latency as long as its CTAs are few, and 16-row tiles have a
-// quarter of a step's products (512 keys of d 128 with 4 key heads: 32 rows 17 us
-// instead of 24, 64 rows 19 instead of 27); once they fill the GPU, 64-row tiles
-// read less shared memory per product (4096 keys, 64 rows: 40 us instead of 67).
+// Tiles of 64 rows, and of 16 for few rows over a prefix.  Those are latency as
+// long as their CTAs are few, and 16-row tiles have a quarter of a step's products
+// (512 keys of d 128 with 4 key heads: 32 rows 17 us instead of 24, 64 rows 19
+// instead of 27); once they fill the GPU, 64-row tiles read less shared memory per
+// product (4096 keys, 64 rows: 40 us instead of 67).
 int tile_rows(const AttnArgs& a) {
     const int64_t rows = (int64_t)a.n_seqs * a.group;
-    const bool few = a.mode == kAttnSuffix  ? a.group <= 16
-                     : a.mode == kAttnPrefix ? rows <= 16 || (rows + 15) / 16 * a.hkv * ((a.prefix_len + 127) / 128) <= 76
-                                             : false;
-    return few ? 16 : 64;
+    const bool few = rows <= 16 || (rows + 15) / 16 * a.hkv * ((a.prefix_len + 127) / 128) <= 76;
+    return a.mode == kAttnPrefix && few ? 16 : 64;
 }
 
 }  // namespace

@@ -148,3 +148,53 @@ def test_two_threads_with_the_same_objects(A):
     [t.start() for t in threads]
     [t.join() for t in threads]
     assert len(good) == 100 and all(good)
+
+
+# ------------------------------------------------------------ float32 single tokens
+
+@pytest.mark.parametrize("page,prefix", [(8, 0), (64, 0), (32, 96)])
+@pytest.mark.parametrize("hq,hkv,d", [(1, 1, 64), (2, 1, 128), (6, 2, 64), (4, 1, 128), (5, 1, 64), (8, 8, 128),
+                                     (11, 1, 128), (32, 1, 64), (33, 1, 64)])
+def test_float32_tokens_around_a_step(A, hq, hkv, d, page, prefix):
+    """Lengths around the 8 and 16 keys of a step, none, and long ones that are cut
+    into pieces; places that hold no key are NaN."""
+    own = [0, 1, 7, 8, 9, 15, 16, 17, 31, 33, 64, 20011, 0, 5003]
+    p = Problem([(1, prefix + t) for t in own], hq, hkv, d, "fp32", page, prefix=prefix, seed=hq + d, fill=float("nan"))
+    lse = torch.full((p.rows, hq), 9.0, device=p.q.device)
+    out = A.attention_decode(A.PagedKVCache(p.kp, p.vp), seqs(A, p, decode=True), p.q, prefix_len=prefix,
+                             prefix_table=p.prefix_table if prefix else None, out=torch.full_like(p.q, 9.0), lse=lse)
+    p.check(out, lse, False)
+
+
+@pytest.mark.parametrize("hq,d", [(1, 64), (3, 128), (4, 64), (20, 128)])
+def test_one_float32_sequence_in_many_pieces(A, hq, d):
+    """Equal scores and one-hot values give the exact count of the keys."""
+    keys = 40000 + 37
+    p = Problem([(1, keys)], hq, 1, d, "fp32", 64, seed=3)
+    p.q.zero_()
+    pid = torch.from_numpy(p.table_np[0].astype(np.int64)).cuda()
+    j = torch.arange(keys, device="cuda:0")
+    p.vp.zero_()
+    p.vp[pid[j // 64], 0, j % 64, j % d] = 1.0
+    lse = torch.empty(1, hq, device="cuda:0")
+    out = A.attention_decode(A.PagedKVCache(p.kp, p.vp), seqs(A, p, decode=True), p.q, lse=lse)
+    want = torch.bincount(j % d, minlength=d).double() / keys
+    # weights 1 and exact sums per piece; a piece's division, and the joining of up to
+    # 1216 pieces by their log2-sums (each to a few 2^-24 of at most 16): 2^-18
+    assert ((out.double() - want).abs() <= 2.0 ** -18 * want).all()
+    assert ((lse.double() - np.log(keys)).abs() <= 2.0 ** -18 * np.log(keys)).all()
+
+
+def test_float32_tokens_large_equal_and_nan_scores(A):
+    """Scores that move the reference again and again, a sequence of equal scores,
+    and one NaN key, which makes its sequence's rows NaN and no other's."""
+    p = Problem([(1, 700), (1, 300), (1, 90), (1, 1)], 4, 1, 64, "fp32", 16, seed=5, q_scale=40.0)
+    for j in range(300):
+        p.kp[int(p.table_np[1, j // 16]), 0, j % 16, :] = 0
+    cache = A.PagedKVCache(p.kp, p.vp)
+    lse = torch.empty(4, 4, device="cuda:0")
+    out = A.attention_decode(cache, seqs(A, p, decode=True), p.q, lse=lse)
+    p.check(out, lse, False)
+    p.kp[int(p.table_np[2, 40 // 16]), 0, 40 % 16, 3] = float("nan")
+    again = A.attention_decode(cache, seqs(A, p, decode=True), p.q)
+    assert torch.isnan(again[2]).all() and torch.equal(again[[0, 1, 3]], out[[0, 1, 3]])
