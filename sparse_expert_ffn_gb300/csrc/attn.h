@@ -49,7 +49,7 @@ struct AttnArgs {
     float* piece_o;
     float* piece_lse;
     uint64_t wait_limit_ns;      // bound of every mbarrier wait
-    int stall_tma;               // failure-detection tests only: a CTA's copies stop at
+    int stall_tma;               // failure-detection tests only: a CTA's copies of Q and K stop at
                                  // this item of its work (1: the first), 0 never
 };
 
