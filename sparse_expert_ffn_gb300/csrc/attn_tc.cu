@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // The two tiles' batches (the product of a step and the next scores) go to
             // the tensor pipe in turn.  Left alone, the pipe shares itself between
             // them, both tiles then finish and start their softmax together, and the
-            // pipe waits for both (8192 tokens: 444 us).
+            // pipe waits for both (8192 tokens: 439 us instead of 356).
             uint32_t batch = 0;
             const auto my_turn = [&]() {
                 if (kOwnP<D>) return;
