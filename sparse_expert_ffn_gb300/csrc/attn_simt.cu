@@ -245,7 +245,7 @@ cudaError_t launch_simt(const AttnArgs& a, cudaStream_t s) {
 // product (4096 keys, 64 rows: 40 us instead of 67).
 int tile_rows(const AttnArgs& a) {
     const int64_t rows = (int64_t)a.n_seqs * a.group;
-    const bool few = rows <= 16 || (rows + 15) / 16 * a.hkv * ((a.prefix_len + 127) / 128) <= 76;
+    const bool few = rows <= 16 || (rows + 15) / 16 * a.hkv * (((int64_t)a.prefix_len + 127) / 128) <= 76;
     return a.mode == kAttnPrefix && few ? 16 : 64;
 }
 
