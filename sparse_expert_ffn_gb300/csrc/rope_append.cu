@@ -100,8 +100,9 @@ __device__ __forceinline__ void row_place(const AppendArgs& a, int row, int* seq
 // heads of a lane group in flight (64 bytes per lane)
 template <typename T> constexpr int kBatch = sizeof(T) == 2 ? 2 : 1;
 // float32: the first key and value heads are loaded during the kind before them
-// (1852 rows of 48 heads 17.3 -> 15.5 us); for bf16 the registers that this takes
-// cost more (15373 rows 71 -> 78 us)
+// (1852 rows of 48 heads 17.3 -> 15.5 us).  For bf16 the registers that this takes
+// cost more (15373 rows 71 -> 78 us); its heads are fetched into L2 two batches
+// ahead, which takes none (71 -> 64 us; all of a row at once: 71).
 template <typename T> constexpr bool kAhead = sizeof(T) == 4;
 template <typename T> using Vecs = Vec8<T>[kBatch<T>][2];
 
@@ -209,7 +210,18 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
                 x[c][1].load(p + (int64_t)(h + c * step) * D + c1);
             }
     };
+    // a batch fetched into L2 ahead of its load
+    const auto touch = [&](const T* p, int h, int heads) {
+        if (kAhead<T>) return;
+#pragma unroll
+        for (int c = 0; c < kBatch<T>; ++c)
+            if (h + c * step < heads) {
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p + (int64_t)(h + c * step) * D + c0));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p + (int64_t)(h + c * step) * D + c1));
+            }
+    };
     if (row < a.n_rows) load(x, q, sub, a.hq);
+    if (row < a.n_rows) touch(q, sub + kBatch<T> * step, a.hq);
     for (int w = tid >> 5; w < rows; w += kThreads / 32) {
         int seq = -1, pos = 0;
         if (row0 + w < a.n_rows) row_place(a, (int)(row0 + w), &seq, &pos);
@@ -248,6 +260,9 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
     if (kAhead<T> && at >= 0) load(y, k, sub, a.hkv);
     for (int h = sub; h < a.hq; h += kBatch<T> * step) {
         if (h != sub) load(x, q, h, a.hq);
+        if (h + 2 * kBatch<T> * step < a.hq) touch(q, h + 2 * kBatch<T> * step, a.hq);
+        else if (h + kBatch<T> * step < a.hq) touch(k, sub, a.hkv);
+        else if (a.v_out) touch(static_cast<const T*>(a.v) + row * a.v_stride, sub, a.hkv);
 #pragma unroll
         for (int c = 0; c < kBatch<T>; ++c) {
             if (h + c * step >= a.hq) break;
