@@ -200,7 +200,8 @@ colibri_status_t colibri_attention_prompt(const colibri_kv_pages_t* kv,
  * seq_start NULL, kv_len and page_table given) over all its kv_len[b] keys.
  * The first prefix_len keys of every sequence are those of prefix_table
  * [prefix_len / page_size] (device; prefix_len a multiple of page_size), read
- * once for the whole batch; page_table's entries for them are not read.
+ * once for the whole batch; page_table's entries for them are not read.  A prefix
+ * of more than 2^31 - 2^20 keys is UNSUPPORTED.
  * prefix_len 0: no shared prefix (prefix_table NULL).  A sequence with
  * kv_len[b] <= prefix_len sees the prefix's first kv_len[b] keys, one with
  * kv_len[b] = 0 gets zeros.  Other arguments as colibri_attention_prompt.

@@ -10,6 +10,10 @@ namespace colibri {
 
 enum class DType : int;
 
+// Keys of a sequence, and of a shared prefix, at most, so that a tile behind the
+// last one still has int32 positions.
+constexpr int kMaxKeys = 0x7ff00000;
+
 // What the rows and keys of a launch are.
 enum AttnMode : int {
     kAttnPrompt = 0,   // rows of seq_start, keys 0 .. kv_len[b] - 1

@@ -8,10 +8,6 @@
 
 namespace colibri {
 
-// Keys of a sequence at most, so that a tile behind the last one still has
-// int32 positions.
-constexpr int kMaxKeys = 0x7ff00000;
-
 // One sequence of a launch: rows row0 .. row0 + n - 1, keys kv0 .. kv - 1.
 struct AttnSeq {
     int row0, n, kv0, kv, raw;

@@ -284,7 +284,7 @@ colibri_status_t check_decode(const colibri_kv_pages_t* kv, const colibri_seqs_t
     if (st == COLIBRI_OK) st = check_kv(kv, true);
     if (st != COLIBRI_OK) return st;
     if (prefix_len < 0 || prefix_len % kv->page_size) return COLIBRI_ERR_INVALID_ARG;
-    if (!countable(kv, seqs, n_q_heads) || !mappable(kv)) return COLIBRI_ERR_UNSUPPORTED;
+    if (prefix_len > kMaxKeys || !countable(kv, seqs, n_q_heads) || !mappable(kv)) return COLIBRI_ERR_UNSUPPORTED;
     return COLIBRI_OK;
 }
 
