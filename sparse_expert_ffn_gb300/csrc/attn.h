@@ -48,7 +48,7 @@ struct AttnArgs {
     int part_slot;
     float* part_o;               // [slots][n_rows * hq][d]
     float* part_lse;             // [slots][n_rows * hq]
-    int beside_prefix;           // suffix mode: the launch before it is the prefix's
+    int beside_prefix;           // launch_attn_decode: the launch before it is the prefix's
     // launch_attn_decode: the cut rows' pieces (attn_decode_pieces() rows)
     float* piece_o;
     float* piece_lse;

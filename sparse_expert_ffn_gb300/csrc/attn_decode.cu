@@ -64,7 +64,7 @@ __device__ __forceinline__ uint32_t bf16x2(float x, float y) {
 }
 
 // A position in a warp's share: the piece it is in, step by step.
-template <typename T, int D>
+template <typename T, int D, bool kEarly>
 struct Walk {
     int b, units;              // sequence, its steps per (head, row tile)
     int64_t in_seq;            // steps of sequence b before the piece
@@ -77,10 +77,10 @@ struct Walk {
     __device__ __forceinline__ bool piece(const AttnArgs& a, int per_seq, int64_t left) {
         if (in_seq == (int64_t)units * per_seq) {
             in_seq = 0, units = 0;
-            while (++b < a.n_seqs && (units = seq_steps<T, D>(a, b)) == 0) {}
+            while (++b < a.n_seqs && (units = seq_steps<T, D, kEarly>(a, b)) == 0) {}
             if (units == 0) return false;                          // (not reached: left > 0)
         }
-        const AttnSeq s = attn_seq(a, b);
+        const AttnSeq s = attn_seq<kEarly>(a, b);
         item = (int)(in_seq / units);
         const int first = (int)(in_seq - (int64_t)item * units);
         count = (int)min((int64_t)(units - first), left);
@@ -94,7 +94,7 @@ struct Walk {
 };
 
 // One warp's copies.  The page ids of up to 32 page parts ahead lie one per lane.
-template <typename T, int D>
+template <typename T, int D, bool kEarly>
 struct Stream {
     static constexpr int kRowBytes = D * (int)sizeof(T);
     static constexpr int kChunks = kRowBytes / 16;                 // 16-byte chunks of a row
@@ -125,7 +125,7 @@ struct Stream {
         const int lane = threadIdx.x & 31;
         window = step;
         const int key = first_key(step + lane / parts) + (lane % parts) * (kStepKeys<T, D> / parts);
-        id = key < hi ? attn_page(a, b, key >> a.page_shift) : -1;
+        id = key < hi ? attn_page<kEarly>(a, b, key >> a.page_shift) : -1;
     }
     __device__ __forceinline__ void copy(const AttnArgs& a, int step, uint32_t stage) {
         const int lane = threadIdx.x & 31, key0 = first_key(step), row0 = lane / kChunks;
@@ -185,6 +185,7 @@ struct TensorRows {
     uint32_t qf[MT][D / 16][4];
     float o[MT][D / 8][4], m[MT][2], l[MT][2];
 
+    template <bool kEarly>
     __device__ __forceinline__ void begin(const AttnArgs& a, int b, int h, int r0) {
         const int lane = threadIdx.x & 31;
         // the group's rows as A operands: row lane / 4 (+ 8), columns 2 (lane % 4) (+ 8)
@@ -197,8 +198,8 @@ struct TensorRows {
                     static_cast<const __nv_bfloat16*>(a.q) + (int64_t)b * a.q_stride + (int64_t)(h * a.group + g) * D);
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
-                    qf[t][x][half] = g < a.group ? __ldg(q + x * 8 + (lane & 3)) : 0u;
-                    qf[t][x][half + 2] = g < a.group ? __ldg(q + x * 8 + 4 + (lane & 3)) : 0u;
+                    qf[t][x][half] = g < a.group ? ld_early<kEarly>(q + x * 8 + (lane & 3)) : 0u;
+                    qf[t][x][half + 2] = g < a.group ? ld_early<kEarly>(q + x * 8 + 4 + (lane & 3)) : 0u;
                 }
             }
 #pragma unroll
@@ -334,6 +335,7 @@ struct FloatRows {
     uint64_t q[G][16], o[G][kPairs];                               // columns 32 (lane / KS) .. + 31 of q
     float m[G], l[G];                                              // l: of this lane's keys
 
+    template <bool kEarly>
     __device__ __forceinline__ void begin(const AttnArgs& a, int b, int h, int r0) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -342,7 +344,7 @@ struct FloatRows {
                                (int64_t)(h * a.group + r0 + g) * D + lane / KS * 32;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float4 v = r0 + g < a.group ? __ldg(reinterpret_cast<const float4*>(row) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 v = r0 + g < a.group ? ld_early<kEarly>(reinterpret_cast<const float4*>(row) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
                 q[g][2 * i] = pack2(v.x, v.y), q[g][2 * i + 1] = pack2(v.z, v.w);
             }
             m[g] = -INFINITY, l[g] = 0.f;
@@ -443,7 +445,7 @@ struct FloatRows {
     }
 };
 
-template <typename Rows>
+template <typename Rows, bool kEarly>
 __device__ __forceinline__ void decode_share(const AttnArgs& a, int per_seq, uint8_t* smem) {
     using T = typename Rows::T;
     constexpr int D = Rows::kD, KS = Rows::KS;
@@ -451,15 +453,15 @@ __device__ __forceinline__ void decode_share(const AttnArgs& a, int per_seq, uin
     const int tiles = row_tiles<T>(a.group);
     // this warp's share of the list, and the sequence that its first step lies in
     int64_t total, left, before = 0, u0;
-    count_steps<T, D>(a, per_seq, 0, &total, &left);
+    count_steps<T, D, kEarly>(a, per_seq, 0, &total, &left);
     if (total == 0) return;
     const int shares = share_count(total);
     if (share >= shares) return;
     u0 = share_begin(total, shares, share);
     left = share_begin(total, shares, share + 1) - u0;             // (at least one)
-    Walk<T, D> load;
+    Walk<T, D, kEarly> load;
     for (int base = 0;; base += 32) {
-        const int mine = base + lane < a.n_seqs ? seq_steps<T, D>(a, base + lane) : 0;
+        const int mine = base + lane < a.n_seqs ? seq_steps<T, D, kEarly>(a, base + lane) : 0;
         int64_t upto = (int64_t)mine * per_seq;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -476,12 +478,12 @@ __device__ __forceinline__ void decode_share(const AttnArgs& a, int per_seq, uin
         }
         before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    Walk<T, D> at = load;
+    Walk<T, D, kEarly> at = load;
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * kRingBytes;
     const uint32_t scratch = (uint32_t)__cvta_generic_to_shared(smem) + kShareWarps * kRingBytes +
                              (threadIdx.x >> 5) * Rows::kScratch;
     int64_t to_load = left;
-    Stream<T, D> st;
+    Stream<T, D, kEarly> st;
     int slot_in = 0, slot_out = 0;
     load.step = load.count = 0;
     const auto copy_next = [&]() {
@@ -502,7 +504,7 @@ __device__ __forceinline__ void decode_share(const AttnArgs& a, int per_seq, uin
     while (left > 0 && at.piece(a, per_seq, left)) {
         const int b = at.b, h = at.item / tiles, r0 = (at.item % tiles) * Rows::kRows;
         Rows rows;
-        rows.begin(a, b, h, r0);
+        rows.template begin<kEarly>(a, b, h, r0);
 #pragma unroll 1
         for (int step = 0; step < at.count; ++step) {
             cp_wait<kStages - 2>();
@@ -538,22 +540,22 @@ __device__ __forceinline__ void decode_share(const AttnArgs& a, int per_seq, uin
     cp_wait<0>();
 }
 
-// Behind a prefix launch (beside_prefix) the kernel starts on the SMs that this
-// one has left: it needs nothing of it, and what came before it is complete when
-// its CTAs let this kernel start.  It waits for it at
-// the end, so that the join, which waits for this kernel, finds both done.
-template <typename Rows>
+// kEarly: behind a prefix launch the kernel starts on the SMs that this one has left;
+// it needs nothing of it (48 rows over a prefix of 16384 keys: 58 us, 69 waiting
+// first; what it reads: ld_early).  It waits for it at the end, so that the join,
+// which waits for this kernel, finds both done.
+template <typename Rows, bool kEarly>
 __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __grid_constant__ AttnArgs a, int per_seq) {
     extern __shared__ __align__(128) uint8_t smem[];
-    if (!a.beside_prefix) pdl_wait();
-    pdl_launch_dependents();
-    decode_share<Rows>(a, per_seq, smem);
-    if (a.beside_prefix) pdl_wait();
+    if constexpr (kEarly) pdl_launch_dependents();
+    else pdl_enter();
+    decode_share<Rows, kEarly>(a, per_seq, smem);
+    if constexpr (kEarly) pdl_wait();
 }
 
 template <typename Rows>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
-    auto kern = attn_decode_kernel<Rows>;
+    auto kern = a.beside_prefix ? attn_decode_kernel<Rows, true> : attn_decode_kernel<Rows, false>;
     const int bytes = kShareWarps * (kRingBytes + Rows::kScratch), per_seq = a.hkv * row_tiles<typename Rows::T>(a.group);
     cudaError_t e = smem_attr((const void*)kern, bytes);
     return e != cudaSuccess ? e : launch_pdl(kern, dim3(kShares / kShareWarps), dim3(kDecThreads), bytes, s, a, per_seq);

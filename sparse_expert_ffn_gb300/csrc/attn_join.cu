@@ -29,15 +29,14 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const __grid_consta
     const int64_t total_rows = (int64_t)a.n_rows * a.hq;
     const int row = (int)(flat / (uint32_t)a.hq), head = (int)(flat % (uint32_t)a.hq);
     const int tile_row = (head % a.group) % row_tile<T>(a.group);
-    // (what is read before the wait was there before the launches that this one
-    // waits for: those waited for it before they let this one start)
+    // (lengths are read before the wait, from L2: see attn_common.cuh)
     if (warp == 0) {
         // live: the row belongs to a sequence; c0 .. c1: the shares that hold its keys
         int live = 1, c0 = 0, c1 = -1, first_is_last = 0;
         if (shares_per_seq) {
             int64_t total, first;
-            count_steps<T, D>(a, shares_per_seq, row, &total, &first);
-            const int steps = seq_steps<T, D>(a, row);
+            count_steps<T, D, true>(a, shares_per_seq, row, &total, &first);
+            const int steps = seq_steps<T, D, true>(a, row);
             if (steps > 0) {
                 const int shares = share_count(total);
                 first += (int64_t)((head / a.group) * row_tiles<T>(a.group) + (head % a.group) / row_tile<T>(a.group)) * steps;
@@ -49,7 +48,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const __grid_consta
         } else if (a.mode == kAttnPrompt) {
             live = 0;
             for (int b = lane; b < a.n_seqs; b += 32)
-                live |= row >= max(__ldg(a.seq_start + b), 0) && row < __ldg(a.seq_start + b + 1);
+                live |= row >= max(ld_early<true>(a.seq_start + b), 0) && row < ld_early<true>(a.seq_start + b + 1);
             live = __any_sync(0xffffffffu, live);
         }
         if (lane == 0) place[0] = live, place[1] = c0, place[2] = c1, place[3] = first_is_last;

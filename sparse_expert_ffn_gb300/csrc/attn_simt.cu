@@ -217,14 +217,11 @@ __device__ __forceinline__ void simt_tile(const AttnArgs& a, SimtSmem<ROWS, D>& 
     }
 }
 
-// (beside a prefix launch: see attn_decode.cu)
 template <int ROWS, int D>
 __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ __align__(16) uint8_t raw[];
-    if (!a.beside_prefix) pdl_wait();
-    pdl_launch_dependents();
+    pdl_enter();
     simt_tile(a, *reinterpret_cast<SimtSmem<ROWS, D>*>(raw));
-    if (a.beside_prefix) pdl_wait();
 }
 
 template <int ROWS, int D>

@@ -170,7 +170,8 @@ __device__ __forceinline__ void pdl_enter() {
 }
 
 // Launch with programmatic stream serialization (see pdl_wait); the kernel
-// must call pdl_wait() before its first global memory access.
+// must call pdl_wait() before its first global memory access (but for the attention
+// kernels that read from L2 before it: attn_common.cuh).
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                               cudaStream_t s, Args... args) {

@@ -2,6 +2,8 @@
 allow, and what the sources keep to."""
 
 import ctypes
+import os
+import re
 
 import pytest
 
@@ -17,3 +19,34 @@ def test_prefixes_end_where_positions_fit(sef, prefix, status):  # noqa: F811
     n = ctypes.c_size_t()
     assert sef.colibri_attention_decode_workspace(ctypes.byref(a.KV), ctypes.byref(a.SQ), 8, prefix,
                                                   ctypes.byref(n)) == status
+
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sparse_expert_ffn_gb300", "csrc")
+
+
+def _source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def test_kernels_read_from_l2_before_they_wait():
+    """A kernel that is launched before its predecessor is done is promised other
+    grids' writes only once it has waited.  Kernels wait first, or read from L2 only
+    (no read-only path, no plain loads of q) what was complete when they started."""
+    for name in ("attn_tc.cu", "attn_simt.cu", "rope_append.cu"):
+        kernels = re.findall(r"__global__[^{]*\{(.*?)\n\}", _source(name), re.S)
+        assert kernels
+        for body in kernels:
+            before = body[:re.search(r"\n    pdl_enter\(\);", body).start()]
+            reads = r"__ldg|attn_seq|attn_item|work_item|row_place|load\(|simt_tile" \
+                r"|\ba\.(q|k|v|o|lse|seq_start|kv_len|table|freq|q_norm|k_norm|q_out|k_out|v_out|part_\w+|piece_\w+)\b"
+            assert not re.search(reads, before), name
+    for name, early in (("attn_decode.cu", "kEarly"), ("attn_join.cu", "true")):
+        text = _source(name)
+        calls = re.findall(r"\b(?:attn_seq|attn_page|seq_steps|count_steps|ld_early)\b(<[^>]*>)?", text)
+        assert calls and all(c.endswith(early + ">") for c in calls) and "__ldg" not in text, name
+    common = _source("attn_common.cuh")
+    for name in ("AttnSeq attn_seq", "int attn_page"):
+        body = common[common.index(name):]
+        assert "ld_early<kEarly>" in body[:body.index("\n}")], name
+    assert "return kEarly ? __ldcg(p) : __ldg(p);" in common
