@@ -1,0 +1,49 @@
+"""Attention operators in calls at the ends of what their documentation allows."""
+
+import pytest
+import torch
+
+from attn_parity import DT, Problem, seqs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def A(lib):
+    from sparse_expert_ffn_gb300 import attention
+    return attention
+
+
+def _bits(t):
+    return t.contiguous().view(torch.int16 if t.dtype == torch.bfloat16 else torch.int32)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d,rot,style", [(64, 32, "half"), (64, 48, "interleaved"), (128, 16, "half"),
+                                         (128, 112, "interleaved"), (64, 0, None), (128, 0, None)])
+def test_elements_that_are_not_rotated_are_copied(A, d, rot, style, dtype):
+    """Elements from rot_dim on, and all of them without a rope: the input's bits,
+    whatever stands beside them (infinities, zeros with a sign)."""
+    p = Problem([(37, 50), (9, 9)], 6, 3, d, dtype, 16, seed=d + rot)
+    dev, g = p.q.device, torch.Generator().manual_seed(5)
+    k, v = (torch.randn(p.rows, 3, d, generator=g).to(p.dt).to(dev) for _ in range(2))
+    rope = A.Rope(A.rope_frequencies(rot)[0].to(dev), style, 1.0) if style else None
+    plain = [x.clone() for x in (p.q, k)]
+    for x in (p.q, k):
+        special = torch.tensor([float("inf"), -float("inf"), 0.0, -0.0, 3.0], dtype=p.dt)
+        at = torch.randint(0, 5, (p.rows, x.shape[1], d - rot), generator=g)
+        hit = torch.rand(at.shape, generator=g).to(dev) < 0.4
+        x[..., rot:] = torch.where(hit, special[at].to(dev), x[..., rot:])
+    sq = A.Sequences(p.seq_start, p.kv_len)
+    want = A.qk_norm_rope(sq, *plain, rope=rope)                   # the rotated part knows no other elements
+    got = A.qk_norm_rope(sq, p.q, k, rope=rope)
+    cache = A.PagedKVCache(p.kp, p.vp)
+    got_q = A.append_qkv(cache, seqs(A, p), p.q, k, v, rope=rope)
+    for x, y, z in zip(got, (p.q, k), want):
+        assert torch.equal(_bits(x[..., rot:]), _bits(y[..., rot:]))
+        assert torch.equal(_bits(x[..., :rot]), _bits(z[..., :rot]))
+    assert torch.equal(_bits(got_q), _bits(got[0]))
+    for b, (n, total) in enumerate(p.lens):
+        for i in (0, n // 2, n - 1):
+            t = total - n + i
+            assert torch.equal(_bits(cache.k[p.page_of(b, t), :, t % 16]), _bits(got[1][int(p.start[b]) + i]))
