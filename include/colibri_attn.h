@@ -64,6 +64,8 @@ typedef struct {
  * sequence's keys including this call's rows, so its row i of n is at
  * position kv_len[b] - n + i; kv_len NULL means kv_len[b] = n.  Position t is
  * row t % page_size of page page_table[b * table_stride + t / page_size].
+ * n_seqs may be 0 (a batch of nothing but padding): arrays without entries may
+ * then be NULL, and outputs are left as they were.
  *
  * The arrays are read on the device, so their values are not checked by the
  * call; whatever they hold, every access stays in bounds: seq_start is cut to

@@ -67,6 +67,7 @@ colibri_status_t check_heads(int n_q_heads, int n_kv_heads, int head_dim, int dt
     return COLIBRI_OK;
 }
 
+// paged: the sizes of pages too (keys without pages: check_prompt).
 colibri_status_t check_kv(const colibri_kv_pages_t* kv, bool paged) {
     if (!kv || !kv->k || !kv->v || !aligned16(kv->k) || !aligned16(kv->v)) return COLIBRI_ERR_INVALID_ARG;
     if (kv->num_pages <= 0 || kv->page_size <= 0) return COLIBRI_ERR_INVALID_ARG;
@@ -76,12 +77,8 @@ colibri_status_t check_kv(const colibri_kv_pages_t* kv, bool paged) {
     if (kv->row_stride < kv->head_dim || (kv->n_kv_heads > 1 && kv->head_stride < kv->head_dim) ||
         (kv->num_pages > 1 && kv->page_stride < kv->head_dim))
         return COLIBRI_ERR_INVALID_ARG;
-    if (paged) {
-        if (kv->page_size < 8 || kv->page_size > 65536 || (kv->page_size & (kv->page_size - 1)))
-            return COLIBRI_ERR_UNSUPPORTED;
-    } else if (kv->num_pages != 1) {
-        return COLIBRI_ERR_INVALID_ARG;
-    }
+    if (paged && (kv->page_size < 8 || kv->page_size > 65536 || (kv->page_size & (kv->page_size - 1))))
+        return COLIBRI_ERR_UNSUPPORTED;
     return COLIBRI_OK;
 }
 
@@ -95,7 +92,8 @@ int64_t kv_extent(const colibri_kv_pages_t* kv) {
 colibri_status_t check_seqs(const colibri_seqs_t* s, int n_q_heads) {
     if (!s || s->n_seqs < 0 || s->n_rows < 0 || s->table_stride < 0) return COLIBRI_ERR_INVALID_ARG;
     if (!s->seq_start && s->n_rows != s->n_seqs) return COLIBRI_ERR_INVALID_ARG;
-    if (s->page_table && (!s->kv_len || s->table_stride <= 0)) return COLIBRI_ERR_INVALID_ARG;
+    // (without sequences the arrays have no entries, and may be NULL)
+    if (s->n_seqs > 0 && s->page_table && (!s->kv_len || s->table_stride <= 0)) return COLIBRI_ERR_INVALID_ARG;
     for (const int32_t* p : {s->seq_start, s->kv_len, s->page_table})
         if ((uintptr_t)p & 3) return COLIBRI_ERR_INVALID_ARG;
     if (((int64_t)s->n_rows + s->n_seqs) * std::max(n_q_heads, 128) > INT32_MAX) return COLIBRI_ERR_INVALID_ARG;
@@ -153,6 +151,7 @@ Plan make_plan(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq, in
     a.n_rows = s->n_rows, a.n_seqs = s->n_seqs, a.hkv = kv->n_kv_heads, a.group = hq / a.hkv, a.mode = mode;
     a.prefix_len = prefix_len;
     Plan p;
+    if (s->n_seqs == 0) return p;
     p.rows = (size_t)s->n_rows * hq;
     if (mode == kAttnSuffix && attn_decode_takes(dtype_of(kv->dtype), a.group)) {
         p.shares = true;
@@ -206,6 +205,7 @@ colibri_status_t check_attention(const colibri_kv_pages_t* kv, const colibri_seq
     if (s->n_rows == 0) return COLIBRI_OK;
     const Rows out = row_bytes(o, o_stride, hq, d, esz);
     if (clash(row_bytes(q, q_stride, hq, d, esz), out, s->n_rows)) return COLIBRI_ERR_INVALID_ARG;
+    if (!s->page_table && s->n_seqs == 0) return COLIBRI_OK;      // no keys, of pages or rows
     for (const void* p : {(const void*)kv->k, (const void*)kv->v}) {
         const Rows packed = {p, kv->row_stride * esz, ((int64_t)(kv->n_kv_heads - 1) * kv->head_stride + d) * esz};
         if (s->page_table ? overlap(p, kv_extent(kv), o, out.extent(s->n_rows)) : clash(packed, out, s->n_rows))
@@ -270,14 +270,15 @@ colibri_status_t check_prompt(const colibri_kv_pages_t* kv, const colibri_seqs_t
     if (st != COLIBRI_OK) return st;
     if (seqs->page_table && !(countable(kv, seqs, n_q_heads) && mappable(kv))) return COLIBRI_ERR_UNSUPPORTED;
     // packed keys: the call's own rows
-    if (!seqs->page_table && (seqs->kv_len || (seqs->n_rows > 0 && kv->page_size != seqs->n_rows)))
+    if (!seqs->page_table && seqs->n_seqs > 0 &&
+        (seqs->kv_len || kv->num_pages != 1 || (seqs->n_rows > 0 && kv->page_size != seqs->n_rows)))
         return COLIBRI_ERR_INVALID_ARG;
     return COLIBRI_OK;
 }
 
 colibri_status_t check_decode(const colibri_kv_pages_t* kv, const colibri_seqs_t* seqs, int n_q_heads,
                               int prefix_len) {
-    if (!kv || !seqs || !seqs->page_table || !seqs->kv_len || seqs->seq_start)
+    if (!kv || !seqs || seqs->seq_start || (seqs->n_seqs > 0 && (!seqs->page_table || !seqs->kv_len)))
         return COLIBRI_ERR_INVALID_ARG;
     colibri_status_t st = check_heads(n_q_heads, kv->n_kv_heads, kv->head_dim, kv->dtype);
     if (st == COLIBRI_OK) st = check_seqs(seqs, n_q_heads);
@@ -337,7 +338,7 @@ colibri_status_t colibri_append_qkv(const colibri_kv_pages_t* cache, const colib
                                     const void* v, int64_t v_stride, const void* q_norm,
                                     const void* k_norm, float eps, void* q_out,
                                     int64_t q_out_stride, void* stream) {
-    if (!cache || !seqs || !seqs->page_table || !seqs->kv_len) return COLIBRI_ERR_INVALID_ARG;
+    if (!cache || !seqs || (seqs->n_seqs > 0 && (!seqs->page_table || !seqs->kv_len))) return COLIBRI_ERR_INVALID_ARG;
     colibri_status_t st = check_heads(n_q_heads, cache->n_kv_heads, cache->head_dim, cache->dtype);
     if (st == COLIBRI_OK) st = check_seqs(seqs, n_q_heads);
     if (st == COLIBRI_OK) st = check_kv(cache, true);

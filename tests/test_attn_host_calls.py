@@ -21,6 +21,29 @@ def test_prefixes_end_where_positions_fit(sef, prefix, status):  # noqa: F811
                                                   ctypes.byref(n)) == status
 
 
+@pytest.mark.parametrize("bad,status", [(dict(), 0), (dict(kv_len=None), 0), (dict(kv_len=None, table_stride=0), 0),
+                                        (dict(q=None), 1), (dict(page_size=0), 1), (dict(n_rows=-1), 1)])
+def test_batches_without_sequences(sef, bad, status):  # noqa: F811
+    """Rows of padding only: the sequences' arrays have no entries, and an empty
+    tensor's address is NULL."""
+    none = dict(n_seqs=0, kv_len=3 * Args.BASE + 64, page_table=None)
+    a = Args(sef, **{**none, **bad})
+    assert a.append() == status
+    a = Args(sef, **{**none, **bad, "ws": None, "wsb": 0})
+    assert a.prompt() == status
+    n = ctypes.c_size_t(1)
+    if "q" not in bad:
+        assert sef.colibri_attention_prompt_workspace(ctypes.byref(a.KV), ctypes.byref(a.SQ), 8,
+                                                      ctypes.byref(n)) == status
+        assert status or n.value == 0
+    assert Args(sef, **{**none, **bad, "scale": 0.0}).prompt() == 1
+    single = dict(seq_start=None, n_rows=0, ws=None, wsb=0)
+    assert Args(sef, **{**none, **single, **bad}).decode() == status
+    # with a sequence they are needed, and packed keys are the call's rows
+    for kw in (dict(page_table=None), dict(page_table=None, kv_len=None)):
+        assert Args(sef, **kw).append() == 1 and Args(sef, **kw).prompt() == 1
+
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sparse_expert_ffn_gb300", "csrc")
 
 

@@ -47,3 +47,23 @@ def test_elements_that_are_not_rotated_are_copied(A, d, rot, style, dtype):
         for i in (0, n // 2, n - 1):
             t = total - n + i
             assert torch.equal(_bits(cache.k[p.page_of(b, t), :, t % 16]), _bits(got[1][int(p.start[b]) + i]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_batch_of_padding(A, dtype):
+    """No sequence and a few padded rows: nothing is written anywhere."""
+    p = Problem([(5, 5)], 4, 2, 64, dtype, 16, seed=1)
+    dev = p.q.device
+    ints = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=dev)  # noqa: E731
+    cache, sq = A.PagedKVCache(p.kp, p.vp), A.Sequences(ints(1), ints(0), ints(0, 7))
+    before = p.kp.clone(), p.vp.clone()
+    k, out = p.q[:, :2].contiguous(), torch.full_like(p.q, 3.0)
+    lse = torch.full((5, 4), 3.0, device=dev)
+    assert A.append_qkv(cache, sq, p.q, k, k, q_out=out) is out
+    assert A.attention_prompt_paged(cache, sq, p.q, out=out, lse=lse) is out
+    A.attention_prompt(A.Sequences(ints(1)), p.q, k, k, out=out, lse=lse)
+    A.qk_norm_rope(sq, p.q, k, q_out=out, k_out=torch.full_like(k, 3.0))
+    empty = A.Sequences(None, ints(0), ints(0, 7))
+    assert A.attention_decode(cache, empty, p.q[:0]).shape == (0, 4, 64)
+    assert (out == 3.0).all() and (lse == 3.0).all()
+    assert torch.equal(p.kp, before[0]) and torch.equal(p.vp, before[1])
