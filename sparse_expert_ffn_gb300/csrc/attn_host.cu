@@ -223,6 +223,14 @@ void place_workspace(AttnArgs& a, const Plan& p, int d, void* ws) {
     if (p.slots() > 0) a.part_lse = lse, a.part_o = o;
 }
 
+// The status of a call's launches.  A launch returns its own errors, so one that an
+// earlier call left behind is not asked for, and none is left to later calls.
+colibri_status_t launched(cudaError_t e) {
+    if (e == cudaSuccess) return COLIBRI_OK;
+    cudaGetLastError();
+    return COLIBRI_ERR_CUDA;
+}
+
 colibri_status_t run_attention(AttnArgs a, const Plan& p, int dtype, int d, int prefix_len,
                                const int32_t* prefix_table, void* ws, cudaStream_t s) {
     place_workspace(a, p, d, ws);
@@ -243,8 +251,7 @@ colibri_status_t run_attention(AttnArgs a, const Plan& p, int dtype, int d, int 
     if (e == cudaSuccess) e = p.shares ? launch_attn_decode(dtype_of(dtype), d, a, s) : launch_attention(dtype, d, a, s);
     if (e == cudaSuccess && (p.shares || p.slots() > 0))
         e = launch_attn_join(dtype_of(dtype), d, a, p.shares ? p.prefix : p.slots(), p.shares, s);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
+    return launched(e);
 }
 
 // The pages can be named by the tensor-core kernel's tensor map.
@@ -377,8 +384,7 @@ colibri_status_t colibri_append_qkv(const colibri_kv_pages_t* cache, const colib
     a.page_stride = cache->page_stride, a.head_stride = cache->head_stride;
     a.row_stride = cache->row_stride, a.num_pages = cache->num_pages;
     while ((1 << a.page_shift) < cache->page_size) ++a.page_shift;
-    const cudaError_t e = launch_append(dtype_of(cache->dtype), d, a, (cudaStream_t)stream);
-    return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
+    return launched(launch_append(dtype_of(cache->dtype), d, a, (cudaStream_t)stream));
 }
 
 colibri_status_t colibri_qk_norm_rope(const colibri_seqs_t* seqs, const colibri_rope_t* rope,
@@ -420,8 +426,7 @@ colibri_status_t colibri_qk_norm_rope(const colibri_seqs_t* seqs, const colibri_
     a.hq = n_q_heads, a.hkv = n_kv_heads;
     a.q_out = q_out, a.q_out_stride = q_out_stride;
     a.k_out = k_out, a.row_stride = k_out_stride, a.head_stride = d;
-    const cudaError_t e = launch_append(dtype_of(dtype), d, a, (cudaStream_t)stream);
-    return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
+    return launched(launch_append(dtype_of(dtype), d, a, (cudaStream_t)stream));
 }
 
 colibri_status_t colibri_attention_prompt_workspace(const colibri_kv_pages_t* kv,

@@ -722,6 +722,7 @@ colibri_status_t init_impl(const colibri_moe_config_t* cfg, const void* w_router
     auto fail = [&](colibri_status_t s) {
         cudaDeviceSynchronize();
         release(h);
+        cudaGetLastError();      // (reported here: not to a later call of another handle)
         return s;
     };
 

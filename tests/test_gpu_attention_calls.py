@@ -1,8 +1,11 @@
 """Attention operators in calls at the ends of what their documentation allows."""
 
+import ctypes
+
 import pytest
 import torch
 
+import synth
 from attn_parity import DT, Problem, seqs
 
 pytestmark = pytest.mark.gpu
@@ -67,3 +70,27 @@ def test_batch_of_padding(A, dtype):
     assert A.attention_decode(cache, empty, p.q[:0]).shape == (0, 4, 64)
     assert (out == 3.0).all() and (lse == 3.0).all()
     assert torch.equal(p.kp, before[0]) and torch.equal(p.vp, before[1])
+
+
+def test_errors_of_other_calls_are_not_reported(lib, A):
+    """An init that asks for more memory than there is (550 GB of expert weights)
+    returns OOM, once: calls after it, of other handles and without one, are fine."""
+    sef = lib
+    shape = synth.LayerShape("small", 128, 128, 4, 2, "bf16")
+    moe = sef.MoELayer(synth.router_weight(shape, 1, 0, "cuda:0"), *synth.expert_weights(shape, 1, 0, "cuda:0"), 2,
+                       max_tokens=16)
+    x = torch.randn(16, 128, device="cuda:0").to(torch.bfloat16)
+    want = moe.forward(x).clone()
+    p = Problem([(40, 40)], 4, 2, 64, "bf16", 0, seed=2)
+    sq = seqs(A, p, paged=False)
+    ref = A.attention_prompt(sq, p.q, p.k, p.v)
+    torch.cuda.synchronize()
+    cfg = sef.ColibriConfig(d_model=16384, d_ff=32768, n_experts=256, top_k=2, max_tokens=16, dtype=sef.DTYPE_BF16,
+                            device=0)
+    h, there = ctypes.c_void_p(), ctypes.c_void_p(x.data_ptr())
+    assert sef.colibri_init(ctypes.byref(cfg), there, None, there, there, there, 1, ctypes.byref(h)) == 2
+    assert torch.equal(A.attention_prompt(sq, p.q, p.k, p.v), ref)
+    assert sef.colibri_init(ctypes.byref(cfg), there, None, there, there, there, 1, ctypes.byref(h)) == 2
+    assert torch.equal(moe.forward(x), want)
+    assert moe.check() == sef.OK
+    moe.close()
