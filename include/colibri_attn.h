@@ -219,6 +219,15 @@ colibri_status_t colibri_attention_decode(const colibri_kv_pages_t* cache,
                                           void* o, int64_t o_stride, float* lse, void* workspace,
                                           size_t workspace_bytes, void* stream);
 
+/*
+ * colibri_attention_waits - for later calls of the process: the bound of the
+ * tensor-core kernel's waits in nanoseconds (0: 2 s, the default), and, for
+ * failure-detection tests, the work item from which on a CTA's copies stop (1:
+ * the first; 0: never).  Until it is called they are what COLIBRI_WAIT_LIMIT_NS and
+ * COLIBRI_TEST_STALL_TMA said at the process's first attention call.
+ */
+colibri_status_t colibri_attention_waits(uint64_t limit_ns, int32_t stall);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,6 +16,7 @@ and run on the tensors' device and its current stream (or ``stream``):
 from __future__ import annotations
 
 import ctypes
+import os
 import threading
 from typing import Optional
 
@@ -257,6 +258,21 @@ def _outputs(q, out, lse, stream):
     return out, (None if lse is None else lse.data_ptr()), _same(out, "out", hq, D, q.dtype, q.device, rows)
 
 
+# what os.environ holds, without the microsecond that a look-up through it takes
+_env = getattr(os.environb, "_data", os.environb)
+_waits = (None, None)
+
+
+def _pass_on_waits():
+    """Hands the two variables of failure detection to the library when they have
+    changed: it reads the environment itself only once."""
+    global _waits
+    now = (_env.get(b"COLIBRI_WAIT_LIMIT_NS"), _env.get(b"COLIBRI_TEST_STALL_TMA"))
+    if now != _waits:
+        _sef._check(_sef.library().colibri_attention_waits(*(int(v or 0) for v in now)), "colibri_attention_waits")
+        _waits = now
+
+
 class _Kept(threading.local):
     place, tensor = None, None
 
@@ -298,6 +314,7 @@ def _prompt(kv, kv_ref, seqs, q, scale, causal, out, lse, stream):
     _sef._check(lib.colibri_attention_prompt_workspace(kv_ref, ref, hq, ctypes.byref(need)),
                 "colibri_attention_prompt_workspace")
     ws = _workspace(need.value, dev, stream)
+    _pass_on_waits()
     _on(dev, lib.colibri_attention_prompt, "colibri_attention_prompt", kv_ref, ref, hq, q.data_ptr(), stride,
         D ** -0.5 if scale is None else float(scale), int(causal), out.data_ptr(), o_stride, lse_ptr,
         None if ws is None else ws.data_ptr(), need.value, _stream(stream, dev))
@@ -369,6 +386,7 @@ def attention_decode(cache: PagedKVCache, seqs: Sequences, q, *, prefix_len: int
     _sef._check(lib.colibri_attention_decode_workspace(cache._ref, ref, hq, int(prefix_len), ctypes.byref(need)),
                 "colibri_attention_decode_workspace")
     ws = _workspace(need.value, dev, stream)
+    _pass_on_waits()
     _on(dev, lib.colibri_attention_decode, "colibri_attention_decode", cache._ref, ref, hq, q.data_ptr(), stride,
         D ** -0.5 if scale is None else float(scale), int(prefix_len), table, out.data_ptr(), o_stride, lse_ptr,
         None if ws is None else ws.data_ptr(), need.value, _stream(stream, dev))

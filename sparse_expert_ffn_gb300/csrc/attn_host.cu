@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -171,6 +172,23 @@ cudaError_t launch_attention(int dtype, int d, const AttnArgs& a, cudaStream_t s
     return launch_attn_simt(d, a, s);
 }
 
+// The bound of the tensor-core kernel's waits, and where copies stop in the
+// failure-detection tests (colibri_attention_waits).  The environment gives what they
+// start with and is read once: a getenv per call would race with other threads' setenv.
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+struct Waits {
+    std::atomic<uint64_t> limit_ns{kWaitLimitNs};
+    std::atomic<int> stall{0};
+    Waits() {
+        if (const char* e = std::getenv("COLIBRI_WAIT_LIMIT_NS")) limit_ns = std::strtoull(e, nullptr, 10);
+        if (const char* e = std::getenv("COLIBRI_TEST_STALL_TMA")) stall = std::atoi(e);
+    }
+};
+Waits& waits() {
+    static Waits w;
+    return w;
+}
+
 AttnArgs make_args(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq, const void* q,
                    int64_t q_stride, float scale, void* o, int64_t o_stride, float* lse) {
     AttnArgs a{};
@@ -187,11 +205,8 @@ AttnArgs make_args(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq
     while ((1 << a.page_shift) < kv->page_size) ++a.page_shift;
     a.scale_log2 = scale * 1.44269504088896340736f;
     a.splits = 1;
-    // the bound of the tensor-core kernel's waits, and the producer that copies
-    // nothing of the failure-detection tests
-    a.wait_limit_ns = 2000000000ull;
-    if (const char* e = std::getenv("COLIBRI_WAIT_LIMIT_NS")) a.wait_limit_ns = std::strtoull(e, nullptr, 10);
-    if (const char* e = std::getenv("COLIBRI_TEST_STALL_TMA")) a.stall_tma = std::atoi(e);
+    a.wait_limit_ns = waits().limit_ns.load(std::memory_order_relaxed);
+    a.stall_tma = waits().stall.load(std::memory_order_relaxed);
     return a;
 }
 
@@ -427,6 +442,13 @@ colibri_status_t colibri_qk_norm_rope(const colibri_seqs_t* seqs, const colibri_
     a.q_out = q_out, a.q_out_stride = q_out_stride;
     a.k_out = k_out, a.row_stride = k_out_stride, a.head_stride = d;
     return launched(launch_append(dtype_of(dtype), d, a, (cudaStream_t)stream));
+}
+
+colibri_status_t colibri_attention_waits(uint64_t limit_ns, int32_t stall) {
+    if (stall < 0) return COLIBRI_ERR_INVALID_ARG;
+    waits().limit_ns = limit_ns ? limit_ns : kWaitLimitNs;
+    waits().stall = stall;
+    return COLIBRI_OK;
 }
 
 colibri_status_t colibri_attention_prompt_workspace(const colibri_kv_pages_t* kv,

@@ -44,6 +44,26 @@ def test_batches_without_sequences(sef, bad, status):  # noqa: F811
         assert Args(sef, **kw).append() == 1 and Args(sef, **kw).prompt() == 1
 
 
+def test_waits_are_set_and_the_environment_is_read_once(sef, monkeypatch):  # noqa: F811
+    from sparse_expert_ffn_gb300 import attention as A
+    assert sef.colibri_attention_waits(5, -1) == 1
+    said = []
+    monkeypatch.setattr(sef.library(), "colibri_attention_waits", lambda *a: said.append(a) or 0)
+    A._pass_on_waits()
+    assert said == []
+    monkeypatch.setenv("COLIBRI_WAIT_LIMIT_NS", "123")
+    A._pass_on_waits(), A._pass_on_waits()
+    monkeypatch.setenv("COLIBRI_TEST_STALL_TMA", "2")
+    A._pass_on_waits()
+    monkeypatch.delenv("COLIBRI_WAIT_LIMIT_NS")
+    monkeypatch.delenv("COLIBRI_TEST_STALL_TMA")
+    A._pass_on_waits(), A._pass_on_waits()
+    assert said == [(123, 0), (123, 2), (0, 0)]
+    host = _source("attn_host.cu")
+    once = host[host.index("    Waits() {"):]
+    assert host.count("getenv") == once[:once.index("    }\n};")].count("getenv") == 2
+
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sparse_expert_ffn_gb300", "csrc")
 
 

@@ -1,6 +1,7 @@
 """Attention operators in calls at the ends of what their documentation allows."""
 
 import ctypes
+import os
 
 import pytest
 import torch
@@ -94,3 +95,20 @@ def test_errors_of_other_calls_are_not_reported(lib, A):
     assert torch.equal(moe.forward(x), want)
     assert moe.check() == sef.OK
     moe.close()
+
+
+def test_the_environment_is_not_read_by_calls(lib, A):
+    """A variable that another thread's setenv puts into the process's environment
+    (not into os.environ, which the binding looks at) changes nothing."""
+    p = Problem([(200, 200), (9, 9)], 4, 2, 64, "bf16", 0, seed=1)
+    sq = seqs(A, p, paged=False)
+    ref = A.attention_prompt(sq, p.q, p.k, p.v)
+    os.putenv("COLIBRI_WAIT_LIMIT_NS", "20000000")
+    os.putenv("COLIBRI_TEST_STALL_TMA", "1")
+    try:
+        got = A.attention_prompt(sq, p.q, p.k, p.v)
+        torch.cuda.synchronize()
+    finally:
+        os.unsetenv("COLIBRI_WAIT_LIMIT_NS")
+        os.unsetenv("COLIBRI_TEST_STALL_TMA")
+    assert torch.equal(got, ref)
