@@ -186,7 +186,7 @@ colibri_status_t colibri_qk_norm_rope(const colibri_seqs_t* seqs, const colibri_
  * length may hold anything (NaN included).  Inside a sequence a non-finite
  * value row may also reach rows that do not see it, through a weight of 0.
  * Waits of the tensor-core kernel are bounded; rows whose wait gave up are
- * filled with NaN.
+ * filled with NaN, and colibri_attention_check reports it.
  */
 colibri_status_t colibri_attention_prompt_workspace(const colibri_kv_pages_t* kv,
                                                     const colibri_seqs_t* seqs,
@@ -218,6 +218,14 @@ colibri_status_t colibri_attention_decode(const colibri_kv_pages_t* cache,
                                           int32_t prefix_len, const int32_t* prefix_table,
                                           void* o, int64_t o_stride, float* lse, void* workspace,
                                           size_t workspace_bytes, void* stream);
+
+/*
+ * colibri_attention_check - wait for `stream` (of the current device; not while it
+ * is being captured), then COLIBRI_ERR_TIMEOUT when a wait of a prompt or decode call
+ * on this device gave up since the last check, whatever stream it ran on;
+ * COLIBRI_ERR_CUDA for a CUDA error.
+ */
+colibri_status_t colibri_attention_check(void* stream);
 
 /*
  * colibri_attention_waits - for later calls of the process: the bound of the

@@ -104,6 +104,7 @@ def _load():
         "colibri_attention_prompt": ([KV, SQ, I32, P, I64, F32, I32, P, I64, P, P, SZ, P], I32),
         "colibri_attention_decode_workspace": ([KV, SQ, I32, I32, SZP], I32),
         "colibri_attention_decode": ([KV, SQ, I32, P, I64, F32, I32, P, P, I64, P, P, SZ, P], I32),
+        "colibri_attention_check": ([P], I32),
         "colibri_attention_waits": ([ctypes.c_uint64, I32], I32),
         "colibri_free": ([P], None),
         "colibri_status_str": ([I32], ctypes.c_char_p),
@@ -125,7 +126,8 @@ _C_NAMES = ("colibri_init", "colibri_init_int8", "colibri_quantize_int8_block64"
             "colibri_forward_routed", "colibri_gather_rows", "colibri_combine_rows",
             "colibri_rope_frequencies", "colibri_append_qkv", "colibri_qk_norm_rope",
             "colibri_attention_prompt_workspace", "colibri_attention_prompt",
-            "colibri_attention_decode_workspace", "colibri_attention_decode", "colibri_attention_waits",
+            "colibri_attention_decode_workspace", "colibri_attention_decode",
+            "colibri_attention_check", "colibri_attention_waits",
             "colibri_free")
 
 

@@ -10,7 +10,8 @@ and run on the tensors' device and its current stream (or ``stream``):
   and the write into the cache in one pass;
 * :func:`attention_prompt`, :func:`attention_prompt_paged`: packed sequences of
   different lengths, grouped heads, causal or full;
-* :func:`attention_decode`: one row per sequence, with a shared prefix.
+* :func:`attention_decode`: one row per sequence, with a shared prefix;
+* :func:`check`: whether a kernel's bounded wait has given up.
 """
 
 from __future__ import annotations
@@ -391,3 +392,16 @@ def attention_decode(cache: PagedKVCache, seqs: Sequences, q, *, prefix_len: int
         D ** -0.5 if scale is None else float(scale), int(prefix_len), table, out.data_ptr(), o_stride, lse_ptr,
         None if ws is None else ws.data_ptr(), need.value, _stream(stream, dev))
     return out
+
+
+def check(stream=None, device=None) -> int:
+    """Wait for the stream (the current one of ``device``, by default the current
+    device); returns the library status: ``ERR_TIMEOUT`` when a wait of an attention
+    kernel on the device gave up since the last check and left rows of NaN, 0 = OK."""
+    if device is None:
+        device = torch.device("cuda", torch.cuda.current_device()) if stream is None else stream.device
+    device = torch.device(device)
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    with torch.cuda.device(device):
+        return _sef.library().colibri_attention_check(_stream(stream, device))

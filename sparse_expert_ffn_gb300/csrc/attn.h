@@ -67,6 +67,8 @@ int64_t attn_tc_items(const AttnArgs& a);    // row tiles of the launch, per key
 // Pages and heads as one dimension of a tensor map; false: more than 2^31 - 1 of them.
 bool attn_tc_units(const AttnArgs& a, int64_t* unit, int* per_page, int* per_head, int* count);
 cudaError_t launch_attn_tc(int d, const AttnArgs& a, cudaStream_t s);
+// Waits for s; *status is DEV_TIMEOUT when a wait has given up since the last time.
+cudaError_t attn_tc_status(int* status, cudaStream_t s);
 
 // Rows of suffix mode, equal shares of the key list per warp (bf16, and float32
 // groups of up to 32 heads).  part_o null: no prefix; otherwise slot part_slot

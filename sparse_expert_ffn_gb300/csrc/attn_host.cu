@@ -451,6 +451,12 @@ colibri_status_t colibri_attention_waits(uint64_t limit_ns, int32_t stall) {
     return COLIBRI_OK;
 }
 
+colibri_status_t colibri_attention_check(void* stream) {
+    int status = DEV_OK;
+    const colibri_status_t st = launched(attn_tc_status(&status, (cudaStream_t)stream));
+    return st == COLIBRI_OK && status != DEV_OK ? COLIBRI_ERR_TIMEOUT : st;
+}
+
 colibri_status_t colibri_attention_prompt_workspace(const colibri_kv_pages_t* kv,
                                                     const colibri_seqs_t* seqs, int32_t n_q_heads,
                                                     size_t* bytes) {

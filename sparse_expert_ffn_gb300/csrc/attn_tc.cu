@@ -64,6 +64,10 @@ template <int D> constexpr uint32_t kTileBytes = (D / 64) * kHalfBytes;
 // of the two tiles is left to the pipe.
 template <int D> constexpr bool kOwnP = D == 64;
 
+// DEV_TIMEOUT once a wait of any launch on this device has given up
+// (colibri_attention_check).
+__device__ int wait_status;
+
 // A work item, as every role needs it.
 struct Item {
     int b;                    // sequence, < 0: no more items
@@ -821,6 +825,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (bars.abort && tid == 0) {
+        atomicExch(&wait_status, DEV_TIMEOUT);
         // none of the copies stays in flight: each slot's last one
         for (uint32_t slot = 0; slot < kSlots<D>; ++slot) {
             int last = -1;
@@ -931,6 +936,15 @@ bool attn_tc_units(const AttnArgs& a, int64_t* unit, int* per_page, int* per_hea
     if (n > 0x7fffffff) return false;
     *unit = g, *per_page = (int)pp, *per_head = (int)ph, *count = (int)n;
     return true;
+}
+
+cudaError_t attn_tc_status(int* status, cudaStream_t s) {
+    cudaError_t e = cudaMemcpyFromSymbolAsync(status, wait_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess || *status == DEV_OK) return e;
+    const int ok = DEV_OK;
+    e = cudaMemcpyToSymbolAsync(wait_status, &ok, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+    return e != cudaSuccess ? e : cudaStreamSynchronize(s);
 }
 
 cudaError_t launch_attn_tc(int d, const AttnArgs& a, cudaStream_t s) {

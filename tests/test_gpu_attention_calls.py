@@ -112,3 +112,37 @@ def test_the_environment_is_not_read_by_calls(lib, A):
         os.unsetenv("COLIBRI_WAIT_LIMIT_NS")
         os.unsetenv("COLIBRI_TEST_STALL_TMA")
     assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("decode", [False, True])
+def test_waits_that_gave_up_are_reported(lib, A, monkeypatch, decode):
+    """Rows of NaN from a wait that gave up come with a status, which is reported
+    once; NaN that was in the inputs does not."""
+    sef = lib
+    p = Problem([(1, 1300 + i) for i in range(5)], 8, 2, 64, "bf16", 16, prefix=1024, seed=2)
+    cache = A.PagedKVCache(p.kp, p.vp)
+    sq = seqs(A, p, decode=True)
+    packed = Problem([(150, 150)], 8, 2, 64, "bf16", 0, seed=3)
+    psq = seqs(A, packed, paged=False)
+
+    def call():
+        if decode:
+            return A.attention_decode(cache, sq, p.q, prefix_len=1024, prefix_table=p.prefix_table)
+        return A.attention_prompt(psq, packed.q, packed.k, packed.v)
+
+    A.check()                                                      # (what an earlier test left)
+    ref = call()
+    assert A.check() == sef.OK
+    monkeypatch.setenv("COLIBRI_WAIT_LIMIT_NS", "20000000")
+    monkeypatch.setenv("COLIBRI_TEST_STALL_TMA", "1")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        bad = call()
+    assert A.check(stream=side) == sef.ERR_TIMEOUT and bad.isnan().all()
+    monkeypatch.delenv("COLIBRI_WAIT_LIMIT_NS")
+    monkeypatch.delenv("COLIBRI_TEST_STALL_TMA")
+    assert A.check() == sef.OK and A.check(device="cuda") == sef.OK
+    assert torch.equal(call(), ref) and A.check() == sef.OK
+    p.q.fill_(float("nan")), packed.q.fill_(float("nan"))
+    assert call().isnan().all() and A.check() == sef.OK
