@@ -64,6 +64,42 @@ def test_waits_are_set_and_the_environment_is_read_once(sef, monkeypatch):  # no
     assert host.count("getenv") == once[:once.index("    }\n};")].count("getenv") == 2
 
 
+B = Args.BASE
+
+
+@pytest.mark.parametrize("o,ok", [(5 * B + 1024, True), (5 * B + 4096 - 1024, True), (5 * B - 1024, True),
+                                  (9 * B, True), (5 * B + 512, False), (5 * B + 1008, False), (5 * B, False),
+                                  (5 * B + 4096 - 512, False), (5 * B - 512, False), (5 * B + 4096 * 9 + 512, False),
+                                  (5 * B + 4096 * 10, True), (2 * B + 64, False), (B - 10 * 4096 + 3072, True),
+                                  (B - 16, False)])
+def test_outputs_between_the_columns_of_q(sef, o, ok):  # noqa: F811
+    """10 rows of q, 1024 bytes each, 4096 bytes apart, the cache at B and 2 B: o may
+    lie between q's columns and nowhere in them or in the cache.  No sequences, so that
+    an accepted call does nothing, and a workspace, so that only the overlap refuses."""
+    kw = dict(q=5 * B, qs=2048, o=o, os=2048)
+    assert Args(sef, n_seqs=0, **kw).prompt() == (0 if ok else 1)
+    if not ok:
+        assert Args(sef, **kw).prompt() == 1                       # (two sequences)
+        assert Args(sef, seq_start=None, n_seqs=10, **kw).decode() == 1
+
+
+@pytest.mark.parametrize("qo,stride,ok", [(5 * B + 2048, 2048, True), (5 * B + 3072, 2048, True), (5 * B, 2048, True),
+                                          (9 * B, 512, True), (5 * B + 1024, 2048, False), (5 * B + 16, 2048, False),
+                                          (5 * B + 1536, 2048, False), (5 * B + 2048 - 16, 2048, False),
+                                          (5 * B + 3088, 2048, False), (5 * B + 2048, 512, False), (5 * B, 512, False),
+                                          (B, 512, False), (2 * B + 4096, 512, False), (B - 512, 512, False)])
+def test_append_outputs_between_the_columns_of_a_projection(sef, qo, stride, ok):  # noqa: F811
+    """q, k and v side by side in rows of 4096 bytes of which they take 2048: q_out may
+    be q, or lie in what is left."""
+    def call(n_seqs):
+        a = Args(sef, q=5 * B, qs=2048, ks=2048, vs=2048, qo=qo, qos=stride, n_seqs=n_seqs)
+        a.at.update(k=5 * B + 1024, v=5 * B + 1536)
+        return a.append()
+    assert call(0) == (0 if ok else 1)
+    if not ok:
+        assert call(2) == 1
+
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sparse_expert_ffn_gb300", "csrc")
 
 

@@ -146,3 +146,17 @@ def test_waits_that_gave_up_are_reported(lib, A, monkeypatch, decode):
     assert torch.equal(call(), ref) and A.check() == sef.OK
     p.q.fill_(float("nan")), packed.q.fill_(float("nan"))
     assert call().isnan().all() and A.check() == sef.OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_results_between_the_columns_of_the_inputs(A, dtype):
+    """q, k, v and the output as column ranges of one tensor's rows."""
+    p = Problem([(150, 150), (40, 40)], 4, 2, 64, dtype, 0, seed=6)
+    wide = torch.full((190, 896), 5.0, dtype=p.dt, device=p.q.device)
+    q, o, k, v = (wide[:, a:b].unflatten(1, (-1, 64)) for a, b in ((0, 256), (256, 512), (576, 704), (768, 896)))
+    q.copy_(p.q), k.copy_(p.k), v.copy_(p.v)
+    was = wide.clone()
+    A.attention_prompt(seqs(A, p, paged=False), q, k, v, out=o)
+    p.check(o, None, True)
+    wide[:, 256:512] = was[:, 256:512]
+    assert torch.equal(wide, was)
