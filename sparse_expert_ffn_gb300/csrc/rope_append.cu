@@ -7,11 +7,13 @@
 //   (a, b) -> mscale (a cos t f_i - b sin t f_i, b cos t f_i + a sin t f_i)
 // for the pairs (a, b) of y; float32, rounded once at the end.
 //
-// The angle: f_i / 2 pi as a 64-bit fraction of a turn; t times it, wrapped by
-// the integer product itself, is exact to 2^-33 turn at any int32 position,
-// where a float32 product would be off by 2^-24 of t f_i radians.  sin and cos
-// of the top 32 bits are then good to float32 rounding.  One set of angles
-// serves every head of a row.
+// The angle: f_i / 2 pi, formed in double, as a 64-bit fraction of a turn; t times
+// it, wrapped by the integer product itself, of which the top 32 bits are taken:
+// off by at most 2^-32 turn and t (f_i 2^-55 + 2^-64) turns (the double product and
+// its constant, and the fraction's end).  That is 2^-32 turn at positions that
+// contexts have and 2^-24 at 2^31, where a float32 product would be off by 2^-24 of
+// t f_i radians.  sin and cos of it are good to float32 rounding.  One set of
+// angles serves every head of a row.
 //
 // Bound by HBM (each element is read once and written once), and close to it by
 // instruction issue, so the work per element is kept small: a head is held by

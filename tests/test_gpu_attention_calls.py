@@ -3,11 +3,12 @@
 import ctypes
 import os
 
+import numpy as np
 import pytest
 import torch
 
 import synth
-from attn_parity import DT, Problem, seqs
+from attn_parity import HALF, U, Problem, f64, seqs
 
 pytestmark = pytest.mark.gpu
 
@@ -160,3 +161,31 @@ def test_results_between_the_columns_of_the_inputs(A, dtype):
     p.check(o, None, True)
     wide[:, 256:512] = was[:, 256:512]
     assert torch.equal(wide, was)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("style", ["half", "interleaved"])
+def test_angles_of_far_positions(A, style, dtype):
+    """Up to the last int32 position.  Beside attn_parity's 32 u for the pair, the
+    angle is off by 2^-32 turn and t (f 2^-55 + 2^-64) turns: the double f / 2 pi is off
+    by 2^-53 of itself for the product and 2^-53.8 for the constant, together less than
+    f 2^-55, its fraction ends at 2^-64, and the position multiplies both.  The
+    oracle's angles are taken in 200 bits (a double product of 2^31 f is off by 2^-22)."""
+    mp = pytest.importorskip("mpmath")
+    d, kv = 128, [2 ** 31 - 1, 2 ** 28 + 5, 2 ** 24 + 1, 70]
+    p = Problem([(3, t) for t in kv], 2, 1, d, dtype, 0, seed=12)
+    freq = A.rope_frequencies(d, 10000.0)[0]
+    sq = A.Sequences(p.seq_start, p.kv_len)
+    got, _ = A.qk_norm_rope(sq, p.q, p.k, rope=A.Rope(freq.cuda(), style))
+    pos = np.concatenate([np.arange(t - 3, t) for t in kv])
+    with mp.workprec(200):
+        angle = [[mp.fmod(mp.mpf(int(t)) * mp.mpf(f.item()), 2 * mp.pi) for f in freq] for t in pos]
+        cos, sin = (np.array([[float(fn(a)) for a in row] for row in angle])[:, None] for fn in (mp.cos, mp.sin))
+    x, y, f = f64(p.q), f64(got), freq.numpy()
+    first, second = (slice(0, 64), slice(64, 128)) if style == "half" else (slice(0, 128, 2), slice(1, 128, 2))
+    a, b = x[..., first], x[..., second]
+    off = 2 * np.pi * (2.0 ** -32 + pos[:, None] * (f * 2.0 ** -55 + 2.0 ** -64))[:, None]
+    for z, want in ((y[..., first], a * cos - b * sin), (y[..., second], b * cos + a * sin)):
+        r = HALF[p.dt]
+        tol = r * np.abs(want) + (1 + r) * (32 * U + off) * (np.abs(a) + np.abs(b))
+        assert (np.abs(z - want) <= tol).all(), float((np.abs(z - want) / tol).max())
