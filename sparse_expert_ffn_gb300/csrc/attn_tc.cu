@@ -921,9 +921,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
 
 int64_t attn_tc_items(const AttnArgs& a) {
     const int per = 2 * (128 / a.group);
-    if (a.mode == kAttnPrompt) return a.n_rows / per + a.n_seqs;
-    if (a.mode == kAttnPrefix) return (a.n_seqs + per - 1) / per;
-    return a.n_seqs;
+    return a.mode == kAttnPrompt ? a.n_rows / per + a.n_seqs : (a.n_seqs + per - 1) / per;
 }
 
 // Pages and heads in units of the greatest common divisor of their strides.
