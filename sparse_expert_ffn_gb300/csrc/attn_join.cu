@@ -17,46 +17,67 @@ namespace {
 
 constexpr int kBatch = 8;
 
+// Where a row's parts are.
+struct Place {
+    int live;             // the row belongs to a sequence, and has parts to join
+    int c0, c1;           // shares that hold its keys
+    int first_is_last;    // its piece of share c0 is that share's last
+};
+
+// Called by a whole warp.
+template <typename T, int D, bool kEarly>
+__device__ __forceinline__ Place row_parts(const AttnArgs& a, int row, int head, int slots, int shares_per_seq) {
+    Place p = {1, 0, -1, 0};
+    if (shares_per_seq) {
+        int64_t total, first;
+        count_steps<T, D, kEarly>(a, shares_per_seq, row, &total, &first);
+        const int steps = seq_steps<T, D, kEarly>(a, row);
+        if (steps > 0) {
+            const int shares = share_count(total);
+            first += (int64_t)((head / a.group) * row_tiles<T>(a.group) + (head % a.group) / row_tile<T>(a.group)) * steps;
+            p.c0 = share_of(total, shares, first);
+            p.c1 = share_of(total, shares, first + steps - 1);
+            p.first_is_last = share_begin(total, shares, p.c0) < first;
+        }
+        p.live = p.c0 != p.c1 || slots > 0;                        // (else written by the one share)
+    } else if (a.mode == kAttnPrompt) {
+        p.live = 0;
+        for (int b = threadIdx.x & 31; b < a.n_seqs; b += 32)
+            p.live |= row >= max(ld_early<kEarly>(a.seq_start + b), 0) && row < ld_early<kEarly>(a.seq_start + b + 1);
+        p.live = __any_sync(0xffffffffu, p.live);
+    }
+    return p;
+}
+
+// Lengths are read before the wait, from L2 (ld_early), while they are few: the long
+// sequence of 65421 keys takes 48 us instead of 50, 64 sequences 50 instead of 51.
+// Every CTA reads all of them, and many come faster through L1: 256 sequences of 1000
+// keys 183 instead of 185 us, 4096 3960 instead of 5550.
+constexpr int kEarlySeqs = 128;
+
 template <typename T, int D, int kThreads>
 __global__ void __launch_bounds__(kThreads) attn_join_kernel(const __grid_constant__ AttnArgs a, int slots,
                                                              int shares_per_seq) {
     constexpr int kWarps = kThreads / 32;
     __shared__ float4 rows[kWarps][D / 4];
     __shared__ float tops[kWarps], sums[kWarps];
-    __shared__ int place[4];
+    __shared__ Place place;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t flat = blockIdx.x;
     const int64_t total_rows = (int64_t)a.n_rows * a.hq;
     const int row = (int)(flat / (uint32_t)a.hq), head = (int)(flat % (uint32_t)a.hq);
     const int tile_row = (head % a.group) % row_tile<T>(a.group);
-    // (lengths are read before the wait, from L2: see attn_common.cuh)
+    const bool early = a.n_seqs <= kEarlySeqs;
+    if (!early) pdl_enter();
     if (warp == 0) {
-        // live: the row belongs to a sequence; c0 .. c1: the shares that hold its keys
-        int live = 1, c0 = 0, c1 = -1, first_is_last = 0;
-        if (shares_per_seq) {
-            int64_t total, first;
-            count_steps<T, D, true>(a, shares_per_seq, row, &total, &first);
-            const int steps = seq_steps<T, D, true>(a, row);
-            if (steps > 0) {
-                const int shares = share_count(total);
-                first += (int64_t)((head / a.group) * row_tiles<T>(a.group) + (head % a.group) / row_tile<T>(a.group)) * steps;
-                c0 = share_of(total, shares, first);
-                c1 = share_of(total, shares, first + steps - 1);
-                first_is_last = share_begin(total, shares, c0) < first;
-            }
-            live = c0 != c1 || slots > 0;                          // (else written by the one share)
-        } else if (a.mode == kAttnPrompt) {
-            live = 0;
-            for (int b = lane; b < a.n_seqs; b += 32)
-                live |= row >= max(ld_early<true>(a.seq_start + b), 0) && row < ld_early<true>(a.seq_start + b + 1);
-            live = __any_sync(0xffffffffu, live);
-        }
-        if (lane == 0) place[0] = live, place[1] = c0, place[2] = c1, place[3] = first_is_last;
+        const Place p = early ? row_parts<T, D, true>(a, row, head, slots, shares_per_seq)
+                              : row_parts<T, D, false>(a, row, head, slots, shares_per_seq);
+        if (lane == 0) place = p;
     }
-    pdl_enter();
+    if (early) pdl_enter();
     __syncthreads();
-    if (!place[0]) return;
-    const int c0 = place[1], c1 = place[2];
+    if (!place.live) return;
+    const int c0 = place.c0, c1 = place.c1;
     const bool one = shares_per_seq && c0 == c1;                   // whole, in slot part_slot
     const int in_slots = slots + (one ? 1 : 0), parts = in_slots + (one ? 0 : c1 - c0 + 1);
     float top = -INFINITY, sum = 0.f;
@@ -72,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const __grid_consta
                 const int c = c0 + i - in_slots;
                 const bool slot = i < in_slots;
                 const int64_t at = slot ? i * total_rows + flat
-                                        : ((int64_t)c * 2 + (c == c0 && place[3])) * piece_rows<T>(a.group) + tile_row;
+                                        : ((int64_t)c * 2 + (c == c0 && place.first_is_last)) * piece_rows<T>(a.group) + tile_row;
                 w[k] = (slot ? a.part_lse : a.piece_lse)[at];
                 if (lane < D / 4)
                     v[k] = *reinterpret_cast<const float4*>((slot ? a.part_o : a.piece_o) + at * D + lane * 4);

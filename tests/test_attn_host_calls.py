@@ -120,10 +120,16 @@ def test_kernels_read_from_l2_before_they_wait():
             reads = r"__ldg|attn_seq|attn_item|work_item|row_place|load\(|simt_tile" \
                 r"|\ba\.(q|k|v|o|lse|seq_start|kv_len|table|freq|q_norm|k_norm|q_out|k_out|v_out|part_\w+|piece_\w+)\b"
             assert not re.search(reads, before), name
-    for name, early in (("attn_decode.cu", "kEarly"), ("attn_join.cu", "true")):
+    for name in ("attn_decode.cu", "attn_join.cu"):
         text = _source(name)
         calls = re.findall(r"\b(?:attn_seq|attn_page|seq_steps|count_steps|ld_early)\b(<[^>]*>)?", text)
-        assert calls and all(c.endswith(early + ">") for c in calls) and "__ldg" not in text, name
+        assert calls and all(c.endswith("kEarly>") for c in calls) and "__ldg" not in text, name
+    # the kernels of kEarly and not: who waits first may read through L1
+    assert "if constexpr (kEarly) pdl_launch_dependents();\n    else pdl_enter();\n    decode_share<Rows, kEarly>" in \
+        _source("attn_decode.cu")
+    join = re.sub(r"\s+", " ", _source("attn_join.cu"))
+    assert "if (!early) pdl_enter(); if (warp == 0) { const Place p = early ? row_parts<T, D, true>" in join
+    assert ": row_parts<T, D, false>" in join and "} if (early) pdl_enter(); __syncthreads();" in join
     common = _source("attn_common.cuh")
     for name in ("AttnSeq attn_seq", "int attn_page"):
         body = common[common.index(name):]

@@ -189,3 +189,30 @@ def test_angles_of_far_positions(A, style, dtype):
         r = HALF[p.dt]
         tol = r * np.abs(want) + (1 + r) * (32 * U + off) * (np.abs(a) + np.abs(b))
         assert (np.abs(z - want) <= tol).all(), float((np.abs(z - want) / tol).max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("count,prefix", [(128, 0), (129, 0), (129, 64), (300, 0), (300, 64)])
+def test_batches_of_many_sequences(A, count, prefix, dtype):
+    """Around and above the count of sequences from which the join waits before it
+    looks at their lengths; some cut into pieces, some empty."""
+    r = np.random.default_rng(count)
+    own = r.integers(0, 60, count)
+    own[[3, count // 2, count - 1]] = [6000, 3001, 900]
+    p = Problem([(1, prefix + int(t)) for t in own], 2, 1, 64, dtype, 16, prefix=prefix, seed=count, fill=float("nan"))
+    lse = torch.full((p.rows, 2), 9.0, device=p.q.device)
+    out = A.attention_decode(A.PagedKVCache(p.kp, p.vp), seqs(A, p, decode=True), p.q, prefix_len=prefix,
+                             prefix_table=p.prefix_table if prefix else None, lse=lse)
+    p.check(out, lse, False)
+
+
+@pytest.mark.parametrize("count", [100, 140])
+def test_ranges_of_many_short_prompts(A, count):
+    """float32 prompts of one or two rows far into a context: key ranges and a join."""
+    r = np.random.default_rng(count)
+    p = Problem([(int(n), 300 + int(t)) for n, t in zip(r.integers(1, 3, count), r.integers(0, 500, count))], 2, 1, 64,
+                "fp32", 16, seed=count, spare=2, fill=float("nan"))
+    lse = torch.full((p.rows, 2), 9.0, device=p.q.device)
+    out = A.attention_prompt_paged(A.PagedKVCache(p.kp, p.vp), seqs(A, p), p.q, out=torch.full_like(p.q, 9.0), lse=lse)
+    p.check(out, lse, True)
+    assert (out[-2:] == 9.0).all() and (lse[-2:] == 9.0).all()
