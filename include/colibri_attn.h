@@ -177,7 +177,7 @@ colibri_status_t colibri_qk_norm_rope(const colibri_seqs_t* seqs, const colibri_
  *         ranges of one tensor's rows may lie between each other)
  *   lse   [n_rows, n_q_heads] float32 or NULL: ln sum_j exp(scale * q . k_j),
  *         -infinity for a row that sees no key
- *   scale positive and finite
+ *   scale positive, scale * log2(e) finite
  *   workspace  colibri_attention_prompt_workspace() bytes, 256-byte aligned;
  *         may be NULL where that is 0
  * Scores, maxima and sums are float32; for bf16 the weights are rounded to bf16

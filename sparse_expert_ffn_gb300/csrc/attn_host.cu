@@ -136,6 +136,8 @@ int choose_splits(int64_t items, int64_t keys, int slots, int step) {
     return (int)std::max<int64_t>(1, std::min({slots / std::max<int64_t>(items, 1), most, (int64_t)kMaxSplits}));
 }
 
+constexpr float kLog2e = 1.44269504088896340736f;
+
 // bf16 prompts and prefixes run on the tensor cores.
 bool on_tensor_cores(int dtype, int mode) { return dtype == COLIBRI_DTYPE_BF16 && mode != kAttnSuffix; }
 
@@ -203,7 +205,7 @@ AttnArgs make_args(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq
     a.num_pages = kv->num_pages, a.page_size = kv->page_size;
     a.page_shift = 0;
     while ((1 << a.page_shift) < kv->page_size) ++a.page_shift;
-    a.scale_log2 = scale * 1.44269504088896340736f;
+    a.scale_log2 = scale * kLog2e;
     a.splits = 1;
     a.wait_limit_ns = waits().limit_ns.load(std::memory_order_relaxed);
     a.stall_tma = waits().stall.load(std::memory_order_relaxed);
@@ -216,7 +218,7 @@ colibri_status_t check_attention(const colibri_kv_pages_t* kv, const colibri_seq
     const int esz = elem_size(kv->dtype), d = kv->head_dim;
     if (!rows_ok(q, q_stride, hq, d, esz) || !rows_ok(o, o_stride, hq, d, esz) || ((uintptr_t)lse & 3))
         return COLIBRI_ERR_INVALID_ARG;
-    if (!(scale > 0.f) || !std::isfinite(scale)) return COLIBRI_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !std::isfinite(scale * kLog2e)) return COLIBRI_ERR_INVALID_ARG;
     if (s->n_rows == 0) return COLIBRI_OK;
     const Rows out = row_bytes(o, o_stride, hq, d, esz);
     if (clash(row_bytes(q, q_stride, hq, d, esz), out, s->n_rows)) return COLIBRI_ERR_INVALID_ARG;

@@ -44,6 +44,14 @@ def test_batches_without_sequences(sef, bad, status):  # noqa: F811
         assert Args(sef, **kw).append() == 1 and Args(sef, **kw).prompt() == 1
 
 
+@pytest.mark.parametrize("scale,status", [(2.3e38, 0), (2.4e38, 1), (3.4e38, 1), (1e-45, 0)])
+def test_scales_whose_product_with_log2_e_is_finite(sef, scale, status):  # noqa: F811
+    """The kernels multiply scores by scale * log2(e): an infinite one would make equal
+    scores NaN."""
+    assert Args(sef, n_seqs=0, scale=scale).prompt() == status
+    assert Args(sef, seq_start=None, n_seqs=0, n_rows=0, scale=scale).decode() == status
+
+
 def test_waits_are_set_and_the_environment_is_read_once(sef, monkeypatch):  # noqa: F811
     from sparse_expert_ffn_gb300 import attention as A
     assert sef.colibri_attention_waits(5, -1) == 1
