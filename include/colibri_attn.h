@@ -183,8 +183,9 @@ colibri_status_t colibri_qk_norm_rope(const colibri_seqs_t* seqs, const colibri_
  * Scores, maxima and sums are float32; for bf16 the weights are rounded to bf16
  * for the product with v, and sums are formed of weights up to 2^24, so
  * |v| * keys * 2^24 has to stay in float32's range.  Key rows beyond a sequence's
- * length may hold anything (NaN included).  Inside a sequence a non-finite
- * value row may also reach rows that do not see it, through a weight of 0.
+ * length may hold anything (NaN included).  Inside a sequence, and inside the part
+ * of a shared prefix that some row sees, a non-finite value row may also reach rows
+ * that do not see it, through a weight of 0.
  * Waits of the tensor-core kernel are bounded; rows whose wait gave up are
  * filled with NaN, and colibri_attention_check reports it.
  */

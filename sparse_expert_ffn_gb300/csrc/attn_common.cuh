@@ -52,9 +52,14 @@ __device__ __forceinline__ int attn_limit(const AttnArgs& a, const AttnSeq& s, i
     return min(max(s.raw - (s.n - 1 - i), 0), s.kv);
 }
 
-// Largest limit of rows i0 .. i1 - 1 (i0 < i1); for the prefix, the prefix.
-__device__ __forceinline__ int attn_limit_max(const AttnArgs& a, const AttnSeq& s, int i1) {
-    return a.mode == kAttnPrefix ? s.kv : attn_limit(a, s, i1 - 1);
+// Largest limit of rows i0 .. i1 - 1 (i0 < i1); called by a whole warp.  Of a prefix
+// that is where a tile's keys end, however long the prefix is: values that no row of
+// the tile sees are not read (or cleared), whatever they hold.
+__device__ __forceinline__ int attn_limit_max(const AttnArgs& a, const AttnSeq& s, int i0, int i1) {
+    if (a.mode != kAttnPrefix) return attn_limit(a, s, i1 - 1);
+    int most = 0;
+    for (int i = i0 + (threadIdx.x & 31); i < i1; i += 32) most = max(most, attn_limit(a, s, i));
+    return __reduce_max_sync(0xffffffffu, most);
 }
 
 // Page id of keys at page index `p` of sequence b, -1 where there is none.

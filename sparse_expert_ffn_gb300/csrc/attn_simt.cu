@@ -29,7 +29,7 @@ struct SimtSmem {
     float k[2][kKeys][D + 4];
     float v[2][kKeys][D];
     float p[ROWS][kKeys + 4];
-    int item[2];
+    int item[3];
 };
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
@@ -42,7 +42,11 @@ __device__ __forceinline__ void simt_tile(const AttnArgs& a, SimtSmem<ROWS, D>& 
     if (tid < 32) {
         int b = 0, tile = 0;
         const bool ok = attn_item(a, blockIdx.x / a.hkv, a.group, ROWS, gridDim.x * gridDim.y > 304, &b, &tile);
-        if (tid == 0) sm.item[0] = ok ? b : -1, sm.item[1] = tile;
+        int end = 0;
+        if (ok && a.mode == kAttnPrefix)
+            end = attn_limit_max(a, attn_seq(a, b), tile * ROWS / a.group,
+                                 (min((tile + 1) * ROWS, a.n_seqs * a.group) - 1) / a.group + 1);
+        if (tid == 0) sm.item[0] = ok ? b : -1, sm.item[1] = tile, sm.item[2] = end;
     }
     __syncthreads();
     const int b = sm.item[0];
@@ -58,7 +62,7 @@ __device__ __forceinline__ void simt_tile(const AttnArgs& a, SimtSmem<ROWS, D>& 
     constexpr int kPasses = kKeys * kChunks / kThreads;
     const int ty = tid >> 4, tx = tid & 15;
     int lo, hi;
-    attn_split(a, sp, kKeys, sq.kv0, attn_limit_max(a, sq, (r0 + rows - 1) / a.group + 1), &lo, &hi);
+    attn_split(a, sp, kKeys, sq.kv0, a.mode == kAttnPrefix ? sm.item[2] : attn_limit(a, sq, (r0 + rows - 1) / a.group), &lo, &hi);
 
     // copies of a 64-key tile; the page ids of the tile after it are read ahead
     const int row_in = tid / kChunks, chunk = tid % kChunks;

@@ -257,11 +257,16 @@ __device__ __forceinline__ Item work_item(const AttnArgs& a, int x, int y, int t
     }
     it.seq = attn_seq(a, it.b);
     it.tok0 = tile * 2 * tokens;
-    attn_split(a, y, kTileKeys, it.seq.kv0, attn_limit_max(a, it.seq, min(it.tok0 + 2 * tokens, it.seq.n)), &it.lo, &it.hi);
+    int ends[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const int first = it.tok0 + t * tokens, last = min(first + tokens, it.seq.n);
-        const int end = first < it.seq.n ? min(it.hi, attn_limit_max(a, it.seq, last)) : it.lo;
+        ends[t] = first < it.seq.n ? attn_limit_max(a, it.seq, first, last) : 0;
+    }
+    attn_split(a, y, kTileKeys, it.seq.kv0, max(ends[0], ends[1]), &it.lo, &it.hi);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int end = min(it.hi, ends[t]);
         it.steps[t] = end > it.lo ? (end - it.lo + kTileKeys - 1) / kTileKeys : 0;
     }
     return it;

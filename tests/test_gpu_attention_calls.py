@@ -216,3 +216,17 @@ def test_ranges_of_many_short_prompts(A, count):
     out = A.attention_prompt_paged(A.PagedKVCache(p.kp, p.vp), seqs(A, p), p.q, out=torch.full_like(p.q, 9.0), lse=lse)
     p.check(out, lse, True)
     assert (out[-2:] == 9.0).all() and (lse[-2:] == 9.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("fill", [float("nan"), float("inf")])
+@pytest.mark.parametrize("hq,hkv,d,page,prefix,kv", [
+    (8, 2, 64, 16, 1040, [0, 0, 0]), (8, 2, 128, 16, 1040, [5, 0, 700, 129]), (4, 4, 128, 64, 4096, [128, 128, 64]),
+    (16, 1, 64, 128, 2048, [0] * 19 + [1300]), (33, 1, 64, 16, 512, [1, 511, 300]), (3, 3, 64, 8, 64, [63] * 200 + [0])])
+def test_prefixes_that_no_sequence_reaches_the_end_of(A, hq, hkv, d, page, prefix, kv, fill, dtype):
+    """Keys and values of the prefix behind every sequence's length may hold anything."""
+    p = Problem([(1, t) for t in kv], hq, hkv, d, dtype, page, prefix=prefix, seed=prefix, fill=fill)
+    lse = torch.full((p.rows, hq), 9.0, device=p.q.device)
+    out = A.attention_decode(A.PagedKVCache(p.kp, p.vp), seqs(A, p, decode=True), p.q, prefix_len=prefix,
+                             prefix_table=p.prefix_table, out=torch.full_like(p.q, 9.0), lse=lse)
+    p.check(out, lse, False)
