@@ -169,14 +169,15 @@ colibri_status_t colibri_qk_norm_rope(const colibri_seqs_t* seqs, const colibri_
  * colibri_attention_prompt - for row i of n of sequence b and query head h
  *   o = sum_j w_j v_j,  w = softmax_j(scale * q . k_j)
  * over the keys j < kv_len[b] (causal == 0) or j <= kv_len[b] - n + i (causal
- * != 0) of the head's key head.  A row that sees no key gets zeros.
+ * != 0) of the head's key head.  A row that sees no key, or none
+ * whose score is above -infinity, gets zeros.
  *   kv    a paged cache (seqs->page_table and kv_len given), or the prompt's
  *         own packed keys (page_table and kv_len NULL, num_pages 1,
  *         page_size n_rows)
  *   q, o  [n_rows, n_q_heads, head_dim]; o must not overlap q, k or v (column
  *         ranges of one tensor's rows may lie between each other)
  *   lse   [n_rows, n_q_heads] float32 or NULL: ln sum_j exp(scale * q . k_j),
- *         -infinity for a row that sees no key
+ *         -infinity for a row that gets zeros
  *   scale positive, scale * log2(e) finite
  *   workspace  colibri_attention_prompt_workspace() bytes, 256-byte aligned;
  *         may be NULL where that is 0

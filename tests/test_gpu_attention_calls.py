@@ -230,3 +230,60 @@ def test_prefixes_that_no_sequence_reaches_the_end_of(A, hq, hkv, d, page, prefi
     out = A.attention_decode(A.PagedKVCache(p.kp, p.vp), seqs(A, p, decode=True), p.q, prefix_len=prefix,
                              prefix_table=p.prefix_table, out=torch.full_like(p.q, 9.0), lse=lse)
     p.check(out, lse, False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("paged", [False, True])
+def test_rows_before_the_first_sequence(A, paged, dtype):
+    """seq_start may begin behind row 0: the rows before it belong to no sequence."""
+    p = Problem([(150, 150), (0, 0), (70, 200 if paged else 70)], 4, 2, 64, dtype, 16 if paged else 0, seed=3)
+    pad = lambda t, x: torch.cat([torch.full_like(t[:9], x), t])  # noqa: E731
+    sq = A.Sequences(p.seq_start + 9, p.kv_len if paged else None, p.table if paged else None)
+    out, lse = torch.full_like(pad(p.q, 0), 9.0), torch.full((p.rows + 9, 4), 9.0, device=p.q.device)
+    q = pad(p.q, float("nan"))
+    if paged:
+        cache = A.PagedKVCache(p.kp, p.vp)
+        A.attention_prompt_paged(cache, sq, q, out=out, lse=lse)
+    else:
+        A.attention_prompt(sq, q, pad(p.k, float("nan")), pad(p.v, float("inf")), out=out, lse=lse)
+    p.check(out[9:], lse[9:], True)
+    assert (out[:9] == 9.0).all() and (lse[:9] == 9.0).all()
+    if paged:
+        k, v = (torch.randn(p.rows, 2, 64, device=p.q.device).to(p.dt) for _ in range(2))
+        want = A.append_qkv(cache, seqs(A, p), p.q, k, v)
+        after = p.kp.clone(), p.vp.clone()
+        p.kp.fill_(1.0), p.vp.fill_(1.0)
+        got = A.append_qkv(cache, sq, q, pad(k, float("nan")), pad(v, float("nan")), q_out=torch.full_like(q, 9.0))
+        assert torch.equal(got[9:], want) and (got[:9] == 9.0).all()
+        for b, (n, total) in enumerate(p.lens):
+            for t in range(total - n, total):
+                at = p.page_of(b, t), slice(None), t % 16
+                assert torch.equal(p.kp[at], after[0][at]) and torch.equal(p.vp[at], after[1][at])
+        assert p.kp.isfinite().all() and p.vp.isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_scores_that_are_all_minus_infinity(A, dtype):
+    """Rows whose scores are all -infinity get zeros, like rows that see no key; one
+    finite score among them, and its value is the result."""
+    p = Problem([(1, 700), (1, 5), (1, 20000)], 4, 2, 64, dtype, 16, seed=3)
+    p.q.zero_(), p.q[..., 0].fill_(-float("inf"))
+    p.kp[..., 0] = 1.0
+    cache, lse = A.PagedKVCache(p.kp, p.vp), torch.empty(3, 4, device=p.q.device)
+    for call in (lambda: A.attention_decode(cache, seqs(A, p, decode=True), p.q, lse=lse),
+                 lambda: A.attention_prompt_paged(cache, seqs(A, p), p.q, lse=lse)):
+        assert (call() == 0).all() and lse.isneginf().all()
+    packed = Problem([(300, 300)], 4, 2, 64, dtype, 0, seed=4)
+    packed.q.zero_(), packed.q[..., 0].fill_(-float("inf"))
+    packed.k[..., 0] = 1.0
+    lse = torch.empty(300, 4, device=p.q.device)
+    psq = seqs(A, packed, paged=False)
+    assert (A.attention_prompt(psq, packed.q, packed.k, packed.v, lse=lse) == 0).all() and lse.isneginf().all()
+    # -infinity through one column of the keys instead: key 170 alone is finite
+    packed.q.fill_(1.0)
+    packed.k[..., 0], packed.k[170] = -float("inf"), 0.25
+    out = A.attention_prompt(psq, packed.q, packed.k, packed.v, lse=lse)
+    assert (out[:170] == 0).all() and lse[:170].isneginf().all()
+    assert torch.equal(out[170:], packed.v[170].repeat_interleave(2, 0).expand(130, 4, 64))
+    # 64 * 0.25 / 8, through log2(e) and ln 2 of 24 bits each
+    assert ((lse[170:].double() - 2.0).abs() <= 4 * U * 2.0).all()
