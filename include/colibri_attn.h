@@ -13,7 +13,7 @@
  * No handle: every call works on the caller's buffers, allocates nothing,
  * runs on the current device ordered on `stream` (a cudaStream_t, NULL = the
  * legacy default stream) and returns without waiting, so it can be captured
- * into a CUDA graph.  Argument checks run on the host before any CUDA call:
+ * into a CUDA graph (but for colibri_attention_check, which waits).  Argument checks run on the host before any CUDA call:
  * INVALID_ARG for pointers, sizes, strides and alignment that cannot be right,
  * UNSUPPORTED for shapes that this build does not run.  Every device pointer
  * belongs to the current device.  Calls that may overlap on the GPU must not

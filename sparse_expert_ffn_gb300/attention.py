@@ -12,6 +12,9 @@ and run on the tensors' device and its current stream (or ``stream``):
   different lengths, grouped heads, causal or full;
 * :func:`attention_decode`: one row per sequence, with a shared prefix;
 * :func:`check`: whether a kernel's bounded wait has given up.
+
+Results carry no gradient: the operators have no backward pass, and inputs that
+require one are read like any others.
 """
 
 from __future__ import annotations
@@ -287,7 +290,10 @@ def _workspace(nbytes, device, stream):
     thread's last call there: the thread's calls follow each other on the stream,
     as their uses of a block that the caching allocator hands out again would, and a
     step of a few tokens takes 12 us of the host instead of 17.  Other threads,
-    streams and devices, and graphs that are being captured, have their own."""
+    streams and devices, and graphs that are being captured, have their own.  It is
+    kept, up to 16 MB, until the thread calls on another stream, needs a larger one, or
+    ends; calls that need more (single rows of groups from 14 heads of 128 on) have
+    theirs from the caching allocator every time."""
     if not nbytes:
         return None
     if stream is not None or nbytes > _KEPT_BYTES or _current_device() != device.index or _capturing():

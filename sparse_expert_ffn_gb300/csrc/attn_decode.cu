@@ -26,11 +26,12 @@
 // and a quarter (d 128) or half (d 64) of its columns in the scores, whose query
 // rows lie in registers, and d / 32 columns of all keys in the product with V.  A
 // step of 4 rows takes a quarter of the issue slots that its 8 KB leave: 48
-// sequences of 4000 keys of 16 heads of 128 take 458 us, 6.9 TB/s (tiles of 16 rows
-// of a CTA, which read K and V from shared memory for every row, 2135 us).  More
-// rows' queries do not fit the registers: a group is cut into tiles of 4, and its
-// keys are read once per tile (4 key heads of d 128: groups of 8 239 us instead of
-// 716 in one tile of attn_simt.cu, of 32 856 instead of 1007).
+// sequences of 4000 keys of 16 heads of 128 take 447 to 458 us, 6.9 TB/s (tiles of 16
+// rows of a CTA, which read K and V from shared memory for every row, 2135 us).  More
+// rows' queries do not fit a warp's registers, so a group is cut into tiles of 4, and
+// since every warp streams for itself, the keys are read once per tile (4 key heads of
+// d 128: groups of 4 take 120 us, of 8 236 instead of 716 in one tile of attn_simt.cu,
+// of 32 865 instead of 1007).
 #include <cuda_runtime.h>
 
 #include "attn_common.cuh"

@@ -126,8 +126,11 @@ struct Plan {
 };
 
 // Key ranges per row tile of a launch with `items` tiles over up to `keys`
-// keys, of which the GPU holds `slots` at a time: as many as one wave takes, of
-// at least two steps of `step` keys each.  More tiles than that are not split: the
+// keys, in `slots` CTAs: as many as those take, of at least two steps of `step` keys
+// each.  `keys` is what the page table could hold, since lengths are on the device: a
+// prompt of 37 rows takes 8.4 us (in a graph) with a table of 2 pages of 32 keys and
+// 13.9 with one of 1024, for which it is cut into 19 ranges and joined.  More
+// tiles than slots are not split: the
 // partial rows' way through memory costs more than an even last wave gives
 // (2560 rows in 3 chunks over up to 9000 keys: 233 us in one range, 355 us in
 // the number that evened the waves).
@@ -141,7 +144,11 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // bf16 prompts and prefixes run on the tensor cores.
 bool on_tensor_cores(int dtype, int mode) { return dtype == COLIBRI_DTYPE_BF16 && mode != kAttnSuffix; }
 
-// (one tensor-core CTA per SM, two of the CUDA-core kernel)
+// The slots: one tensor-core CTA per SM.  Two of the CUDA-core kernel, which is what an
+// SM holds at d 64 (101 KB of shared memory); at d 128 it holds one (183 KB), but two
+// waves of shorter ranges take less than one of longer: 64 rows of 16 heads over 1024
+// keys 25 us instead of 33, 600 packed rows 71 instead of 82, 200 rows over a prefix of
+// 4096 248 instead of 291 (8 rows of group 64 over 4000 keys 61 instead of 40).
 int splits_for(const AttnArgs& a, const colibri_kv_pages_t* kv, int64_t keys) {
     const bool tc = on_tensor_cores(kv->dtype, a.mode);
     return tc ? choose_splits(attn_tc_items(a) * kv->n_kv_heads, keys, kSms, 128)

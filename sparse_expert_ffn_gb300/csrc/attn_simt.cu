@@ -11,7 +11,8 @@
 // instruction leaves no issue slots for the shared-memory reads; the next keys
 // are copied during the products.  Prompts are bound by the f32 pipes and the
 // shared-memory reads that feed them (4 x 4 products per thread, 256 threads:
-// 1721 rows of 16 heads 123 us; 8 x 4, 128 threads, 132 us: too few warps).
+// 1721 rows of 16 heads of 64 take 126 us, of 128 188 us; 8 x 4, 128 threads, 132 us at
+// d 64: too few warps).
 #include <cuda_runtime.h>
 
 #include "attn_common.cuh"
@@ -41,6 +42,7 @@ __device__ __forceinline__ void simt_tile(const AttnArgs& a, SimtSmem<ROWS, D>& 
     const int tid = threadIdx.x;
     if (tid < 32) {
         int b = 0, tile = 0;
+        // (in order of length from two CTAs per SM on, like the plan of the ranges: attn_host.cu)
         const bool ok = attn_item(a, blockIdx.x / a.hkv, a.group, ROWS, gridDim.x * gridDim.y > 304, &b, &tile);
         int end = 0;
         if (ok && a.mode == kAttnPrefix)
