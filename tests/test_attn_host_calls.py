@@ -78,7 +78,7 @@ B = Args.BASE
 @pytest.mark.parametrize("o,ok", [(5 * B + 1024, True), (5 * B + 4096 - 1024, True), (5 * B - 1024, True),
                                   (9 * B, True), (5 * B + 512, False), (5 * B + 1008, False), (5 * B, False),
                                   (5 * B + 4096 - 512, False), (5 * B - 512, False), (5 * B + 4096 * 9 + 512, False),
-                                  (5 * B + 4096 * 10, True), (2 * B + 64, False), (B - 10 * 4096 + 3072, True),
+                                  (5 * B + 4096 * 10, True), (2 * B + 64, False), (B - 9 * 4096 - 1024, True),
                                   (B - 16, False)])
 def test_outputs_between_the_columns_of_q(sef, o, ok):  # noqa: F811
     """10 rows of q, 1024 bytes each, 4096 bytes apart, the cache at B and 2 B: o may
@@ -91,7 +91,7 @@ def test_outputs_between_the_columns_of_q(sef, o, ok):  # noqa: F811
         assert Args(sef, seq_start=None, n_seqs=10, **kw).decode() == 1
 
 
-@pytest.mark.parametrize("qo,stride,ok", [(5 * B + 2048, 2048, True), (5 * B + 3072, 2048, True), (5 * B, 2048, True),
+@pytest.mark.parametrize("qo,stride,ok", [(5 * B + 2048, 2048, True), (5 * B + 2560, 2048, True), (5 * B, 2048, True),
                                           (9 * B, 512, True), (5 * B + 1024, 2048, False), (5 * B + 16, 2048, False),
                                           (5 * B + 1536, 2048, False), (5 * B + 2048 - 16, 2048, False),
                                           (5 * B + 3088, 2048, False), (5 * B + 2048, 512, False), (5 * B, 512, False),
