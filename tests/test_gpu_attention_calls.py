@@ -287,3 +287,81 @@ def test_scores_that_are_all_minus_infinity(A, dtype):
     assert torch.equal(out[170:], packed.v[170].repeat_interleave(2, 0).expand(130, 4, 64))
     # 64 * 0.25 / 8, through log2(e) and ln 2 of 24 bits each
     assert ((lse[170:].double() - 2.0).abs() <= 4 * U * 2.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_rows_beyond_32_bits(A, dtype):
+    """270000 rows of 64 heads: q and the output have more than 2^31 elements.  The last
+    sequences against the oracle, and against the same rows by themselves."""
+    n, count, hq, d = 900, 300, 64, 128
+    tail = Problem([(n, n)], hq, 1, d, dtype, 0, seed=21)
+    dev, rows = tail.q.device, n * count
+    assert rows * hq * d > 1 << 31
+    q = torch.zeros(rows, hq, d, dtype=tail.dt, device=dev)
+    k, v = (torch.zeros(rows, 1, d, dtype=tail.dt, device=dev) for _ in range(2))
+    q[-n:], k[-n:], v[-n:] = tail.q, tail.k, tail.v
+    q[:n], k[:n], v[:n] = tail.q, tail.k, tail.v
+    sq = A.Sequences(torch.arange(0, rows + 1, n, dtype=torch.int32, device=dev))
+    lse = torch.empty(rows, hq, device=dev)
+    out = A.attention_prompt(sq, q, k, v, lse=lse)
+    assert torch.equal(out[-n:], out[:n]) and torch.equal(lse[-n:], lse[:n])
+    tail.check(out[-n:], lse[-n:], True, rows=np.array([0, 1, 127, 128, 500, n - 1]))
+    assert (out[n:-n] == 0).all()
+    del out
+    f, _ = A.rope_frequencies(d)
+    rope = A.Rope(f.to(dev))
+    got, gk = A.qk_norm_rope(sq, q, k, rope=rope, q_out=q)         # in place
+    want, wk = A.qk_norm_rope(seqs(A, tail, paged=False), tail.q, tail.k, rope=rope)
+    assert torch.equal(got[-n:], want) and torch.equal(gk[-n:], wk) and torch.equal(got[:n], want)
+    del q, got, gk, k, v, lse
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d", [("bf16", 8, 2, 128), ("bf16", 16, 16, 64), ("fp32", 8, 2, 64)])
+def test_steps_behind_each_other_see_what_was_just_written(A, dtype, hq, hkv, d):
+    """300 decode steps over a prefix without a wait between them: lengths, queries,
+    keys and tables of every step were written just before it, by small kernels and by
+    the append.  The bits of the same steps with a wait after every call."""
+    steps, count, prefix, page = 300, 5, 256, 16
+    g = torch.Generator().manual_seed(5)
+    p = Problem([(1, prefix + steps + 40)] * count, hq, hkv, d, dtype, page, prefix=prefix, seed=6)
+    dev = p.q.device
+    new = lambda h: torch.randn(steps, count, h, d, generator=g).to(p.dt).to(dev)  # noqa: E731
+    qs, ks, vs = new(hq), new(hkv), new(hkv)
+    first = torch.tensor([prefix + 3 * b for b in range(count)], dtype=torch.int32, device=dev)
+    f, _ = A.rope_frequencies(d)
+    rope = A.Rope(f.to(dev))
+    before = p.kp.clone(), p.vp.clone()
+    shuffled = torch.randperm(count, generator=g).to(dev)
+
+    def run(wait):
+        p.kp.copy_(before[0]), p.vp.copy_(before[1])
+        kv, table = first.clone(), p.table.clone()
+        q, k, v = (torch.empty_like(x[0]) for x in (qs, ks, vs))
+        cache, sq = A.PagedKVCache(p.kp, p.vp), A.Sequences(None, kv, table)
+        out = torch.empty(steps, count, hq, d, dtype=p.dt, device=dev)
+        lse = torch.empty(steps, count, hq, device=dev)
+        sync = torch.cuda.synchronize if wait else (lambda: None)
+        sync()
+        for s in range(steps):
+            kv.add_(1), sync()
+            if s % 7 == 3:                                         # the sequences change places
+                table.copy_(table[shuffled]), sync()
+                kv.copy_(kv[shuffled]), sync()
+            for to, x in ((q, qs), (k, ks), (v, vs)):
+                to.copy_(x[s]), sync()
+            A.append_qkv(cache, sq, q, k, v, rope=rope, q_out=q), sync()
+            A.attention_decode(cache, sq, q, prefix_len=prefix, prefix_table=p.prefix_table, out=out[s], lse=lse[s])
+            sync()
+        return out, lse, p.kp.clone()
+
+    want = run(True)
+    got = run(False)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()                                 # (no gaps between the launches)
+    with torch.cuda.graph(graph):
+        got = run(False)
+    for _ in range(5):
+        [x.fill_(0) for x in got]
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
