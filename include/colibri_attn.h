@@ -166,6 +166,41 @@ colibri_status_t colibri_qk_norm_rope(const colibri_seqs_t* seqs, const colibri_
                                       void* stream);
 
 /*
+ * Rotary positions of several axes, as the tokens of images and video have (time,
+ * height, width): the position of row r of the call on axis x is
+ * at[x * axis_stride + r], any int32, and pair i of a head turns by
+ * at[axis[i] * axis_stride + r] * freq[i].  axis NULL: every pair by axis 0; an axis[i]
+ * of n_axes or more counts as n_axes - 1.  n_axes is 1 to 8, axis_stride at least
+ * n_rows where there are several.  Places in the cache follow from the lengths as
+ * ever.  Arrays are read on the device.
+ */
+typedef struct {
+    const int32_t* at;     /* [n_axes][n_rows] device */
+    const uint8_t* axis;   /* [rot_dim / 2] device, or NULL */
+    int64_t axis_stride;
+    int32_t n_axes;
+} colibri_positions_t;
+
+/*
+ * colibri_append_qkv_at, colibri_qk_norm_rope_at - colibri_append_qkv and
+ * colibri_qk_norm_rope with positions of their own for the rows (rope given);
+ * positions NULL: those that follow from the lengths.
+ */
+colibri_status_t colibri_append_qkv_at(const colibri_kv_pages_t* cache, const colibri_seqs_t* seqs,
+                                       const colibri_rope_t* rope, const colibri_positions_t* positions,
+                                       int32_t n_q_heads, const void* q, int64_t q_stride, const void* k,
+                                       int64_t k_stride, const void* v, int64_t v_stride,
+                                       const void* q_norm, const void* k_norm, float eps, void* q_out,
+                                       int64_t q_out_stride, void* stream);
+colibri_status_t colibri_qk_norm_rope_at(const colibri_seqs_t* seqs, const colibri_rope_t* rope,
+                                         const colibri_positions_t* positions, int32_t n_q_heads,
+                                         int32_t n_kv_heads, int32_t head_dim, int32_t dtype,
+                                         const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                         const void* q_norm, const void* k_norm, float eps, void* q_out,
+                                         int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                                         void* stream);
+
+/*
  * colibri_attention_prompt - for row i of n of sequence b and query head h
  *   o = sum_j w_j v_j,  w = softmax_j(scale * q . k_j)
  * over the keys j < kv_len[b] (causal == 0) or j <= kv_len[b] - n + i (causal
@@ -237,6 +272,88 @@ colibri_status_t colibri_attention_check(void* stream);
  * COLIBRI_TEST_STALL_TMA said at the process's first attention call.
  */
 colibri_status_t colibri_attention_waits(uint64_t limit_ns, int32_t stall);
+
+/*
+ * A cache held in 8 bits, for bf16 rows: a key or value element is code * scale, with
+ * one scale for each block of `block` tokens of each key head.  Codes lie as the
+ * elements of colibri_kv_pages_t do (strides in bytes, multiples of 16); the scale of
+ * block j of head h of page p is at [(p * n_kv_heads + h) * (page_size / block) + j]
+ * of k_scale and of v_scale.
+ *   code   E4M3 numbers, or INT8 whole numbers
+ *   block  16, 32 or 64, at most page_size
+ * page_size is a power of two from 16 to 65536.  Attention takes any codes and any
+ * finite scales; an E4M3 code that is no number (0x7f, 0xff) must not stand where a
+ * row sees it.  What stands behind a sequence's last key may be anything, the scale of
+ * a block without keys included.
+ */
+typedef enum { COLIBRI_CODE_E4M3 = 0, COLIBRI_CODE_INT8 = 1 } colibri_code_t;
+
+typedef struct {
+    void* k;               /* device */
+    void* v;               /* device */
+    float* k_scale;        /* device */
+    float* v_scale;        /* device */
+    int64_t page_stride;
+    int64_t head_stride;
+    int64_t row_stride;
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t code;          /* colibri_code_t */
+    int32_t block;
+} colibri_kv_pages8_t;
+
+/*
+ * colibri_append_qkv8 - colibri_append_qkv(_at) of bf16 rows into such a cache.  q' goes
+ * to q_out in bf16; k' and v go to their places as codes, rounded once from float32:
+ *   code = round(x * (1 / scale)), to nearest, ties to even.
+ * Of the elements x that the call brings to a block, let m be the largest magnitude.
+ * A block that holds earlier rows of the sequence keeps its scale where m <= largest
+ * code * scale (448, 127).  Otherwise its scale becomes the smallest power of two 2^e,
+ * e >= -100, with m <= largest code * 2^e, and the codes of its earlier rows, if it has
+ * any, become round(code * (old scale / scale)).  A block of a head that is given an
+ * element that is not finite gets the scale NaN, and all its values are NaN until a
+ * call writes the block from its first row on.
+ * Blocks of the cache that get no row, and codes behind the call's last row, stay as
+ * they are.  No two sequences of a call may append to one page.
+ */
+colibri_status_t colibri_append_qkv8(const colibri_kv_pages8_t* cache, const colibri_seqs_t* seqs,
+                                     const colibri_rope_t* rope, const colibri_positions_t* positions,
+                                     int32_t n_q_heads, const void* q, int64_t q_stride, const void* k,
+                                     int64_t k_stride, const void* v, int64_t v_stride,
+                                     const void* q_norm, const void* k_norm, float eps, void* q_out,
+                                     int64_t q_out_stride, void* stream);
+
+/*
+ * colibri_values8 - the values of pages, code * scale in bf16: of page pages[i] (pages
+ * [n_pages] device; NULL: page i) into k_out and v_out [n_pages, n_kv_heads, page_size,
+ * head_dim].  An id that no page has gives zeros.
+ */
+colibri_status_t colibri_values8(const colibri_kv_pages8_t* cache, const int32_t* pages, int32_t n_pages,
+                                 void* k_out, void* v_out, void* stream);
+
+/*
+ * colibri_attention_prompt8, colibri_attention_decode8 - colibri_attention_prompt over
+ * pages (seq_start, page_table and kv_len given) and colibri_attention_decode over an
+ * 8-bit cache; q and o are bf16.
+ */
+colibri_status_t colibri_attention_prompt8_workspace(const colibri_kv_pages8_t* cache,
+                                                     const colibri_seqs_t* seqs, int32_t n_q_heads,
+                                                     size_t* bytes);
+colibri_status_t colibri_attention_prompt8(const colibri_kv_pages8_t* cache, const colibri_seqs_t* seqs,
+                                           int32_t n_q_heads, const void* q, int64_t q_stride,
+                                           float scale, int32_t causal, void* o, int64_t o_stride,
+                                           float* lse, void* workspace, size_t workspace_bytes,
+                                           void* stream);
+colibri_status_t colibri_attention_decode8_workspace(const colibri_kv_pages8_t* cache,
+                                                     const colibri_seqs_t* seqs, int32_t n_q_heads,
+                                                     int32_t prefix_len, size_t* bytes);
+colibri_status_t colibri_attention_decode8(const colibri_kv_pages8_t* cache, const colibri_seqs_t* seqs,
+                                           int32_t n_q_heads, const void* q, int64_t q_stride,
+                                           float scale, int32_t prefix_len, const int32_t* prefix_table,
+                                           void* o, int64_t o_stride, float* lse, void* workspace,
+                                           size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -6,6 +6,7 @@ Definitions, one sequence or one head at a time:
   (linear, ntk: theta raised; yarn: by parts, Peng et al., 2023);
 * ``norm_rotate``: RMSNorm of each head, then the rotation of its pairs, the
   pair (a, b) taken as the complex number a + i b times e^(i t f);
+* ``nearest_code``, ``code_step``, ``fitting_scale``: the numbers of an 8-bit cache;
 * ``attend``: softmax(scale q k^T) v over the first ``limit`` keys of each row,
   zeros and a log-sum of -inf for a row without keys.
 """
@@ -36,14 +37,15 @@ def rope_frequencies(rot, theta=10000.0, scaling="none", factor=1.0, trained=409
 
 
 def norm_rotate(x, pos, freq=None, style="half", mscale=1.0, weight=None, eps=0.0):
-    """x [n, heads, d] at positions pos [n]."""
+    """x [n, heads, d] at positions pos [n], or [n, pairs]: one for each pair."""
     x = np.array(x, dtype=np.float64)
     if weight is not None:
         x = x / np.sqrt((x ** 2).mean(-1, keepdims=True) + eps) * weight
     if freq is None:
         return x
     half = len(freq)
-    turn = mscale * np.exp(1j * np.asarray(pos, dtype=np.float64)[:, None] * freq)[:, None, :]
+    pos = np.asarray(pos, dtype=np.float64)
+    turn = mscale * np.exp(1j * (pos if pos.ndim == 2 else pos[:, None]) * freq)[:, None, :]
     a, b = (x[..., :half], x[..., half:2 * half]) if style == "half" else \
         (x[..., 0:2 * half:2], x[..., 1:2 * half:2])
     z = (a + 1j * b) * turn
@@ -52,6 +54,32 @@ def norm_rotate(x, pos, freq=None, style="half", mscale=1.0, weight=None, eps=0.
     else:
         x[..., 0:2 * half:2], x[..., 1:2 * half:2] = z.real, z.imag
     return x
+
+
+CODE_MOST = {"e4m3": 448.0, "int8": 127.0}
+
+
+def code_step(y, code):
+    """The distance of neighbouring codes around y."""
+    y = np.abs(np.asarray(y, dtype=np.float64))
+    if code == "int8":
+        return np.ones_like(y)
+    return np.exp2(np.maximum(np.floor(np.log2(np.maximum(y, 2.0 ** -20))), -6.0) - 3.0)
+
+
+def nearest_code(y, code):
+    """y rounded to the code's numbers, ties to even."""
+    y = np.asarray(y, dtype=np.float64)
+    step = code_step(y, code)
+    return np.rint(y / step) * step
+
+
+def fitting_scale(most, code):
+    """The smallest power of two from 2^-100 on that codes reach `most` with."""
+    e = -100
+    while CODE_MOST[code] * 2.0 ** e < most:
+        e += 1
+    return 2.0 ** e
 
 
 def attend(q, k, v, limit, scale):

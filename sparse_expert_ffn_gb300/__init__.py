@@ -57,6 +57,20 @@ class ColibriRope(ctypes.Structure):
                 ("mscale", ctypes.c_float)]
 
 
+class ColibriPositions(ctypes.Structure):
+    _fields_ = [("at", ctypes.c_void_p), ("axis", ctypes.c_void_p), ("axis_stride", ctypes.c_int64),
+                ("n_axes", ctypes.c_int32)]
+
+
+class ColibriKVPages8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("code", ctypes.c_int32),
+                ("block", ctypes.c_int32)]
+
+
 class ColibriError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -72,6 +86,7 @@ def _load():
     P, I32, U64P = ctypes.c_void_p, ctypes.c_int32, ctypes.POINTER(ctypes.c_uint64)
     I64, F32, F64, SZ = ctypes.c_int64, ctypes.c_float, ctypes.c_double, ctypes.c_size_t
     KV, SQ, RP, SZP = (ctypes.POINTER(t) for t in (ColibriKVPages, ColibriSeqs, ColibriRope, SZ))
+    K8, PS = ctypes.POINTER(ColibriKVPages8), ctypes.POINTER(ColibriPositions)
     sig = {
         "colibri_init": ([ctypes.POINTER(ColibriConfig), P, P, P, P, P, ctypes.c_int,
                           ctypes.POINTER(P)], I32),
@@ -100,6 +115,15 @@ def _load():
         "colibri_append_qkv": ([KV, SQ, RP, I32, P, I64, P, I64, P, I64, P, P, F32, P, I64, P], I32),
         "colibri_qk_norm_rope": ([SQ, RP, I32, I32, I32, I32, P, I64, P, I64, P, P, F32, P, I64, P, I64,
                                   P], I32),
+        "colibri_append_qkv_at": ([KV, SQ, RP, PS, I32, P, I64, P, I64, P, I64, P, P, F32, P, I64, P], I32),
+        "colibri_qk_norm_rope_at": ([SQ, RP, PS, I32, I32, I32, I32, P, I64, P, I64, P, P, F32, P, I64, P,
+                                     I64, P], I32),
+        "colibri_append_qkv8": ([K8, SQ, RP, PS, I32, P, I64, P, I64, P, I64, P, P, F32, P, I64, P], I32),
+        "colibri_values8": ([K8, P, I32, P, P, P], I32),
+        "colibri_attention_prompt8_workspace": ([K8, SQ, I32, SZP], I32),
+        "colibri_attention_prompt8": ([K8, SQ, I32, P, I64, F32, I32, P, I64, P, P, SZ, P], I32),
+        "colibri_attention_decode8_workspace": ([K8, SQ, I32, I32, SZP], I32),
+        "colibri_attention_decode8": ([K8, SQ, I32, P, I64, F32, I32, P, P, I64, P, P, SZ, P], I32),
         "colibri_attention_prompt_workspace": ([KV, SQ, I32, SZP], I32),
         "colibri_attention_prompt": ([KV, SQ, I32, P, I64, F32, I32, P, I64, P, P, SZ, P], I32),
         "colibri_attention_decode_workspace": ([KV, SQ, I32, I32, SZP], I32),
@@ -128,6 +152,9 @@ _C_NAMES = ("colibri_init", "colibri_init_int8", "colibri_quantize_int8_block64"
             "colibri_attention_prompt_workspace", "colibri_attention_prompt",
             "colibri_attention_decode_workspace", "colibri_attention_decode",
             "colibri_attention_check", "colibri_attention_waits",
+            "colibri_append_qkv_at", "colibri_qk_norm_rope_at", "colibri_append_qkv8", "colibri_values8",
+            "colibri_attention_prompt8_workspace", "colibri_attention_prompt8",
+            "colibri_attention_decode8_workspace", "colibri_attention_decode8",
             "colibri_free")
 
 

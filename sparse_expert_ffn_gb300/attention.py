@@ -11,6 +11,8 @@ and run on the tensors' device and its current stream (or ``stream``):
 * :func:`attention_prompt`, :func:`attention_prompt_paged`: packed sequences of
   different lengths, grouped heads, causal or full;
 * :func:`attention_decode`: one row per sequence, with a shared prefix;
+* a :class:`PagedKVCache8` in the place of a :class:`PagedKVCache`: the same over
+  a cache held in 8 bits with a scale for each block of tokens and head;
 * :func:`check`: whether a kernel's bounded wait has given up.
 
 Results carry no gradient: the operators have no backward pass, and inputs that
@@ -22,7 +24,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import Optional
+from typing import Optional, Union
 
 import torch
 
@@ -32,7 +34,10 @@ _STYLE = {"half": 0, "interleaved": 1}
 _SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 _DTYPE = {torch.float32: _sef.DTYPE_FP32, torch.bfloat16: _sef.DTYPE_BF16}
 
+_CODE = {torch.float8_e4m3fn: 0, torch.int8: 1}
+
 KVPages, Seqs, RopeArgs = _sef.ColibriKVPages, _sef.ColibriSeqs, _sef.ColibriRope
+KVPages8, Positions = _sef.ColibriKVPages8, _sef.ColibriPositions
 
 
 def _int32(t, name, dim, device=None):
@@ -57,17 +62,46 @@ def rope_frequencies(rot_dim: int, theta: float = 10000.0, scaling: str = "none"
     return freq, mscale.value
 
 
+def rope_axes(sections, interleaved: bool = False):
+    """The axis that each pair of a head turns by (uint8 CPU tensor, for
+    :class:`Rope`), sections[x] pairs by axis x: runs of pairs, or with
+    ``interleaved`` the axes in turn while they have pairs left."""
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= 8 or min(left) < 0:
+        raise ValueError("sections must be 1 to 8 numbers of pairs")
+    if not interleaved:
+        return torch.tensor([x for x, n in enumerate(left) for _ in range(n)], dtype=torch.uint8)
+    order = []
+    while any(left):
+        for x, n in enumerate(left):
+            if n:
+                order.append(x)
+                left[x] -= 1
+    return torch.tensor(order, dtype=torch.uint8)
+
+
 class Rope:
     """Rotary positions: ``freq`` [rot_dim / 2] float64 on the GPU (radians per
     position), pairing ``style`` "half" or "interleaved", ``mscale`` the factor
-    of cos and sin."""
+    of cos and sin.  ``axes`` [rot_dim / 2] uint8 on the GPU (:func:`rope_axes`):
+    the axis of the call's ``positions`` that each pair turns by."""
 
-    def __init__(self, freq, style: str = "half", mscale: float = 1.0):
+    def __init__(self, freq, style: str = "half", mscale: float = 1.0, axes=None):
         if freq.dtype != torch.float64 or freq.dim() != 1 or not freq.is_cuda or not freq.is_contiguous():
             raise ValueError("freq must be a contiguous CUDA float64 vector")
+        if axes is not None and (axes.dtype != torch.uint8 or axes.shape != freq.shape or
+                                 axes.device != freq.device or not axes.is_contiguous()):
+            raise ValueError("axes must be a contiguous uint8 vector of freq's length on its device")
+        self.axes = axes
         self.freq, self.device = freq, freq.device
         self._c = RopeArgs(freq.data_ptr(), 2 * freq.numel(), _STYLE[style], float(mscale))
         self._ref = ctypes.byref(self._c)
+
+
+def _pages4(k, v):
+    if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.stride(3) != 1:
+        raise ValueError("k and v must be [pages, kv_heads, page_size, head_dim] with equal strides "
+                         "and a contiguous last dimension")
 
 
 class PagedKVCache:
@@ -76,10 +110,11 @@ class PagedKVCache:
     ``transpose(1, 2)`` of [pages, page_size, kv_heads, head_dim] storage
     serves as well).  The program owns the tensors and hands out the pages."""
 
+    _append, _append_at = "colibri_append_qkv", "colibri_append_qkv_at"
+    _prompt, _decode = "colibri_attention_prompt", "colibri_attention_decode"
+
     def __init__(self, k, v):
-        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.stride(3) != 1:
-            raise ValueError("k and v must be [pages, kv_heads, page_size, head_dim] with equal strides "
-                             "and a contiguous last dimension")
+        _pages4(k, v)
         if k.dtype not in _DTYPE or v.dtype != k.dtype or not k.is_cuda or v.device != k.device:
             raise ValueError("k and v must be float32 or bfloat16 tensors of one CUDA device")
         self.k, self.v, self.dtype, self.device = k, v, k.dtype, k.device
@@ -93,6 +128,60 @@ class PagedKVCache:
               dtype=torch.bfloat16, device="cuda"):
         shape = (num_pages, n_kv_heads, page_size, head_dim)
         return cls(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device))
+
+
+class PagedKVCache8:
+    """A cache held in 8 bits, for bfloat16 rows: ``k`` and ``v`` as of
+    :class:`PagedKVCache`, float8_e4m3fn or int8 codes, and the scales ``k_scale``
+    and ``v_scale`` [pages, kv_heads, page_size / block] float32, contiguous, one
+    for each block of 16, 32 or 64 tokens of a key head (element = code * scale).
+    :func:`append_qkv` chooses the scales (``include/colibri_attn.h`` says how)."""
+
+    _append = _append_at = "colibri_append_qkv8"
+    _prompt, _decode = "colibri_attention_prompt8", "colibri_attention_decode8"
+
+    def __init__(self, k, v, k_scale, v_scale):
+        _pages4(k, v)
+        if k.dtype not in _CODE or v.dtype != k.dtype or not k.is_cuda or v.device != k.device:
+            raise ValueError("k and v must be float8_e4m3fn or int8 tensors of one CUDA device")
+        for t in (k_scale, v_scale):
+            if t.dim() != 3 or t.shape[:2] != k.shape[:2] or t.shape != k_scale.shape or t.shape[2] == 0 or \
+                    k.shape[2] % t.shape[2] or t.dtype != torch.float32 or t.device != k.device or not t.is_contiguous():
+                raise ValueError("k_scale and v_scale must be contiguous [pages, kv_heads, page_size / block] "
+                                 "float32 tensors on the codes' device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.dtype, self.code_dtype, self.device = torch.bfloat16, k.dtype, k.device
+        self.num_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
+        self.block = self.page_size // k_scale.shape[2]
+        self._c = KVPages8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k.stride(0), k.stride(1),
+                           k.stride(2), k.shape[0], k.shape[2], k.shape[1], k.shape[3], _CODE[k.dtype], self.block)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, n_kv_heads: int, head_dim: int, block: int = 16,
+              dtype=torch.float8_e4m3fn, device="cuda"):
+        shape, scales = (num_pages, n_kv_heads, page_size, head_dim), (num_pages, n_kv_heads, page_size // block)
+        return cls(*(torch.empty(shape, dtype=dtype, device=device) for _ in range(2)),
+                   *(torch.empty(scales, dtype=torch.float32, device=device) for _ in range(2)))
+
+    def values(self, pages=None, *, out=None, stream=None):
+        """What the pages hold, code * scale in bfloat16: (k, v), each [n, kv_heads,
+        page_size, head_dim], of ``pages`` [n] (int32 CUDA tensor; default: all) into
+        ``out`` (two contiguous tensors; new ones by default)."""
+        if pages is not None:
+            _int32(pages, "pages", 1, self.device)
+        n = self.num_pages if pages is None else pages.shape[0]
+        shape = (n, self.n_kv_heads, self.page_size, self.head_dim)
+        if out is None:
+            out = tuple(_empty(shape, self.dtype, self.device, stream) for _ in range(2))
+        for t in out:
+            if t.shape != shape or t.dtype != self.dtype or t.device != self.device or not t.is_contiguous():
+                raise ValueError(f"out must be two contiguous {list(shape)} bfloat16 tensors on {self.device}")
+        k, v = out
+        if n:
+            _on(self.device, _sef.library().colibri_values8, "colibri_values8", self._ref, _sef._ptr(pages), n,
+                k.data_ptr(), v.data_ptr(), _stream(stream, self.device))
+        return k, v
 
 
 class Sequences:
@@ -201,16 +290,34 @@ def _rope_ref(rope, device):
     return rope._ref
 
 
+def _positions_ref(positions, rope, rows, device):
+    """The C description of a call's positions."""
+    if positions is None:
+        return None
+    if rope is None:
+        raise ValueError("positions need a rope")
+    p = positions if positions.dim() == 2 else positions.unsqueeze(0)
+    if p.dtype != torch.int32 or p.dim() != 2 or p.shape[1] != rows or not 1 <= p.shape[0] <= 8 or \
+            p.device != device or (rows > 1 and p.stride(1) != 1):
+        raise ValueError(f"positions must be an int32 [axes, {rows}] (or [{rows}]) tensor on {device}, 1 to 8 axes, "
+                         "rows contiguous")
+    stride = p.stride(0) if p.shape[0] > 1 else rows
+    return ctypes.byref(Positions(p.data_ptr(), _sef._ptr(rope.axes), stride, p.shape[0]))
+
+
 def _rows3(q):
     if q.dim() != 3 or q.dtype not in _DTYPE or not q.is_cuda:
         raise ValueError("q must be a [rows, heads, head_dim] float32 or bfloat16 CUDA tensor")
 
 
-def append_qkv(cache: PagedKVCache, seqs: Sequences, q, k, v, *, rope: Optional[Rope] = None, q_norm=None,
-               k_norm=None, eps: float = 1e-6, q_out=None, stream=None):
+def append_qkv(cache: Union[PagedKVCache, PagedKVCache8], seqs: Sequences, q, k, v, *, rope: Optional[Rope] = None, q_norm=None,
+               k_norm=None, eps: float = 1e-6, positions=None, q_out=None, stream=None):
     """Normalise (q_norm / k_norm given) and rotate (rope given) the rows' query
-    and key heads; keys and values go to their places in the cache, the queries
-    to ``q_out`` (a new tensor by default, may be ``q``), which is returned."""
+    and key heads; keys and values go to their places in the cache (of either
+    kind), the queries to ``q_out`` (a new tensor by default, may be ``q``), which is
+    returned.  ``positions`` [axes, rows] int32: the rows' rotary positions on each
+    axis of ``rope.axes`` (default: those that follow from the lengths); their
+    places in the cache follow from the lengths in any case."""
     _rows3(q)
     dev, dt, D, rows = cache.device, cache.dtype, cache.head_dim, q.shape[0]
     hq, hkv = q.shape[1], cache.n_kv_heads
@@ -218,19 +325,23 @@ def append_qkv(cache: PagedKVCache, seqs: Sequences, q, k, v, *, rope: Optional[
         raise ValueError(f"seqs must be on {dev}")
     if q_out is None:
         q_out = _empty((rows, hq, D), dt, dev, stream)
-    args = (_rope_ref(rope, dev), hq, q.data_ptr(), _same(q, "q", hq, D, dt, dev, rows),
+    where = _positions_ref(positions, rope, rows, dev)
+    args = (hq, q.data_ptr(), _same(q, "q", hq, D, dt, dev, rows),
             k.data_ptr(), _same(k, "k", hkv, D, dt, dev, rows), v.data_ptr(), _same(v, "v", hkv, D, dt, dev, rows),
             _norm(q_norm, "q_norm", D, dt, dev), _norm(k_norm, "k_norm", D, dt, dev), float(eps),
             q_out.data_ptr(), _same(q_out, "q_out", hq, D, dt, dev, rows))
     if rows == 0:
         return q_out
-    _on(dev, _sef.library().colibri_append_qkv, "colibri_append_qkv", cache._ref, seqs._rows(q), *args,
-        _stream(stream, dev))
+    how = (_rope_ref(rope, dev),)
+    name = cache._append
+    if where is not None or name == cache._append_at:
+        name, how = cache._append_at, (*how, where)
+    _on(dev, getattr(_sef.library(), name), name, cache._ref, seqs._rows(q), *how, *args, _stream(stream, dev))
     return q_out
 
 
 def qk_norm_rope(seqs: Sequences, q, k, *, rope: Optional[Rope] = None, q_norm=None, k_norm=None,
-                 eps: float = 1e-6, q_out=None, k_out=None, stream=None):
+                 eps: float = 1e-6, positions=None, q_out=None, k_out=None, stream=None):
     """:func:`append_qkv` for rows that go to no cache; returns (q_out, k_out)."""
     _rows3(q)
     dev, dt, D, rows, hq, hkv = q.device, q.dtype, q.shape[2], q.shape[0], q.shape[1], k.shape[1]
@@ -240,15 +351,18 @@ def qk_norm_rope(seqs: Sequences, q, k, *, rope: Optional[Rope] = None, q_norm=N
         q_out = _empty((rows, hq, D), dt, dev, stream)
     if k_out is None:
         k_out = _empty((rows, hkv, D), dt, dev, stream)
-    args = (_rope_ref(rope, dev), hq, hkv, D, _DTYPE[dt], q.data_ptr(), _same(q, "q", hq, D, dt, dev, rows),
+    where = _positions_ref(positions, rope, rows, dev)
+    args = (hq, hkv, D, _DTYPE[dt], q.data_ptr(), _same(q, "q", hq, D, dt, dev, rows),
             k.data_ptr(), _same(k, "k", hkv, D, dt, dev, rows),
             _norm(q_norm, "q_norm", D, dt, dev), _norm(k_norm, "k_norm", D, dt, dev), float(eps),
             q_out.data_ptr(), _same(q_out, "q_out", hq, D, dt, dev, rows),
             k_out.data_ptr(), _same(k_out, "k_out", hkv, D, dt, dev, rows))
     if rows == 0:
         return q_out, k_out
-    _on(dev, _sef.library().colibri_qk_norm_rope, "colibri_qk_norm_rope", seqs._rows(q), *args,
-        _stream(stream, dev))
+    name, how = "colibri_qk_norm_rope", (_rope_ref(rope, dev),)
+    if where is not None:
+        name, how = "colibri_qk_norm_rope_at", (*how, where)
+    _on(dev, getattr(_sef.library(), name), name, seqs._rows(q), *how, *args, _stream(stream, dev))
     return q_out, k_out
 
 
@@ -318,11 +432,11 @@ def _prompt(kv, kv_ref, seqs, q, scale, causal, out, lse, stream):
     if rows == 0:
         return out
     ref, lib, need = seqs._rows(q), _sef.library(), ctypes.c_size_t()
-    _sef._check(lib.colibri_attention_prompt_workspace(kv_ref, ref, hq, ctypes.byref(need)),
-                "colibri_attention_prompt_workspace")
+    name = kv._prompt
+    _sef._check(getattr(lib, name + "_workspace")(kv_ref, ref, hq, ctypes.byref(need)), name + "_workspace")
     ws = _workspace(need.value, dev, stream)
     _pass_on_waits()
-    _on(dev, lib.colibri_attention_prompt, "colibri_attention_prompt", kv_ref, ref, hq, q.data_ptr(), stride,
+    _on(dev, getattr(lib, name), name, kv_ref, ref, hq, q.data_ptr(), stride,
         D ** -0.5 if scale is None else float(scale), int(causal), out.data_ptr(), o_stride, lse_ptr,
         None if ws is None else ws.data_ptr(), need.value, _stream(stream, dev))
     return out
@@ -330,6 +444,8 @@ def _prompt(kv, kv_ref, seqs, q, scale, causal, out, lse, stream):
 
 class _Packed:
     """k and v rows [rows, kv_heads, head_dim] as one page."""
+
+    _prompt = "colibri_attention_prompt"
 
     def __init__(self, k, v):
         rows, hkv, D = k.shape
@@ -356,21 +472,22 @@ def attention_prompt(seqs: Sequences, q, k, v, *, scale: Optional[float] = None,
     return _prompt(kv, ctypes.byref(kv._c), seqs, q, scale, causal, out, lse, stream)
 
 
-def attention_prompt_paged(cache: PagedKVCache, seqs: Sequences, q, *, scale: Optional[float] = None,
+def attention_prompt_paged(cache: Union[PagedKVCache, PagedKVCache8], seqs: Sequences, q, *, scale: Optional[float] = None,
                            causal: bool = True, out=None, lse=None, stream=None):
     """:func:`attention_prompt` over a cache's pages (seqs with kv_len and
-    page_table): row i of n of sequence b stands at position kv_len[b] - n + i."""
+    page_table): row i of n of sequence b stands at position kv_len[b] - n + i.
+    The cache may be of either kind."""
     if seqs.page_table is None or seqs.kv_len is None:
         raise ValueError("seqs needs kv_len and page_table")
     return _prompt(cache, cache._ref, seqs, q, scale, causal, out, lse, stream)
 
 
-def attention_decode(cache: PagedKVCache, seqs: Sequences, q, *, prefix_len: int = 0, prefix_table=None,
+def attention_decode(cache: Union[PagedKVCache, PagedKVCache8], seqs: Sequences, q, *, prefix_len: int = 0, prefix_table=None,
                      scale: Optional[float] = None, out=None, lse=None, stream=None):
     """Attention of one row per sequence (q [B, heads, head_dim]) over its
     kv_len[b] keys.  The first prefix_len keys (a multiple of the page size) of
     every sequence are those of prefix_table [prefix_len / page_size], read once
-    for the batch."""
+    for the batch.  The cache may be of either kind."""
     _rows3(q)
     dev, rows, hq, D = q.device, q.shape[0], q.shape[1], q.shape[2]
     if seqs.page_table is None or seqs.kv_len is None or seqs.seq_start is not None:
@@ -390,11 +507,12 @@ def attention_decode(cache: PagedKVCache, seqs: Sequences, q, *, prefix_len: int
     if rows == 0:
         return out
     ref, lib, need = seqs._rows(q), _sef.library(), ctypes.c_size_t()
-    _sef._check(lib.colibri_attention_decode_workspace(cache._ref, ref, hq, int(prefix_len), ctypes.byref(need)),
-                "colibri_attention_decode_workspace")
+    name = cache._decode
+    _sef._check(getattr(lib, name + "_workspace")(cache._ref, ref, hq, int(prefix_len), ctypes.byref(need)),
+                name + "_workspace")
     ws = _workspace(need.value, dev, stream)
     _pass_on_waits()
-    _on(dev, lib.colibri_attention_decode, "colibri_attention_decode", cache._ref, ref, hq, q.data_ptr(), stride,
+    _on(dev, getattr(lib, name), name, cache._ref, ref, hq, q.data_ptr(), stride,
         D ** -0.5 if scale is None else float(scale), int(prefix_len), table, out.data_ptr(), o_stride, lse_ptr,
         None if ws is None else ws.data_ptr(), need.value, _stream(stream, dev))
     return out

@@ -89,6 +89,12 @@ struct AppendArgs {
     const void *q_norm, *k_norm;     // or null
     float eps;
     const double* freq;              // null: no rotation
+    // null: positions follow from the lengths; otherwise row r's on axis x is
+    // positions[x * axis_stride + r], and pair i turns by axis[i]'s (null: axis 0)
+    const int32_t* positions;
+    int64_t axis_stride;
+    const uint8_t* axis;
+    int n_axes;
     int rot_dim, interleaved;
     float mscale;
     const int32_t *seq_start, *kv_len, *table;
@@ -100,7 +106,28 @@ struct AppendArgs {
     void *k_out, *v_out;
     int64_t page_stride, head_stride, row_stride;
     int num_pages, page_shift;
+    // codes: scales [num_pages][hkv][page >> block_shift]
+    float *k_scale, *v_scale;
+    int block_shift;
 };
 cudaError_t launch_append(DType dt, int d, const AppendArgs& a, cudaStream_t s);
+// The same into pages of 8-bit codes (k_out, v_out; bf16 rows).
+cudaError_t launch_append8(bool int8, int d, const AppendArgs& a, cudaStream_t s);
+
+// Pages of 8-bit codes as bf16 [n_pages, hkv, page_size, d]; ids that no page has
+// give zeros.
+struct ValuesArgs {
+    const void *k, *v;
+    const float *k_scale, *v_scale;
+    int64_t page_stride, head_stride, row_stride;
+    int num_pages, page_size, page_shift, block_shift, hkv;
+    const int32_t* pages;            // [n_pages], null: 0 .. n_pages - 1
+    int n_pages;
+    void *k_out, *v_out;
+    int width, first, n_keys, base;
+    const int32_t* kv_len;
+    int32_t* table_out;
+};
+cudaError_t launch_values8(bool int8, int d, const ValuesArgs& a, cudaStream_t s);
 
 }  // namespace colibri

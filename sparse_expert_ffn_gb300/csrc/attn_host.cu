@@ -25,8 +25,10 @@ constexpr int kMaxSplits = 64;
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
-int elem_size(int dtype) { return dtype == COLIBRI_DTYPE_BF16 ? 2 : 4; }
-DType dtype_of(int dtype) { return dtype == COLIBRI_DTYPE_BF16 ? DType::BF16 : DType::F32; }
+constexpr int kCodes = -8;         // dtype of a view of 8-bit pages
+int elem_size(int dtype) { return dtype == COLIBRI_DTYPE_BF16 ? 2 : dtype == kCodes ? 1 : 4; }
+int rows_of(int dtype) { return dtype == kCodes ? (int)COLIBRI_DTYPE_BF16 : dtype; }      // dtype of q and o
+DType dtype_of(int dtype) { return rows_of(dtype) == COLIBRI_DTYPE_BF16 ? DType::BF16 : DType::F32; }
 
 // A row tensor [rows, heads, d] with `stride` elements from row to row.
 bool rows_ok(const void* p, int64_t stride, int heads, int d, int esz) {
@@ -110,6 +112,114 @@ colibri_status_t check_rope(const colibri_rope_t* r, int head_dim) {
         return COLIBRI_ERR_INVALID_ARG;
     return COLIBRI_OK;
 }
+
+colibri_status_t check_positions(const colibri_positions_t* p, const colibri_rope_t* rope, int n_rows) {
+    if (!p) return COLIBRI_OK;
+    if (!rope || p->n_axes < 1 || p->n_axes > 8 || ((uintptr_t)p->at & 3) || (n_rows > 0 && !p->at) ||
+        (p->n_axes > 1 && p->axis_stride < n_rows) || p->axis_stride >= ((int64_t)1 << 37))
+        return COLIBRI_ERR_INVALID_ARG;
+    return COLIBRI_OK;
+}
+
+void set_rope(AppendArgs& a, const colibri_rope_t* rope, const colibri_positions_t* p) {
+    if (!rope) return;
+    a.freq = rope->freq, a.rot_dim = rope->rot_dim, a.mscale = rope->mscale;
+    a.interleaved = rope->style == COLIBRI_ROPE_INTERLEAVED;
+    if (p) a.positions = p->at, a.axis_stride = p->axis_stride, a.axis = p->axis, a.n_axes = p->n_axes;
+}
+
+int shift_of(int n) {
+    int s = 0;
+    while ((1 << s) < n) ++s;
+    return s;
+}
+
+// 8-bit pages as pages whose elements are bytes.
+colibri_kv_pages_t view(const colibri_kv_pages8_t* c) {
+    return {c->k, c->v, c->page_stride, c->head_stride, c->row_stride, c->num_pages,
+            c->page_size, c->n_kv_heads, c->head_dim, kCodes};
+}
+int64_t scale_bytes(const colibri_kv_pages8_t* c) {
+    return (int64_t)c->num_pages * c->n_kv_heads * (c->page_size / c->block) * 4;
+}
+
+colibri_status_t check_kv8(const colibri_kv_pages8_t* c) {
+    if (!c) return COLIBRI_ERR_INVALID_ARG;
+    if (!c->k_scale || !c->v_scale || ((uintptr_t)c->k_scale & 3) || ((uintptr_t)c->v_scale & 3) || c->block <= 0 ||
+        (c->code != COLIBRI_CODE_E4M3 && c->code != COLIBRI_CODE_INT8))
+        return COLIBRI_ERR_INVALID_ARG;
+    colibri_status_t st = check_heads(c->n_kv_heads, c->n_kv_heads, c->head_dim, COLIBRI_DTYPE_BF16);
+    const colibri_kv_pages_t kv = view(c);
+    if (st == COLIBRI_OK) st = check_kv(&kv, true);
+    if (st != COLIBRI_OK) return st;
+    if ((c->block != 16 && c->block != 32 && c->block != 64) || c->block > c->page_size) return COLIBRI_ERR_UNSUPPORTED;
+    return COLIBRI_OK;
+}
+
+ValuesArgs values_args(const colibri_kv_pages8_t* c) {
+    ValuesArgs a{};
+    a.k = c->k, a.v = c->v, a.k_scale = c->k_scale, a.v_scale = c->v_scale;
+    a.page_stride = c->page_stride, a.head_stride = c->head_stride, a.row_stride = c->row_stride;
+    a.num_pages = c->num_pages, a.page_size = c->page_size, a.page_shift = shift_of(c->page_size);
+    a.block_shift = shift_of(c->block), a.hkv = c->n_kv_heads;
+    return a;
+}
+
+// The rows of an append.
+struct Projection {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const void *q_norm, *k_norm;
+    float eps;
+    void* q_out;
+    int64_t q_out_stride;
+};
+
+// Checks an append of rows of `dtype` and describes it; a->n_rows is 0 where there is
+// nothing to do.
+colibri_status_t check_append(const colibri_kv_pages_t* cache, int dtype, const colibri_seqs_t* seqs,
+                              const colibri_rope_t* rope, const colibri_positions_t* positions, int n_q_heads,
+                              const Projection& p, AppendArgs* out_args) {
+    if (!seqs || (seqs->n_seqs > 0 && (!seqs->page_table || !seqs->kv_len))) return COLIBRI_ERR_INVALID_ARG;
+    colibri_status_t st = check_heads(n_q_heads, cache->n_kv_heads, cache->head_dim, dtype);
+    if (st == COLIBRI_OK) st = check_seqs(seqs, n_q_heads);
+    if (st == COLIBRI_OK) st = check_kv(cache, true);
+    if (st == COLIBRI_OK) st = check_rope(rope, cache->head_dim);
+    if (st == COLIBRI_OK) st = check_positions(positions, rope, seqs->n_rows);
+    if (st != COLIBRI_OK) return st;
+    const int d = cache->head_dim, esz = elem_size(dtype), hkv = cache->n_kv_heads;
+    if (!rows_ok(p.q, p.q_stride, n_q_heads, d, esz) || !rows_ok(p.k, p.k_stride, hkv, d, esz) ||
+        !rows_ok(p.v, p.v_stride, hkv, d, esz) || !rows_ok(p.q_out, p.q_out_stride, n_q_heads, d, esz) ||
+        !aligned16(p.q_norm) || !aligned16(p.k_norm) || !(p.eps >= 0.f))
+        return COLIBRI_ERR_INVALID_ARG;
+    if (p.q_out == p.q && p.q_out_stride != p.q_stride) return COLIBRI_ERR_INVALID_ARG;
+    const Rows out = row_bytes(p.q_out, p.q_out_stride, n_q_heads, d, esz);
+    if ((p.q_out != p.q && clash(row_bytes(p.q, p.q_stride, n_q_heads, d, esz), out, seqs->n_rows)) ||
+        clash(row_bytes(p.k, p.k_stride, hkv, d, esz), out, seqs->n_rows) ||
+        clash(row_bytes(p.v, p.v_stride, hkv, d, esz), out, seqs->n_rows))
+        return COLIBRI_ERR_INVALID_ARG;
+    for (const void* pages : {(const void*)cache->k, (const void*)cache->v})
+        for (const Rows& r : {row_bytes(p.q, p.q_stride, n_q_heads, d, esz), row_bytes(p.k, p.k_stride, hkv, d, esz),
+                              row_bytes(p.v, p.v_stride, hkv, d, esz), out})
+            if (seqs->n_rows > 0 && overlap(pages, kv_extent(cache), r.p, r.extent(seqs->n_rows)))
+                return COLIBRI_ERR_INVALID_ARG;
+    if (seqs->n_rows == 0 || seqs->n_seqs == 0) return COLIBRI_OK;
+    AppendArgs& a = *out_args;
+    a.q = p.q, a.k = p.k, a.v = p.v;
+    a.q_stride = p.q_stride, a.k_stride = p.k_stride, a.v_stride = p.v_stride;
+    a.q_norm = p.q_norm, a.k_norm = p.k_norm, a.eps = p.eps;
+    set_rope(a, rope, positions);
+    a.seq_start = seqs->seq_start, a.kv_len = seqs->kv_len, a.table = seqs->page_table;
+    a.n_seqs = seqs->n_seqs, a.n_rows = seqs->n_rows, a.table_stride = seqs->table_stride;
+    a.hq = n_q_heads, a.hkv = hkv;
+    a.q_out = p.q_out, a.q_out_stride = p.q_out_stride;
+    a.k_out = cache->k, a.v_out = cache->v;
+    a.page_stride = cache->page_stride, a.head_stride = cache->head_stride;
+    a.row_stride = cache->row_stride, a.num_pages = cache->num_pages;
+    a.page_shift = shift_of(cache->page_size);
+    return COLIBRI_OK;
+}
+
 
 // How a call's keys are split: ranges of the shared prefix and of the
 // sequences' own keys, each leaving a partial row per (row, head).  shares: the
@@ -210,8 +320,7 @@ AttnArgs make_args(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq
     a.hq = hq, a.hkv = kv->n_kv_heads, a.group = hq / kv->n_kv_heads;
     a.table_stride = s->table_stride;
     a.num_pages = kv->num_pages, a.page_size = kv->page_size;
-    a.page_shift = 0;
-    while ((1 << a.page_shift) < kv->page_size) ++a.page_shift;
+    a.page_shift = shift_of(kv->page_size);
     a.scale_log2 = scale * kLog2e;
     a.splits = 1;
     a.wait_limit_ns = waits().limit_ns.load(std::memory_order_relaxed);
@@ -222,7 +331,7 @@ AttnArgs make_args(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq
 colibri_status_t check_attention(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq,
                                  const void* q, int64_t q_stride, float scale, const void* o,
                                  int64_t o_stride, const float* lse) {
-    const int esz = elem_size(kv->dtype), d = kv->head_dim;
+    const int esz = elem_size(rows_of(kv->dtype)), d = kv->head_dim;
     if (!rows_ok(q, q_stride, hq, d, esz) || !rows_ok(o, o_stride, hq, d, esz) || ((uintptr_t)lse & 3))
         return COLIBRI_ERR_INVALID_ARG;
     if (!(scale > 0.f) || !std::isfinite(scale * kLog2e)) return COLIBRI_ERR_INVALID_ARG;
@@ -295,7 +404,7 @@ bool countable(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int n_q_he
 
 colibri_status_t check_prompt(const colibri_kv_pages_t* kv, const colibri_seqs_t* seqs, int n_q_heads) {
     if (!kv || !seqs) return COLIBRI_ERR_INVALID_ARG;
-    colibri_status_t st = check_heads(n_q_heads, kv->n_kv_heads, kv->head_dim, kv->dtype);
+    colibri_status_t st = check_heads(n_q_heads, kv->n_kv_heads, kv->head_dim, rows_of(kv->dtype));
     if (st == COLIBRI_OK) st = check_seqs(seqs, n_q_heads);
     if (st == COLIBRI_OK) st = check_kv(kv, seqs->page_table != nullptr);
     if (st != COLIBRI_OK) return st;
@@ -311,13 +420,61 @@ colibri_status_t check_decode(const colibri_kv_pages_t* kv, const colibri_seqs_t
                               int prefix_len) {
     if (!kv || !seqs || seqs->seq_start || (seqs->n_seqs > 0 && (!seqs->page_table || !seqs->kv_len)))
         return COLIBRI_ERR_INVALID_ARG;
-    colibri_status_t st = check_heads(n_q_heads, kv->n_kv_heads, kv->head_dim, kv->dtype);
+    colibri_status_t st = check_heads(n_q_heads, kv->n_kv_heads, kv->head_dim, rows_of(kv->dtype));
     if (st == COLIBRI_OK) st = check_seqs(seqs, n_q_heads);
     if (st == COLIBRI_OK) st = check_kv(kv, true);
     if (st != COLIBRI_OK) return st;
     if (prefix_len < 0 || prefix_len % kv->page_size) return COLIBRI_ERR_INVALID_ARG;
     if (prefix_len > kMaxKeys || !countable(kv, seqs, n_q_heads) || !mappable(kv)) return COLIBRI_ERR_UNSUPPORTED;
     return COLIBRI_OK;
+}
+
+// o shares no byte with the scales.
+bool apart_from_scales(const colibri_kv_pages8_t* c, int hq, const void* o, int64_t o_stride, int rows) {
+    if (rows <= 0) return true;
+    const int64_t n = row_bytes(o, o_stride, hq, c->head_dim, 2).extent(rows);
+    return !overlap(c->k_scale, scale_bytes(c), o, n) && !overlap(c->v_scale, scale_bytes(c), o, n);
+}
+
+// Attention over 8-bit pages: the pages that the sequences (and the prefix) name as
+// bf16 pages in the workspace, then attention over those.
+struct Wide {
+    colibri_kv_pages_t kv;
+    colibri_seqs_t seqs;
+    int64_t own, shared;             // pages of the sequences, of the prefix
+    size_t table, pages;             // bytes: the tables, one of k and v
+    size_t bytes() const { return table + 2 * pages; }
+};
+colibri_status_t widen(const colibri_kv_pages8_t* c, const colibri_seqs_t* s, int prefix_len, Wide* w) {
+    const int hkv = c->n_kv_heads, d = c->head_dim;
+    w->own = (int64_t)s->n_seqs * s->table_stride, w->shared = prefix_len / c->page_size;
+    const int64_t n = w->own + w->shared, page = (int64_t)hkv * c->page_size * d;
+    if (n * hkv > INT32_MAX) return COLIBRI_ERR_UNSUPPORTED;
+    w->table = (size_t)(n * 4 + 255) & ~(size_t)255;
+    w->pages = (size_t)(n * page * 2 + 255) & ~(size_t)255;
+    w->kv = {c->k, c->v, page, (int64_t)c->page_size * d, d, (int32_t)std::max<int64_t>(n, 1),
+             c->page_size, hkv, d, COLIBRI_DTYPE_BF16};
+    w->seqs = *s;
+    return COLIBRI_OK;
+}
+cudaError_t run_widen(const colibri_kv_pages8_t* c, const int32_t* prefix_table, int prefix_len, Wide& w, uint8_t* ws,
+                      cudaStream_t s) {
+    ValuesArgs a = values_args(c);
+    w.kv.k = ws + w.table, w.kv.v = ws + w.table + w.pages;
+    const bool int8 = c->code == COLIBRI_CODE_INT8;
+    const int64_t per = (int64_t)c->n_kv_heads * c->page_size * c->head_dim * 2;
+    a.pages = w.seqs.page_table, a.n_pages = (int)w.own, a.width = w.seqs.table_stride, a.kv_len = w.seqs.kv_len;
+    a.first = prefix_len / c->page_size, a.table_out = reinterpret_cast<int32_t*>(ws);
+    a.k_out = w.kv.k, a.v_out = w.kv.v;
+    cudaError_t e = launch_values8(int8, c->head_dim, a, s);
+    w.seqs.page_table = a.table_out;
+    if (w.shared > 0 && e == cudaSuccess) {
+        a.pages = prefix_table, a.n_pages = a.width = (int)w.shared, a.kv_len = nullptr, a.n_keys = prefix_len;
+        a.first = 0, a.base = (int)w.own, a.table_out += w.own;
+        a.k_out = ws + w.table + w.own * per, a.v_out = ws + w.table + w.pages + w.own * per;
+        e = launch_values8(int8, c->head_dim, a, s);
+    }
+    return e;
 }
 
 }  // namespace
@@ -369,46 +526,70 @@ colibri_status_t colibri_append_qkv(const colibri_kv_pages_t* cache, const colib
                                     const void* v, int64_t v_stride, const void* q_norm,
                                     const void* k_norm, float eps, void* q_out,
                                     int64_t q_out_stride, void* stream) {
-    if (!cache || !seqs || (seqs->n_seqs > 0 && (!seqs->page_table || !seqs->kv_len))) return COLIBRI_ERR_INVALID_ARG;
-    colibri_status_t st = check_heads(n_q_heads, cache->n_kv_heads, cache->head_dim, cache->dtype);
-    if (st == COLIBRI_OK) st = check_seqs(seqs, n_q_heads);
-    if (st == COLIBRI_OK) st = check_kv(cache, true);
-    if (st == COLIBRI_OK) st = check_rope(rope, cache->head_dim);
-    if (st != COLIBRI_OK) return st;
-    const int d = cache->head_dim, esz = elem_size(cache->dtype), hkv = cache->n_kv_heads;
-    if (!rows_ok(q, q_stride, n_q_heads, d, esz) || !rows_ok(k, k_stride, hkv, d, esz) ||
-        !rows_ok(v, v_stride, hkv, d, esz) || !rows_ok(q_out, q_out_stride, n_q_heads, d, esz) ||
-        !aligned16(q_norm) || !aligned16(k_norm) || !(eps >= 0.f))
-        return COLIBRI_ERR_INVALID_ARG;
-    if (q_out == q && q_out_stride != q_stride) return COLIBRI_ERR_INVALID_ARG;
-    const Rows out = row_bytes(q_out, q_out_stride, n_q_heads, d, esz);
-    if ((q_out != q && clash(row_bytes(q, q_stride, n_q_heads, d, esz), out, seqs->n_rows)) ||
-        clash(row_bytes(k, k_stride, hkv, d, esz), out, seqs->n_rows) ||
-        clash(row_bytes(v, v_stride, hkv, d, esz), out, seqs->n_rows))
-        return COLIBRI_ERR_INVALID_ARG;
-    for (const void* p : {(const void*)cache->k, (const void*)cache->v})
-        for (const Rows& r : {row_bytes(q, q_stride, n_q_heads, d, esz), row_bytes(k, k_stride, hkv, d, esz),
-                              row_bytes(v, v_stride, hkv, d, esz), out})
-            if (seqs->n_rows > 0 && overlap(p, kv_extent(cache), r.p, r.extent(seqs->n_rows)))
-                return COLIBRI_ERR_INVALID_ARG;
-    if (seqs->n_rows == 0 || seqs->n_seqs == 0) return COLIBRI_OK;
+    return colibri_append_qkv_at(cache, seqs, rope, nullptr, n_q_heads, q, q_stride, k, k_stride, v, v_stride, q_norm,
+                                 k_norm, eps, q_out, q_out_stride, stream);
+}
+
+colibri_status_t colibri_append_qkv_at(const colibri_kv_pages_t* cache, const colibri_seqs_t* seqs,
+                                       const colibri_rope_t* rope, const colibri_positions_t* positions,
+                                       int32_t n_q_heads, const void* q, int64_t q_stride, const void* k,
+                                       int64_t k_stride, const void* v, int64_t v_stride,
+                                       const void* q_norm, const void* k_norm, float eps, void* q_out,
+                                       int64_t q_out_stride, void* stream) {
+    if (!cache) return COLIBRI_ERR_INVALID_ARG;
+    const Projection p = {q, k, v, q_stride, k_stride, v_stride, q_norm, k_norm, eps, q_out, q_out_stride};
     AppendArgs a{};
-    a.q = q, a.k = k, a.v = v;
-    a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
-    a.q_norm = q_norm, a.k_norm = k_norm, a.eps = eps;
-    if (rope) {
-        a.freq = rope->freq, a.rot_dim = rope->rot_dim, a.mscale = rope->mscale;
-        a.interleaved = rope->style == COLIBRI_ROPE_INTERLEAVED;
+    const colibri_status_t st = check_append(cache, cache->dtype, seqs, rope, positions, n_q_heads, p, &a);
+    if (st != COLIBRI_OK || a.n_rows == 0) return st;
+    return launched(launch_append(dtype_of(cache->dtype), cache->head_dim, a, (cudaStream_t)stream));
+}
+
+colibri_status_t colibri_append_qkv8(const colibri_kv_pages8_t* cache, const colibri_seqs_t* seqs,
+                                     const colibri_rope_t* rope, const colibri_positions_t* positions,
+                                     int32_t n_q_heads, const void* q, int64_t q_stride, const void* k,
+                                     int64_t k_stride, const void* v, int64_t v_stride,
+                                     const void* q_norm, const void* k_norm, float eps, void* q_out,
+                                     int64_t q_out_stride, void* stream) {
+    colibri_status_t st = check_kv8(cache);
+    if (st != COLIBRI_OK) return st;
+    const colibri_kv_pages_t kv = view(cache);
+    const Projection p = {q, k, v, q_stride, k_stride, v_stride, q_norm, k_norm, eps, q_out, q_out_stride};
+    AppendArgs a{};
+    st = check_append(&kv, COLIBRI_DTYPE_BF16, seqs, rope, positions, n_q_heads, p, &a);
+    if (st != COLIBRI_OK) return st;
+    const int d = kv.head_dim, hkv = kv.n_kv_heads;
+    for (const float* scale : {cache->k_scale, cache->v_scale})
+        for (const Rows& r : {row_bytes(q, q_stride, n_q_heads, d, 2), row_bytes(k, k_stride, hkv, d, 2),
+                              row_bytes(v, v_stride, hkv, d, 2), row_bytes(q_out, q_out_stride, n_q_heads, d, 2)})
+            if (seqs->n_rows > 0 && overlap(scale, scale_bytes(cache), r.p, r.extent(seqs->n_rows)))
+                return COLIBRI_ERR_INVALID_ARG;
+    if (a.n_rows == 0) return COLIBRI_OK;
+    a.k_scale = cache->k_scale, a.v_scale = cache->v_scale;
+    a.block_shift = shift_of(cache->block);
+    return launched(launch_append8(cache->code == COLIBRI_CODE_INT8, d, a, (cudaStream_t)stream));
+}
+
+colibri_status_t colibri_values8(const colibri_kv_pages8_t* cache, const int32_t* pages, int32_t n_pages,
+                                 void* k_out, void* v_out, void* stream) {
+    const colibri_status_t st = check_kv8(cache);
+    if (st != COLIBRI_OK) return st;
+    if (n_pages < 0 || ((uintptr_t)pages & 3) || (!pages && n_pages > cache->num_pages)) return COLIBRI_ERR_INVALID_ARG;
+    if (n_pages == 0) return COLIBRI_OK;
+    if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return COLIBRI_ERR_INVALID_ARG;
+    if ((int64_t)n_pages * cache->n_kv_heads > INT32_MAX) return COLIBRI_ERR_UNSUPPORTED;
+    const colibri_kv_pages_t kv = view(cache);
+    const int64_t bytes = (int64_t)n_pages * kv.n_kv_heads * kv.page_size * kv.head_dim * 2;
+    if (overlap(k_out, bytes, v_out, bytes)) return COLIBRI_ERR_INVALID_ARG;
+    for (const void* to : {k_out, v_out}) {
+        for (const void* p : {(const void*)kv.k, (const void*)kv.v})
+            if (overlap(p, kv_extent(&kv), to, bytes)) return COLIBRI_ERR_INVALID_ARG;
+        for (const float* p : {cache->k_scale, cache->v_scale})
+            if (overlap(p, scale_bytes(cache), to, bytes)) return COLIBRI_ERR_INVALID_ARG;
     }
-    a.seq_start = seqs->seq_start, a.kv_len = seqs->kv_len, a.table = seqs->page_table;
-    a.n_seqs = seqs->n_seqs, a.n_rows = seqs->n_rows, a.table_stride = seqs->table_stride;
-    a.hq = n_q_heads, a.hkv = hkv;
-    a.q_out = q_out, a.q_out_stride = q_out_stride;
-    a.k_out = cache->k, a.v_out = cache->v;
-    a.page_stride = cache->page_stride, a.head_stride = cache->head_stride;
-    a.row_stride = cache->row_stride, a.num_pages = cache->num_pages;
-    while ((1 << a.page_shift) < cache->page_size) ++a.page_shift;
-    return launched(launch_append(dtype_of(cache->dtype), d, a, (cudaStream_t)stream));
+    ValuesArgs a = values_args(cache);
+    a.pages = pages, a.n_pages = n_pages;
+    a.k_out = k_out, a.v_out = v_out;
+    return launched(launch_values8(cache->code == COLIBRI_CODE_INT8, kv.head_dim, a, (cudaStream_t)stream));
 }
 
 colibri_status_t colibri_qk_norm_rope(const colibri_seqs_t* seqs, const colibri_rope_t* rope,
@@ -418,10 +599,22 @@ colibri_status_t colibri_qk_norm_rope(const colibri_seqs_t* seqs, const colibri_
                                       const void* k_norm, float eps, void* q_out,
                                       int64_t q_out_stride, void* k_out, int64_t k_out_stride,
                                       void* stream) {
+    return colibri_qk_norm_rope_at(seqs, rope, nullptr, n_q_heads, n_kv_heads, head_dim, dtype, q, q_stride, k, k_stride,
+                                   q_norm, k_norm, eps, q_out, q_out_stride, k_out, k_out_stride, stream);
+}
+
+colibri_status_t colibri_qk_norm_rope_at(const colibri_seqs_t* seqs, const colibri_rope_t* rope,
+                                         const colibri_positions_t* positions, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                      int32_t dtype, const void* q, int64_t q_stride,
+                                      const void* k, int64_t k_stride, const void* q_norm,
+                                      const void* k_norm, float eps, void* q_out,
+                                      int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                                      void* stream) {
     if (!seqs) return COLIBRI_ERR_INVALID_ARG;
     colibri_status_t st = check_heads(n_q_heads, n_kv_heads, head_dim, dtype);
     if (st == COLIBRI_OK) st = check_seqs(seqs, n_q_heads);
     if (st == COLIBRI_OK) st = check_rope(rope, head_dim);
+    if (st == COLIBRI_OK) st = check_positions(positions, rope, seqs->n_rows);
     if (st != COLIBRI_OK) return st;
     const int d = head_dim, esz = elem_size(dtype);
     if (!rows_ok(q, q_stride, n_q_heads, d, esz) || !rows_ok(k, k_stride, n_kv_heads, d, esz) ||
@@ -441,10 +634,7 @@ colibri_status_t colibri_qk_norm_rope(const colibri_seqs_t* seqs, const colibri_
     a.q = q, a.k = k;
     a.q_stride = q_stride, a.k_stride = k_stride;
     a.q_norm = q_norm, a.k_norm = k_norm, a.eps = eps;
-    if (rope) {
-        a.freq = rope->freq, a.rot_dim = rope->rot_dim, a.mscale = rope->mscale;
-        a.interleaved = rope->style == COLIBRI_ROPE_INTERLEAVED;
-    }
+    set_rope(a, rope, positions);
     a.seq_start = seqs->seq_start, a.kv_len = seqs->kv_len;
     a.n_seqs = seqs->n_seqs, a.n_rows = seqs->n_rows;
     a.hq = n_q_heads, a.hkv = n_kv_heads;
@@ -527,6 +717,84 @@ colibri_status_t colibri_attention_decode(const colibri_kv_pages_t* cache, const
     AttnArgs a = make_args(cache, seqs, n_q_heads, q, q_stride, scale, o, o_stride, lse);
     return run_attention(a, p, cache->dtype, cache->head_dim, prefix_len, prefix_table, workspace,
                          (cudaStream_t)stream);
+}
+
+colibri_status_t colibri_attention_prompt8_workspace(const colibri_kv_pages8_t* cache, const colibri_seqs_t* seqs,
+                                                     int32_t n_q_heads, size_t* bytes) {
+    if (!bytes) return COLIBRI_ERR_INVALID_ARG;
+    colibri_status_t st = check_kv8(cache);
+    if (st != COLIBRI_OK) return st;
+    const colibri_kv_pages_t kv = view(cache);
+    st = check_prompt(&kv, seqs, n_q_heads);
+    if (st == COLIBRI_OK && seqs->n_seqs > 0 && (!seqs->seq_start || !seqs->page_table)) st = COLIBRI_ERR_INVALID_ARG;
+    if (st != COLIBRI_OK) return st;
+    Wide w;
+    if ((st = widen(cache, seqs, 0, &w)) != COLIBRI_OK) return st;
+    st = colibri_attention_prompt_workspace(&w.kv, &w.seqs, n_q_heads, bytes);
+    *bytes += w.bytes();
+    return st;
+}
+
+colibri_status_t colibri_attention_prompt8(const colibri_kv_pages8_t* cache, const colibri_seqs_t* seqs,
+                                           int32_t n_q_heads, const void* q, int64_t q_stride, float scale,
+                                           int32_t causal, void* o, int64_t o_stride, float* lse,
+                                           void* workspace, size_t workspace_bytes, void* stream) {
+    size_t need;
+    colibri_status_t st = colibri_attention_prompt8_workspace(cache, seqs, n_q_heads, &need);
+    if (st != COLIBRI_OK) return st;
+    const colibri_kv_pages_t kv = view(cache);
+    st = check_attention(&kv, seqs, n_q_heads, q, q_stride, scale, o, o_stride, lse);
+    if (st != COLIBRI_OK) return st;
+    if (!apart_from_scales(cache, n_q_heads, o, o_stride, seqs->n_rows)) return COLIBRI_ERR_INVALID_ARG;
+    if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255))) return COLIBRI_ERR_INVALID_ARG;
+    if (seqs->n_rows == 0 || seqs->n_seqs == 0) return COLIBRI_OK;
+    Wide w;
+    widen(cache, seqs, 0, &w);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const cudaError_t e = run_widen(cache, nullptr, 0, w, ws, (cudaStream_t)stream);
+    if (e != cudaSuccess) return launched(e);
+    return colibri_attention_prompt(&w.kv, &w.seqs, n_q_heads, q, q_stride, scale, causal, o, o_stride, lse,
+                                    ws + w.bytes(), need - w.bytes(), stream);
+}
+
+colibri_status_t colibri_attention_decode8_workspace(const colibri_kv_pages8_t* cache, const colibri_seqs_t* seqs,
+                                                     int32_t n_q_heads, int32_t prefix_len, size_t* bytes) {
+    if (!bytes) return COLIBRI_ERR_INVALID_ARG;
+    colibri_status_t st = check_kv8(cache);
+    if (st != COLIBRI_OK) return st;
+    const colibri_kv_pages_t kv = view(cache);
+    st = check_decode(&kv, seqs, n_q_heads, prefix_len);
+    if (st != COLIBRI_OK) return st;
+    Wide w;
+    if ((st = widen(cache, seqs, prefix_len, &w)) != COLIBRI_OK) return st;
+    st = colibri_attention_decode_workspace(&w.kv, &w.seqs, n_q_heads, prefix_len, bytes);
+    *bytes += w.bytes();
+    return st;
+}
+
+colibri_status_t colibri_attention_decode8(const colibri_kv_pages8_t* cache, const colibri_seqs_t* seqs,
+                                           int32_t n_q_heads, const void* q, int64_t q_stride, float scale,
+                                           int32_t prefix_len, const int32_t* prefix_table, void* o,
+                                           int64_t o_stride, float* lse, void* workspace,
+                                           size_t workspace_bytes, void* stream) {
+    size_t need;
+    colibri_status_t st = colibri_attention_decode8_workspace(cache, seqs, n_q_heads, prefix_len, &need);
+    if (st != COLIBRI_OK) return st;
+    const colibri_kv_pages_t kv = view(cache);
+    st = check_attention(&kv, seqs, n_q_heads, q, q_stride, scale, o, o_stride, lse);
+    if (st != COLIBRI_OK) return st;
+    if (!apart_from_scales(cache, n_q_heads, o, o_stride, seqs->n_rows) || (prefix_len > 0) != (prefix_table != nullptr) ||
+        ((uintptr_t)prefix_table & 3)) return COLIBRI_ERR_INVALID_ARG;
+    if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255))) return COLIBRI_ERR_INVALID_ARG;
+    if (seqs->n_rows == 0 || seqs->n_seqs == 0) return COLIBRI_OK;
+    Wide w;
+    widen(cache, seqs, prefix_len, &w);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const cudaError_t e = run_widen(cache, prefix_table, prefix_len, w, ws, (cudaStream_t)stream);
+    if (e != cudaSuccess) return launched(e);
+    return colibri_attention_decode(&w.kv, &w.seqs, n_q_heads, q, q_stride, scale, prefix_len,
+                                    prefix_len ? reinterpret_cast<const int32_t*>(ws) + w.own : nullptr, o, o_stride,
+                                    lse, ws + w.bytes(), need - w.bytes(), stream);
 }
 
 }  // extern "C"

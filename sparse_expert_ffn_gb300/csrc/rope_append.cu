@@ -23,81 +23,13 @@
 // cosines and sines, times the norm weights, stay in registers.
 #include <cuda_runtime.h>
 
-#include "attn.h"
-#include "common.cuh"
 #include "kernels.h"
+#include "rope_common.cuh"
 
 namespace colibri {
 namespace {
 
 constexpr int kThreads = 256;
-
-// 8 consecutive elements (not read through the read-only path: q_out may be q).
-template <typename T>
-struct Vec8;
-template <>
-struct Vec8<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
-        a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    }
-    __device__ __forceinline__ void store(float* p) const {
-        reinterpret_cast<float4*>(p)[0] = a, reinterpret_cast<float4*>(p)[1] = b;
-    }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    }
-    __device__ __forceinline__ void set(const float (&v)[8]) {
-        a = make_float4(v[0], v[1], v[2], v[3]), b = make_float4(v[4], v[5], v[6], v[7]);
-    }
-};
-template <>
-struct Vec8<__nv_bfloat16> {
-    uint4 a;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = a; }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-    __device__ __forceinline__ void set(const float (&v)[8]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        a = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-};
-
-// Position and sequence of a row; called by a whole warp.  seq < 0: the row
-// belongs to no sequence.
-__device__ __forceinline__ void row_place(const AppendArgs& a, int row, int* seq, int* pos) {
-    const int lane = threadIdx.x & 31;
-    if (!a.seq_start) {
-        *seq = row < a.n_seqs ? row : -1;
-        *pos = *seq >= 0 && a.kv_len ? max(__ldg(a.kv_len + row), 0) - 1 : 0;
-        return;
-    }
-    *seq = -1, *pos = 0;
-    for (int base = 0; base < a.n_seqs; base += 32) {
-        const int b = base + lane;
-        int s0 = 0, s1 = 0;
-        if (b < a.n_seqs) s0 = max(__ldg(a.seq_start + b), 0), s1 = min(__ldg(a.seq_start + b + 1), a.n_rows);
-        const unsigned hit = __ballot_sync(0xffffffffu, row >= s0 && row < s1);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            s0 = __shfl_sync(0xffffffffu, s0, src);
-            s1 = __shfl_sync(0xffffffffu, s1, src);
-            *seq = base + src;
-            const int total = a.kv_len ? max(__ldg(a.kv_len + *seq), 0) : s1 - s0;
-            *pos = total - (s1 - row);
-            return;
-        }
-    }
-}
 
 // heads of a lane group in flight (64 bytes per lane)
 template <typename T> constexpr int kBatch = sizeof(T) == 2 ? 2 : 1;
@@ -107,87 +39,6 @@ template <typename T> constexpr int kBatch = sizeof(T) == 2 ? 2 : 1;
 // ahead, which takes none (71 -> 64 us; all of a row at once: 71).
 template <typename T> constexpr bool kAhead = sizeof(T) == 4;
 template <typename T> using Vecs = Vec8<T>[kBatch<T>][2];
-
-// Heads h0, h0 + step, ... of one kind (query or key) of a row: loaded, normalised,
-// rotated and stored.  Element order in a lane: c0 .. c0 + 7, c1 .. c1 + 7.
-template <typename T, int D, bool kInterleaved>
-struct Heads {
-    static constexpr int kLanes = D / 16;
-    // (u, w) -> (u m[0] - w m[1], w m[2] + u m[3]): rotation and norm weights.  A lane
-    // whose elements are not rotated leaves the second products out: 0 times an
-    // infinite neighbour would not be 0.
-    float m[8][4];
-    bool norm, turns;
-    float eps;
-
-    __device__ __forceinline__ void prepare(const T* weight, float e, const float2* turn, int lane, bool rotated, int c0,
-                                            int c1) {
-        norm = weight != nullptr, eps = e, turns = rotated;
-        float g[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) g[i] = 1.f;
-        if (norm) {
-            Vec8<T> v;
-            float f[8];
-            v.load(weight + c0);
-            v.get(f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] = f[i];
-            v.load(weight + c1);
-            v.get(f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[8 + i] = f[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 t = turns ? turn[8 * lane + i] : make_float2(1.f, 0.f);
-            const float gu = g[kInterleaved ? 2 * i : i], gw = g[kInterleaved ? 2 * i + 1 : i + 8];
-            m[i][0] = gu * t.x, m[i][1] = gw * t.y, m[i][2] = gw * t.x, m[i][3] = gu * t.y;
-        }
-    }
-    __device__ __forceinline__ void apply(Vec8<T> (&x)[2]) const {
-        float p[16];
-        {
-            float f[8];
-            x[0].get(f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = f[i];
-            x[1].get(f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[8 + i] = f[i];
-        }
-        float inv = 1.f;
-        if (norm) {
-            float ss = 0.f, st = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(p[i], p[i], ss), st = fmaf(p[8 + i], p[8 + i], st);
-            ss += st;
-            // (the lanes of the head only: other groups of the warp may have fewer heads)
-            const uint32_t mine = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mine, ss, o);
-            inv = rsqrtf(fmaf(ss, 1.f / D, eps));
-        }
-        float y[2][8];
-        const auto products = [&](auto second) {                   // second(): with the second products
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float u = p[kInterleaved ? 2 * i : i] * inv, w = p[kInterleaved ? 2 * i + 1 : i + 8] * inv;
-                float yu = u * m[i][0], yw = w * m[i][2];
-                if (second()) yu -= w * m[i][1], yw += u * m[i][3];
-                if (kInterleaved) y[i / 4][i % 4 * 2] = yu, y[i / 4][i % 4 * 2 + 1] = yw;
-                else y[0][i] = yu, y[1][i] = yw;
-            }
-        };
-        // (one branch or a select per element: bf16 15373 rows 66 or 64 us, float32
-        // 1852 rows 15.7 or 16.2 us, by the registers that they take)
-        if (sizeof(T) == 2) products([&] { return turns; });
-        else if (turns) products([] { return true; });
-        else products([] { return false; });
-        x[0].set(y[0]);
-        x[1].set(y[1]);
-    }
-};
 
 // A CTA takes kGroups / per_row rows, `per_row` lane groups each (a power of two);
 // group `sub` of a row takes heads sub, sub + step, ... of q's, of k's and of v's
@@ -241,14 +92,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
     }
     __syncthreads();
     for (int e = tid; e < rows * pairs; e += kThreads) {
-        // a frequency's fraction of a turn, 2^64 to the turn (formed in double:
-        // freq / 2 pi is rounded once, at 2^-53 of itself)
-        const double t = __ldg(a.freq + e % pairs) * 0.15915494309189533577;
-        const uint64_t unit = __double2ull_rd((t - floor(t)) * 18446744073709551616.0);
-        const int32_t top = (int32_t)((unit * (uint64_t)(int64_t)place[e / pairs][1]) >> 32);
-        float sn, cs;
-        sincospif((float)top * 4.656612873077392578125e-10f, &sn, &cs);   // 2^-31: half turns
-        turn[e] = make_float2(cs * a.mscale, sn * a.mscale);
+        turn[e] = row_turn(a, row0 + e / pairs, place[e / pairs][1], e % pairs);
     }
     __syncthreads();
     const int seq = place[r][0], pos = place[r][1];
