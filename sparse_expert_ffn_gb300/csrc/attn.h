@@ -52,6 +52,11 @@ struct AttnArgs {
     // launch_attn_decode: the cut rows' pieces (attn_decode_pieces() rows)
     float* piece_o;
     float* piece_lse;
+    // keys and values as 8-bit codes: scales [num_pages][hkv][page_size >> block_shift]
+    // (null: k and v are of the rows' type)
+    const float* k_scale;
+    const float* v_scale;
+    int block_shift, int8;
     uint64_t wait_limit_ns;      // bound of every mbarrier wait
     int stall_tma;               // failure-detection tests only: a CTA's copies of Q and K stop at
                                  // this item of its work (1: the first), 0 never
@@ -76,6 +81,8 @@ cudaError_t attn_tc_status(int* status, cudaStream_t s);
 bool attn_decode_takes(DType dt, int group);
 size_t attn_decode_pieces(DType dt, int group);
 cudaError_t launch_attn_decode(DType dt, int d, const AttnArgs& a, cudaStream_t s);
+// The same over codes (bf16 rows; pieces as of bf16).
+cudaError_t launch_attn_decode8(int d, const AttnArgs& a, cudaStream_t s);
 
 // o, lse from the partial rows of `slots` slots, and of the pieces that
 // launch_attn_decode left (shares; slot part_slot then holds the rows it wrote

@@ -252,7 +252,7 @@ int choose_splits(int64_t items, int64_t keys, int slots, int step) {
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // bf16 prompts and prefixes run on the tensor cores.
-bool on_tensor_cores(int dtype, int mode) { return dtype == COLIBRI_DTYPE_BF16 && mode != kAttnSuffix; }
+bool on_tensor_cores(int dtype, int mode) { return rows_of(dtype) == COLIBRI_DTYPE_BF16 && mode != kAttnSuffix; }
 
 // The slots: one tensor-core CTA per SM.  Two of the CUDA-core kernel, which is what an
 // SM holds at d 64 (101 KB of shared memory); at d 128 it holds one (183 KB), but two
@@ -364,8 +364,9 @@ colibri_status_t launched(cudaError_t e) {
     return COLIBRI_ERR_CUDA;
 }
 
+// wide: the prefix's pages in the rows' type, where the cache is held in codes.
 colibri_status_t run_attention(AttnArgs a, const Plan& p, int dtype, int d, int prefix_len,
-                               const int32_t* prefix_table, void* ws, cudaStream_t s) {
+                               const int32_t* prefix_table, void* ws, cudaStream_t s, const colibri_kv_pages_t* wide = nullptr) {
     place_workspace(a, p, d, ws);
     a.prefix_len = prefix_len;
     cudaError_t e = cudaSuccess;
@@ -376,12 +377,20 @@ colibri_status_t run_attention(AttnArgs a, const Plan& p, int dtype, int d, int 
         f.table = prefix_table;
         f.splits = p.prefix;
         f.part_slot = 0;
+        if (wide) {
+            f.k = wide->k, f.v = wide->v, f.num_pages = wide->num_pages;
+            f.page_stride = wide->page_stride, f.head_stride = wide->head_stride, f.row_stride = wide->row_stride;
+            f.k_scale = f.v_scale = nullptr;
+        }
         e = launch_attention(dtype, d, f, s);
     }
     a.splits = p.own;
     a.part_slot = p.prefix;
     a.beside_prefix = p.prefix > 0;
-    if (e == cudaSuccess) e = p.shares ? launch_attn_decode(dtype_of(dtype), d, a, s) : launch_attention(dtype, d, a, s);
+    if (e == cudaSuccess)
+        e = !p.shares   ? launch_attention(dtype, d, a, s)
+            : a.k_scale ? launch_attn_decode8(d, a, s)
+                        : launch_attn_decode(dtype_of(dtype), d, a, s);
     if (e == cudaSuccess && (p.shares || p.slots() > 0))
         e = launch_attn_join(dtype_of(dtype), d, a, p.shares ? p.prefix : p.slots(), p.shares, s);
     return launched(e);
@@ -765,11 +774,12 @@ colibri_status_t colibri_attention_decode8_workspace(const colibri_kv_pages8_t* 
     const colibri_kv_pages_t kv = view(cache);
     st = check_decode(&kv, seqs, n_q_heads, prefix_len);
     if (st != COLIBRI_OK) return st;
+    colibri_seqs_t none{};
     Wide w;
-    if ((st = widen(cache, seqs, prefix_len, &w)) != COLIBRI_OK) return st;
-    st = colibri_attention_decode_workspace(&w.kv, &w.seqs, n_q_heads, prefix_len, bytes);
-    *bytes += w.bytes();
-    return st;
+    if ((st = widen(cache, &none, prefix_len, &w)) != COLIBRI_OK) return st;
+    *bytes = make_plan(&kv, seqs, n_q_heads, kAttnSuffix, prefix_len).bytes(kv.head_dim);
+    if (prefix_len > 0) *bytes = ((*bytes + 255) & ~(size_t)255) + w.bytes();
+    return COLIBRI_OK;
 }
 
 colibri_status_t colibri_attention_decode8(const colibri_kv_pages8_t* cache, const colibri_seqs_t* seqs,
@@ -784,17 +794,25 @@ colibri_status_t colibri_attention_decode8(const colibri_kv_pages8_t* cache, con
     st = check_attention(&kv, seqs, n_q_heads, q, q_stride, scale, o, o_stride, lse);
     if (st != COLIBRI_OK) return st;
     if (!apart_from_scales(cache, n_q_heads, o, o_stride, seqs->n_rows) || (prefix_len > 0) != (prefix_table != nullptr) ||
-        ((uintptr_t)prefix_table & 3)) return COLIBRI_ERR_INVALID_ARG;
+        ((uintptr_t)prefix_table & 3))
+        return COLIBRI_ERR_INVALID_ARG;
     if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255))) return COLIBRI_ERR_INVALID_ARG;
-    if (seqs->n_rows == 0 || seqs->n_seqs == 0) return COLIBRI_OK;
+    if (seqs->n_rows == 0) return COLIBRI_OK;
+    const Plan p = make_plan(&kv, seqs, n_q_heads, kAttnSuffix, prefix_len);
+    AttnArgs a = make_args(&kv, seqs, n_q_heads, q, q_stride, scale, o, o_stride, lse);
+    a.k_scale = cache->k_scale, a.v_scale = cache->v_scale;
+    a.block_shift = shift_of(cache->block), a.int8 = cache->code == COLIBRI_CODE_INT8;
     Wide w;
-    widen(cache, seqs, prefix_len, &w);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const cudaError_t e = run_widen(cache, prefix_table, prefix_len, w, ws, (cudaStream_t)stream);
-    if (e != cudaSuccess) return launched(e);
-    return colibri_attention_decode(&w.kv, &w.seqs, n_q_heads, q, q_stride, scale, prefix_len,
-                                    prefix_len ? reinterpret_cast<const int32_t*>(ws) + w.own : nullptr, o, o_stride,
-                                    lse, ws + w.bytes(), need - w.bytes(), stream);
+    if (prefix_len > 0) {
+        colibri_seqs_t none{};
+        widen(cache, &none, prefix_len, &w);
+        uint8_t* at = static_cast<uint8_t*>(workspace) + need - w.bytes();
+        const cudaError_t e = run_widen(cache, prefix_table, prefix_len, w, at, (cudaStream_t)stream);
+        if (e != cudaSuccess) return launched(e);
+        prefix_table = reinterpret_cast<const int32_t*>(at);
+    }
+    return run_attention(a, p, kCodes, kv.head_dim, prefix_len, prefix_table, workspace, (cudaStream_t)stream,
+                         prefix_len > 0 ? &w.kv : nullptr);
 }
 
 }  // extern "C"

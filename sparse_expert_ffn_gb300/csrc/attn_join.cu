@@ -9,6 +9,8 @@
 // log2-sum (scores that are NaN, rows whose wait gave up) makes the row NaN.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "attn_common.cuh"
 #include "kernels.h"
 
@@ -58,6 +60,7 @@ constexpr int kEarlySeqs = 128;
 template <typename T, int D, int kThreads>
 __global__ void __launch_bounds__(kThreads) attn_join_kernel(const __grid_constant__ AttnArgs a, int slots,
                                                              int shares_per_seq) {
+    using Out = std::conditional_t<sizeof(T) == 4, float, __nv_bfloat16>;
     constexpr int kWarps = kThreads / 32;
     __shared__ float4 rows[kWarps][D / 4];
     __shared__ float tops[kWarps], sums[kWarps];
@@ -129,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const __grid_consta
         if (tid < D) v = fmaf(f, reinterpret_cast<const float*>(rows[w])[tid], v);
     }
     const float inv = sum > 0.f ? 1.f / sum : sum;                 // no key: 0; NaN stays
-    if (tid < D) static_cast<T*>(a.o)[(int64_t)row * a.o_stride + (int64_t)head * D + tid] = from_f32<T>(v * inv);
+    if (tid < D) static_cast<Out*>(a.o)[(int64_t)row * a.o_stride + (int64_t)head * D + tid] = from_f32<Out>(v * inv);
     if (tid == 0 && a.lse) a.lse[flat] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
 }
 
@@ -147,6 +150,7 @@ cudaError_t launch(const AttnArgs& a, int slots, bool shares, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_attn_join(DType dt, int d, const AttnArgs& a, int slots, bool shares, cudaStream_t s) {
+    if (a.k_scale) return d == 64 ? launch<uint8_t, 64>(a, slots, shares, s) : launch<uint8_t, 128>(a, slots, shares, s);
     if (dt == DType::F32) return d == 64 ? launch<float, 64>(a, slots, shares, s) : launch<float, 128>(a, slots, shares, s);
     return d == 64 ? launch<__nv_bfloat16, 64>(a, slots, shares, s) : launch<__nv_bfloat16, 128>(a, slots, shares, s);
 }

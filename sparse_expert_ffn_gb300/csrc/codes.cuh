@@ -17,6 +17,27 @@ struct E4M3 {
         const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
         return lo | hi << 16;
     }
+    // codes 0, 1 and 2, 3 as f16 pairs
+    static __device__ __forceinline__ void halves(uint32_t c, uint32_t& lo, uint32_t& hi) {
+        asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+            : "=r"(lo), "=r"(hi) : "r"(c));
+    }
+    // codes 0, 2 and 1, 3 as bf16 pairs: the code's bits moved to bf16's places are the
+    // number times 2^-120, subnormal numbers included
+    static __device__ __forceinline__ void evens_odds(uint32_t c, uint32_t& even, uint32_t& odd) {
+        even = widen(__byte_perm(c, 0, 0x2404)), odd = widen(__byte_perm(c, 0, 0x3414));
+    }
+    // codes 0, 1 and 2, 3 as bf16 pairs
+    static __device__ __forceinline__ void pairs(uint32_t c, uint32_t& lo, uint32_t& hi) {
+        lo = widen(__byte_perm(c, 0, 0x1404)), hi = widen(__byte_perm(c, 0, 0x3424));
+    }
+    static __device__ __forceinline__ uint32_t widen(uint32_t p) {
+        const uint32_t b = (p & 0x80008000u) | ((p >> 4) & 0x07f007f0u);
+        uint32_t r;
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(b), "r"(0x7b807b80u));   // 2^120
+        return r;
+    }
     static __device__ __forceinline__ void decode4(uint32_t c, float* v) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -34,6 +55,26 @@ struct I8 {
         asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(hi) : "r"(__float2int_rn(v[3])), "r"(__float2int_rn(v[2])), "r"(0));
         asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(__float2int_rn(v[1])), "r"(__float2int_rn(v[0])), "r"(hi));
         return d;
+    }
+    // codes 0, 1 and 2, 3 as f16 pairs: 1024 + (code + 128), less 1152
+    static __device__ __forceinline__ void halves(uint32_t c, uint32_t& lo, uint32_t& hi) {
+        const uint32_t u = c ^ 0x80808080u;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(0x64806480u));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(0x64806480u));
+    }
+    // codes 0, 2 and 1, 3 as bf16 pairs
+    static __device__ __forceinline__ void evens_odds(uint32_t c, uint32_t& even, uint32_t& odd) {
+        even = widen(__byte_perm(c, 0x43434343u, 0x4240)), odd = widen(__byte_perm(c, 0x43434343u, 0x4341));
+    }
+    // codes 0, 1 and 2, 3 as bf16 pairs
+    static __device__ __forceinline__ void pairs(uint32_t c, uint32_t& lo, uint32_t& hi) {
+        lo = widen(__byte_perm(c, 0x43434343u, 0x4140)), hi = widen(__byte_perm(c, 0x43434343u, 0x4342));
+    }
+    // 128 + (the lower seven bits), less 128 + 128 (the sign bit)
+    static __device__ __forceinline__ uint32_t widen(uint32_t p) {
+        uint32_t r;
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(p & 0xff7fff7fu), "r"(p & 0xff80ff80u));
+        return r;
     }
     static __device__ __forceinline__ void decode4(uint32_t c, float* v) {
 #pragma unroll

@@ -265,13 +265,13 @@ DECODE = [
 
 @pytest.mark.parametrize("kv,hq,hkv,d,code,block,page,layout,prefix", DECODE)
 def test_decode8(A, kv, hq, hkv, d, code, block, page, layout, prefix):
-    p = Problem8([(1, t) for t in kv], hq, hkv, d, code, block, page, layout, prefix=prefix, seed=prefix + d, wide=5, pow2=True)
+    p = Problem8([(1, t) for t in kv], hq, hkv, d, code, block, page, layout, prefix=prefix, seed=prefix + d, wide=5, pow2=page == 64 or prefix > 0)
     lse = torch.full((p.rows, hq), 9.0, device=p.q.device)
     out = A.attention_decode(p.cache(A), seqs(A, p, decode=True), p.q, prefix_len=prefix,
                              prefix_table=p.prefix_table if prefix else None, out=torch.full_like(p.q, 9.0), lse=lse)
     torch.cuda.synchronize()
     p.check(out, lse, False)
-    if not prefix:                                             # the prompt form of the same rows
+    if not prefix and page == 64:                              # the prompt form of the same rows
         lse2 = torch.empty_like(lse)
         p.check(A.attention_prompt_paged(p.cache(A), seqs(A, p), p.q, lse=lse2), lse2, True)
 
