@@ -23,12 +23,12 @@ struct E4M3 {
             "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
             : "=r"(lo), "=r"(hi) : "r"(c));
     }
-    // codes 0, 2 and 1, 3 as bf16 pairs: the code's bits moved to bf16's places are the
-    // number times 2^-120, subnormal numbers included
+    // codes 0, 2 and 1, 3
     static __device__ __forceinline__ void evens_odds(uint32_t c, uint32_t& even, uint32_t& odd) {
-        even = widen(__byte_perm(c, 0, 0x2404)), odd = widen(__byte_perm(c, 0, 0x3414));
+        halves(__byte_perm(c, 0, 0x3120), even, odd);
     }
-    // codes 0, 1 and 2, 3 as bf16 pairs
+    // codes 0, 1 and 2, 3 as bf16 pairs: the code's bits moved to bf16's places are the
+    // number times 2^-120, subnormal numbers included
     static __device__ __forceinline__ void pairs(uint32_t c, uint32_t& lo, uint32_t& hi) {
         lo = widen(__byte_perm(c, 0, 0x1404)), hi = widen(__byte_perm(c, 0, 0x3424));
     }
@@ -62,9 +62,9 @@ struct I8 {
         asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(0x64806480u));
         asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(0x64806480u));
     }
-    // codes 0, 2 and 1, 3 as bf16 pairs
+    // codes 0, 2 and 1, 3
     static __device__ __forceinline__ void evens_odds(uint32_t c, uint32_t& even, uint32_t& odd) {
-        even = widen(__byte_perm(c, 0x43434343u, 0x4240)), odd = widen(__byte_perm(c, 0x43434343u, 0x4341));
+        halves(__byte_perm(c, 0, 0x3120), even, odd);
     }
     // codes 0, 1 and 2, 3 as bf16 pairs
     static __device__ __forceinline__ void pairs(uint32_t c, uint32_t& lo, uint32_t& hi) {
