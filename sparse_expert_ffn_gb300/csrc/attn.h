@@ -79,9 +79,9 @@ cudaError_t attn_tc_status(int* status, cudaStream_t s);
 // groups of up to 32 heads).  part_o null: no prefix; otherwise slot part_slot
 // takes the rows written in one piece.
 bool attn_decode_takes(DType dt, int group);
-size_t attn_decode_pieces(DType dt, int group);
+size_t attn_decode_pieces(DType dt, int group, bool codes);
 cudaError_t launch_attn_decode(DType dt, int d, const AttnArgs& a, cudaStream_t s);
-// The same over codes (bf16 rows; pieces as of bf16).
+// The same over codes (bf16 rows).
 cudaError_t launch_attn_decode8(int d, const AttnArgs& a, cudaStream_t s);
 
 // o, lse from the partial rows of `slots` slots, and of the pieces that

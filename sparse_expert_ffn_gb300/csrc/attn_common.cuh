@@ -212,7 +212,12 @@ __host__ __device__ constexpr int piece_rows(int group) {
 }
 template <typename T, int D> constexpr int kStepKeys = 4096 / (D * (int)sizeof(T));
 constexpr int kShareWarps = 4;                    // per CTA
-constexpr int kShares = 2 * 152 * kShareWarps;    // 2 CTAs per SM
+// CTAs per SM: 3 where registers allow it.
+template <typename T>
+__host__ __device__ constexpr int share_ctas(int group) { return sizeof(T) == 1 && group <= 8 ? 3 : 2; }
+template <typename T>
+__host__ __device__ constexpr int most_shares(int group) { return share_ctas<T>(group) * 152 * kShareWarps; }
+constexpr int kMostShares = 3 * 152 * kShareWarps;
 constexpr int kMinSteps = 4;                      // steps of a share at least
 
 // Steps of sequence b per (head, row tile).
@@ -243,13 +248,13 @@ __device__ __forceinline__ void count_steps(const AttnArgs& a, int per_seq, int 
 }
 
 // Shares of the list, share c's first step, and the share that step u falls into.
-__device__ __forceinline__ int share_count(int64_t total) {
-    const int64_t most = (total + kMinSteps - 1) / kMinSteps;
-    return most < kShares ? (int)most : kShares;
+__device__ __forceinline__ int share_count(int64_t total, int most) {
+    const int64_t n = (total + kMinSteps - 1) / kMinSteps;
+    return n < most ? (int)n : most;
 }
 // (in 32 bits where the products fit them: a 64-bit division is some 100 instructions)
 constexpr int64_t kSmallList = 1 << 21;
-static_assert(kSmallList * kShares < ((int64_t)1 << 32), "fits 32 bits");
+static_assert(kSmallList * kMostShares < ((int64_t)1 << 32), "fits 32 bits");
 __device__ __forceinline__ int64_t share_begin(int64_t total, int shares, int c) {
     return total < kSmallList ? (uint32_t)total * (uint32_t)c / (uint32_t)shares : total * c / shares;
 }

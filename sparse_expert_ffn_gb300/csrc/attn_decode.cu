@@ -44,7 +44,7 @@ template <int D, int MT>
 struct TensorRows {
     using T = __nv_bfloat16;
     using Out = T;
-    static constexpr int kD = D, kRows = 16 * MT, KS = kStepKeys<T, D>, kScratch = 0;
+    static constexpr int kD = D, kRows = 16 * MT, KS = kStepKeys<T, D>, kScratch = 0, kStages = 3, kCtas = 2;
     uint32_t qf[MT][D / 16][4];
     float o[MT][D / 8][4], m[MT][2], l[MT][2];
 
@@ -193,7 +193,7 @@ template <int D, int G>
 struct FloatRows {
     using T = float;
     using Out = T;
-    static constexpr int kD = D, kRows = row_tile<T>(0), KS = kStepKeys<T, D>, kParts = 32 / KS;
+    static constexpr int kD = D, kRows = row_tile<T>(0), KS = kStepKeys<T, D>, kParts = 32 / KS, kStages = 3, kCtas = 2;
     static constexpr int kScratch = G * KS * 4;                    // a step's weights
     static constexpr int kPairs = D / 64;                          // column pairs of a lane
     uint64_t q[G][16], o[G][kPairs];                               // columns 32 (lane / KS) .. + 31 of q
@@ -311,8 +311,10 @@ struct FloatRows {
 
 }  // namespace
 
-size_t attn_decode_pieces(DType dt, int group) {
-    return (size_t)kShares * 2 * (dt == DType::BF16 ? piece_rows<__nv_bfloat16>(group) : piece_rows<float>(group));
+size_t attn_decode_pieces(DType dt, int group, bool codes) {
+    if (codes) return (size_t)most_shares<uint8_t>(group) * 2 * piece_rows<uint8_t>(group);
+    return dt == DType::BF16 ? (size_t)most_shares<__nv_bfloat16>(group) * 2 * piece_rows<__nv_bfloat16>(group)
+                             : (size_t)most_shares<float>(group) * 2 * piece_rows<float>(group);
 }
 
 // (a float32 group of 64 would be read 16 times)

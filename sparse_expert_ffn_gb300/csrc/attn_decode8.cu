@@ -65,6 +65,7 @@ struct CodeRows {
     using T = uint8_t;
     using Out = __nv_bfloat16;
     static constexpr int kD = D, kRows = 8 * NT, KS = kStepKeys<T, D>, kScratch = 0;
+    static constexpr int kCtas = share_ctas<T>(kRows), kStages = kCtas == 3 ? 2 : 3;
     uint32_t qf[NT][D / 16][2];                                    // row g
     // rows 2 c and 2 c + 1; o: columns 16 x + 2 g of both, then 16 x + 2 g + 1
     float o[NT][D / 16][4], m[NT][2], l[NT][2], f[NT][2];          // f: scale * log2(e) / 2^e

@@ -275,7 +275,7 @@ Plan make_plan(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq, in
     p.rows = (size_t)s->n_rows * hq;
     if (mode == kAttnSuffix && attn_decode_takes(dtype_of(kv->dtype), a.group)) {
         p.shares = true;
-        p.pieces = attn_decode_pieces(dtype_of(kv->dtype), a.group);
+        p.pieces = attn_decode_pieces(dtype_of(kv->dtype), a.group, kv->dtype == kCodes);
     } else {
         p.own = splits_for(a, kv, std::max<int64_t>(keys - prefix_len, 1));
     }

@@ -35,7 +35,7 @@ __device__ __forceinline__ Place row_parts(const AttnArgs& a, int row, int head,
         count_steps<T, D, kEarly>(a, shares_per_seq, row, &total, &first);
         const int steps = seq_steps<T, D, kEarly>(a, row);
         if (steps > 0) {
-            const int shares = share_count(total);
+            const int shares = share_count(total, most_shares<T>(a.group));
             first += (int64_t)((head / a.group) * row_tiles<T>(a.group) + (head % a.group) / row_tile<T>(a.group)) * steps;
             p.c0 = share_of(total, shares, first);
             p.c1 = share_of(total, shares, first + steps - 1);

@@ -10,9 +10,7 @@ namespace colibri {
 namespace {
 
 constexpr int kDecThreads = 32 * kShareWarps;
-constexpr int kStages = 3;
 constexpr int kStageBytes = 8192;                                 // K then V of one step
-constexpr int kRingBytes = kStages * kStageBytes;
 
 __device__ __forceinline__ void ldm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -171,14 +169,14 @@ struct Stream {
 template <typename Rows, bool kEarly>
 __device__ __forceinline__ void decode_share(const AttnArgs& a, int per_seq, uint8_t* smem) {
     using T = typename Rows::T;
-    constexpr int D = Rows::kD, KS = Rows::KS;
+    constexpr int D = Rows::kD, KS = Rows::KS, kStages = Rows::kStages, kRingBytes = kStages * kStageBytes;
     const int lane = threadIdx.x & 31, share = blockIdx.x * kShareWarps + (threadIdx.x >> 5);
     const int tiles = row_tiles<T>(a.group);
     // this warp's share of the list, and the sequence that its first step lies in
     int64_t total, left, before = 0, u0;
     count_steps<T, D, kEarly>(a, per_seq, 0, &total, &left);
     if (total == 0) return;
-    const int shares = share_count(total);
+    const int shares = share_count(total, most_shares<T>(a.group));
     if (share >= shares) return;
     u0 = share_begin(total, shares, share);
     left = share_begin(total, shares, share + 1) - u0;             // (at least one)
@@ -239,7 +237,7 @@ __device__ __forceinline__ void decode_share(const AttnArgs& a, int per_seq, uin
             cp_commit();
             const uint32_t ks = ring + slot_out * kStageBytes, vs = ks + kStageBytes / 2;
             slot_out = slot_out == kStages - 1 ? 0 : slot_out + 1;
-            if constexpr (sizeof(T) == 1) rows.step(a, ks, vs, at.hi - (at.lo + step * KS), st.scale);
+            if constexpr (sizeof(T) == 1) rows.step(a, ks, vs, at.hi - (at.lo + step * KS), kStages == 2 ? st.waiting : st.scale);
             else rows.step(a, ks, vs, at.hi - (at.lo + step * KS), scratch);
         }
         left -= at.count;
@@ -271,7 +269,7 @@ __device__ __forceinline__ void decode_share(const AttnArgs& a, int per_seq, uin
 // first; what it reads: ld_early).  It waits for it at the end, so that the join,
 // which waits for this kernel, finds both done.
 template <typename Rows, bool kEarly>
-__global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __grid_constant__ AttnArgs a, int per_seq) {
+__global__ void __launch_bounds__(kDecThreads, Rows::kCtas) attn_decode_kernel(const __grid_constant__ AttnArgs a, int per_seq) {
     extern __shared__ __align__(128) uint8_t smem[];
     if constexpr (kEarly) pdl_launch_dependents();
     else pdl_enter();
@@ -282,9 +280,10 @@ __global__ void __launch_bounds__(kDecThreads, 2) attn_decode_kernel(const __gri
 template <typename Rows>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     auto kern = a.beside_prefix ? attn_decode_kernel<Rows, true> : attn_decode_kernel<Rows, false>;
-    const int bytes = kShareWarps * (kRingBytes + Rows::kScratch), per_seq = a.hkv * row_tiles<typename Rows::T>(a.group);
+    using T = typename Rows::T;
+    const int bytes = kShareWarps * (Rows::kStages * kStageBytes + Rows::kScratch), per_seq = a.hkv * row_tiles<T>(a.group);
     cudaError_t e = smem_attr((const void*)kern, bytes);
-    return e != cudaSuccess ? e : launch_pdl(kern, dim3(kShares / kShareWarps), dim3(kDecThreads), bytes, s, a, per_seq);
+    return e != cudaSuccess ? e : launch_pdl(kern, dim3(most_shares<T>(a.group) / kShareWarps), dim3(kDecThreads), bytes, s, a, per_seq);
 }
 
 }  // namespace

@@ -64,7 +64,9 @@ struct I8 {
     }
     // codes 0, 2 and 1, 3
     static __device__ __forceinline__ void evens_odds(uint32_t c, uint32_t& even, uint32_t& odd) {
-        halves(__byte_perm(c, 0, 0x3120), even, odd);
+        const uint32_t u = c ^ 0x80808080u;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(even) : "r"(__byte_perm(u, 0x64646464u, 0x4240)), "r"(0x64806480u));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(odd) : "r"(__byte_perm(u, 0x64646464u, 0x4341)), "r"(0x64806480u));
     }
     // codes 0, 1 and 2, 3 as bf16 pairs
     static __device__ __forceinline__ void pairs(uint32_t c, uint32_t& lo, uint32_t& hi) {
