@@ -275,11 +275,6 @@ __global__ void __launch_bounds__(256) values8_kernel(const __grid_constant__ Va
         const int kind = (int)(piece & 1), h = (int)((piece >> 1) % (uint32_t)a.hkv);
         const int64_t i = (piece >> 1) / (uint32_t)a.hkv;
         const int id = a.pages ? __ldg(a.pages + i) : (int)i;
-        if (a.width) {
-            const int b = (int)(i / a.width), p = (int)(i - (int64_t)b * a.width);
-            if (p < a.first || ((int64_t)p << a.page_shift) + row >= (a.kv_len ? __ldg(a.kv_len + b) : a.n_keys)) continue;
-            if ((piece >> 1) % (uint32_t)a.hkv == 0 && kind == 0 && chunk == 0) a.table_out[i] = (int)i + a.base;
-        }
         BF* to = static_cast<BF*>(kind ? a.v_out : a.k_out) + ((i * a.hkv + h) * rows + row) * D + 16 * chunk;
         uint32_t w[8] = {};
         if ((unsigned)id < (unsigned)a.num_pages) {

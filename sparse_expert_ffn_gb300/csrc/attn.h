@@ -131,9 +131,6 @@ struct ValuesArgs {
     const int32_t* pages;            // [n_pages], null: 0 .. n_pages - 1
     int n_pages;
     void *k_out, *v_out;
-    int width, first, n_keys, base;
-    const int32_t* kv_len;
-    int32_t* table_out;
 };
 cudaError_t launch_values8(bool int8, int d, const ValuesArgs& a, cudaStream_t s);
 

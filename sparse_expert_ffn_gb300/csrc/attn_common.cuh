@@ -199,7 +199,7 @@ __device__ __forceinline__ void attn_split(const AttnArgs& a, int sp, int kt, in
 // goes to one warp.
 template <typename T>
 __host__ __device__ constexpr int row_tile(int group) {
-    return sizeof(T) == 4 ? 4 : sizeof(T) == 1 && group <= 8 ? 8 : group <= 16 ? 16 : 32;
+    return sizeof(T) == 4 ? 4 : sizeof(T) == 1 && group <= 8 ? 8 : sizeof(T) == 1 || group <= 16 ? 16 : 32;
 }
 template <typename T>
 __host__ __device__ constexpr int row_tiles(int group) {

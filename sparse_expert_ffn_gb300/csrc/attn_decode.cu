@@ -34,6 +34,7 @@
 // of 32 865 instead of 1007).
 #include <cuda_runtime.h>
 
+#include "attn_rows8.cuh"
 #include "attn_share.cuh"
 
 namespace colibri {
@@ -309,6 +310,28 @@ struct FloatRows {
     }
 };
 
+// kEarly: behind a prefix launch the kernel starts on the SMs that this one has left;
+// it needs nothing of it (48 rows over a prefix of 16384 keys: 58 us, 69 waiting
+// first; what it reads: ld_early).  It waits for it at the end, so that the join,
+// which waits for this kernel, finds both done.
+template <typename Rows, bool kEarly>
+__global__ void __launch_bounds__(kDecThreads, Rows::kCtas) attn_decode_kernel(const __grid_constant__ AttnArgs a, int per_seq) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    if constexpr (kEarly) pdl_launch_dependents();
+    else pdl_enter();
+    decode_share<Rows, kEarly>(a, per_seq, smem);
+    if constexpr (kEarly) pdl_wait();
+}
+
+template <typename Rows>
+cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
+    auto kern = a.beside_prefix ? attn_decode_kernel<Rows, true> : attn_decode_kernel<Rows, false>;
+    using T = typename Rows::T;
+    const int bytes = kShareWarps * (Rows::kStages * kStageBytes + Rows::kScratch), per_seq = a.hkv * row_tiles<T>(a.group);
+    cudaError_t e = smem_attr((const void*)kern, bytes);
+    return e != cudaSuccess ? e : launch_pdl(kern, dim3(most_shares<T>(a.group) / kShareWarps), dim3(kDecThreads), bytes, s, a, per_seq);
+}
+
 }  // namespace
 
 size_t attn_decode_pieces(DType dt, int group, bool codes) {
@@ -331,6 +354,19 @@ static cudaError_t launch_rows(DType dt, const AttnArgs& a, cudaStream_t s) {
 
 cudaError_t launch_attn_decode(DType dt, int d, const AttnArgs& a, cudaStream_t s) {
     return d == 64 ? launch_rows<64>(dt, a, s) : launch_rows<128>(dt, a, s);
+}
+
+template <int D>
+static cudaError_t launch_codes(const AttnArgs& a, cudaStream_t s) {
+    const auto pick = [&](auto code) {
+        using C = decltype(code);
+        return a.group <= 8 ? launch<CodeRows<C, D, 1>>(a, s) : launch<CodeRows<C, D, 2>>(a, s);
+    };
+    return a.int8 ? pick(I8{}) : pick(E4M3{});
+}
+
+cudaError_t launch_attn_decode8(int d, const AttnArgs& a, cudaStream_t s) {
+    return d == 64 ? launch_codes<64>(a, s) : launch_codes<128>(a, s);
 }
 
 }  // namespace colibri

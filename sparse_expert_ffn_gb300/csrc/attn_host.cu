@@ -364,9 +364,8 @@ colibri_status_t launched(cudaError_t e) {
     return COLIBRI_ERR_CUDA;
 }
 
-// wide: the prefix's pages in the rows' type, where the cache is held in codes.
 colibri_status_t run_attention(AttnArgs a, const Plan& p, int dtype, int d, int prefix_len,
-                               const int32_t* prefix_table, void* ws, cudaStream_t s, const colibri_kv_pages_t* wide = nullptr) {
+                               const int32_t* prefix_table, void* ws, cudaStream_t s) {
     place_workspace(a, p, d, ws);
     a.prefix_len = prefix_len;
     cudaError_t e = cudaSuccess;
@@ -377,11 +376,6 @@ colibri_status_t run_attention(AttnArgs a, const Plan& p, int dtype, int d, int 
         f.table = prefix_table;
         f.splits = p.prefix;
         f.part_slot = 0;
-        if (wide) {
-            f.k = wide->k, f.v = wide->v, f.num_pages = wide->num_pages;
-            f.page_stride = wide->page_stride, f.head_stride = wide->head_stride, f.row_stride = wide->row_stride;
-            f.k_scale = f.v_scale = nullptr;
-        }
         e = launch_attention(dtype, d, f, s);
     }
     a.splits = p.own;
@@ -417,7 +411,7 @@ colibri_status_t check_prompt(const colibri_kv_pages_t* kv, const colibri_seqs_t
     if (st == COLIBRI_OK) st = check_seqs(seqs, n_q_heads);
     if (st == COLIBRI_OK) st = check_kv(kv, seqs->page_table != nullptr);
     if (st != COLIBRI_OK) return st;
-    if (seqs->page_table && !(countable(kv, seqs, n_q_heads) && mappable(kv))) return COLIBRI_ERR_UNSUPPORTED;
+    if (seqs->page_table && !(countable(kv, seqs, n_q_heads) && (kv->dtype == kCodes || mappable(kv)))) return COLIBRI_ERR_UNSUPPORTED;
     // packed keys: the call's own rows
     if (!seqs->page_table && seqs->n_seqs > 0 &&
         (seqs->kv_len || kv->num_pages != 1 || (seqs->n_rows > 0 && kv->page_size != seqs->n_rows)))
@@ -434,7 +428,8 @@ colibri_status_t check_decode(const colibri_kv_pages_t* kv, const colibri_seqs_t
     if (st == COLIBRI_OK) st = check_kv(kv, true);
     if (st != COLIBRI_OK) return st;
     if (prefix_len < 0 || prefix_len % kv->page_size) return COLIBRI_ERR_INVALID_ARG;
-    if (prefix_len > kMaxKeys || !countable(kv, seqs, n_q_heads) || !mappable(kv)) return COLIBRI_ERR_UNSUPPORTED;
+    if (prefix_len > kMaxKeys || !countable(kv, seqs, n_q_heads) || (kv->dtype != kCodes && !mappable(kv)))
+        return COLIBRI_ERR_UNSUPPORTED;
     return COLIBRI_OK;
 }
 
@@ -445,45 +440,30 @@ bool apart_from_scales(const colibri_kv_pages8_t* c, int hq, const void* o, int6
     return !overlap(c->k_scale, scale_bytes(c), o, n) && !overlap(c->v_scale, scale_bytes(c), o, n);
 }
 
-// Attention over 8-bit pages: the pages that the sequences (and the prefix) name as
-// bf16 pages in the workspace, then attention over those.
-struct Wide {
-    colibri_kv_pages_t kv;
-    colibri_seqs_t seqs;
-    int64_t own, shared;             // pages of the sequences, of the prefix
-    size_t table, pages;             // bytes: the tables, one of k and v
-    size_t bytes() const { return table + 2 * pages; }
-};
-colibri_status_t widen(const colibri_kv_pages8_t* c, const colibri_seqs_t* s, int prefix_len, Wide* w) {
-    const int hkv = c->n_kv_heads, d = c->head_dim;
-    w->own = (int64_t)s->n_seqs * s->table_stride, w->shared = prefix_len / c->page_size;
-    const int64_t n = w->own + w->shared, page = (int64_t)hkv * c->page_size * d;
-    if (n * hkv > INT32_MAX) return COLIBRI_ERR_UNSUPPORTED;
-    w->table = (size_t)(n * 4 + 255) & ~(size_t)255;
-    w->pages = (size_t)(n * page * 2 + 255) & ~(size_t)255;
-    w->kv = {c->k, c->v, page, (int64_t)c->page_size * d, d, (int32_t)std::max<int64_t>(n, 1),
-             c->page_size, hkv, d, COLIBRI_DTYPE_BF16};
-    w->seqs = *s;
-    return COLIBRI_OK;
+colibri_status_t check_prompt8(const colibri_kv_pages8_t* c, const colibri_seqs_t* s, int hq) {
+    const colibri_status_t st = check_kv8(c);
+    if (st != COLIBRI_OK) return st;
+    if (!s || (s->n_seqs > 0 && (!s->page_table || !s->kv_len))) return COLIBRI_ERR_INVALID_ARG;
+    const colibri_kv_pages_t kv = view(c);
+    return check_prompt(&kv, s, hq);
 }
-cudaError_t run_widen(const colibri_kv_pages8_t* c, const int32_t* prefix_table, int prefix_len, Wide& w, uint8_t* ws,
-                      cudaStream_t s) {
-    ValuesArgs a = values_args(c);
-    w.kv.k = ws + w.table, w.kv.v = ws + w.table + w.pages;
-    const bool int8 = c->code == COLIBRI_CODE_INT8;
-    const int64_t per = (int64_t)c->n_kv_heads * c->page_size * c->head_dim * 2;
-    a.pages = w.seqs.page_table, a.n_pages = (int)w.own, a.width = w.seqs.table_stride, a.kv_len = w.seqs.kv_len;
-    a.first = prefix_len / c->page_size, a.table_out = reinterpret_cast<int32_t*>(ws);
-    a.k_out = w.kv.k, a.v_out = w.kv.v;
-    cudaError_t e = launch_values8(int8, c->head_dim, a, s);
-    w.seqs.page_table = a.table_out;
-    if (w.shared > 0 && e == cudaSuccess) {
-        a.pages = prefix_table, a.n_pages = a.width = (int)w.shared, a.kv_len = nullptr, a.n_keys = prefix_len;
-        a.first = 0, a.base = (int)w.own, a.table_out += w.own;
-        a.k_out = ws + w.table + w.own * per, a.v_out = ws + w.table + w.pages + w.own * per;
-        e = launch_values8(int8, c->head_dim, a, s);
-    }
-    return e;
+
+colibri_status_t check_attention8(const colibri_kv_pages8_t* c, const colibri_seqs_t* s, int hq, const void* q,
+                                  int64_t q_stride, float scale, const void* o, int64_t o_stride, const float* lse) {
+    const colibri_kv_pages_t kv = view(c);
+    const colibri_status_t st = check_attention(&kv, s, hq, q, q_stride, scale, o, o_stride, lse);
+    if (st != COLIBRI_OK) return st;
+    return apart_from_scales(c, hq, o, o_stride, s->n_rows) ? COLIBRI_OK : COLIBRI_ERR_INVALID_ARG;
+}
+
+// make_args for a cache of codes.
+AttnArgs make_args8(const colibri_kv_pages8_t* c, const colibri_seqs_t* s, int hq, const void* q, int64_t q_stride,
+                    float scale, void* o, int64_t o_stride, float* lse) {
+    const colibri_kv_pages_t kv = view(c);
+    AttnArgs a = make_args(&kv, s, hq, q, q_stride, scale, o, o_stride, lse);
+    a.k_scale = c->k_scale, a.v_scale = c->v_scale;
+    a.block_shift = shift_of(c->block), a.int8 = c->code == COLIBRI_CODE_INT8;
+    return a;
 }
 
 }  // namespace
@@ -731,39 +711,29 @@ colibri_status_t colibri_attention_decode(const colibri_kv_pages_t* cache, const
 colibri_status_t colibri_attention_prompt8_workspace(const colibri_kv_pages8_t* cache, const colibri_seqs_t* seqs,
                                                      int32_t n_q_heads, size_t* bytes) {
     if (!bytes) return COLIBRI_ERR_INVALID_ARG;
-    colibri_status_t st = check_kv8(cache);
+    const colibri_status_t st = check_prompt8(cache, seqs, n_q_heads);
     if (st != COLIBRI_OK) return st;
     const colibri_kv_pages_t kv = view(cache);
-    st = check_prompt(&kv, seqs, n_q_heads);
-    if (st == COLIBRI_OK && seqs->n_seqs > 0 && (!seqs->seq_start || !seqs->page_table)) st = COLIBRI_ERR_INVALID_ARG;
-    if (st != COLIBRI_OK) return st;
-    Wide w;
-    if ((st = widen(cache, seqs, 0, &w)) != COLIBRI_OK) return st;
-    st = colibri_attention_prompt_workspace(&w.kv, &w.seqs, n_q_heads, bytes);
-    *bytes += w.bytes();
-    return st;
+    *bytes = make_plan(&kv, seqs, n_q_heads, seqs->seq_start ? kAttnPrompt : kAttnSuffix, 0).bytes(kv.head_dim);
+    return COLIBRI_OK;
 }
 
 colibri_status_t colibri_attention_prompt8(const colibri_kv_pages8_t* cache, const colibri_seqs_t* seqs,
                                            int32_t n_q_heads, const void* q, int64_t q_stride, float scale,
                                            int32_t causal, void* o, int64_t o_stride, float* lse,
                                            void* workspace, size_t workspace_bytes, void* stream) {
-    size_t need;
-    colibri_status_t st = colibri_attention_prompt8_workspace(cache, seqs, n_q_heads, &need);
+    colibri_status_t st = check_prompt8(cache, seqs, n_q_heads);
+    if (st == COLIBRI_OK) st = check_attention8(cache, seqs, n_q_heads, q, q_stride, scale, o, o_stride, lse);
     if (st != COLIBRI_OK) return st;
     const colibri_kv_pages_t kv = view(cache);
-    st = check_attention(&kv, seqs, n_q_heads, q, q_stride, scale, o, o_stride, lse);
-    if (st != COLIBRI_OK) return st;
-    if (!apart_from_scales(cache, n_q_heads, o, o_stride, seqs->n_rows)) return COLIBRI_ERR_INVALID_ARG;
-    if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255))) return COLIBRI_ERR_INVALID_ARG;
+    const Plan p = make_plan(&kv, seqs, n_q_heads, seqs->seq_start ? kAttnPrompt : kAttnSuffix, 0);
+    const size_t need = p.bytes(kv.head_dim);
+    if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255)))
+        return COLIBRI_ERR_INVALID_ARG;
     if (seqs->n_rows == 0 || seqs->n_seqs == 0) return COLIBRI_OK;
-    Wide w;
-    widen(cache, seqs, 0, &w);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const cudaError_t e = run_widen(cache, nullptr, 0, w, ws, (cudaStream_t)stream);
-    if (e != cudaSuccess) return launched(e);
-    return colibri_attention_prompt(&w.kv, &w.seqs, n_q_heads, q, q_stride, scale, causal, o, o_stride, lse,
-                                    ws + w.bytes(), need - w.bytes(), stream);
+    AttnArgs a = make_args8(cache, seqs, n_q_heads, q, q_stride, scale, o, o_stride, lse);
+    a.causal = causal != 0;
+    return run_attention(a, p, kCodes, kv.head_dim, 0, nullptr, workspace, (cudaStream_t)stream);
 }
 
 colibri_status_t colibri_attention_decode8_workspace(const colibri_kv_pages8_t* cache, const colibri_seqs_t* seqs,
@@ -774,11 +744,7 @@ colibri_status_t colibri_attention_decode8_workspace(const colibri_kv_pages8_t* 
     const colibri_kv_pages_t kv = view(cache);
     st = check_decode(&kv, seqs, n_q_heads, prefix_len);
     if (st != COLIBRI_OK) return st;
-    colibri_seqs_t none{};
-    Wide w;
-    if ((st = widen(cache, &none, prefix_len, &w)) != COLIBRI_OK) return st;
     *bytes = make_plan(&kv, seqs, n_q_heads, kAttnSuffix, prefix_len).bytes(kv.head_dim);
-    if (prefix_len > 0) *bytes = ((*bytes + 255) & ~(size_t)255) + w.bytes();
     return COLIBRI_OK;
 }
 
@@ -789,30 +755,17 @@ colibri_status_t colibri_attention_decode8(const colibri_kv_pages8_t* cache, con
                                            size_t workspace_bytes, void* stream) {
     size_t need;
     colibri_status_t st = colibri_attention_decode8_workspace(cache, seqs, n_q_heads, prefix_len, &need);
+    if (st == COLIBRI_OK) st = check_attention8(cache, seqs, n_q_heads, q, q_stride, scale, o, o_stride, lse);
     if (st != COLIBRI_OK) return st;
-    const colibri_kv_pages_t kv = view(cache);
-    st = check_attention(&kv, seqs, n_q_heads, q, q_stride, scale, o, o_stride, lse);
-    if (st != COLIBRI_OK) return st;
-    if (!apart_from_scales(cache, n_q_heads, o, o_stride, seqs->n_rows) || (prefix_len > 0) != (prefix_table != nullptr) ||
-        ((uintptr_t)prefix_table & 3))
+    if ((prefix_len > 0) != (prefix_table != nullptr) || ((uintptr_t)prefix_table & 3))
         return COLIBRI_ERR_INVALID_ARG;
-    if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255))) return COLIBRI_ERR_INVALID_ARG;
+    if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255)))
+        return COLIBRI_ERR_INVALID_ARG;
     if (seqs->n_rows == 0) return COLIBRI_OK;
+    const colibri_kv_pages_t kv = view(cache);
     const Plan p = make_plan(&kv, seqs, n_q_heads, kAttnSuffix, prefix_len);
-    AttnArgs a = make_args(&kv, seqs, n_q_heads, q, q_stride, scale, o, o_stride, lse);
-    a.k_scale = cache->k_scale, a.v_scale = cache->v_scale;
-    a.block_shift = shift_of(cache->block), a.int8 = cache->code == COLIBRI_CODE_INT8;
-    Wide w;
-    if (prefix_len > 0) {
-        colibri_seqs_t none{};
-        widen(cache, &none, prefix_len, &w);
-        uint8_t* at = static_cast<uint8_t*>(workspace) + need - w.bytes();
-        const cudaError_t e = run_widen(cache, prefix_table, prefix_len, w, at, (cudaStream_t)stream);
-        if (e != cudaSuccess) return launched(e);
-        prefix_table = reinterpret_cast<const int32_t*>(at);
-    }
-    return run_attention(a, p, kCodes, kv.head_dim, prefix_len, prefix_table, workspace, (cudaStream_t)stream,
-                         prefix_len > 0 ? &w.kv : nullptr);
+    const AttnArgs a = make_args8(cache, seqs, n_q_heads, q, q_stride, scale, o, o_stride, lse);
+    return run_attention(a, p, kCodes, kv.head_dim, prefix_len, prefix_table, workspace, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -29,7 +29,7 @@
 // one load and holds the same 16 elements of q.  Values come by ldmatrix.trans as
 // 16-bit pairs of neighbouring codes of two keys, and the byte permutation that widens
 // a pair also parts even columns from odd ones.
-#include <cuda_runtime.h>
+#pragma once
 
 #include "attn_share.cuh"
 #include "codes.cuh"
@@ -246,21 +246,5 @@ struct CodeRows {
     }
 };
 
-template <int D>
-cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s) {
-    const auto pick = [&](auto code) {
-        using C = decltype(code);
-        return a.group <= 8    ? launch<CodeRows<C, D, 1>>(a, s)
-               : a.group <= 16 ? launch<CodeRows<C, D, 2>>(a, s)
-                               : launch<CodeRows<C, D, 4>>(a, s);
-    };
-    return a.int8 ? pick(I8{}) : pick(E4M3{});
-}
-
 }  // namespace
-
-cudaError_t launch_attn_decode8(int d, const AttnArgs& a, cudaStream_t s) {
-    return d == 64 ? launch_rows<64>(a, s) : launch_rows<128>(a, s);
-}
-
 }  // namespace colibri

@@ -1,5 +1,5 @@
 // Equal shares of the list of all keys, one per warp: the frame of the kernels for
-// single rows (attn_decode.cu, attn_decode8.cu).  A kernel brings `Rows`: the rows of
+// single rows (attn_decode.cu).  A kernel brings `Rows`: the rows of
 // a group, what a step of keys adds to them, and how they are written.
 #pragma once
 
@@ -262,28 +262,6 @@ __device__ __forceinline__ void decode_share(const AttnArgs& a, int per_seq, uin
         first_piece = false;
     }
     cp_wait<0>();
-}
-
-// kEarly: behind a prefix launch the kernel starts on the SMs that this one has left;
-// it needs nothing of it (48 rows over a prefix of 16384 keys: 58 us, 69 waiting
-// first; what it reads: ld_early).  It waits for it at the end, so that the join,
-// which waits for this kernel, finds both done.
-template <typename Rows, bool kEarly>
-__global__ void __launch_bounds__(kDecThreads, Rows::kCtas) attn_decode_kernel(const __grid_constant__ AttnArgs a, int per_seq) {
-    extern __shared__ __align__(128) uint8_t smem[];
-    if constexpr (kEarly) pdl_launch_dependents();
-    else pdl_enter();
-    decode_share<Rows, kEarly>(a, per_seq, smem);
-    if constexpr (kEarly) pdl_wait();
-}
-
-template <typename Rows>
-cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
-    auto kern = a.beside_prefix ? attn_decode_kernel<Rows, true> : attn_decode_kernel<Rows, false>;
-    using T = typename Rows::T;
-    const int bytes = kShareWarps * (Rows::kStages * kStageBytes + Rows::kScratch), per_seq = a.hkv * row_tiles<T>(a.group);
-    cudaError_t e = smem_attr((const void*)kern, bytes);
-    return e != cudaSuccess ? e : launch_pdl(kern, dim3(most_shares<T>(a.group) / kShareWarps), dim3(kDecThreads), bytes, s, a, per_seq);
 }
 
 }  // namespace

@@ -41,8 +41,10 @@
 #include <cuda_runtime.h>
 
 #include <numeric>
+#include <type_traits>
 
 #include "attn_common.cuh"
+#include "codes.cuh"
 #include "kernels.h"
 #include "tc_common.cuh"
 
@@ -51,13 +53,18 @@ namespace {
 
 using namespace tc;
 
-constexpr int kTcThreads = 384;               // 2 softmax warpgroups, 1 of MMA issue and copies
+// 2 softmax warpgroups, 1 of MMA issue and copies; one that widens codes
+template <typename Code> constexpr bool kOfCodes = !std::is_void_v<Code>;
+template <typename Code> constexpr int kTcThreads = kOfCodes<Code> ? 640 : 384;
 constexpr int kTileKeys = 128;
 constexpr uint32_t kHalfBytes = 128 * 128;      // 128 rows of one 128-byte swizzle atom
 
-// Ring slots of 128 keys: 5 of 32 KB, 8 of 16 KB (d = 64).
-template <int D> constexpr int kSlots = D == 128 ? 5 : 8;
+// Ring slots of 128 keys: 5 of 32 KB (4 beside tiles of codes), 8 of 16 KB (d = 64).
+template <int D, typename Code = void> constexpr int kRingSlots = D == 64 ? 8 : kOfCodes<Code> ? 4 : 5;
 template <int D> constexpr uint32_t kTileBytes = (D / 64) * kHalfBytes;
+// Codes: tiles on their way to the widening threads, and steps whose scales are kept.
+template <int D> constexpr int kStaged = D == 64 ? 4 : 2;
+template <int D> constexpr int kScaleSteps = D == 64 ? 16 : 8;
 
 // d = 64 leaves tensor memory for P in columns of its own: S(j + 1) is then formed
 // as soon as S(j) is no longer needed, during the softmax of step j, and the order
@@ -94,6 +101,7 @@ struct TcBars {
     uint64_t item_empty[2];
     uint64_t taken_full;
     uint64_t drain[2];
+    uint64_t near_end;        // codes: the item's last tiles are asked for
     uint64_t never;           // failure-detection tests: nothing arrives
     uint32_t tmem;
     int abort;
@@ -103,11 +111,13 @@ struct TcBars {
     Item item[3];
 };
 
-template <int D>
+template <int D, typename Code>
 constexpr size_t tc_smem_bytes() {
-    return 1024 + 2 * kTileBytes<D> + kSlots<D> * kTileBytes<D> + sizeof(TcBars);
+    return 1024 + 2 * kTileBytes<D> + kRingSlots<D, Code> * kTileBytes<D> + sizeof(TcBars) +
+           (kOfCodes<Code> ? kStaged<D> * kTileKeys * D + kScaleSteps<D> * 64 : 0);
 }
-static_assert(tc_smem_bytes<128>() <= 232448 && tc_smem_bytes<64>() <= 232448, "fits an SM");
+static_assert(tc_smem_bytes<128, void>() <= 232448 && tc_smem_bytes<64, void>() <= 232448, "fits an SM");
+static_assert(tc_smem_bytes<128, E4M3>() <= 232448 && tc_smem_bytes<64, E4M3>() <= 232448, "fits an SM");
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
                                             int c3, uint32_t bar) {
@@ -272,14 +282,18 @@ __device__ __forceinline__ Item work_item(const AttnArgs& a, int x, int y, int t
     return it;
 }
 
-template <int D, bool kPaged>
-__global__ void __launch_bounds__(kTcThreads, 1)
+template <int D, bool kPaged, typename Code>
+__global__ void __launch_bounds__(kTcThreads<Code>, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, AttnArgs a, int tokens, int box, Units units) {
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    constexpr bool kCodes = kOfCodes<Code>;
+    constexpr int kSlots = kRingSlots<D, Code>;
     uint8_t* skv = smem + 2 * kTileBytes<D>;
-    TcBars& bars = *reinterpret_cast<TcBars*>(skv + kSlots<D> * kTileBytes<D>);
+    TcBars& bars = *reinterpret_cast<TcBars*>(skv + kSlots * kTileBytes<D> + (kCodes ? kStaged<D> * kTileKeys * D : 0));
+    // codes: [step of the CTA % kScaleSteps][k, v][16 keys]
+    [[maybe_unused]] float* scales = reinterpret_cast<float*>(&bars + 1);
     const uint32_t q0 = smem_u32(smem), kv0 = smem_u32(skv);
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
@@ -293,16 +307,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(smem_u32(&bars.o_done[t]), 1);
             mbar_init(smem_u32(&bars.s_read[t]), 4);
             mbar_init(smem_u32(&bars.item_full[t]), 1);
-            mbar_init(smem_u32(&bars.item_empty[t]), 11);       // softmax and MMA warps, V's copies
+            mbar_init(smem_u32(&bars.item_empty[t]), kCodes ? 18 : 11);   // softmax and MMA warps, V's copies or the widening warps
             mbar_init(smem_u32(&bars.drain[t]), 1);
             mbar_init(smem_u32(&bars.tail[t]), 2);
             mbar_init(smem_u32(&bars.turn[t]), 1);
         }
-        for (int s = 0; s < kSlots<D>; ++s) {
-            mbar_init(smem_u32(&bars.kv_full[s]), 1);
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(smem_u32(&bars.kv_full[s]), kCodes ? 8 : 1);
             mbar_init(smem_u32(&bars.kv_empty[s]), 2);
         }
         mbar_init(smem_u32(&bars.taken_full), 1);
+        mbar_init(smem_u32(&bars.near_end), 8);
         for (const CUtensorMap* m : {&tm_q, &tm_k, &tm_v})
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
         mbar_init(smem_u32(&bars.never), 1);
@@ -394,7 +409,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (warp < 8) {
         // ------------------------------------------------ softmax, one row per thread
         // (384 x 168 registers at launch = 256 x 208 + 128 x 88)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        // (codes: 640 x 96 = 256 x 152 + 128 x 48 + 256 x 64)
+        if constexpr (kCodes) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int t = warp >> 2, r = tid & 127;
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ts = lane_base + t * 128, to = lane_base + kColO + t * D, tp = lane_base + kColP + t * kStepP;
@@ -406,6 +423,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(bar));
         };
         uint32_t step_no = 0, done_no = 0;                      // of this tile, over all items
+        [[maybe_unused]] uint32_t all_no = 0;                   // of both tiles: steps before this item
         // The warp stays together whatever a wait says: a lane whose wait gave up
         // goes on without waiting, to the end of the item, whose rows become NaN.
         bool ok = true;
@@ -431,9 +449,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int left = lim - (lo + j * kTileKeys);       // keys of this step that the row sees
                 uint32_t s[4][32], p[3][16];
                 uint64_t sum[4], c2 = pack2(c, c), ref2;
-                const auto weights = [&](const uint32_t (&sx)[32], uint32_t (&px)[16]) {
+                [[maybe_unused]] uint64_t v2 = 0;
+                // codes: of 16 keys (sub-chunk u of the step), what their scores are multiplied
+                // by, and their weights.  Keys that the row does not see have neither: their
+                // scales may be anything.  A product that is zero would make NaN of a
+                // masked score.
+                const auto score_scale = [&](int u) {
+                    const float by = scales[(all_no + j) % kScaleSteps<D> * 16 + u] * c;
+                    return left <= 16 * u ? 1.f : by < 1.17549435e-38f ? 1.17549435e-38f : by;
+                };
+                const auto value_scale = [&](int u) {
+                    return left <= 16 * u ? 0.f : scales[(all_no + j) % kScaleSteps<D> * 16 + 8 + u];
+                };
+                const auto weights = [&](const uint32_t (&sx)[32], uint32_t (&px)[16], [[maybe_unused]] int x) {
 #pragma unroll
                     for (int y = 0; y < 16; ++y) {
+                        if constexpr (kCodes) {
+                            if (y % 8 == 0) {
+                                const float by = score_scale(2 * x + y / 8), v = value_scale(2 * x + y / 8);
+                                c2 = pack2(by, by), v2 = pack2(v, v);
+                            }
+                            const float2 e =
+                                unpack2(fma2(pack2(__uint_as_float(sx[2 * y]), __uint_as_float(sx[2 * y + 1])), c2, ref2));
+                            const uint64_t p = pack2(ex2(e.x), ex2(e.y));
+                            sum[y & 3] = add2(sum[y & 3], p);
+                            const float2 w = unpack2(mul2(p, v2));
+                            px[y] = pack_h2<false>(w.x, w.y);
+                            continue;
+                        }
                         const float2 e =
                             unpack2(fma2(pack2(__uint_as_float(sx[2 * y]), __uint_as_float(sx[2 * y + 1])), c2, ref2));
                         const float p0 = ex2(e.x), p1 = ex2(e.y);
@@ -442,20 +485,41 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                 };
                 // S of the step, -infinity where the row sees no key
+                const auto mask = [&](int x) {
+                    if (left >= 32 * x + 32) return;               // (rows of a warp differ by few keys)
+#pragma unroll
+                    for (int y = 0; y < 32; ++y)
+                        if (x * 32 + y >= left) s[x][y] = 0xff800000u;
+                };
                 const auto load_scores = [&]() {
 #pragma unroll
                     for (int x = 0; x < 4; ++x) tmem_ld32(ts + 32 * x, s[x]);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        if (left >= 32 * x + 32) continue;         // (rows of a warp differ by few keys)
-#pragma unroll
-                        for (int y = 0; y < 32; ++y)
-                            if (x * 32 + y >= left) s[x][y] = 0xff800000u;
-                    }
+                    for (int x = 0; x < 4; ++x) mask(x);
                 };
                 // largest of chunks from .. 3, times c
                 const auto largest = [&](int from) {
+                    if constexpr (kCodes) {
+                        float most = -INFINITY;
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            if (u >= 2 * from) {
+                                if (from == 0 && u % 2 == 0) {     // (read again, a quarter at a time)
+                                    tmem_ld32(ts + 16 * u, s[u / 2]);
+                                    tmem_ld_wait();
+                                    mask(u / 2);
+                                }
+                                const uint32_t* z = &s[u / 2][u % 2 * 16];
+                                float top[4];
+#pragma unroll
+                                for (int y = 0; y < 4; ++y)
+                                    top[y] = max3(__uint_as_float(z[4 * y]), __uint_as_float(z[4 * y + 1]),
+                                                  fmaxf(__uint_as_float(z[4 * y + 2]), __uint_as_float(z[4 * y + 3])));
+                                most = fmaxf(most, max3(top[0], top[1], fmaxf(top[2], top[3])) * score_scale(u));
+                            }
+                        return most;
+                    }
                     float top[8];
 #pragma unroll
                     for (int x = 0; x < 8; ++x) top[x] = -INFINITY;
@@ -471,21 +535,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 bool waited = false;                               // for the last step's product
 #pragma unroll 1
                 for (int pass = 0;; ++pass) {
-                    load_scores();
+                    if (!kCodes) load_scores();
                     // The weights are formed on the reference as it is.  Whether it
                     // stands shows in their sum (of the first 96; of the last 32, not
                     // formed yet, in the largest score): a maximum is taken only in
                     // the few steps where it does not
                     ref2 = pack2(-m, -m);
                     sum[0] = sum[1] = sum[2] = sum[3] = 0;
+                    if (kCodes) {
+                        // (a quarter at a time, the next on its way: the widening warps
+                        // leave too few registers for all of S)
+                        tmem_ld32(ts, s[0]);
+                        tmem_ld_wait();
+                    }
 #pragma unroll
-                    for (int x = 0; x < 3; ++x) weights(s[x], p[x]);
+                    for (int x = 0; x < 3; ++x) {
+                        if (kCodes) {
+                            tmem_ld32(ts + 32 * x + 32, s[x + 1]);
+                            mask(x);
+                        }
+                        weights(s[x], p[x], x);
+                        if (kCodes) tmem_ld_wait();
+                    }
+                    if (kCodes) mask(3);
                     const float2 some = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
                     const float most = largest(3), weight = some.x + some.y;
                     const bool high = !(weight <= 16777216.f) || most > m + 24.f;
                     const bool low = l == 0.f && left > 0 && weight < 5.421010862427522e-20f && most < m - 64.f;   // 2^-64
                     if (pass > 0 || !__any_sync(0xffffffffu, live && (high || low))) break;
-                    load_scores();
+                    if (!kCodes) load_scores();
                     const float mn = largest(0);
                     // (a sum above 2^24 has a weight above 2^17)
                     const bool move = live && (mn > m + 16.f || (l == 0.f && mn < m - 64.f && mn != -INFINITY));
@@ -520,7 +598,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                 for (int x = 0; x < 3; ++x) tmem_st16(tp + 16 * x, p[x]);
                 hand_over(&bars.p_most[t]);                        // the product with V starts on these
-                weights(s[3], p[0]);
+                weights(s[3], p[0], 3);
                 tmem_st16(tp + 48, p[0]);
                 hand_over(&bars.p_ready[t]);
                 const float2 sums = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
@@ -528,11 +606,149 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             if (steps > 0) wait(&bars.o_done[t], (kOwnP<D> ? step_no - 1 : done_no++) & 1);
             ok = __all_sync(0xffffffffu, ok);
+            if constexpr (kCodes) all_no += uniform(max(it.steps[0], it.steps[1]));
             write_row(it, t, ok, steps > 0, l, m, to);
             item_left(item_no++);
         }
+    } else if (kCodes && warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if constexpr (kCodes) {
+            // ------------------------------------------------ codes to bf16: each thread copies the
+            // 16 codes that it will widen, kStaged tiles ahead, so that nothing but its own
+            // copies has to be waited for.  A pass of a warp is 8 keys x 64 columns.
+            constexpr int kHalves = D / 64;
+            const int w = warp - 12, row0 = w * 16 + (lane >> 2);
+            const uint32_t staged = kv0 + kSlots * kTileBytes<D> + (w * 32 + lane) * 16;
+            // where 16 codes of a row go: two chunks of its 128-byte swizzled half
+            const uint32_t to = (lane >> 2) * 128 + (((lane & 3) * 2 ^ (lane >> 2)) << 4);
+            struct {                                            // the tile to be copied next
+                int step = 0, nsteps = 0, lo = 0, hi = 0, h = 0, b = 0;
+            } at;
+            // This warp's 16 keys of 32 steps, a step per lane, and of the 32 after them: where
+            // their first row lies (< 0: nowhere), and their scales.  They are read a window
+            // ahead, so that a tile's copies take few instructions.
+            struct Keys {
+                int64_t row;
+                float scale[2];
+            } here, ahead;
+            const int64_t lane_row = (int64_t)(lane >> 2) * a.row_stride + (lane & 3) * 16, next8 = 8 * a.row_stride;
+            const uint8_t *head_k = nullptr, *head_v = nullptr; // row 0 of the head in page 0, this lane's part
+            uint32_t copied = 0, widened = 0, all_no = 0;       // tiles of K and V, steps, over all items
+            bool more = true, loaded = false;
+            const auto look = [&](int step) {
+                Keys x = {-1, {0.f, 0.f}};
+                const int key = at.lo + (step + lane) * kTileKeys + w * 16;
+                const int page = key < at.hi ? attn_page(a, at.b, key >> a.page_shift) : -1;
+                if (page >= 0) {
+                    const int row = key & (a.page_size - 1);
+                    x.row = (int64_t)page * a.page_stride + (int64_t)row * a.row_stride;
+                    const int64_t i = (((int64_t)page * a.hkv + at.h) << (a.page_shift - a.block_shift)) + (row >> a.block_shift);
+                    x.scale[0] = __ldg(a.k_scale + i), x.scale[1] = __ldg(a.v_scale + i);
+                }
+                return x;
+            };
+            const auto copy = [&]() {
+                const int step = at.step, kind = copied & 1;
+                if (kind == 0) {
+                    if (step > 0 && step % 32 == 0) here = ahead, ahead = look(step + 32);
+                    if (step + 1 == at.nsteps) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&bars.near_end));
+                    }
+                    if (lane == step % 32) {
+                        float* to = scales + (all_no + step) % kScaleSteps<D> * 16 + w;
+                        to[0] = here.scale[0], to[8] = here.scale[1];
+                    }
+                }
+                const uint32_t dst = staged + copied % kStaged<D> * (kTileKeys * D);
+                const int keys = at.hi - (at.lo + step * kTileKeys + row0);     // of this lane's first row on
+                const int64_t row = __shfl_sync(0xffffffffu, here.row, step % 32);
+                const uint8_t* src = (kind ? head_v : head_k) + (row >= 0 ? row : 0);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const bool there = row >= 0 && keys > 8 * y;
+                    const uint8_t* from = there ? src + y * next8 : src - lane_row;
+#pragma unroll
+                    for (int x = 0; x < kHalves; ++x) cp16(dst + (y * kHalves + x) * 4096, from + 64 * x, there);
+                }
+                cp_commit();
+                ++copied;
+                if (kind) ++at.step;
+            };
+            bool ok = true;
+            while (ok) {
+                // tiles are asked for as long as there is room; a next item that is not
+                // there yet is waited for only when nothing is left to widen
+                while (more && copied - widened < kStaged<D>) {
+                    if (at.step == at.nsteps) {
+                        if (loaded) all_no += at.nsteps;
+                        loaded = false;
+                        at.step = at.nsteps = 0;
+                        const bool known = item_no == 0 ||
+                            (copied == widened ? item_there(item_no)
+                                               : __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&bars.item_full[item_no & 1]),
+                                                                                       ((item_no >> 1) - !(item_no & 1)) & 1)) != 0);
+                        if (!known) {
+                            if (copied == widened) ok = false;
+                            break;
+                        }
+                        const Item& it = bars.item[item_no & 1];
+                        const int nsteps = uniform(max(it.steps[0], it.steps[1]));
+                        at.lo = uniform(it.lo), at.hi = uniform(it.hi), at.h = uniform(it.h), at.b = uniform(it.b);
+                        if (at.b < 0) {
+                            more = false;
+                            break;
+                        }
+                        at.nsteps = nsteps, loaded = true;
+                        item_left(item_no++);
+                        if (nsteps == 0) {
+                            if (lane == 0) mbar_arrive(smem_u32(&bars.near_end));
+                            continue;
+                        }
+                        here = look(0), ahead = look(32);
+                        head_k = static_cast<const uint8_t*>(a.k) + (int64_t)at.h * a.head_stride + lane_row;
+                        head_v = static_cast<const uint8_t*>(a.v) + (int64_t)at.h * a.head_stride + lane_row;
+                    }
+                    copy();
+                }
+                if (!ok || copied == widened) break;
+                if (copied - widened == kStaged<D>) cp_wait<kStaged<D> - 1>();
+                else cp_wait<0>();
+                const uint32_t slot = widened % kSlots;
+                if (widened >= kSlots) ok = warp_wait(&bars.kv_empty[slot], (widened / kSlots - 1) & 1);
+                if (!ok) break;
+                const uint32_t from = staged + widened % kStaged<D> * (kTileKeys * D);
+                const uint32_t dst = kv0 + slot * kTileBytes<D> + w * 2 * kGroupBytes<D, kPaged> + to;
+                // (all codes are loaded before the first are widened)
+                uint32_t c[2 * kHalves][4];
+#pragma unroll
+                for (int j = 0; j < 2 * kHalves; ++j)
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(c[j][0]), "=r"(c[j][1]), "=r"(c[j][2]), "=r"(c[j][3])
+                                 : "r"(from + j * 4096)
+                                 : "memory");
+#pragma unroll
+                for (int j = 0; j < 2 * kHalves; ++j) {
+                    uint32_t v[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) Code::pairs(c[j][i], v[2 * i], v[2 * i + 1]);
+                    const uint32_t p = dst + j / kHalves * kGroupBytes<D, kPaged> + j % kHalves * kColumnBytes<kPaged>;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p ^ (i << 4)), "r"(v[4 * i]),
+                                     "r"(v[4 * i + 1]), "r"(v[4 * i + 2]), "r"(v[4 * i + 3])
+                                     : "memory");
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars.kv_full[slot]));
+                ++widened;
+            }
+            cp_wait<0>();
+        }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if constexpr (kCodes) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 8 || warp == 10) {
             // ------------------------------------------------ MMA issue, one tile each
             const int t = warp == 8 ? 0 : 1;
@@ -561,7 +777,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             int slot = -1;
             uint32_t lap = 0;
             const auto next = [&]() {
-                if (++slot == kSlots<D>) slot = 0, lap ^= 1;
+                if (++slot == kSlots) slot = 0, lap ^= 1;
                 wait(&bars.kv_full[slot], lap);
                 return slot;
             };
@@ -620,7 +836,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     vslot = next();
                     if (j + 1 < nsteps) kslot = next();
                     const uint32_t v = kv0 + vslot * kTileBytes<D>;
-                    if (j + 1 == nsteps && have > 0) {
+                    if (!kCodes && j + 1 == nsteps && have > 0) {
                         // rows behind the last key: their weights are 0, and 0
                         // times whatever lies there has to be 0.  Each of the
                         // two warps clears half of them.
@@ -692,6 +908,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // the work list; warp 11 V.  Tile i of K is number 2 i of the ring, of V
             // 2 i + 1.  (One code for both warps: a kernel as short as a prefix's takes
             // 2 us more with two, which have to be fetched.)
+            // Codes: warp 9 alone, for Q and the work list.
             const int kind = warp == 11;
             uint32_t filled = 0;                                    // tiles so far, over all items
             uint32_t q_no[2] = {0, 0};
@@ -700,6 +917,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const bool leader = elect_one();
             // (failure-detection tests: no Q and K are copied from item stall_tma on)
             bool ok = kind || a.stall_tma != 1 || warp_wait(&bars.never, 0);
+            if (kCodes && kind) ok = false;
             bool asked = false;
             if (!kind && lane == 0) bars.announced = 1;
             while (ok) {
@@ -732,15 +950,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     __syncwarp();
                 }
+                if constexpr (kCodes) {
+                    // the next item is taken when the last tiles are asked for
+                    ok = ok && warp_wait(&bars.near_end, item_no & 1);
+                    if (!ok) break;
+                    ask();
+                    if (a.stall_tma > 1 && item_no + 1 >= a.stall_tma) ok = warp_wait(&bars.never, 0);
+                }
                 // page ids of 32 boxes, one per lane, and of the 32 after them
                 const int per_step = kTileKeys / box;
                 const auto look = [&](int first) {
                     const int key = lo + (first + lane) * box;
                     return kPaged && key < hi ? attn_page(a, it.b, key >> a.page_shift) : -1;
                 };
-                int ids = look(0), ids_ahead = look(32), page = -1;
-                for (int j = 0; j < nsteps && ok; ++j) {
-                    const uint32_t n = 2 * filled + kind, slot = n % kSlots<D>;
+                int ids = kCodes ? -1 : look(0), ids_ahead = kCodes ? -1 : look(32), page = -1;
+                for (int j = 0; !kCodes && j < nsteps && ok; ++j) {
+                    const uint32_t n = 2 * filled + kind, slot = n % kSlots;
                     const int base = lo + j * kTileKeys;
                     if (kPaged) {
                         const int first = j * per_step;
@@ -754,7 +979,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (a.stall_tma > 1 && item_no + 1 >= a.stall_tma) ok = warp_wait(&bars.never, 0);
                         if (!ok) break;
                     }
-                    if (n >= kSlots<D>) ok = warp_wait(&bars.kv_empty[slot], (n / kSlots<D> - 1) & 1);
+                    if (n >= kSlots) ok = warp_wait(&bars.kv_empty[slot], (n / kSlots - 1) & 1);
                     if (!ok) break;
                     const uint32_t bar = smem_u32(&bars.kv_full[slot]);
                     const uint32_t dst = kv0 + slot * kTileBytes<D>;
@@ -781,7 +1006,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     item_left(item_no++);
                     continue;
                 }
-                if (nsteps == 0) ask();
+                if (!kCodes && nsteps == 0) ask();
                 // the next item
                 ok = warp_wait(&bars.taken_full, item_no & 1);
                 if (!ok) break;
@@ -832,12 +1057,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (bars.abort && tid == 0) {
         atomicExch(&wait_status, DEV_TIMEOUT);
         // none of the copies stays in flight: each slot's last one
-        for (uint32_t slot = 0; slot < kSlots<D>; ++slot) {
+        for (uint32_t slot = 0; slot < kSlots; ++slot) {
             int last = -1;
             for (int kind = 0; kind < 2; ++kind)
-                for (int i = max((int)bars.filled[kind] - kSlots<D>, 0); i < (int)bars.filled[kind]; ++i)
-                    if ((2 * i + kind) % kSlots<D> == (int)slot) last = max(last, 2 * i + kind);
-            if (last >= 0) mbar_wait_drain(smem_u32(&bars.kv_full[slot]), (last / kSlots<D>) & 1, kDrainLimitNs);
+                for (int i = max((int)bars.filled[kind] - kSlots, 0); i < (int)bars.filled[kind]; ++i)
+                    if ((2 * i + kind) % kSlots == (int)slot) last = max(last, 2 * i + kind);
+            if (last >= 0) mbar_wait_drain(smem_u32(&bars.kv_full[slot]), (last / kSlots) & 1, kDrainLimitNs);
         }
     }
     if (bars.abort && warp < 8) {
@@ -890,7 +1115,7 @@ bool encode(CUtensorMap* m, const void* p, int rank, const int64_t* dims, const 
     return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && call();
 }
 
-template <int D, bool kPaged>
+template <int D, bool kPaged, typename Code = void>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     const int tokens = 128 / a.group;
     CUtensorMap tq, tk, tv;
@@ -899,7 +1124,9 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     bool ok = encode(&tq, a.q, 4, qd, qs, qb);
     int box = kTileKeys;
     Units units{};
-    if (kPaged) {
+    if constexpr (kOfCodes<Code>) {
+        tk = tv = tq;                                          // (not used)
+    } else if (kPaged) {
         box = a.page_size < kTileKeys ? a.page_size : kTileKeys;
         int64_t unit;
         if (!attn_tc_units(a, &unit, &units.per_page, &units.per_head, &units.count)) return cudaErrorInvalidValue;
@@ -913,12 +1140,12 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
         ok = ok && encode(&tk, a.k, 4, kd, ks, kb) && encode(&tv, a.v, 4, kd, ks, kb);
     }
     if (!ok) return cudaErrorInvalidValue;
-    auto kern = attn_tc_kernel<D, kPaged>;
-    const int bytes = (int)tc_smem_bytes<D>();
+    auto kern = attn_tc_kernel<D, kPaged, Code>;
+    const int bytes = (int)tc_smem_bytes<D, Code>();
     cudaError_t e = smem_attr((const void*)kern, bytes);
     if (e != cudaSuccess) return e;
     const int64_t items = attn_tc_items(a);
-    return launch_pdl(kern, dim3((unsigned)(items * a.hkv), a.splits), dim3(kTcThreads), bytes, s, tq, tk, tv, a, tokens,
+    return launch_pdl(kern, dim3((unsigned)(items * a.hkv), a.splits), dim3(kTcThreads<Code>), bytes, s, tq, tk, tv, a, tokens,
                       box, units);
 }
 
@@ -951,6 +1178,8 @@ cudaError_t attn_tc_status(int* status, cudaStream_t s) {
 }
 
 cudaError_t launch_attn_tc(int d, const AttnArgs& a, cudaStream_t s) {
+    if (a.k_scale && a.int8) return d == 64 ? launch<64, true, I8>(a, s) : launch<128, true, I8>(a, s);
+    if (a.k_scale) return d == 64 ? launch<64, true, E4M3>(a, s) : launch<128, true, E4M3>(a, s);
     if (a.table) return d == 64 ? launch<64, true>(a, s) : launch<128, true>(a, s);
     return d == 64 ? launch<64, false>(a, s) : launch<128, false>(a, s);
 }

@@ -242,7 +242,7 @@ PROMPT = [
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("lens,hq,hkv,d,code,block,page,layout", PROMPT)
 def test_prompt8(A, lens, hq, hkv, d, code, block, page, layout, causal):
-    p = Problem8(lens, hq, hkv, d, code, block, page, layout, seed=page + d, spare=1, pow2=True)
+    p = Problem8(lens, hq, hkv, d, code, block, page, layout, seed=page + d, spare=1, pow2=d == 64)
     lse = torch.full((p.rows, hq), 9.0, device=p.q.device)
     out = A.attention_prompt_paged(p.cache(A), seqs(A, p), p.q, causal=causal, out=torch.full_like(p.q, 9.0), lse=lse)
     torch.cuda.synchronize()
@@ -265,13 +265,13 @@ DECODE = [
 
 @pytest.mark.parametrize("kv,hq,hkv,d,code,block,page,layout,prefix", DECODE)
 def test_decode8(A, kv, hq, hkv, d, code, block, page, layout, prefix):
-    p = Problem8([(1, t) for t in kv], hq, hkv, d, code, block, page, layout, prefix=prefix, seed=prefix + d, wide=5, pow2=page == 64 or prefix > 0)
+    p = Problem8([(1, t) for t in kv], hq, hkv, d, code, block, page, layout, prefix=prefix, seed=prefix + d, wide=5, pow2=page == 64)
     lse = torch.full((p.rows, hq), 9.0, device=p.q.device)
     out = A.attention_decode(p.cache(A), seqs(A, p, decode=True), p.q, prefix_len=prefix,
                              prefix_table=p.prefix_table if prefix else None, out=torch.full_like(p.q, 9.0), lse=lse)
     torch.cuda.synchronize()
     p.check(out, lse, False)
-    if not prefix and page == 64:                              # the prompt form of the same rows
+    if not prefix:                                             # the prompt form of the same rows
         lse2 = torch.empty_like(lse)
         p.check(A.attention_prompt_paged(p.cache(A), seqs(A, p), p.q, lse=lse2), lse2, True)
 
@@ -289,11 +289,11 @@ def test_every_code(A, d, code):
     raw = every[torch.arange(hkv * d) % 256].view(1, hkv, 1, d).expand(1, hkv, 16, d).cuda()
     for t in (c.k, c.v):
         t.view(torch.uint8).copy_(raw)
-    c.k_scale.fill_(2.0 ** -10), c.v_scale.fill_(0.5)
+    c.k_scale.fill_(2.0 ** -10), c.v_scale.fill_(0.375)
     q = torch.randn(1, hkv, d, generator=g).cuda().to(BF)
     one = torch.ones(1, dtype=torch.int32, device="cuda")
     table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
-    want = (c.v[0, :, 0].float() * 0.5).to(BF)               # (exact)
+    want = (c.v[0, :, 0].float() * 0.375).to(BF)               # (exact)
     lse = torch.empty(1, hkv, device="cuda")
     got = A.attention_decode(c, A.Sequences(None, one, table), q, lse=lse)
     assert (got[0].float() - want.float()).abs().max() <= 2.0 ** -8 * 2 * 168
@@ -301,12 +301,12 @@ def test_every_code(A, d, code):
     assert np.abs(lse[0].double().cpu().numpy() - scores).max() <= 2.0 ** -20 * (1 + np.abs(scores).max())
     for t in (got, A.attention_prompt_paged(c, A.Sequences(torch.tensor([0, 1], dtype=torch.int32, device="cuda"), one,
                                                            table), q)):
-        e = (t[0].float() - c.v[0, :, 0].float() * 0.5).abs()
-        assert (e <= (2.0 ** -7 + 2.0 ** -15) * c.v[0, :, 0].float().abs() * 0.5).all()
+        e = (t[0].float() - c.v[0, :, 0].float() * 0.375).abs()
+        assert (e <= (2.0 ** -7 + 2.0 ** -15) * c.v[0, :, 0].float().abs() * 0.375).all()
 
 
 def test_page_ids_out_of_range_read_zeros(A):
-    p = Problem8([(1, 40), (1, 64)], 4, 2, 64, "e4m3", 16, 16, seed=2, pow2=True)
+    p = Problem8([(1, 40), (1, 64)], 4, 2, 64, "e4m3", 16, 16, seed=2)
     p.table[0, 1], p.table[1, 3] = -1, 10 ** 6
     out = A.attention_decode(p.cache(A), seqs(A, p, decode=True), p.q)
     rows = A.attention_prompt_paged(p.cache(A), seqs(A, p), p.q)
