@@ -57,6 +57,10 @@ struct AttnArgs {
     const float* k_scale;
     const float* v_scale;
     int block_shift, int8;
+    // launch_attn_decode8: rows (token, head of the group) of a sequence that meet a key at
+    // once, 8 or 16, and of a piece
+    int tile_rows, piece_rows;
+    int group_tiles;             // suffix mode: tiles per key head
     uint64_t wait_limit_ns;      // bound of every mbarrier wait
     int stall_tma;               // failure-detection tests only: a CTA's copies of Q and K stop at
                                  // this item of its work (1: the first), 0 never
@@ -79,9 +83,11 @@ cudaError_t attn_tc_status(int* status, cudaStream_t s);
 // groups of up to 32 heads).  part_o null: no prefix; otherwise slot part_slot
 // takes the rows written in one piece.
 bool attn_decode_takes(DType dt, int group);
-size_t attn_decode_pieces(DType dt, int group, bool codes);
+size_t attn_decode_pieces(DType dt, int group);
 cudaError_t launch_attn_decode(DType dt, int d, const AttnArgs& a, cudaStream_t s);
-// The same over codes (bf16 rows).
+// The same over codes (bf16 rows), in suffix mode or prompt mode: tiles of tile_rows rows
+// of a sequence; its pieces.
+size_t attn_decode8_pieces(int tile_rows, int piece_rows);
 cudaError_t launch_attn_decode8(int d, const AttnArgs& a, cudaStream_t s);
 
 // o, lse from the partial rows of `slots` slots, and of the pieces that

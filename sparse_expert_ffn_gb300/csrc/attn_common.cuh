@@ -35,8 +35,8 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
     if (a.mode == kAttnSuffix) {
         s.row0 = b, s.n = 1, s.kv0 = a.prefix_len;
     } else {
-        s.row0 = min(max(__ldg(a.seq_start + b), 0), a.n_rows);
-        s.n = min(max(__ldg(a.seq_start + b + 1), s.row0), a.n_rows) - s.row0;
+        s.row0 = min(max(ld_early<kEarly>(a.seq_start + b), 0), a.n_rows);
+        s.n = min(max(ld_early<kEarly>(a.seq_start + b + 1), s.row0), a.n_rows) - s.row0;
         s.kv0 = 0;
     }
     s.raw = !a.kv_len ? s.n : max(ld_early<kEarly>(a.kv_len + b), 0);
@@ -196,10 +196,20 @@ __device__ __forceinline__ void attn_split(const AttnArgs& a, int sp, int kt, in
 
 // Equal shares of the key list (attn_decode.cu).  The list is made of steps of
 // 4 KB of keys of one (sequence, key head, row tile), one after another; a share
-// goes to one warp.
+// goes to one warp.  Tiles of 8-bit caches may hold rows of several tokens, so that
+// a sequence's number of tiles follows from its rows; others are a group's.
 template <typename T>
 __host__ __device__ constexpr int row_tile(int group) {
-    return sizeof(T) == 4 ? 4 : sizeof(T) == 1 && group <= 8 ? 8 : sizeof(T) == 1 || group <= 16 ? 16 : 32;
+    return sizeof(T) == 4 ? 4 : group <= 16 ? 16 : 32;
+}
+template <typename T>
+__device__ __forceinline__ int tile_rows(const AttnArgs& a) {
+    return sizeof(T) == 1 ? a.tile_rows : row_tile<T>(a.group);
+}
+template <typename T>
+__device__ __forceinline__ int tile_shift(const AttnArgs& a) {
+    const int rows = tile_rows<T>(a);
+    return rows == 4 ? 2 : rows == 8 ? 3 : rows == 16 ? 4 : 5;
 }
 template <typename T>
 __host__ __device__ constexpr int row_tiles(int group) {
@@ -214,9 +224,9 @@ template <typename T, int D> constexpr int kStepKeys = 4096 / (D * (int)sizeof(T
 constexpr int kShareWarps = 4;                    // per CTA
 // CTAs per SM: 3 where registers allow it.
 template <typename T>
-__host__ __device__ constexpr int share_ctas(int group) { return sizeof(T) == 1 && group <= 8 ? 3 : 2; }
+__host__ __device__ constexpr int share_ctas(int rows) { return sizeof(T) == 1 && rows <= 8 ? 3 : 2; }
 template <typename T>
-__host__ __device__ constexpr int most_shares(int group) { return share_ctas<T>(group) * 152 * kShareWarps; }
+__host__ __device__ constexpr int most_shares(int rows) { return share_ctas<T>(rows) * 152 * kShareWarps; }
 constexpr int kMostShares = 3 * 152 * kShareWarps;
 constexpr int kMinSteps = 4;                      // steps of a share at least
 
@@ -224,17 +234,23 @@ constexpr int kMinSteps = 4;                      // steps of a share at least
 template <typename T, int D, bool kEarly>
 __device__ __forceinline__ int seq_steps(const AttnArgs& a, int b) {
     const AttnSeq s = attn_seq<kEarly>(a, b);
-    return s.kv > s.kv0 ? (s.kv - s.kv0 + kStepKeys<T, D> - 1) / kStepKeys<T, D> : 0;
+    return s.kv > s.kv0 && s.n > 0 ? (s.kv - s.kv0 + kStepKeys<T, D> - 1) / kStepKeys<T, D> : 0;
+}
+// Row tiles of sequence b per head.
+template <typename T, bool kEarly>
+__device__ __forceinline__ int seq_tiles(const AttnArgs& a, int b) {
+    if (sizeof(T) > 1) return row_tiles<T>(a.group);
+    if (a.mode == kAttnSuffix) return a.group_tiles;
+    return (attn_seq<kEarly>(a, b).n * a.group + a.tile_rows - 1) >> tile_shift<T>(a);
 }
 
 // The whole list: its length, and the steps before sequence `upto`.  Called by
 // a whole warp.
 template <typename T, int D, bool kEarly>
-__device__ __forceinline__ void count_steps(const AttnArgs& a, int per_seq, int upto, int64_t* total,
-                                            int64_t* before) {
+__device__ __forceinline__ void count_steps(const AttnArgs& a, int upto, int64_t* total, int64_t* before) {
     int64_t all = 0, part = 0;
     for (int b = threadIdx.x & 31; b < a.n_seqs; b += 32) {
-        const int64_t u = (int64_t)seq_steps<T, D, kEarly>(a, b) * per_seq;
+        const int64_t u = (int64_t)seq_steps<T, D, kEarly>(a, b) * seq_tiles<T, kEarly>(a, b) * a.hkv;
         all += u;
         if (b < upto) part += u;
     }

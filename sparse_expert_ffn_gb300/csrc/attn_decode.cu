@@ -46,6 +46,7 @@ struct TensorRows {
     using T = __nv_bfloat16;
     using Out = T;
     static constexpr int kD = D, kRows = 16 * MT, KS = kStepKeys<T, D>, kScratch = 0, kStages = 3, kCtas = 2;
+    static constexpr bool kMany = false;
     uint32_t qf[MT][D / 16][4];
     float o[MT][D / 8][4], m[MT][2], l[MT][2];
 
@@ -195,6 +196,7 @@ struct FloatRows {
     using T = float;
     using Out = T;
     static constexpr int kD = D, kRows = row_tile<T>(0), KS = kStepKeys<T, D>, kParts = 32 / KS, kStages = 3, kCtas = 2;
+    static constexpr bool kMany = false;
     static constexpr int kScratch = G * KS * 4;                    // a step's weights
     static constexpr int kPairs = D / 64;                          // column pairs of a lane
     uint64_t q[G][16], o[G][kPairs];                               // columns 32 (lane / KS) .. + 31 of q
@@ -315,11 +317,11 @@ struct FloatRows {
 // first; what it reads: ld_early).  It waits for it at the end, so that the join,
 // which waits for this kernel, finds both done.
 template <typename Rows, bool kEarly>
-__global__ void __launch_bounds__(kDecThreads, Rows::kCtas) attn_decode_kernel(const __grid_constant__ AttnArgs a, int per_seq) {
+__global__ void __launch_bounds__(kDecThreads, Rows::kCtas) attn_decode_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
     if constexpr (kEarly) pdl_launch_dependents();
     else pdl_enter();
-    decode_share<Rows, kEarly>(a, per_seq, smem);
+    decode_share<Rows, kEarly>(a, smem);
     if constexpr (kEarly) pdl_wait();
 }
 
@@ -327,15 +329,18 @@ template <typename Rows>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     auto kern = a.beside_prefix ? attn_decode_kernel<Rows, true> : attn_decode_kernel<Rows, false>;
     using T = typename Rows::T;
-    const int bytes = kShareWarps * (Rows::kStages * kStageBytes + Rows::kScratch), per_seq = a.hkv * row_tiles<T>(a.group);
+    const int bytes = kShareWarps * (Rows::kStages * kStageBytes + Rows::kScratch);
     cudaError_t e = smem_attr((const void*)kern, bytes);
-    return e != cudaSuccess ? e : launch_pdl(kern, dim3(most_shares<T>(a.group) / kShareWarps), dim3(kDecThreads), bytes, s, a, per_seq);
+    return e != cudaSuccess ? e : launch_pdl(kern, dim3(most_shares<T>(Rows::kRows) / kShareWarps), dim3(kDecThreads), bytes, s, a);
 }
 
 }  // namespace
 
-size_t attn_decode_pieces(DType dt, int group, bool codes) {
-    if (codes) return (size_t)most_shares<uint8_t>(group) * 2 * piece_rows<uint8_t>(group);
+size_t attn_decode8_pieces(int tile_rows, int piece_rows) {
+    return (size_t)most_shares<uint8_t>(tile_rows) * 2 * piece_rows;
+}
+
+size_t attn_decode_pieces(DType dt, int group) {
     return dt == DType::BF16 ? (size_t)most_shares<__nv_bfloat16>(group) * 2 * piece_rows<__nv_bfloat16>(group)
                              : (size_t)most_shares<float>(group) * 2 * piece_rows<float>(group);
 }
@@ -360,7 +365,9 @@ template <int D>
 static cudaError_t launch_codes(const AttnArgs& a, cudaStream_t s) {
     const auto pick = [&](auto code) {
         using C = decltype(code);
-        return a.group <= 8 ? launch<CodeRows<C, D, 1>>(a, s) : launch<CodeRows<C, D, 2>>(a, s);
+        if (a.mode == kAttnPrompt)
+            return a.tile_rows == 8 ? launch<CodeRows<C, D, 1, true>>(a, s) : launch<CodeRows<C, D, 2, true>>(a, s);
+        return a.tile_rows == 8 ? launch<CodeRows<C, D, 1, false>>(a, s) : launch<CodeRows<C, D, 2, false>>(a, s);
     };
     return a.int8 ? pick(I8{}) : pick(E4M3{});
 }

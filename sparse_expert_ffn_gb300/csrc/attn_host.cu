@@ -229,6 +229,7 @@ struct Plan {
     int prefix = 0;      // ranges of the prefix (0: no prefix launch)
     int own = 1;         // ranges of the sequences' own keys
     bool shares = false;
+    int tile_rows = 0, piece_rows = 0;         // of launch_attn_decode8
     size_t rows = 0, pieces = 0;     // partial rows of a slot; piece rows
     int slots() const { return prefix == 0 && own == 1 ? 0 : prefix + own; }
     size_t lse_bytes() const { return ((slots() * rows + pieces) * 4 + 255) & ~(size_t)255; }
@@ -265,6 +266,18 @@ int splits_for(const AttnArgs& a, const colibri_kv_pages_t* kv, int64_t keys) {
               : choose_splits(attn_simt_items(a) * kv->n_kv_heads, keys, 2 * kSms, 64);
 }
 
+// Prompts over codes whose sequences have few rows each (drafts to be verified): tiles of
+// 16 rows read the keys once each, at HBM's rate, where the tensor-core kernel walks
+// them with one or two tiles per CTA and waits for one step's chain after another.
+constexpr int kFewRows = 32;
+bool few_rows(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int group, int64_t keys) {
+    const int64_t rows = (int64_t)s->n_rows * group;
+    // (and the list of steps is counted in 64 bits, times the shares, even where every
+    // sequence claims all rows)
+    return rows <= kFewRows * (int64_t)s->n_seqs &&
+           ((double)keys / 32 + 1) * kv->n_kv_heads * ((double)rows / 8 + 1) * s->n_seqs <= 1e15;
+}
+
 Plan make_plan(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq, int mode, int prefix_len) {
     const int64_t keys = s->page_table ? (int64_t)s->table_stride * kv->page_size : s->n_rows;
     AttnArgs a{};
@@ -273,9 +286,15 @@ Plan make_plan(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int hq, in
     Plan p;
     if (s->n_seqs == 0) return p;
     p.rows = (size_t)s->n_rows * hq;
-    if (mode == kAttnSuffix && attn_decode_takes(dtype_of(kv->dtype), a.group)) {
+    if (kv->dtype == kCodes && (mode == kAttnSuffix || few_rows(kv, s, a.group, keys))) {
+        const int64_t rows = (int64_t)s->n_rows * a.group;         // (one token each: n_rows sequences)
         p.shares = true;
-        p.pieces = attn_decode_pieces(dtype_of(kv->dtype), a.group, kv->dtype == kCodes);
+        p.tile_rows = rows <= 8 * (int64_t)s->n_seqs ? 8 : 16;
+        p.piece_rows = mode == kAttnSuffix ? std::min(a.group, p.tile_rows) : p.tile_rows;
+        p.pieces = attn_decode8_pieces(p.tile_rows, p.piece_rows);
+    } else if (mode == kAttnSuffix && attn_decode_takes(dtype_of(kv->dtype), a.group)) {
+        p.shares = true;
+        p.pieces = attn_decode_pieces(dtype_of(kv->dtype), a.group);
     } else {
         p.own = splits_for(a, kv, std::max<int64_t>(keys - prefix_len, 1));
     }
@@ -379,6 +398,8 @@ colibri_status_t run_attention(AttnArgs a, const Plan& p, int dtype, int d, int 
         e = launch_attention(dtype, d, f, s);
     }
     a.splits = p.own;
+    a.tile_rows = p.tile_rows, a.piece_rows = p.piece_rows;
+    if (p.tile_rows) a.group_tiles = (a.group + p.tile_rows - 1) / p.tile_rows;
     a.part_slot = p.prefix;
     a.beside_prefix = p.prefix > 0;
     if (e == cudaSuccess)

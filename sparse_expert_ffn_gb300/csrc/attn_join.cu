@@ -24,19 +24,37 @@ struct Place {
     int live;             // the row belongs to a sequence, and has parts to join
     int c0, c1;           // shares that hold its keys
     int first_is_last;    // its piece of share c0 is that share's last
+    int tile_row;         // the row's number in a piece
 };
 
 // Called by a whole warp.
 template <typename T, int D, bool kEarly>
-__device__ __forceinline__ Place row_parts(const AttnArgs& a, int row, int head, int slots, int shares_per_seq) {
-    Place p = {1, 0, -1, 0};
-    if (shares_per_seq) {
+__device__ __forceinline__ Place row_parts(const AttnArgs& a, int row, int head, int slots, bool in_shares) {
+    Place p = {1, 0, -1, 0, 0};
+    if (in_shares) {
         int64_t total, first;
-        count_steps<T, D, kEarly>(a, shares_per_seq, row, &total, &first);
-        const int steps = seq_steps<T, D, kEarly>(a, row);
+        int b = row, in_seq = head % a.group;                      // the row's sequence, its number there
+        if (sizeof(T) == 1 && a.mode == kAttnPrompt) {
+            b = -1;
+            for (int base = 0; base < a.n_seqs && b < 0; base += 32) {
+                const int q = base + (threadIdx.x & 31);
+                const bool holds = q < a.n_seqs && row >= max(ld_early<kEarly>(a.seq_start + q), 0) &&
+                                   row < ld_early<kEarly>(a.seq_start + q + 1);
+                const unsigned hit = __ballot_sync(0xffffffffu, holds);
+                if (hit) b = base + __ffs(hit) - 1;
+            }
+            if (b < 0) {
+                p.live = 0;
+                return p;
+            }
+            in_seq += (row - attn_seq<kEarly>(a, b).row0) * a.group;
+        }
+        p.tile_row = in_seq & (tile_rows<T>(a) - 1);
+        count_steps<T, D, kEarly>(a, b, &total, &first);
+        const int steps = seq_steps<T, D, kEarly>(a, b);
         if (steps > 0) {
-            const int shares = share_count(total, most_shares<T>(a.group));
-            first += (int64_t)((head / a.group) * row_tiles<T>(a.group) + (head % a.group) / row_tile<T>(a.group)) * steps;
+            const int shares = share_count(total, most_shares<T>(tile_rows<T>(a)));
+            first += (int64_t)((head / a.group) * seq_tiles<T, kEarly>(a, b) + (in_seq >> tile_shift<T>(a))) * steps;
             p.c0 = share_of(total, shares, first);
             p.c1 = share_of(total, shares, first + steps - 1);
             p.first_is_last = share_begin(total, shares, p.c0) < first;
@@ -59,7 +77,7 @@ constexpr int kEarlySeqs = 128;
 
 template <typename T, int D, int kThreads>
 __global__ void __launch_bounds__(kThreads) attn_join_kernel(const __grid_constant__ AttnArgs a, int slots,
-                                                             int shares_per_seq) {
+                                                             bool in_shares) {
     using Out = std::conditional_t<sizeof(T) == 4, float, __nv_bfloat16>;
     constexpr int kWarps = kThreads / 32;
     __shared__ float4 rows[kWarps][D / 4];
@@ -69,19 +87,18 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const __grid_consta
     const uint32_t flat = blockIdx.x;
     const int64_t total_rows = (int64_t)a.n_rows * a.hq;
     const int row = (int)(flat / (uint32_t)a.hq), head = (int)(flat % (uint32_t)a.hq);
-    const int tile_row = (head % a.group) % row_tile<T>(a.group);
     const bool early = a.n_seqs <= kEarlySeqs;
     if (!early) pdl_enter();
     if (warp == 0) {
-        const Place p = early ? row_parts<T, D, true>(a, row, head, slots, shares_per_seq)
-                              : row_parts<T, D, false>(a, row, head, slots, shares_per_seq);
+        const Place p = early ? row_parts<T, D, true>(a, row, head, slots, in_shares)
+                              : row_parts<T, D, false>(a, row, head, slots, in_shares);
         if (lane == 0) place = p;
     }
     if (early) pdl_enter();
     __syncthreads();
     if (!place.live) return;
     const int c0 = place.c0, c1 = place.c1;
-    const bool one = shares_per_seq && c0 == c1;                   // whole, in slot part_slot
+    const bool one = in_shares && c0 == c1;                   // whole, in slot part_slot
     const int in_slots = slots + (one ? 1 : 0), parts = in_slots + (one ? 0 : c1 - c0 + 1);
     float top = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -96,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const __grid_consta
                 const int c = c0 + i - in_slots;
                 const bool slot = i < in_slots;
                 const int64_t at = slot ? i * total_rows + flat
-                                        : ((int64_t)c * 2 + (c == c0 && place.first_is_last)) * piece_rows<T>(a.group) + tile_row;
+                                        : ((int64_t)c * 2 + (c == c0 && place.first_is_last)) * (sizeof(T) == 1 ? a.piece_rows : piece_rows<T>(a.group)) + place.tile_row;
                 w[k] = (slot ? a.part_lse : a.piece_lse)[at];
                 if (lane < D / 4)
                     v[k] = *reinterpret_cast<const float4*>((slot ? a.part_o : a.piece_o) + at * D + lane * 4);
@@ -140,11 +157,10 @@ template <typename T, int D>
 cudaError_t launch(const AttnArgs& a, int slots, bool shares, cudaStream_t s) {
     const int64_t rows = (int64_t)a.n_rows * a.hq;
     if (rows == 0) return cudaSuccess;
-    const int per_seq = shares ? a.hkv * row_tiles<T>(a.group) : 0;
     // few rows may have many pieces each (one sequence: 32 rows of 152), many rows few
     if (rows <= 2 * 152)
-        return launch_pdl(attn_join_kernel<T, D, 512>, dim3((unsigned)rows), dim3(512), 0, s, a, slots, per_seq);
-    return launch_pdl(attn_join_kernel<T, D, 128>, dim3((unsigned)rows), dim3(128), 0, s, a, slots, per_seq);
+        return launch_pdl(attn_join_kernel<T, D, 512>, dim3((unsigned)rows), dim3(512), 0, s, a, slots, shares);
+    return launch_pdl(attn_join_kernel<T, D, 128>, dim3((unsigned)rows), dim3(128), 0, s, a, slots, shares);
 }
 
 }  // namespace

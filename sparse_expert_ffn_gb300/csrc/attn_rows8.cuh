@@ -59,9 +59,11 @@ __device__ __forceinline__ uint32_t turned8x8(uint32_t v) {
 
 constexpr float kHigh = 15.f, kSet = 6.f;      // log2 of a row's largest weight: at most, and once set
 
-// Up to 8 NT rows of a group.  g = lane / 4, c = lane % 4.
-template <typename Code, int D, int NT>
+// Up to 8 NT rows of a group, or (kTokens) of several tokens times a group.  g = lane / 4,
+// c = lane % 4.
+template <typename Code, int D, int NT, bool kTokens>
 struct CodeRows {
+    static constexpr bool kMany = kTokens;
     using T = uint8_t;
     using Out = __nv_bfloat16;
     static constexpr int kD = D, kRows = 8 * NT, KS = kStepKeys<T, D>, kScratch = 0;
@@ -69,22 +71,32 @@ struct CodeRows {
     uint32_t qf[NT][D / 16][2];                                    // row g
     // rows 2 c and 2 c + 1; o: columns 16 x + 2 g of both, then 16 x + 2 g + 1
     float o[NT][D / 16][4], m[NT][2], l[NT][2], f[NT][2];          // f: scale * log2(e) / 2^e
+    int limit[NT][2], least;                                       // keys that the rows see, and all of them
 
     template <bool kEarly>
-    __device__ __forceinline__ void begin(const AttnArgs& a, int b, int h, int r0) {
+    __device__ __forceinline__ void begin(const AttnArgs& a, const AttnSeq& q_rows, int h, int r0) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             // of each 64 columns of row g the 16 from 16 c on
-            const int row = r0 + 8 * t + (lane >> 2);
-            const uint4* q = reinterpret_cast<const uint4*>(
-                static_cast<const __nv_bfloat16*>(a.q) + (int64_t)b * a.q_stride + (int64_t)(h * a.group + row) * D);
+            const int row = r0 + 8 * t + (lane >> 2), token = kTokens ? row / a.group : 0;
+            const bool there = row < q_rows.n * a.group;
+            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                            (int64_t)(q_rows.row0 + token) * a.q_stride +
+                                                            (int64_t)(h * a.group + row - token * a.group) * D);
+            if constexpr (kTokens) {
+                const int sees = there ? attn_limit(a, q_rows, token) : q_rows.kv;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) limit[t][j] = __shfl_sync(0xffffffffu, sees, 4 * (2 * (lane & 3) + j));
+                least = t == 0 ? sees : min(least, sees);
+                least = __reduce_min_sync(0xffffffffu, least);
+            }
             uint32_t w[D / 64][8], top = 0;
 #pragma unroll
             for (int y = 0; y < D / 64; ++y)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint4 v = row < a.group ? ld_early<kEarly>(q + y * 8 + (lane & 3) * 2 + i) : make_uint4(0u, 0u, 0u, 0u);
+                    const uint4 v = there ? ld_early<kEarly>(q + y * 8 + (lane & 3) * 2 + i) : make_uint4(0u, 0u, 0u, 0u);
                     w[y][4 * i] = v.x, w[y][4 * i + 1] = v.y, w[y][4 * i + 2] = v.z, w[y][4 * i + 3] = v.w;
                 }
             // (magnitudes as whole numbers: NaN and infinity on top)
@@ -111,8 +123,9 @@ struct CodeRows {
             for (int x = 0; x < D / 16; ++x) o[t][x][0] = o[t][x][1] = o[t][x][2] = o[t][x][3] = 0.f;
         }
     }
-    // K and V of `keys` keys at ks and vs; scale: lane 4 kind + s has that of keys 16 s ..
-    __device__ __forceinline__ void step(const AttnArgs& a, uint32_t ks, uint32_t vs, int keys, float scale) {
+    // K and V of keys key0 .. hi - 1 (KS of them at most) at ks and vs; scale: lane
+    // 4 kind + s has that of keys 16 s ..
+    __device__ __forceinline__ void step(const AttnArgs& a, uint32_t ks, uint32_t vs, int hi, int key0, float scale) {
         const int lane = threadIdx.x & 31, g = lane >> 2;
         const auto at = [](int key, int chunk) {
             return key * D + (D == 64 ? (chunk ^ (key >> 1 & 3)) << 4 : (chunk ^ code_turn(key)) << 4);
@@ -156,15 +169,14 @@ struct CodeRows {
                     const float by = sk[n] * f[t][j];
                     s[t][n][j] *= by, s[t][n][j + 2] *= by;
                 }
-        if (keys < KS) {
+        if ((kTokens ? min(hi, least) : hi) - key0 < KS) {
 #pragma unroll
-            for (int n = 0; n < KS / 16; ++n)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (n * 16 + (e >> 1) * 8 + g >= keys) {
+                for (int n = 0; n < KS / 16; ++n)
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) s[t][n][e] = -INFINITY;
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        if (key0 + n * 16 + (e >> 1) * 8 + g >= (kTokens ? min(hi, limit[t][e & 1]) : hi)) s[t][n][e] = -INFINITY;
         }
         uint32_t pf[NT][KS / 16][2];
 #pragma unroll

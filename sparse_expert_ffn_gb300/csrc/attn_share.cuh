@@ -34,7 +34,7 @@ __device__ __forceinline__ uint32_t bf16x2(float x, float y) {
 // A position in a warp's share: the piece it is in, step by step.
 template <typename T, int D, bool kEarly>
 struct Walk {
-    int b, units;              // sequence, its steps per (head, row tile)
+    int b, units, tiles;       // sequence, its steps per (head, row tile), its row tiles per head
     int64_t in_seq;            // steps of sequence b before the piece
     int item;                  // (head, row tile) of the sequence
     int lo, hi;                // keys of the piece
@@ -42,11 +42,12 @@ struct Walk {
     bool whole;                // the piece is all of the sequence's steps
 
     // The piece at in_seq, of at most `left` steps.  False: nothing there.
-    __device__ __forceinline__ bool piece(const AttnArgs& a, int per_seq, int64_t left) {
-        if (in_seq == (int64_t)units * per_seq) {
+    __device__ __forceinline__ bool piece(const AttnArgs& a, int64_t left) {
+        if (in_seq == (int64_t)units * tiles * a.hkv) {
             in_seq = 0, units = 0;
             while (++b < a.n_seqs && (units = seq_steps<T, D, kEarly>(a, b)) == 0) {}
             if (units == 0) return false;                          // (not reached: left > 0)
+            tiles = seq_tiles<T, kEarly>(a, b);
         }
         const AttnSeq s = attn_seq<kEarly>(a, b);
         item = (int)(in_seq / units);
@@ -167,23 +168,23 @@ struct Stream {
 };
 
 template <typename Rows, bool kEarly>
-__device__ __forceinline__ void decode_share(const AttnArgs& a, int per_seq, uint8_t* smem) {
+__device__ __forceinline__ void decode_share(const AttnArgs& a, uint8_t* smem) {
     using T = typename Rows::T;
     constexpr int D = Rows::kD, KS = Rows::KS, kStages = Rows::kStages, kRingBytes = kStages * kStageBytes;
     const int lane = threadIdx.x & 31, share = blockIdx.x * kShareWarps + (threadIdx.x >> 5);
-    const int tiles = row_tiles<T>(a.group);
     // this warp's share of the list, and the sequence that its first step lies in
     int64_t total, left, before = 0, u0;
-    count_steps<T, D, kEarly>(a, per_seq, 0, &total, &left);
+    count_steps<T, D, kEarly>(a, 0, &total, &left);
     if (total == 0) return;
-    const int shares = share_count(total, most_shares<T>(a.group));
+    const int shares = share_count(total, most_shares<T>(tile_rows<T>(a)));
     if (share >= shares) return;
     u0 = share_begin(total, shares, share);
     left = share_begin(total, shares, share + 1) - u0;             // (at least one)
     Walk<T, D, kEarly> load;
     for (int base = 0;; base += 32) {
         const int mine = base + lane < a.n_seqs ? seq_steps<T, D, kEarly>(a, base + lane) : 0;
-        int64_t upto = (int64_t)mine * per_seq;
+        const int tiles = mine ? seq_tiles<T, kEarly>(a, base + lane) : 0;
+        int64_t upto = (int64_t)mine * tiles * a.hkv;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
@@ -194,7 +195,8 @@ __device__ __forceinline__ void decode_share(const AttnArgs& a, int per_seq, uin
             const int src = __ffs(holds) - 1;
             load.b = base + src;
             load.units = __shfl_sync(0xffffffffu, mine, src);
-            load.in_seq = u0 - before - (__shfl_sync(0xffffffffu, upto, src) - (int64_t)load.units * per_seq);
+            load.tiles = __shfl_sync(0xffffffffu, tiles, src);
+            load.in_seq = u0 - before - (__shfl_sync(0xffffffffu, upto, src) - (int64_t)load.units * load.tiles * a.hkv);
             break;
         }
         before += __shfl_sync(0xffffffffu, upto, 31);
@@ -212,8 +214,8 @@ __device__ __forceinline__ void decode_share(const AttnArgs& a, int per_seq, uin
         if constexpr (sizeof(T) == 1) st.shift_scales();
         if (to_load > 0) {
             if (load.step == load.count) {
-                if (!load.piece(a, per_seq, to_load)) return;
-                st.begin(a, load.b, load.item / tiles, load.lo, load.hi);
+                if (!load.piece(a, to_load)) return;
+                st.begin(a, load.b, load.item / load.tiles, load.lo, load.hi);
             }
             st.copy(a, load.step++, ring + slot_in * kStageBytes);
             --to_load;
@@ -224,10 +226,19 @@ __device__ __forceinline__ void decode_share(const AttnArgs& a, int per_seq, uin
     for (int i = 0; i < kStages - 1; ++i) copy_next(), cp_commit();
     bool first_piece = true;
 #pragma unroll 1
-    while (left > 0 && at.piece(a, per_seq, left)) {
-        const int b = at.b, h = at.item / tiles, r0 = (at.item % tiles) * Rows::kRows;
+    while (left > 0 && at.piece(a, left)) {
+        const int b = at.b, h = at.item / at.tiles, r0 = (at.item % at.tiles) * Rows::kRows;
         Rows rows;
-        rows.template begin<kEarly>(a, b, h, r0);
+        // the sequence's first row and its rows times heads of the group
+        int first_row = b, count = a.group;
+        if constexpr (sizeof(T) == 1) {
+            AttnSeq s = {b, 1, 0, 0, 0};
+            if constexpr (Rows::kMany) s = attn_seq<kEarly>(a, b);
+            first_row = s.row0, count = s.n * a.group;
+            rows.template begin<kEarly>(a, s, h, r0);
+        } else {
+            rows.template begin<kEarly>(a, b, h, r0);
+        }
 #pragma unroll 1
         for (int step = 0; step < at.count; ++step) {
             cp_wait<kStages - 2>();
@@ -237,25 +248,27 @@ __device__ __forceinline__ void decode_share(const AttnArgs& a, int per_seq, uin
             cp_commit();
             const uint32_t ks = ring + slot_out * kStageBytes, vs = ks + kStageBytes / 2;
             slot_out = slot_out == kStages - 1 ? 0 : slot_out + 1;
-            if constexpr (sizeof(T) == 1) rows.step(a, ks, vs, at.hi - (at.lo + step * KS), kStages == 2 ? st.waiting : st.scale);
+            if constexpr (sizeof(T) == 1) rows.step(a, ks, vs, at.hi, at.lo + step * KS, kStages == 2 ? st.waiting : st.scale);
             else rows.step(a, ks, vs, at.hi - (at.lo + step * KS), scratch);
         }
         left -= at.count;
         // the piece's rows: the result, or a part of it
         rows.end([&](int row, float m, float sum, bool writes_sum, auto write) {
-            const int g = r0 + row;
-            if (g >= a.group) return;
+            int g = r0 + row, to_row = first_row;
+            if (g >= count) return;
+            if (Rows::kMany) to_row += g / a.group, g %= a.group;
             const float inv = sum > 0.f ? 1.f / sum : sum;         // no key: 0; NaN stays
             const float lse2 = sum == 0.f ? -INFINITY : m + log2f(sum);
             const int head = h * a.group + g;
-            const int64_t flat = (int64_t)b * a.hq + head;
+            const int64_t flat = (int64_t)to_row * a.hq + head;
             if (at.whole && !a.part_o) {
-                write(static_cast<typename Rows::Out*>(a.o) + (int64_t)b * a.o_stride + (int64_t)head * D, inv);
+                write(static_cast<typename Rows::Out*>(a.o) + (int64_t)to_row * a.o_stride + (int64_t)head * D, inv);
                 if (writes_sum && a.lse) a.lse[flat] = lse2 * kLn2;
                 return;
             }
             const int64_t to = at.whole ? (int64_t)a.part_slot * a.n_rows * a.hq + flat
-                                        : ((int64_t)share * 2 + (first_piece ? 0 : 1)) * piece_rows<T>(a.group) + row;
+                                        : ((int64_t)share * 2 + (first_piece ? 0 : 1)) *
+                                                  (sizeof(T) == 1 ? a.piece_rows : piece_rows<T>(a.group)) + row;
             write((at.whole ? a.part_o : a.piece_o) + to * D, inv);
             if (writes_sum) (at.whole ? a.part_lse : a.piece_lse)[to] = lse2;
         });

@@ -236,6 +236,9 @@ PROMPT = [
     ([(16, 5000)], 8, 1, 128, "e4m3", 16, 32, "heads"),                # few rows far into a context
     ([(2, 900), (5, 33), (7, 1031), (3, 3)], 32, 8, 128, "int8", 32, 64, "rows"),   # drafts
     ([(3, 40)], 128, 1, 64, "e4m3", 16, 16, "heads"),
+    ([(5, 700), (0, 100), (12, 12), (1, 2000), (9, 31)], 6, 2, 64, "e4m3", 32, 32, "heads"),
+    ([(1, 300)] * 5 + [(2, 64)] + [(1, 0)], 3, 3, 128, "int8", 16, 16, "rows"),
+    ([(6, 1500 + 40 * i) for i in range(40)], 16, 4, 128, "e4m3", 16, 64, "heads"),   # more drafts than shares' ends
 ]
 
 
