@@ -84,19 +84,39 @@ __global__ void __launch_bounds__(kThreads, 3) append8_kernel(const __grid_const
     __shared__ Span span;
     __shared__ uint32_t most[2][kSliceHeads];
     __shared__ float2 fit[2][kSliceHeads];         // 1 / scale, old scale / scale
+    __shared__ uint64_t unit[64];
     pdl_enter();
     const int tid = threadIdx.x, lane = tid % kLanes, grp = tid / kLanes;
+    const int pairs = a.freq ? a.rot_dim >> 1 : 0;
     if (tid < 32) {
         const Span s = find_span(a, blockIdx.x);
         if (tid == 0) span = s;
+    } else if (tid >= kThreads - 64 && tid - (kThreads - 64) < pairs) {
+        unit[tid - (kThreads - 64)] = pair_unit(a, tid - (kThreads - 64));
     }
     for (int i = tid; i < 2 * kSliceHeads; i += kThreads) most[i / kSliceHeads][i % kSliceHeads] = 0;
     __syncthreads();
     const Span sp = span;
     if (sp.seq < 0) return;
-    const int pairs = a.freq ? a.rot_dim >> 1 : 0;
+    // heads y, y + slices, ...; lane groups take units (query heads, then keys, then
+    // values) of one row in turn, `per` groups a row (a power of two)
+    const int slices = gridDim.y, y0 = blockIdx.y;
+    const int nq = (a.hq - y0 + slices - 1) / slices;
+    int per = 1;
+    while (2 * per * sp.rows <= kGroups) per *= 2;
+    const int sub = grp % per;
+    const auto first_of = [&](int base) { return (sub - base) & (per - 1); };   // of the units from base on
+    // rows' heads are fetched into L2 ahead of their loads
+    const auto touch = [&](const BF* row, int h, int heads) {
+        if (h < heads) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + (int64_t)(y0 + h * slices) * D + 16 * lane));
+    };
+    if (grp / per < sp.rows) {
+        const int64_t row = sp.row0 + grp / per;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) touch(static_cast<const BF*>(a.q) + row * a.q_stride, sub + c * per, nq);
+    }
     for (int e = tid; e < sp.rows * pairs; e += kThreads)
-        turn[e] = row_turn(a, sp.row0 + e / pairs, sp.lo + e / pairs, e % pairs);
+        turn[e] = row_turn(a, sp.row0 + e / pairs, sp.lo + e / pairs, e % pairs, unit[e % pairs]);
     // the block's place
     int page = -1;
     if (sp.lo >= 0 && (sp.lo >> a.page_shift) < a.table_stride) {
@@ -105,14 +125,7 @@ __global__ void __launch_bounds__(kThreads, 3) append8_kernel(const __grid_const
     }
     __syncthreads();
 
-    // heads y, y + slices, ...; lane groups take units (query heads, then keys, then
-    // values) of one row in turn, `per` groups a row (a power of two)
-    const int slices = gridDim.y, y0 = blockIdx.y;
-    const int nq = (a.hq - y0 + slices - 1) / slices, nk = page >= 0 ? (a.hkv - y0 + slices - 1) / slices : 0;
-    int per = 1;
-    while (2 * per * sp.rows <= kGroups) per *= 2;
-    const int sub = grp % per;
-    const auto first_of = [&](int base) { return (sub - base) & (per - 1); };   // of the units from base on
+    const int nk = page >= 0 ? (a.hkv - y0 + slices - 1) / slices : 0;
     // this lane's elements (rope_append.cu)
     int c0 = 16 * lane, c1 = 16 * lane + 8;
     const bool turns = 16 * lane < 2 * pairs;
@@ -141,6 +154,16 @@ __global__ void __launch_bounds__(kThreads, 3) append8_kernel(const __grid_const
         hd.prepare(static_cast<const BF*>(a.q_norm), a.eps, turn + r * pairs, lane, turns, c0, c1);
         for (int h = sub; h < nq; h += 2 * per) {
             Vec8<BF> x[2][2];
+#pragma unroll
+            for (int c = 4; c < 6; ++c) touch(q, h + c * per, nq);
+            // (keys and values behind the last query heads)
+            if (h + 4 * per >= nq) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    touch(k, first_of(nq) + (h / per + c) % 8 * per, nk);
+                    touch(v, first_of(nq + nk) + (h / per + c) % 8 * per, nk);
+                }
+            }
 #pragma unroll
             for (int c = 0; c < 2; ++c)
                 if (h + c * per < nq) {
@@ -255,12 +278,20 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t s) {
     // a sequence of n rows touches at most (n - 2) / block + 2 blocks of tokens, and n
     const int64_t items = std::min<int64_t>(a.n_rows, a.n_rows / block + 2 * (int64_t)a.n_seqs);
     int slices = (a.hkv + kSliceHeads - 1) / kSliceHeads;
-    while (items * slices < 152 && 2 * slices <= a.hkv) slices *= 2;
+    // a few rows are spread over the SMs; of many, enough CTAs that the last ones to start
+    // are a small part (three run on an SM)
+    while (items * slices < (items < 152 ? 152 : 4 * 3 * 152) && 2 * slices <= a.hkv) slices *= 2;
     const int bytes = a.freq ? std::min(block, a.n_rows) * (a.rot_dim / 2) * (int)sizeof(float2) : 0;
     return launch_pdl(kern, dim3((unsigned)items, slices), dim3(kThreads), bytes, s, a);
 }
 
-// 16 codes of a row per thread.
+// (16-byte boundaries are what is asked of the outputs)
+__device__ __forceinline__ void store32(BF* to, const uint32_t (&w)[8]) {
+    reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// 16 codes of a row of k and of v per thread.
 template <typename Code, int D>
 __global__ void __launch_bounds__(256) values8_kernel(const __grid_constant__ ValuesArgs a) {
     constexpr int kChunks = D / 16;
@@ -268,41 +299,42 @@ __global__ void __launch_bounds__(256) values8_kernel(const __grid_constant__ Va
     const int chunk = threadIdx.x % kChunks, r = threadIdx.x / kChunks;
     const int per = 256 / kChunks;                                  // rows of a CTA's pass
     const int rows = a.page_size;
-    const int64_t all = (int64_t)a.n_pages * a.hkv * 2 * rows;      // (page, head, kind), below 2^32, times rows
+    const int64_t all = (int64_t)a.n_pages * a.hkv * rows;          // (page, head), below 2^31, times rows
     for (int64_t e = (int64_t)blockIdx.x * per + r; e < all; e += (int64_t)gridDim.x * per) {
         const int row = (int)(e & (rows - 1));
-        const uint32_t piece = (uint32_t)(e >> a.page_shift);
-        const int kind = (int)(piece & 1), h = (int)((piece >> 1) % (uint32_t)a.hkv);
-        const int64_t i = (piece >> 1) / (uint32_t)a.hkv;
-        const int id = a.pages ? __ldg(a.pages + i) : (int)i;
-        BF* to = static_cast<BF*>(kind ? a.v_out : a.k_out) + ((i * a.hkv + h) * rows + row) * D + 16 * chunk;
-        uint32_t w[8] = {};
-        if ((unsigned)id < (unsigned)a.num_pages) {
-            const uint4 c = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kind ? a.v : a.k) +
-                                                                 (int64_t)id * a.page_stride + (int64_t)h * a.head_stride +
-                                                                 (int64_t)row * a.row_stride + 16 * chunk));
-            const float s = __ldg((kind ? a.v_scale : a.k_scale) +
-                                  (((int64_t)id * a.hkv + h) << (a.page_shift - a.block_shift)) + (row >> a.block_shift));
-            const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+        const uint32_t piece = (uint32_t)(e >> a.page_shift), i = piece / (uint32_t)a.hkv;
+        const int h = (int)(piece - i * (uint32_t)a.hkv), id = a.pages ? __ldg(a.pages + i) : (int)i;
+        const bool there = (unsigned)id < (unsigned)a.num_pages;
+        const int64_t to = ((int64_t)piece * rows + row) * D + 16 * chunk;
+        const int64_t from = there ? (int64_t)id * a.page_stride + (int64_t)h * a.head_stride + (int64_t)row * a.row_stride + 16 * chunk : 0;
+        const int64_t at = there ? (((int64_t)id * a.hkv + h) << (a.page_shift - a.block_shift)) + (row >> a.block_shift) : 0;
+        uint4 c[2];
+        float s[2];
+        c[0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.k) + from));
+        c[1] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.v) + from));
+        s[0] = __ldg(a.k_scale + at), s[1] = __ldg(a.v_scale + at);
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind) {
+            const uint32_t in[4] = {c[kind].x, c[kind].y, c[kind].z, c[kind].w};
+            uint32_t w[8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float f[4];
                 Code::decode4(in[j], f);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * x] * s, f[2 * x + 1] * s);
-                    w[2 * j + x] = *reinterpret_cast<const uint32_t*>(&p);
+                    const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * x] * s[kind], f[2 * x + 1] * s[kind]);
+                    w[2 * j + x] = there ? *reinterpret_cast<const uint32_t*>(&p) : 0u;
                 }
             }
+            store32(static_cast<BF*>(kind ? a.v_out : a.k_out) + to, w);
         }
-        reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
 }
 
 template <typename Code, int D>
 cudaError_t launch_values(const ValuesArgs& a, cudaStream_t s) {
-    const int64_t rows = (int64_t)a.n_pages * a.hkv * 2 * a.page_size, per = 256 / (D / 16);
+    const int64_t rows = (int64_t)a.n_pages * a.hkv * a.page_size, per = 256 / (D / 16);
     const int64_t ctas = std::min<int64_t>((rows + per - 1) / per, 152 * 8);
     return launch_pdl(values8_kernel<Code, D>, dim3((unsigned)ctas), dim3(256), 0, s, a);
 }

@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
     constexpr int kGroups = kThreads / kLanes;
     __shared__ float2 turn[2 * kThreads];          // rows x pairs: mscale * (cos, sin)
     __shared__ int place[16][2];
+    __shared__ uint64_t unit[64];
     pdl_enter();
     const int tid = threadIdx.x, lane = tid % kLanes, grp = tid / kLanes;
     const int rows = kGroups / per_row, r = grp / per_row;
@@ -85,6 +86,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
     };
     if (row < a.n_rows) load(x, q, sub, a.hq);
     if (row < a.n_rows) touch(q, sub + kBatch<T> * step, a.hq);
+    if (tid >= kThreads - 64 && tid - (kThreads - 64) < pairs) unit[tid - (kThreads - 64)] = pair_unit(a, tid - (kThreads - 64));
     for (int w = tid >> 5; w < rows; w += kThreads / 32) {
         int seq = -1, pos = 0;
         if (row0 + w < a.n_rows) row_place(a, (int)(row0 + w), &seq, &pos);
@@ -92,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
     }
     __syncthreads();
     for (int e = tid; e < rows * pairs; e += kThreads) {
-        turn[e] = row_turn(a, row0 + e / pairs, place[e / pairs][1], e % pairs);
+        turn[e] = row_turn(a, row0 + e / pairs, place[e / pairs][1], e % pairs, unit[e % pairs]);
     }
     __syncthreads();
     const int seq = place[r][0], pos = place[r][1];

@@ -74,16 +74,19 @@ __device__ __forceinline__ void row_place(const AppendArgs& a, int row, int* seq
     }
 }
 
-// (mscale cos, mscale sin) of pair `pair` of a row at position pos.
-__device__ __forceinline__ float2 row_turn(const AppendArgs& a, int64_t row, int pos, int pair) {
+// Pair `pair`'s fraction of a turn per position, 2^64 to the turn (formed in double:
+// freq / 2 pi is rounded once, at 2^-53 of itself).  Once per CTA: f64 is slow.
+__device__ __forceinline__ uint64_t pair_unit(const AppendArgs& a, int pair) {
+    const double t = __ldg(a.freq + pair) * 0.15915494309189533577;
+    return __double2ull_rd((t - floor(t)) * 18446744073709551616.0);
+}
+
+// (mscale cos, mscale sin) of pair `pair`, of pair_unit `unit`, of a row at position pos.
+__device__ __forceinline__ float2 row_turn(const AppendArgs& a, int64_t row, int pos, int pair, uint64_t unit) {
     if (a.positions && row < a.n_rows) {
         const int axis = a.axis ? min((int)__ldg(a.axis + pair), a.n_axes - 1) : 0;
         pos = __ldg(a.positions + axis * a.axis_stride + row);
     }
-    // a frequency's fraction of a turn, 2^64 to the turn (formed in double:
-    // freq / 2 pi is rounded once, at 2^-53 of itself)
-    const double t = __ldg(a.freq + pair) * 0.15915494309189533577;
-    const uint64_t unit = __double2ull_rd((t - floor(t)) * 18446744073709551616.0);
     const int32_t top = (int32_t)((unit * (uint64_t)(int64_t)pos) >> 32);
     float sn, cs;
     sincospif((float)top * 4.656612873077392578125e-10f, &sn, &cs);   // 2^-31: half turns
