@@ -432,7 +432,7 @@ colibri_status_t check_prompt(const colibri_kv_pages_t* kv, const colibri_seqs_t
     if (st == COLIBRI_OK) st = check_seqs(seqs, n_q_heads);
     if (st == COLIBRI_OK) st = check_kv(kv, seqs->page_table != nullptr);
     if (st != COLIBRI_OK) return st;
-    if (seqs->page_table && !(countable(kv, seqs, n_q_heads) && (kv->dtype == kCodes || mappable(kv)))) return COLIBRI_ERR_UNSUPPORTED;
+    if (seqs->page_table && !(countable(kv, seqs, n_q_heads) && mappable(kv))) return COLIBRI_ERR_UNSUPPORTED;
     // packed keys: the call's own rows
     if (!seqs->page_table && seqs->n_seqs > 0 &&
         (seqs->kv_len || kv->num_pages != 1 || (seqs->n_rows > 0 && kv->page_size != seqs->n_rows)))
@@ -449,7 +449,7 @@ colibri_status_t check_decode(const colibri_kv_pages_t* kv, const colibri_seqs_t
     if (st == COLIBRI_OK) st = check_kv(kv, true);
     if (st != COLIBRI_OK) return st;
     if (prefix_len < 0 || prefix_len % kv->page_size) return COLIBRI_ERR_INVALID_ARG;
-    if (prefix_len > kMaxKeys || !countable(kv, seqs, n_q_heads) || (kv->dtype != kCodes && !mappable(kv)))
+    if (prefix_len > kMaxKeys || !countable(kv, seqs, n_q_heads) || !mappable(kv))
         return COLIBRI_ERR_UNSUPPORTED;
     return COLIBRI_OK;
 }

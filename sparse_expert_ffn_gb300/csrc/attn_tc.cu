@@ -101,7 +101,8 @@ struct TcBars {
     uint64_t item_empty[2];
     uint64_t taken_full;
     uint64_t drain[2];
-    uint64_t near_end;        // codes: the item's last tiles are asked for
+    uint64_t staged_full[8];  // codes: a tile of them is there
+    uint64_t staged_empty[8]; // the widening warps have read it
     uint64_t never;           // failure-detection tests: nothing arrives
     uint32_t tmem;
     int abort;
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(kTcThreads<Code>, 1)
             mbar_init(smem_u32(&bars.o_done[t]), 1);
             mbar_init(smem_u32(&bars.s_read[t]), 4);
             mbar_init(smem_u32(&bars.item_full[t]), 1);
-            mbar_init(smem_u32(&bars.item_empty[t]), kCodes ? 18 : 11);   // softmax and MMA warps, V's copies or the widening warps
+            mbar_init(smem_u32(&bars.item_empty[t]), kCodes ? 19 : 11);   // softmax and MMA warps, V's copies, the widening warps
             mbar_init(smem_u32(&bars.drain[t]), 1);
             mbar_init(smem_u32(&bars.tail[t]), 2);
             mbar_init(smem_u32(&bars.turn[t]), 1);
@@ -317,7 +318,10 @@ __global__ void __launch_bounds__(kTcThreads<Code>, 1)
             mbar_init(smem_u32(&bars.kv_empty[s]), 2);
         }
         mbar_init(smem_u32(&bars.taken_full), 1);
-        mbar_init(smem_u32(&bars.near_end), 8);
+        for (int i = 0; kCodes && i < kStaged<D>; ++i) {
+            mbar_init(smem_u32(&bars.staged_full[i]), 1);
+            mbar_init(smem_u32(&bars.staged_empty[i]), 8);
+        }
         for (const CUtensorMap* m : {&tm_q, &tm_k, &tm_v})
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
         mbar_init(smem_u32(&bars.never), 1);
@@ -409,7 +413,7 @@ __global__ void __launch_bounds__(kTcThreads<Code>, 1)
     if (warp < 8) {
         // ------------------------------------------------ softmax, one row per thread
         // (384 x 168 registers at launch = 256 x 208 + 128 x 88)
-        // (codes: 640 x 96 = 256 x 152 + 128 x 48 + 256 x 64)
+        // (codes: 640 x 96 = 256 x 152 + 128 x 64 + 256 x 56)
         if constexpr (kCodes) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int t = warp >> 2, r = tid & 127;
@@ -611,143 +615,62 @@ __global__ void __launch_bounds__(kTcThreads<Code>, 1)
             item_left(item_no++);
         }
     } else if (kCodes && warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if constexpr (kCodes) {
-            // ------------------------------------------------ codes to bf16: each thread copies the
-            // 16 codes that it will widen, kStaged tiles ahead, so that nothing but its own
-            // copies has to be waited for.  A pass of a warp is 8 keys x 64 columns.
-            constexpr int kHalves = D / 64;
-            const int w = warp - 12, row0 = w * 16 + (lane >> 2);
-            const uint32_t staged = kv0 + kSlots * kTileBytes<D> + (w * 32 + lane) * 16;
+            // ------------------------------------------------ codes to bf16, tile by tile: a warp takes
+            // 16 keys, a pass of it 8 keys x 64 columns.  The rows of four lanes are chosen so
+            // that eight lanes meet all banks, in the rows of codes (128 bytes, swizzled by
+            // TMA, or 64) as in those they go to.
+            constexpr int kHalves = D / 64, kPasses = 2 * kHalves;
+            const int w = warp - 12, quad = lane >> 2, k = lane & 3;
+            const int row = D == 64 ? quad : (quad >> 1) ^ (quad & 1) * 5;
+            const uint32_t codes0 = kv0 + kSlots * kTileBytes<D> + (w * 16 + row) * D + ((D == 64 ? k : k ^ row) << 4);
             // where 16 codes of a row go: two chunks of its 128-byte swizzled half
-            const uint32_t to = (lane >> 2) * 128 + (((lane & 3) * 2 ^ (lane >> 2)) << 4);
-            struct {                                            // the tile to be copied next
-                int step = 0, nsteps = 0, lo = 0, hi = 0, h = 0, b = 0;
-            } at;
-            // This warp's 16 keys of 32 steps, a step per lane, and of the 32 after them: where
-            // their first row lies (< 0: nowhere), and their scales.  They are read a window
-            // ahead, so that a tile's copies take few instructions.
-            struct Keys {
-                int64_t row;
-                float scale[2];
-            } here, ahead;
-            const int64_t lane_row = (int64_t)(lane >> 2) * a.row_stride + (lane & 3) * 16, next8 = 8 * a.row_stride;
-            const uint8_t *head_k = nullptr, *head_v = nullptr; // row 0 of the head in page 0, this lane's part
-            uint32_t copied = 0, widened = 0, all_no = 0;       // tiles of K and V, steps, over all items
-            bool more = true, loaded = false;
-            const auto look = [&](int step) {
-                Keys x = {-1, {0.f, 0.f}};
-                const int key = at.lo + (step + lane) * kTileKeys + w * 16;
-                const int page = key < at.hi ? attn_page(a, at.b, key >> a.page_shift) : -1;
-                if (page >= 0) {
-                    const int row = key & (a.page_size - 1);
-                    x.row = (int64_t)page * a.page_stride + (int64_t)row * a.row_stride;
-                    const int64_t i = (((int64_t)page * a.hkv + at.h) << (a.page_shift - a.block_shift)) + (row >> a.block_shift);
-                    x.scale[0] = __ldg(a.k_scale + i), x.scale[1] = __ldg(a.v_scale + i);
-                }
-                return x;
-            };
-            const auto copy = [&]() {
-                const int step = at.step, kind = copied & 1;
-                if (kind == 0) {
-                    if (step > 0 && step % 32 == 0) here = ahead, ahead = look(step + 32);
-                    if (step + 1 == at.nsteps) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&bars.near_end));
-                    }
-                    if (lane == step % 32) {
-                        float* to = scales + (all_no + step) % kScaleSteps<D> * 16 + w;
-                        to[0] = here.scale[0], to[8] = here.scale[1];
-                    }
-                }
-                const uint32_t dst = staged + copied % kStaged<D> * (kTileKeys * D);
-                const int keys = at.hi - (at.lo + step * kTileKeys + row0);     // of this lane's first row on
-                const int64_t row = __shfl_sync(0xffffffffu, here.row, step % 32);
-                const uint8_t* src = (kind ? head_v : head_k) + (row >= 0 ? row : 0);
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const bool there = row >= 0 && keys > 8 * y;
-                    const uint8_t* from = there ? src + y * next8 : src - lane_row;
-#pragma unroll
-                    for (int x = 0; x < kHalves; ++x) cp16(dst + (y * kHalves + x) * 4096, from + 64 * x, there);
-                }
-                cp_commit();
-                ++copied;
-                if (kind) ++at.step;
-            };
+            const uint32_t to = kv0 + w * 2 * kGroupBytes<D, kPaged> + row * 128 + ((k * 2 ^ row) << 4);
+            uint32_t n = 0;                                     // tiles of K and V, over all items
             bool ok = true;
             while (ok) {
-                // tiles are asked for as long as there is room; a next item that is not
-                // there yet is waited for only when nothing is left to widen
-                while (more && copied - widened < kStaged<D>) {
-                    if (at.step == at.nsteps) {
-                        if (loaded) all_no += at.nsteps;
-                        loaded = false;
-                        at.step = at.nsteps = 0;
-                        const bool known = item_no == 0 ||
-                            (copied == widened ? item_there(item_no)
-                                               : __all_sync(0xffffffffu, mbar_try_wait(smem_u32(&bars.item_full[item_no & 1]),
-                                                                                       ((item_no >> 1) - !(item_no & 1)) & 1)) != 0);
-                        if (!known) {
-                            if (copied == widened) ok = false;
-                            break;
-                        }
-                        const Item& it = bars.item[item_no & 1];
-                        const int nsteps = uniform(max(it.steps[0], it.steps[1]));
-                        at.lo = uniform(it.lo), at.hi = uniform(it.hi), at.h = uniform(it.h), at.b = uniform(it.b);
-                        if (at.b < 0) {
-                            more = false;
-                            break;
-                        }
-                        at.nsteps = nsteps, loaded = true;
-                        item_left(item_no++);
-                        if (nsteps == 0) {
-                            if (lane == 0) mbar_arrive(smem_u32(&bars.near_end));
-                            continue;
-                        }
-                        here = look(0), ahead = look(32);
-                        head_k = static_cast<const uint8_t*>(a.k) + (int64_t)at.h * a.head_stride + lane_row;
-                        head_v = static_cast<const uint8_t*>(a.v) + (int64_t)at.h * a.head_stride + lane_row;
-                    }
-                    copy();
-                }
-                if (!ok || copied == widened) break;
-                if (copied - widened == kStaged<D>) cp_wait<kStaged<D> - 1>();
-                else cp_wait<0>();
-                const uint32_t slot = widened % kSlots;
-                if (widened >= kSlots) ok = warp_wait(&bars.kv_empty[slot], (widened / kSlots - 1) & 1);
+                ok = item_there(item_no);
                 if (!ok) break;
-                const uint32_t from = staged + widened % kStaged<D> * (kTileKeys * D);
-                const uint32_t dst = kv0 + slot * kTileBytes<D> + w * 2 * kGroupBytes<D, kPaged> + to;
-                // (all codes are loaded before the first are widened)
-                uint32_t c[2 * kHalves][4];
+                const Item& it = bars.item[item_no & 1];
+                if (uniform(it.b) < 0) break;
+                const int tiles = 2 * uniform(max(it.steps[0], it.steps[1]));
+                item_left(item_no++);
+                for (int i = 0; i < tiles; ++i, ++n) {
+                    const uint32_t st = n % kStaged<D>, slot = n % kSlots;
+                    ok = warp_wait(&bars.staged_full[st], n / kStaged<D> & 1);
+                    if (!ok) break;
+                    uint32_t c[kPasses][4];
 #pragma unroll
-                for (int j = 0; j < 2 * kHalves; ++j)
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(c[j][0]), "=r"(c[j][1]), "=r"(c[j][2]), "=r"(c[j][3])
-                                 : "r"(from + j * 4096)
-                                 : "memory");
-#pragma unroll
-                for (int j = 0; j < 2 * kHalves; ++j) {
-                    uint32_t v[8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) Code::pairs(c[j][i], v[2 * i], v[2 * i + 1]);
-                    const uint32_t p = dst + j / kHalves * kGroupBytes<D, kPaged> + j % kHalves * kColumnBytes<kPaged>;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p ^ (i << 4)), "r"(v[4 * i]),
-                                     "r"(v[4 * i + 1]), "r"(v[4 * i + 2]), "r"(v[4 * i + 3])
+                    for (int j = 0; j < kPasses; ++j)            // 8 keys j / kHalves, columns 64 (j % kHalves) ..
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(c[j][0]), "=r"(c[j][1]), "=r"(c[j][2]), "=r"(c[j][3])
+                                     : "r"((codes0 + st * (kTileKeys * D) + j / kHalves * (8 * D)) ^ (j % kHalves << 6))
                                      : "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bars.staged_empty[st]));
+                    if (n >= kSlots) ok = warp_wait(&bars.kv_empty[slot], (n / kSlots - 1) & 1);
+                    if (!ok) break;
+#pragma unroll
+                    for (int j = 0; j < kPasses; ++j) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) Code::pairs(c[j][x], v[2 * x], v[2 * x + 1]);
+                        const uint32_t p = to + slot * kTileBytes<D> + j / kHalves * kGroupBytes<D, kPaged> + j % kHalves * kColumnBytes<kPaged>;
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p ^ (x << 4)), "r"(v[4 * x]),
+                                         "r"(v[4 * x + 1]), "r"(v[4 * x + 2]), "r"(v[4 * x + 3])
+                                         : "memory");
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bars.kv_full[slot]));
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars.kv_full[slot]));
-                ++widened;
             }
-            cp_wait<0>();
         }
     } else {
-        if constexpr (kCodes) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if constexpr (kCodes) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 8 || warp == 10) {
             // ------------------------------------------------ MMA issue, one tile each
@@ -908,7 +831,11 @@ __global__ void __launch_bounds__(kTcThreads<Code>, 1)
             // the work list; warp 11 V.  Tile i of K is number 2 i of the ring, of V
             // 2 i + 1.  (One code for both warps: a kernel as short as a prefix's takes
             // 2 us more with two, which have to be fetched.)
-            // Codes: warp 9 alone, for Q and the work list.
+            // Codes: into a ring of their own, with the scales of a step behind them.
+            constexpr uint32_t kRing = kCodes ? kStaged<D> : kSlots;
+            uint64_t* full = kCodes ? bars.staged_full : bars.kv_full;
+            uint64_t* empty = kCodes ? bars.staged_empty : bars.kv_empty;
+            uint32_t scale_no = 0;                                  // steps so far
             const int kind = warp == 11;
             uint32_t filled = 0;                                    // tiles so far, over all items
             uint32_t q_no[2] = {0, 0};
@@ -917,7 +844,6 @@ __global__ void __launch_bounds__(kTcThreads<Code>, 1)
             const bool leader = elect_one();
             // (failure-detection tests: no Q and K are copied from item stall_tma on)
             bool ok = kind || a.stall_tma != 1 || warp_wait(&bars.never, 0);
-            if (kCodes && kind) ok = false;
             bool asked = false;
             if (!kind && lane == 0) bars.announced = 1;
             while (ok) {
@@ -950,22 +876,25 @@ __global__ void __launch_bounds__(kTcThreads<Code>, 1)
                     }
                     __syncwarp();
                 }
-                if constexpr (kCodes) {
-                    // the next item is taken when the last tiles are asked for
-                    ok = ok && warp_wait(&bars.near_end, item_no & 1);
-                    if (!ok) break;
-                    ask();
-                    if (a.stall_tma > 1 && item_no + 1 >= a.stall_tma) ok = warp_wait(&bars.never, 0);
-                }
                 // page ids of 32 boxes, one per lane, and of the 32 after them
                 const int per_step = kTileKeys / box;
                 const auto look = [&](int first) {
                     const int key = lo + (first + lane) * box;
                     return kPaged && key < hi ? attn_page(a, it.b, key >> a.page_shift) : -1;
                 };
-                int ids = kCodes ? -1 : look(0), ids_ahead = kCodes ? -1 : look(32), page = -1;
-                for (int j = 0; !kCodes && j < nsteps && ok; ++j) {
-                    const uint32_t n = 2 * filled + kind, slot = n % kSlots;
+                int ids = look(0), ids_ahead = look(32), page = -1;
+                // codes: the scales of 16 keys of a step, a lane each, of k and from lane 8 on of v
+                const auto scale_of = [&](int step) {
+                    const int key = lo + step * kTileKeys + (lane & 7) * 16;
+                    const int id = kCodes && lane < 16 && key < hi && step < nsteps ? attn_page(a, it.b, key >> a.page_shift) : -1;
+                    if (id < 0) return 0.f;
+                    return __ldg((lane & 8 ? a.v_scale : a.k_scale) +
+                                 (((int64_t)id * a.hkv + h) << (a.page_shift - a.block_shift)) +
+                                 ((key & (a.page_size - 1)) >> a.block_shift));
+                };
+                float scale = kCodes && !kind ? scale_of(0) : 0.f;
+                for (int j = 0; j < nsteps && ok; ++j) {
+                    const uint32_t n = 2 * filled + kind, slot = n % kRing;
                     const int base = lo + j * kTileKeys;
                     if (kPaged) {
                         const int first = j * per_step;
@@ -979,11 +908,22 @@ __global__ void __launch_bounds__(kTcThreads<Code>, 1)
                         if (a.stall_tma > 1 && item_no + 1 >= a.stall_tma) ok = warp_wait(&bars.never, 0);
                         if (!ok) break;
                     }
-                    if (n >= kSlots) ok = warp_wait(&bars.kv_empty[slot], (n / kSlots - 1) & 1);
+                    if (n >= kRing) ok = warp_wait(&empty[slot], (n / kRing - 1) & 1);
                     if (!ok) break;
-                    const uint32_t bar = smem_u32(&bars.kv_full[slot]);
-                    const uint32_t dst = kv0 + slot * kTileBytes<D>;
-                    if (kPaged) {
+                    const uint32_t bar = smem_u32(&full[slot]);
+                    const uint32_t dst = kCodes ? kv0 + kSlots * kTileBytes<D> + slot * (kTileKeys * D) : kv0 + slot * kTileBytes<D>;
+                    if constexpr (kCodes) {
+                        // (the reader learns of the scales by the tile of keys)
+                        if (!kind && lane < 16) scales[scale_no % kScaleSteps<D> * 16 + lane] = scale;
+                        const int boxes = (min(kTileKeys, hi - base) + box - 1) / box;
+                        __syncwarp();
+                        if (lane == 0) mbar_expect_tx(bar, boxes * box * D);
+                        __syncwarp();
+                        if (lane < boxes)
+                            tma_load_4d(dst + lane * box * D, map, 0, (base + lane * box) & (a.page_size - 1),
+                                        page < 0 ? units.count : page * units.per_page + h * units.per_head, 0, bar);
+                        if (!kind) scale = scale_of(j + 1), ++scale_no;
+                    } else if (kPaged) {
                         // one box per page, lane l has box l; a page that does not
                         // exist lies outside the tensor and gives zeros
                         const int boxes = (min(kTileKeys, hi - base) + box - 1) / box;
@@ -1006,7 +946,7 @@ __global__ void __launch_bounds__(kTcThreads<Code>, 1)
                     item_left(item_no++);
                     continue;
                 }
-                if (!kCodes && nsteps == 0) ask();
+                if (nsteps == 0) ask();
                 // the next item
                 ok = warp_wait(&bars.taken_full, item_no & 1);
                 if (!ok) break;
@@ -1057,12 +997,13 @@ __global__ void __launch_bounds__(kTcThreads<Code>, 1)
     if (bars.abort && tid == 0) {
         atomicExch(&wait_status, DEV_TIMEOUT);
         // none of the copies stays in flight: each slot's last one
-        for (uint32_t slot = 0; slot < kSlots; ++slot) {
+        constexpr int kRing = kCodes ? kStaged<D> : kSlots;
+        for (uint32_t slot = 0; slot < (uint32_t)kRing; ++slot) {
             int last = -1;
             for (int kind = 0; kind < 2; ++kind)
-                for (int i = max((int)bars.filled[kind] - kSlots, 0); i < (int)bars.filled[kind]; ++i)
-                    if ((2 * i + kind) % kSlots == (int)slot) last = max(last, 2 * i + kind);
-            if (last >= 0) mbar_wait_drain(smem_u32(&bars.kv_full[slot]), (last / kSlots) & 1, kDrainLimitNs);
+                for (int i = max((int)bars.filled[kind] - kRing, 0); i < (int)bars.filled[kind]; ++i)
+                    if ((2 * i + kind) % kRing == (int)slot) last = max(last, 2 * i + kind);
+            if (last >= 0) mbar_wait_drain(smem_u32(&(kCodes ? bars.staged_full : bars.kv_full)[slot]), (last / kRing) & 1, kDrainLimitNs);
         }
     }
     if (bars.abort && warp < 8) {
@@ -1091,9 +1032,10 @@ EncodeFn encode_fn() {
     return fn;
 }
 
-// bf16 tensor of `rank` dimensions (innermost first, contiguous) with strides in
-// elements, 128-byte swizzle, zeros outside.
-bool encode(CUtensorMap* m, const void* p, int rank, const int64_t* dims, const int64_t* strides, const int* boxes) {
+// bf16 tensor, or of bytes, of `rank` dimensions (innermost first, contiguous) with
+// strides in elements, 128-byte swizzle (none for rows of 64 bytes), zeros outside.
+bool encode(CUtensorMap* m, const void* p, int rank, const int64_t* dims, const int64_t* strides, const int* boxes,
+            int size = 2) {
     const EncodeFn fn = encode_fn();
     if (!fn) return false;
     cuuint64_t d[5], s[4];
@@ -1101,11 +1043,12 @@ bool encode(CUtensorMap* m, const void* p, int rank, const int64_t* dims, const 
     for (int i = 0; i < rank; ++i) {
         d[i] = (cuuint64_t)dims[i], b[i] = (cuuint32_t)boxes[i], ones[i] = 1;
         // (the stride of a dimension of one entry is never used, but has to be valid)
-        if (i > 0) s[i - 1] = (cuuint64_t)(dims[i] > 1 ? strides[i - 1] : dims[0]) * 2;
+        if (i > 0) s[i - 1] = (cuuint64_t)(dims[i] > 1 ? strides[i - 1] : dims[0]) * size;
     }
     const auto call = [&]() {
-        return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(p), d, s, b, ones,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+        return fn(m, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(p), d, s, b, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  boxes[0] * size == 64 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
     if (call()) return true;
@@ -1125,7 +1068,12 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     int box = kTileKeys;
     Units units{};
     if constexpr (kOfCodes<Code>) {
-        tk = tv = tq;                                          // (not used)
+        box = a.page_size < kTileKeys ? a.page_size : kTileKeys;
+        int64_t unit;
+        if (!attn_tc_units(a, &unit, &units.per_page, &units.per_head, &units.count)) return cudaErrorInvalidValue;
+        const int64_t kd[4] = {D, a.page_size, units.count, 1}, ks[3] = {a.row_stride, unit, 0};
+        const int kb[4] = {D, box, 1, 1};
+        ok = ok && encode(&tk, a.k, 4, kd, ks, kb, 1) && encode(&tv, a.v, 4, kd, ks, kb, 1);
     } else if (kPaged) {
         box = a.page_size < kTileKeys ? a.page_size : kTileKeys;
         int64_t unit;
