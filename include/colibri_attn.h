@@ -282,8 +282,8 @@ colibri_status_t colibri_attention_waits(uint64_t limit_ns, int32_t stall);
  *   code   E4M3 numbers, or INT8 whole numbers
  *   block  16, 32 or 64, at most page_size
  * page_size is a power of two from 16 to 65536.  Attention takes any codes and any
- * finite scales; an E4M3 code that is no number (0x7f, 0xff) must not stand where a
- * row sees it.  What stands behind a sequence's last key may be anything, the scale of
+ * scales that are finite and not negative; an E4M3 code that is no number (0x7f, 0xff) must
+ * not stand where a row sees it.  What stands behind a sequence's last key may be anything, the scale of
  * a block without keys included.
  */
 typedef enum { COLIBRI_CODE_E4M3 = 0, COLIBRI_CODE_INT8 = 1 } colibri_code_t;
@@ -316,7 +316,8 @@ typedef struct {
  * element that is not finite gets the scale NaN, and all its values are NaN until a
  * call writes the block from its first row on.
  * Blocks of the cache that get no row, and codes behind the call's last row, stay as
- * they are.  No two sequences of a call may append to one page.
+ * they are.  No two sequences of a call may append to one page.  k, v and the scales
+ * must not overlap.
  */
 colibri_status_t colibri_append_qkv8(const colibri_kv_pages8_t* cache, const colibri_seqs_t* seqs,
                                      const colibri_rope_t* rope, const colibri_positions_t* positions,
@@ -335,8 +336,12 @@ colibri_status_t colibri_values8(const colibri_kv_pages8_t* cache, const int32_t
 
 /*
  * colibri_attention_prompt8, colibri_attention_decode8 - colibri_attention_prompt over
- * pages (seq_start, page_table and kv_len given) and colibri_attention_decode over an
- * 8-bit cache; q and o are bf16.
+ * pages (page_table and kv_len given) and colibri_attention_decode over an 8-bit cache; q
+ * and o are bf16.  Codes enter the products as they are, scales and sums are float32.
+ * Weights times value scales are rounded for the product with the codes: to bf16, or,
+ * for one row per sequence and prompts of few rows (32 per sequence and key head on
+ * average), to f16 on a reference of the row's largest such product, so that a key's
+ * part below 2^-31 of that is lost.
  */
 colibri_status_t colibri_attention_prompt8_workspace(const colibri_kv_pages8_t* cache,
                                                      const colibri_seqs_t* seqs, int32_t n_q_heads,

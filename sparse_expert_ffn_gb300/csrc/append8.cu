@@ -14,9 +14,13 @@
 // A CTA takes the rows of one block of tokens of a sequence and a slice of the
 // heads, so the scale needs nothing from another CTA.  A block's keys are read
 // twice, for `most` and for the codes (the second time from the caches), rather
-// than held: blocks of 64 tokens do not fit the registers.  Bound by HBM for
-// prompts (2 bytes of each element read, 2 of q and 1 of k and v written), by the
-// chain length -> place -> angle -> head -> scale -> code for single tokens.
+// than held: blocks of 64 tokens do not fit the registers.  Bound by HBM in the end
+// (2 bytes of each element read, 2 of q and 1 of k and v written), but short of it: 15373
+// rows of 32 / 8 heads of 128 take 97 us, where their bytes take 51, waiting on loads and
+// on the chain length -> place -> angle -> head -> scale -> code of each CTA, four barriers
+// long.  Heads are cut into slices so that CTAs are many and short (one slice 137 us with
+// the pages' values read back, two 117, four 118, eight 141, which form each row's angles
+// eight times).  One decode step of 32 sequences takes 8 us, that chain.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -116,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 3) append8_kernel(const __grid_const
         for (int c = 0; c < 4; ++c) touch(static_cast<const BF*>(a.q) + row * a.q_stride, sub + c * per, nq);
     }
     for (int e = tid; e < sp.rows * pairs; e += kThreads)
-        turn[e] = row_turn(a, sp.row0 + e / pairs, sp.lo + e / pairs, e % pairs, unit[e % pairs]);
+        turn[e] = row_turn<true>(a, sp.row0 + e / pairs, sp.lo + e / pairs, e % pairs, unit[e % pairs]);
     // the block's place
     int page = -1;
     if (sp.lo >= 0 && (sp.lo >> a.page_shift) < a.table_stride) {
@@ -185,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 3) append8_kernel(const __grid_const
             float y[2][8];
             const int at = (y0 + h * slices) * D;
             x[0].load(k + at + c0), x[1].load(k + at + c1);
-            hd.turned(x, y);
+            hd.template turned<true>(x, y);
             note(0, h, abs_top(y[1], abs_top(y[0], 0.f)));
         }
         for (int h = first_of(nq + nk); h < nk; h += per) {
@@ -235,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 3) append8_kernel(const __grid_const
             float y[2][8];
             const int at = (y0 + h * slices) * D;
             x[0].load(k + at + c0), x[1].load(k + at + c1);
-            hd.turned(x, y);
+            hd.template turned<true>(x, y);
             put(a.k_out, 0, h, y);
         }
         for (int h = first_of(nq + nk); h < nk; h += per) {

@@ -268,13 +268,17 @@ int splits_for(const AttnArgs& a, const colibri_kv_pages_t* kv, int64_t keys) {
 
 // Prompts over codes whose sequences have few rows each (drafts to be verified): tiles of
 // 16 rows read the keys once each, at HBM's rate, where the tensor-core kernel walks
-// them with one or two tiles per CTA and waits for one step's chain after another.
-constexpr int kFewRows = 32;
+// them with one or two tiles per CTA and waits for one step's chain after another
+// (12 sequences of 4500 keys: 33, 50, 64, 69, 92 us for 8, 16, 24, 32, 48 rows each, on the
+// tensor cores 76 whatever the rows; 48 of 3000 keys and 16 rows: 117 and 157).  How the rows
+// are spread is known on the device only, and one sequence may have nearly all of them: up
+// to kMostRows, so that its keys are read 64 times at most.
+constexpr int kFewRows = 32, kMostRows = 1024;
 bool few_rows(const colibri_kv_pages_t* kv, const colibri_seqs_t* s, int group, int64_t keys) {
     const int64_t rows = (int64_t)s->n_rows * group;
     // (and the list of steps is counted in 64 bits, times the shares, even where every
     // sequence claims all rows)
-    return rows <= kFewRows * (int64_t)s->n_seqs &&
+    return rows <= kFewRows * (int64_t)s->n_seqs && rows <= kMostRows &&
            ((double)keys / 32 + 1) * kv->n_kv_heads * ((double)rows / 8 + 1) * s->n_seqs <= 1e15;
 }
 
@@ -573,6 +577,11 @@ colibri_status_t colibri_append_qkv8(const colibri_kv_pages8_t* cache, const col
                               row_bytes(v, v_stride, hkv, d, 2), row_bytes(q_out, q_out_stride, n_q_heads, d, 2)})
             if (seqs->n_rows > 0 && overlap(scale, scale_bytes(cache), r.p, r.extent(seqs->n_rows)))
                 return COLIBRI_ERR_INVALID_ARG;
+    // (what is written in one part of the cache is not another part)
+    if (overlap(cache->k_scale, scale_bytes(cache), cache->v_scale, scale_bytes(cache))) return COLIBRI_ERR_INVALID_ARG;
+    for (const float* scale : {cache->k_scale, cache->v_scale})
+        for (const void* codes : {cache->k, cache->v})
+            if (overlap(scale, scale_bytes(cache), codes, kv_extent(&kv))) return COLIBRI_ERR_INVALID_ARG;
     if (a.n_rows == 0) return COLIBRI_OK;
     a.k_scale = cache->k_scale, a.v_scale = cache->v_scale;
     a.block_shift = shift_of(cache->block);

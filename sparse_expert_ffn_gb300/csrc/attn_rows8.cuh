@@ -1,19 +1,23 @@
-// Attention of single bf16 rows over a paged cache of 8-bit codes with a scale for
-// each block of tokens and key head: the decode step.
+// Attention of single bf16 rows, and of the few rows of a draft, over a paged cache of
+// 8-bit codes with a scale for each block of tokens and key head.
 //
 // The frame, its equal shares and its rings are attn_decode.cu's (attn_share.cuh); a
-// step of 8 KB holds twice the keys.  What is added is the way from codes to operands:
+// step of 8 KB holds twice the keys.  Bound by HBM as there: from 131072 to 262144 keys
+// of 8 heads the time grows at 7.0 TB/s, above some 15 us for two launches; 64
+// sequences of 100 - 8000 keys take 89 us, 5.4 TB/s.  What is added is the way from codes to operands:
 //   s_j = (q . code_j) (scale_k c / 2^e)       c = scale * log2(e)
 //   o   = sum_j (2^(s_j - m) scale_v) code_j,  l = sum_j 2^(s_j - m)
 // so codes enter the products as they are, exact in 16 bits, and a scale costs one
 // product per score and one per weight instead of one per element.
 //
 // The products are formed with the keys as the rows of mma.sync m16n8k16 and a group's
-// query rows as its 8 columns (2 or 4 column tiles for larger groups): S^T = K Q^T and
-// O^T = V^T P^T.  A group of 4 then fills half of an MMA instead of a quarter, and O
-// takes half the registers (rows of the group as the MMA's rows: 103 us for 64
-// sequences of 100 - 8000 keys, so TODO).  P^T, which lies as the first product
-// leaves it, key by key, is turned by movmatrix.
+// query rows as its 8 columns, or two times 8: S^T = K Q^T and O^T = V^T P^T.  A group
+// of 4 then fills half of an MMA instead of a quarter, O takes half the registers, and
+// three CTAs fit an SM (rows of the group as the MMA's rows and values as bf16: 103
+// instead of 87 us for the 64 sequences).  P^T, which lies as the first product leaves
+// it, key by key, is turned by movmatrix.  More rows are further tiles, which read the
+// keys again: 32 rows at once spill, and take 95 us for one sequence of 65421 keys and
+// groups of 32 where two tiles of 16 take less.
 //
 // Codes become f16, because that takes the fewest instructions (e4m3: one conversion per
 // two codes; whole numbers: 5 instructions per 4).  The query row becomes f16 with

@@ -37,6 +37,19 @@
 //
 // P is rounded to bf16 because the MMA takes both operands in one 16-bit type;
 // l adds the unrounded f32 values.
+//
+// 8-bit caches (Code: what their codes are).  The copying warps bring tiles of codes to a
+// ring of their own, and eight further warps widen them to bf16, which holds every code
+// exactly, into the ring that the MMAs read; scales go to shared memory beside them, one
+// for 16 keys, and the softmax multiplies scores by c scale_k and weights, before they
+// are rounded, by scale_v.  Bound by the softmax (2670 cycles per step and tile, 152
+// registers) and the widening warps (1130 cycles per tile of codes), which share the
+// issue slots: a step of two tiles takes 4080 cycles where bf16 pages take 2800 (chunks
+// 205 us, bf16 149).  S is read in quarters, because all of it does not fit the registers
+// that the widening warps leave.  Measured and left out, chunks: threads that copy what
+// they widen (cp.async, addresses a window ahead) 212 to 231 us; operands in f16, which
+// takes half the instructions per code, with q made f16 by the softmax's threads and
+// weights on a closer reference, 230 and 244 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -53,7 +66,7 @@ namespace {
 
 using namespace tc;
 
-// 2 softmax warpgroups, 1 of MMA issue and copies; one that widens codes
+// 2 softmax warpgroups, 1 of MMA issue and copies; two that widen codes
 template <typename Code> constexpr bool kOfCodes = !std::is_void_v<Code>;
 template <typename Code> constexpr int kTcThreads = kOfCodes<Code> ? 640 : 384;
 constexpr int kTileKeys = 128;

@@ -28,14 +28,16 @@ struct E4M3 {
         halves(__byte_perm(c, 0, 0x3120), even, odd);
     }
     // codes 0, 1 and 2, 3 as bf16 pairs: the code's bits moved to bf16's places are the
-    // number times 2^-120, subnormal numbers included
+    // number times 2^-120, subnormal numbers included.  (A byte with its sign above it,
+    // four bits to the left: the sign, copies of it that go, the other seven bits.)
     static __device__ __forceinline__ void pairs(uint32_t c, uint32_t& lo, uint32_t& hi) {
-        lo = widen(__byte_perm(c, 0, 0x1404)), hi = widen(__byte_perm(c, 0, 0x3424));
+        asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(lo) : "r"(c));
+        asm("prmt.b32 %0, %1, 0, 0xb3a2;" : "=r"(hi) : "r"(c));
+        lo = scaled(lo << 4 & 0x87f087f0u), hi = scaled(hi << 4 & 0x87f087f0u);
     }
-    static __device__ __forceinline__ uint32_t widen(uint32_t p) {
-        const uint32_t b = (p & 0x80008000u) | ((p >> 4) & 0x07f007f0u);
+    static __device__ __forceinline__ uint32_t scaled(uint32_t p) {
         uint32_t r;
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(b), "r"(0x7b807b80u));   // 2^120
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(p), "r"(0x7b807b80u));   // 2^120
         return r;
     }
     static __device__ __forceinline__ void decode4(uint32_t c, float* v) {

@@ -82,6 +82,10 @@ __device__ __forceinline__ uint64_t pair_unit(const AppendArgs& a, int pair) {
 }
 
 // (mscale cos, mscale sin) of pair `pair`, of pair_unit `unit`, of a row at position pos.
+// kFine: the float32 that the angle is rounded to is that of the distance to the nearest
+// quarter turn, so that it is off by 2^-28 turn at most, instead of 2^-26.  Rounded to 8
+// bits, an element that is off in the last bit of float32 may land on the other code.
+template <bool kFine = false>
 __device__ __forceinline__ float2 row_turn(const AppendArgs& a, int64_t row, int pos, int pair, uint64_t unit) {
     if (a.positions && row < a.n_rows) {
         const int axis = a.axis ? min((int)__ldg(a.axis + pair), a.n_axes - 1) : 0;
@@ -89,6 +93,12 @@ __device__ __forceinline__ float2 row_turn(const AppendArgs& a, int64_t row, int
     }
     const int32_t top = (int32_t)((unit * (uint64_t)(int64_t)pos) >> 32);
     float sn, cs;
+    if constexpr (kFine) {
+        const uint32_t quarter = ((uint32_t)top + (1u << 29)) >> 30;
+        sincospif((float)(int32_t)((uint32_t)top - (quarter << 30)) * 4.656612873077392578125e-10f, &sn, &cs);
+        const float c = quarter & 1 ? sn : cs, s = quarter & 1 ? cs : sn;
+        return make_float2((quarter == 1 || quarter == 2 ? -c : c) * a.mscale, (quarter & 2 ? -s : s) * a.mscale);
+    }
     sincospif((float)top * 4.656612873077392578125e-10f, &sn, &cs);   // 2^-31: half turns
     return make_float2(cs * a.mscale, sn * a.mscale);
 }
@@ -136,7 +146,9 @@ struct Heads {
         x[0].set(y[0]);
         x[1].set(y[1]);
     }
-    // the same before it is rounded to T
+    // the same before it is rounded to T; kFine: with the norm's factor rounded once, and
+    // multiplied to what is turned instead of to both elements before
+    template <bool kFine = false>
     __device__ __forceinline__ void turned(const Vec8<T> (&x)[2], float (&y)[2][8]) const {
         float p[16];
         {
@@ -158,14 +170,16 @@ struct Heads {
             const uint32_t mine = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
 #pragma unroll
             for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mine, ss, o);
-            inv = rsqrtf(fmaf(ss, 1.f / D, eps));
+            inv = kFine ? __frsqrt_rn(fmaf(ss, 1.f / D, eps)) : rsqrtf(fmaf(ss, 1.f / D, eps));
         }
         const auto products = [&](auto second) {                   // second(): with the second products
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float u = p[kInterleaved ? 2 * i : i] * inv, w = p[kInterleaved ? 2 * i + 1 : i + 8] * inv;
+                const float before = kFine ? 1.f : inv;
+                const float u = p[kInterleaved ? 2 * i : i] * before, w = p[kInterleaved ? 2 * i + 1 : i + 8] * before;
                 float yu = u * m[i][0], yw = w * m[i][2];
                 if (second()) yu -= w * m[i][1], yw += u * m[i][3];
+                if (kFine) yu *= inv, yw *= inv;
                 if (kInterleaved) y[i / 4][i % 4 * 2] = yu, y[i / 4][i % 4 * 2 + 1] = yw;
                 else y[0][i] = yu, y[1][i] = yw;
             }

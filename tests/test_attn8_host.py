@@ -123,7 +123,7 @@ SQ_BAD = [(dict(n_seqs=-1), 1), (dict(n_rows=-1), 1), (dict(kv_len=None), 1), (d
 @pytest.mark.parametrize("bad,status", KV_BAD + SQ_BAD + [
     (dict(q=None), 1), (dict(q=8), 1), (dict(qs=504), 1), (dict(ks=128), 1), (dict(vs=260), 1), (dict(qn=2), 1),
     (dict(eps=-1.0), 1), (dict(qo=None), 1), (dict(qo=6 * B), 1), (dict(qo=B), 1), (dict(q=13 * B), 1), (dict(qo=14 * B), 1),
-    (dict(vr=14 * B - 256), 1), (dict(rot_dim=72), 1), (dict(freq=None), 1), (dict(at=None), 1), (dict(at=4 * B + 2), 1),
+    (dict(vr=14 * B - 256), 1), (dict(v_scale=13 * B), 1), (dict(k_scale=2 * B + 1024), 1), (dict(rot_dim=72), 1), (dict(freq=None), 1), (dict(at=None), 1), (dict(at=4 * B + 2), 1),
     (dict(n_axes=0), 1), (dict(n_axes=9), 1), (dict(axis_stride=9), 1), (dict(n_rows=0), 0), (dict(n_seqs=0), 0)])
 def test_append8_refusals(sef, bad, status):
     a = Args(sef, **bad)
@@ -183,3 +183,19 @@ def test_workspace8_is_checked(sef):
         assert Args(sef, table_stride=2048, wsb=n.value - 1).prompt() == 1
     for name, args in (("prompt8", ()), ("decode8", (0,))):
         assert getattr(sef, f"colibri_attention_{name}_workspace")(r(a.C), r(a.SQ), 8, *args, None) == 1
+
+
+def test_the_frame_of_single_rows_reads_from_l2_before_it_waits():
+    """What tests/test_attn_host_calls.py asks of the kernels for single rows, of the
+    headers that they are made of."""
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sparse_expert_ffn_gb300", "csrc")
+    for name in ("attn_share.cuh", "attn_rows8.cuh"):
+        with open(os.path.join(csrc, name)) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        calls = re.findall(r"\b(?:attn_seq|attn_page|seq_steps|seq_tiles|count_steps|ld_early)\b(<[^>]*>)", text)
+        assert calls and all(c.endswith("kEarly>") for c in calls) and "__ldg" not in text, name
+    with open(os.path.join(csrc, "append8.cu")) as f:
+        for body in re.findall(r"__global__[^{]*\{(.*?)\n\}", f.read(), re.S):
+            assert not re.search(r"__ldg|find_span|\ba\.(q|k|v|table|kv_len)\b", body[:body.index("pdl_enter();")])

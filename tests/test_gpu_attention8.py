@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from attn8_parity import CODE, Problem8, decoded, random_codes, same
-from attn_parity import U, f64, seqs
+from attn_parity import HALF, U, f64, seqs
 from oracle import attention as oa
 
 pytestmark = pytest.mark.gpu
@@ -115,18 +115,24 @@ def test_append8(A, lens, hq, hkv, d, code, block, page, layout, style, rot, nor
                      eps=1e-5, q_out=out)
     torch.cuda.synchronize()
     assert r is out and (out[n:] == 7.0).all()
-    # the queries: bit for bit those of the 16-bit path
-    q16 = A.qk_norm_rope(A.Sequences(p.seq_start, p.kv_len), p.q, k, rope=rope, positions=positions, q_norm=w[0],
-                         k_norm=w[1], eps=1e-5, q_out=torch.full_like(out, 7.0))[0]
-    assert torch.equal(out, q16)
-    kw = None if not norm else f64(w[1])
-    want = oa.norm_rotate(f64(k)[:n], pos, freq, style, 1.0, kw, 1e-5)
-    mag = np.abs(oa.norm_rotate(f64(k)[:n], pos, None, weight=kw, eps=1e-5))
-    if freq is not None:
-        half = len(freq)
-        sl = (slice(0, half), slice(half, 2 * half)) if style == "half" else (slice(0, 2 * half, 2), slice(1, 2 * half, 2))
-        both = mag[..., sl[0]] + mag[..., sl[1]]
-        mag[..., sl[0]], mag[..., sl[1]] = both, both
+
+    def exact(x, weight):
+        """The rows in 64 bits, and what their float32 error is a multiple of."""
+        weight = None if weight is None else f64(weight)
+        mag = np.abs(oa.norm_rotate(f64(x)[:n], pos, None, weight=weight, eps=1e-5))
+        if freq is not None:
+            half = len(freq)
+            sl = (slice(0, half), slice(half, 2 * half)) if style == "half" else (slice(0, 2 * half, 2), slice(1, 2 * half, 2))
+            both = mag[..., sl[0]] + mag[..., sl[1]]
+            mag[..., sl[0]], mag[..., sl[1]] = both, both
+        return oa.norm_rotate(f64(x)[:n], pos, freq, style, 1.0, weight, 1e-5), mag
+
+    want, mag = exact(p.q, w[0])
+    r = HALF[BF]
+    assert (np.abs(f64(out)[:n] - want) <= r * np.abs(want) + (1 + r) * 32 * U * mag).all()
+    if style is None and not norm:
+        assert torch.equal(out[:n], p.q[:n])
+    want, mag = exact(k, w[1])
     check_append(p, want, 32 * U * mag, p.kc, p.ks, olds[0], olds[1], style is None and not norm)
     check_append(p, f64(v)[:n], np.zeros((n, hkv, d)), p.vc, p.vs, olds[2], olds[3], True)
     # what the codes stand for, of all pages and of some, ids that do not exist among them
