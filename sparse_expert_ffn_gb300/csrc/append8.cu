@@ -20,7 +20,7 @@
 // on the chain length -> place -> angle -> head -> scale -> code of each CTA, four barriers
 // long.  Heads are cut into slices so that CTAs are many and short (one slice 137 us with
 // the pages' values read back, two 117, four 118, eight 141, which form each row's angles
-// eight times).  One decode step of 32 sequences takes 8 us, that chain.
+// eight times).  One decode step of 32 sequences takes 8 us of the GPU, that chain.
 #include <cuda_runtime.h>
 
 #include <algorithm>
