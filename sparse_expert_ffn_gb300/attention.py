@@ -168,16 +168,18 @@ class PagedKVCache8:
         """What the pages hold, code * scale in bfloat16: (k, v), each [n, kv_heads,
         page_size, head_dim], of ``pages`` [n] (int32 CUDA tensor; default: all) into
         ``out`` (two contiguous tensors; new ones by default)."""
+        n = self.num_pages
         if pages is not None:
             _int32(pages, "pages", 1, self.device)
-        n = self.num_pages if pages is None else pages.shape[0]
+            n = pages.shape[0]
         shape = (n, self.n_kv_heads, self.page_size, self.head_dim)
         if out is None:
-            out = tuple(_empty(shape, self.dtype, self.device, stream) for _ in range(2))
-        for t in out:
-            if t.shape != shape or t.dtype != self.dtype or t.device != self.device or not t.is_contiguous():
-                raise ValueError(f"out must be two contiguous {list(shape)} bfloat16 tensors on {self.device}")
-        k, v = out
+            k, v = _empty(shape, self.dtype, self.device, stream), _empty(shape, self.dtype, self.device, stream)
+        else:
+            k, v = out
+            for t in out:
+                if t.shape != shape or t.dtype != self.dtype or t.device != self.device or not t.is_contiguous():
+                    raise ValueError(f"out must be two contiguous {list(shape)} bfloat16 tensors on {self.device}")
         if n:
             _on(self.device, _sef.library().colibri_values8, "colibri_values8", self._ref, _sef._ptr(pages), n,
                 k.data_ptr(), v.data_ptr(), _stream(stream, self.device))

@@ -292,6 +292,26 @@ def test_batches_of_padding_and_of_nothing(A):
         assert same(now, was) if now.element_size() == 1 else torch.equal(now.nan_to_num(2.0), was.nan_to_num(2.0))
 
 
+@pytest.mark.parametrize("count,rows", [(130, 1), (300, 0), (300, 1), (40, 3), (33, 7)])
+def test_batches_of_many_sequences(A, count, rows):
+    """Work lists past 32 and 128 sequences: single tokens (rows 0), and drafts whose rows
+    run in equal shares (up to 32 rows times heads of a group each, 1024 in all) or not."""
+    r = np.random.default_rng(count)
+    kv = r.integers(1, 90, count)
+    kv[r.integers(0, count, 5)] = 0
+    kv[7] = 3000
+    p = Problem8([(max(rows, 1), int(t)) for t in kv], 3 if rows != 7 else 8, 1, 64, "e4m3" if count % 2 else "int8", 16, 16,
+                 spare=2 if rows else 0, seed=count)
+    lse = torch.full((p.rows, p.hq), 9.0, device="cuda")
+    out = torch.full_like(p.q, 9.0)
+    if rows:
+        A.attention_prompt_paged(p.cache(A), seqs(A, p), p.q, out=out, lse=lse)
+        assert (out[-2:] == 9.0).all() and (lse[-2:] == 9.0).all()
+    else:
+        A.attention_decode(p.cache(A), seqs(A, p, decode=True), p.q, out=out, lse=lse)
+    p.check(out, lse, bool(rows))
+
+
 def test_threads_streams_and_repeats_give_the_same_bits(A):
     p = Problem8([(1, 300 + 17 * i) for i in range(30)], 16, 4, 128, "e4m3", 32, 32, seed=5)
     few = Problem8([(4, 500 + 31 * i) for i in range(9)], 8, 2, 64, "int8", 16, 16, seed=6)
