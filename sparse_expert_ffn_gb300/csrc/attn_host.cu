@@ -465,6 +465,9 @@ bool apart_from_scales(const colibri_kv_pages8_t* c, int hq, const void* o, int6
     return !overlap(c->k_scale, scale_bytes(c), o, n) && !overlap(c->v_scale, scale_bytes(c), o, n);
 }
 
+// The caller's description of pages of rows' elements: kCodes is this file's own.
+bool describes_codes(const colibri_kv_pages_t* kv) { return kv && kv->dtype == kCodes; }
+
 colibri_status_t check_prompt8(const colibri_kv_pages8_t* c, const colibri_seqs_t* s, int hq) {
     const colibri_status_t st = check_kv8(c);
     if (st != COLIBRI_OK) return st;
@@ -623,12 +626,12 @@ colibri_status_t colibri_qk_norm_rope(const colibri_seqs_t* seqs, const colibri_
 }
 
 colibri_status_t colibri_qk_norm_rope_at(const colibri_seqs_t* seqs, const colibri_rope_t* rope,
-                                         const colibri_positions_t* positions, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
-                                      int32_t dtype, const void* q, int64_t q_stride,
-                                      const void* k, int64_t k_stride, const void* q_norm,
-                                      const void* k_norm, float eps, void* q_out,
-                                      int64_t q_out_stride, void* k_out, int64_t k_out_stride,
-                                      void* stream) {
+                                         const colibri_positions_t* positions, int32_t n_q_heads,
+                                         int32_t n_kv_heads, int32_t head_dim, int32_t dtype,
+                                         const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                         const void* q_norm, const void* k_norm, float eps, void* q_out,
+                                         int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                                         void* stream) {
     if (!seqs) return COLIBRI_ERR_INVALID_ARG;
     colibri_status_t st = check_heads(n_q_heads, n_kv_heads, head_dim, dtype);
     if (st == COLIBRI_OK) st = check_seqs(seqs, n_q_heads);
@@ -678,7 +681,7 @@ colibri_status_t colibri_attention_check(void* stream) {
 colibri_status_t colibri_attention_prompt_workspace(const colibri_kv_pages_t* kv,
                                                     const colibri_seqs_t* seqs, int32_t n_q_heads,
                                                     size_t* bytes) {
-    if (!bytes) return COLIBRI_ERR_INVALID_ARG;
+    if (!bytes || describes_codes(kv)) return COLIBRI_ERR_INVALID_ARG;
     const colibri_status_t st = check_prompt(kv, seqs, n_q_heads);
     if (st != COLIBRI_OK) return st;
     const int mode = seqs->seq_start ? kAttnPrompt : kAttnSuffix;
@@ -691,6 +694,7 @@ colibri_status_t colibri_attention_prompt(const colibri_kv_pages_t* kv, const co
                                           float scale, int32_t causal, void* o, int64_t o_stride,
                                           float* lse, void* workspace, size_t workspace_bytes,
                                           void* stream) {
+    if (describes_codes(kv)) return COLIBRI_ERR_INVALID_ARG;
     colibri_status_t st = check_prompt(kv, seqs, n_q_heads);
     if (st == COLIBRI_OK) st = check_attention(kv, seqs, n_q_heads, q, q_stride, scale, o, o_stride, lse);
     if (st != COLIBRI_OK) return st;
@@ -708,7 +712,7 @@ colibri_status_t colibri_attention_prompt(const colibri_kv_pages_t* kv, const co
 colibri_status_t colibri_attention_decode_workspace(const colibri_kv_pages_t* cache,
                                                     const colibri_seqs_t* seqs, int32_t n_q_heads,
                                                     int32_t prefix_len, size_t* bytes) {
-    if (!bytes) return COLIBRI_ERR_INVALID_ARG;
+    if (!bytes || describes_codes(cache)) return COLIBRI_ERR_INVALID_ARG;
     const colibri_status_t st = check_decode(cache, seqs, n_q_heads, prefix_len);
     if (st != COLIBRI_OK) return st;
     *bytes = make_plan(cache, seqs, n_q_heads, kAttnSuffix, prefix_len)
@@ -722,6 +726,7 @@ colibri_status_t colibri_attention_decode(const colibri_kv_pages_t* cache, const
                                           const int32_t* prefix_table, void* o, int64_t o_stride,
                                           float* lse, void* workspace, size_t workspace_bytes,
                                           void* stream) {
+    if (describes_codes(cache)) return COLIBRI_ERR_INVALID_ARG;
     colibri_status_t st = check_decode(cache, seqs, n_q_heads, prefix_len);
     if (st == COLIBRI_OK)
         st = check_attention(cache, seqs, n_q_heads, q, q_stride, scale, o, o_stride, lse);

@@ -199,3 +199,17 @@ def test_the_frame_of_single_rows_reads_from_l2_before_it_waits():
     with open(os.path.join(csrc, "append8.cu")) as f:
         for body in re.findall(r"__global__[^{]*\{(.*?)\n\}", f.read(), re.S):
             assert not re.search(r"__ldg|find_span|\ba\.(q|k|v|table|kv_len)\b", body[:body.index("pdl_enter();")])
+
+
+@pytest.mark.parametrize("dtype", range(-20, 0))
+def test_no_number_stands_for_codes_in_calls_of_16_bits(sef, dtype):
+    r, n = ctypes.byref, ctypes.c_size_t()
+    a = Args(sef, dtype=dtype)
+    kv = sef.ColibriKVPages(B, 2 * B, 4 * 32 * 64, 32 * 64, 64, 8, 32, 4, 64, dtype)
+    single = sef.ColibriSeqs(None, 3 * B + 64, 3 * B + 128, 10, 10, 4)
+    assert a.append16() == 1
+    assert sef.colibri_attention_prompt_workspace(r(kv), r(a.SQ), 8, r(n)) == 1
+    assert sef.colibri_attention_decode_workspace(r(kv), r(single), 8, 0, r(n)) == 1
+    args = (8, 5 * B, 512, 0.125)
+    assert sef.colibri_attention_prompt(r(kv), r(a.SQ), *args, 1, 11 * B, 512, None, 32 * B, 1 << 40, None) == 1
+    assert sef.colibri_attention_decode(r(kv), r(single), *args, 0, None, 11 * B, 512, None, 32 * B, 1 << 40, None) == 1
