@@ -170,8 +170,8 @@ colibri_status_t colibri_qk_norm_rope(const colibri_seqs_t* seqs, const colibri_
  * height, width): the position of row r of the call on axis x is
  * at[x * axis_stride + r], any int32, and pair i of a head turns by
  * at[axis[i] * axis_stride + r] * freq[i].  axis NULL: every pair by axis 0; an axis[i]
- * of n_axes or more counts as n_axes - 1.  n_axes is 1 to 8, axis_stride at least
- * n_rows where there are several.  Places in the cache follow from the lengths as
+ * of n_axes or more counts as n_axes - 1.  n_axes is 1 to 8, axis_stride not negative
+ * (0: the axes agree).  Places in the cache follow from the lengths as
  * ever.  Arrays are read on the device.
  */
 typedef struct {

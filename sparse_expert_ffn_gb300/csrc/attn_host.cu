@@ -116,7 +116,7 @@ colibri_status_t check_rope(const colibri_rope_t* r, int head_dim) {
 colibri_status_t check_positions(const colibri_positions_t* p, const colibri_rope_t* rope, int n_rows) {
     if (!p) return COLIBRI_OK;
     if (!rope || p->n_axes < 1 || p->n_axes > 8 || ((uintptr_t)p->at & 3) || (n_rows > 0 && !p->at) ||
-        (p->n_axes > 1 && p->axis_stride < n_rows) || p->axis_stride >= ((int64_t)1 << 37))
+        (p->n_axes > 1 && p->axis_stride < 0) || p->axis_stride >= ((int64_t)1 << 37))
         return COLIBRI_ERR_INVALID_ARG;
     return COLIBRI_OK;
 }

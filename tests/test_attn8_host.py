@@ -124,7 +124,7 @@ SQ_BAD = [(dict(n_seqs=-1), 1), (dict(n_rows=-1), 1), (dict(kv_len=None), 1), (d
     (dict(q=None), 1), (dict(q=8), 1), (dict(qs=504), 1), (dict(ks=128), 1), (dict(vs=260), 1), (dict(qn=2), 1),
     (dict(eps=-1.0), 1), (dict(qo=None), 1), (dict(qo=6 * B), 1), (dict(qo=B), 1), (dict(q=13 * B), 1), (dict(qo=14 * B), 1),
     (dict(vr=14 * B - 256), 1), (dict(v_scale=13 * B), 1), (dict(k_scale=2 * B + 1024), 1), (dict(rot_dim=72), 1), (dict(freq=None), 1), (dict(at=None), 1), (dict(at=4 * B + 2), 1),
-    (dict(n_axes=0), 1), (dict(n_axes=9), 1), (dict(axis_stride=9), 1), (dict(n_rows=0), 0), (dict(n_seqs=0), 0)])
+    (dict(n_axes=0), 1), (dict(n_axes=9), 1), (dict(axis_stride=-1), 1), (dict(n_rows=0), 0), (dict(n_seqs=0), 0)])
 def test_append8_refusals(sef, bad, status):
     a = Args(sef, **bad)
     assert a.append() == status
@@ -134,7 +134,7 @@ def test_append8_refusals(sef, bad, status):
 
 
 @pytest.mark.parametrize("bad,status", [
-    (dict(at=None), 1), (dict(at=4 * B + 2), 1), (dict(n_axes=0), 1), (dict(n_axes=9), 1), (dict(axis_stride=9), 1),
+    (dict(at=None), 1), (dict(at=4 * B + 2), 1), (dict(n_axes=0), 1), (dict(n_axes=9), 1), (dict(axis_stride=1 << 40), 1),
     (dict(axis_stride=-1), 1), (dict(rot_dim=8), 1), (dict(n_rows=0), 0), (dict(n_seqs=0), 0)])
 def test_positions_refusals(sef, bad, status):
     assert Args(sef, **bad).append16() == status and Args(sef, **bad).rotate() == status

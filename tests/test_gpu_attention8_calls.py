@@ -102,6 +102,7 @@ def test_axes_that_agree_are_plain_positions(A, dtype):
     sq = A.Sequences(p.seq_start, p.kv_len)
     ref = A.qk_norm_rope(sq, p.q, k, rope=A.Rope(f))
     for axes, pos in ((A.rope_axes([10, 12, 10]).cuda(), at.repeat(3, 1)), (None, at), (None, at.repeat(2, 1)),
+                      (A.rope_axes([10, 12, 10]).cuda(), at.expand(3, -1)),
                       (torch.full((32,), 255, dtype=torch.uint8, device="cuda"), torch.stack([at + 9, at]))):
         got = A.qk_norm_rope(sq, p.q, k, rope=A.Rope(f, axes=axes), positions=pos)
         assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
