@@ -60,7 +60,9 @@ struct AttnArgs {
     // launch_attn_decode8: rows (token, head of the group) of a sequence that meet a key at
     // once, 8 or 16, and of a piece
     int tile_rows, piece_rows;
-    int group_tiles;             // suffix mode: tiles per key head
+    // launch_attn_decode(8) and the join, where rows are one token's: tiles per key head, and
+    // of all of them (divided on the host: on the device 2 us of a step of some 20)
+    int group_tiles, seq_items;
     uint64_t wait_limit_ns;      // bound of every mbarrier wait
     int stall_tma;               // failure-detection tests only: a CTA's copies of Q and K stop at
                                  // this item of its work (1: the first), 0 never
@@ -83,6 +85,7 @@ cudaError_t attn_tc_status(int* status, cudaStream_t s);
 // groups of up to 32 heads).  part_o null: no prefix; otherwise slot part_slot
 // takes the rows written in one piece.
 bool attn_decode_takes(DType dt, int group);
+int attn_decode_tile(DType dt, int group);   // rows of a group that meet a key at once
 size_t attn_decode_pieces(DType dt, int group);
 cudaError_t launch_attn_decode(DType dt, int d, const AttnArgs& a, cudaStream_t s);
 // The same over codes (bf16 rows), in suffix mode or prompt mode: tiles of tile_rows rows

@@ -234,14 +234,20 @@ constexpr int kMinSteps = 4;                      // steps of a share at least
 template <typename T, int D, bool kEarly>
 __device__ __forceinline__ int seq_steps(const AttnArgs& a, int b) {
     const AttnSeq s = attn_seq<kEarly>(a, b);
-    return s.kv > s.kv0 && s.n > 0 ? (s.kv - s.kv0 + kStepKeys<T, D> - 1) / kStepKeys<T, D> : 0;
+    return s.kv > s.kv0 && (sizeof(T) > 1 || s.n > 0) ? (s.kv - s.kv0 + kStepKeys<T, D> - 1) / kStepKeys<T, D> : 0;
 }
 // Row tiles of sequence b per head.
 template <typename T, bool kEarly>
 __device__ __forceinline__ int seq_tiles(const AttnArgs& a, int b) {
-    if (sizeof(T) > 1) return row_tiles<T>(a.group);
-    if (a.mode == kAttnSuffix) return a.group_tiles;
+    if (sizeof(T) > 1 || a.mode == kAttnSuffix) return a.group_tiles;
     return (attn_seq<kEarly>(a, b).n * a.group + a.tile_rows - 1) >> tile_shift<T>(a);
+}
+
+// (head, row tile) pairs of sequence b.
+template <typename T, bool kEarly>
+__device__ __forceinline__ int64_t seq_items(const AttnArgs& a, int b) {
+    if (sizeof(T) > 1 || a.mode == kAttnSuffix) return a.seq_items;
+    return (int64_t)seq_tiles<T, kEarly>(a, b) * a.hkv;
 }
 
 // The whole list: its length, and the steps before sequence `upto`.  Called by
@@ -250,7 +256,7 @@ template <typename T, int D, bool kEarly>
 __device__ __forceinline__ void count_steps(const AttnArgs& a, int upto, int64_t* total, int64_t* before) {
     int64_t all = 0, part = 0;
     for (int b = threadIdx.x & 31; b < a.n_seqs; b += 32) {
-        const int64_t u = (int64_t)seq_steps<T, D, kEarly>(a, b) * seq_tiles<T, kEarly>(a, b) * a.hkv;
+        const int64_t u = (int64_t)seq_steps<T, D, kEarly>(a, b) * seq_items<T, kEarly>(a, b);
         all += u;
         if (b < upto) part += u;
     }

@@ -345,6 +345,10 @@ size_t attn_decode_pieces(DType dt, int group) {
                              : (size_t)most_shares<float>(group) * 2 * piece_rows<float>(group);
 }
 
+int attn_decode_tile(DType dt, int group) {
+    return dt == DType::BF16 ? row_tile<__nv_bfloat16>(group) : row_tile<float>(group);
+}
+
 // (a float32 group of 64 would be read 16 times)
 bool attn_decode_takes(DType dt, int group) { return dt == DType::BF16 || group <= 32; }
 

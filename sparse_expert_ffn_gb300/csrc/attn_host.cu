@@ -403,7 +403,9 @@ colibri_status_t run_attention(AttnArgs a, const Plan& p, int dtype, int d, int 
     }
     a.splits = p.own;
     a.tile_rows = p.tile_rows, a.piece_rows = p.piece_rows;
-    if (p.tile_rows) a.group_tiles = (a.group + p.tile_rows - 1) / p.tile_rows;
+    const int tile = p.tile_rows ? p.tile_rows : attn_decode_tile(dtype_of(dtype), a.group);
+    a.group_tiles = (a.group + tile - 1) / tile;
+    a.seq_items = a.group_tiles * a.hkv;
     a.part_slot = p.prefix;
     a.beside_prefix = p.prefix > 0;
     if (e == cudaSuccess)

@@ -35,6 +35,7 @@ __device__ __forceinline__ uint32_t bf16x2(float x, float y) {
 template <typename T, int D, bool kEarly>
 struct Walk {
     int b, units, tiles;       // sequence, its steps per (head, row tile), its row tiles per head
+    int64_t end;               // its steps
     int64_t in_seq;            // steps of sequence b before the piece
     int item;                  // (head, row tile) of the sequence
     int lo, hi;                // keys of the piece
@@ -43,11 +44,12 @@ struct Walk {
 
     // The piece at in_seq, of at most `left` steps.  False: nothing there.
     __device__ __forceinline__ bool piece(const AttnArgs& a, int64_t left) {
-        if (in_seq == (int64_t)units * tiles * a.hkv) {
+        if (in_seq == end) {
             in_seq = 0, units = 0;
             while (++b < a.n_seqs && (units = seq_steps<T, D, kEarly>(a, b)) == 0) {}
             if (units == 0) return false;                          // (not reached: left > 0)
             tiles = seq_tiles<T, kEarly>(a, b);
+            end = units * seq_items<T, kEarly>(a, b);
         }
         const AttnSeq s = attn_seq<kEarly>(a, b);
         item = (int)(in_seq / units);
@@ -183,8 +185,8 @@ __device__ __forceinline__ void decode_share(const AttnArgs& a, uint8_t* smem) {
     Walk<T, D, kEarly> load;
     for (int base = 0;; base += 32) {
         const int mine = base + lane < a.n_seqs ? seq_steps<T, D, kEarly>(a, base + lane) : 0;
-        const int tiles = mine ? seq_tiles<T, kEarly>(a, base + lane) : 0;
-        int64_t upto = (int64_t)mine * tiles * a.hkv;
+        const int64_t own = mine ? mine * seq_items<T, kEarly>(a, base + lane) : 0;
+        int64_t upto = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
@@ -195,8 +197,9 @@ __device__ __forceinline__ void decode_share(const AttnArgs& a, uint8_t* smem) {
             const int src = __ffs(holds) - 1;
             load.b = base + src;
             load.units = __shfl_sync(0xffffffffu, mine, src);
-            load.tiles = __shfl_sync(0xffffffffu, tiles, src);
-            load.in_seq = u0 - before - (__shfl_sync(0xffffffffu, upto, src) - (int64_t)load.units * load.tiles * a.hkv);
+            load.tiles = seq_tiles<T, kEarly>(a, load.b);
+            load.end = __shfl_sync(0xffffffffu, own, src);
+            load.in_seq = u0 - before - (__shfl_sync(0xffffffffu, upto, src) - load.end);
             break;
         }
         before += __shfl_sync(0xffffffffu, upto, 31);

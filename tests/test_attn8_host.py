@@ -194,7 +194,7 @@ def test_the_frame_of_single_rows_reads_from_l2_before_it_waits():
     for name in ("attn_share.cuh", "attn_rows8.cuh"):
         with open(os.path.join(csrc, name)) as f:
             text = re.sub(r"//[^\n]*", "", f.read())
-        calls = re.findall(r"\b(?:attn_seq|attn_page|seq_steps|seq_tiles|count_steps|ld_early)\b(<[^>]*>)", text)
+        calls = re.findall(r"\b(?:attn_seq|attn_page|seq_steps|seq_tiles|seq_items|count_steps|ld_early)\b(<[^>]*>)", text)
         assert calls and all(c.endswith("kEarly>") for c in calls) and "__ldg" not in text, name
     with open(os.path.join(csrc, "append8.cu")) as f:
         for body in re.findall(r"__global__[^{]*\{(.*?)\n\}", f.read(), re.S):
