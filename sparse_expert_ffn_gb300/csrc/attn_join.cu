@@ -49,7 +49,7 @@ __device__ __forceinline__ Place row_parts(const AttnArgs& a, int row, int head,
             }
             in_seq += (row - attn_seq<kEarly>(a, b).row0) * a.group;
         }
-        p.tile_row = in_seq & (tile_rows<T>(a) - 1);
+        if (sizeof(T) == 1) p.tile_row = in_seq & (tile_rows<T>(a) - 1);
         count_steps<T, D, kEarly>(a, b, &total, &first);
         const int steps = seq_steps<T, D, kEarly>(a, b);
         if (steps > 0) {
@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const __grid_consta
     if (early) pdl_enter();
     __syncthreads();
     if (!place.live) return;
+    const int tile_row = sizeof(T) == 1 ? place.tile_row : (head % a.group) & (tile_rows<T>(a) - 1);
     const int c0 = place.c0, c1 = place.c1;
     const bool one = in_shares && c0 == c1;                   // whole, in slot part_slot
     const int in_slots = slots + (one ? 1 : 0), parts = in_slots + (one ? 0 : c1 - c0 + 1);
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(const __grid_consta
                 const int c = c0 + i - in_slots;
                 const bool slot = i < in_slots;
                 const int64_t at = slot ? i * total_rows + flat
-                                        : ((int64_t)c * 2 + (c == c0 && place.first_is_last)) * (sizeof(T) == 1 ? a.piece_rows : piece_rows<T>(a.group)) + place.tile_row;
+                                        : ((int64_t)c * 2 + (c == c0 && place.first_is_last)) * (sizeof(T) == 1 ? a.piece_rows : piece_rows<T>(a.group)) + tile_row;
                 w[k] = (slot ? a.part_lse : a.piece_lse)[at];
                 if (lane < D / 4)
                     v[k] = *reinterpret_cast<const float4*>((slot ? a.part_o : a.piece_o) + at * D + lane * 4);
