@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 3) append8_kernel(const __grid_const
                 }
         }
         if (nk == 0) continue;
-        hd.prepare(static_cast<const BF*>(a.k_norm), a.eps, turn + r * pairs, lane, turns, c0, c1);
+        hd.template prepare<true>(static_cast<const BF*>(a.k_norm), a.eps, turn + r * pairs, lane, turns, c0, c1);
         for (int h = first_of(nq); h < nk; h += per) {
             Vec8<BF> x[2];
             float y[2][8];
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 3) append8_kernel(const __grid_const
             *reinterpret_cast<uint2*>(p + c1) = make_uint2(Code::encode4(y[1]), Code::encode4(y[1] + 4));
         };
         if (sp.rows > kGroups)                                     // (else the row's are there from above)
-            hd.prepare(static_cast<const BF*>(a.k_norm), a.eps, turn + r * pairs, lane, turns, c0, c1);
+            hd.template prepare<true>(static_cast<const BF*>(a.k_norm), a.eps, turn + r * pairs, lane, turns, c0, c1);
         for (int h = first_of(nq); h < nk; h += per) {
             Vec8<BF> x[2];
             float y[2][8];

@@ -115,6 +115,8 @@ struct Heads {
     bool norm, turns;
     float eps;
 
+    // (kFine: norm weights u, w, cosine and sine as they are, for turned<true>)
+    template <bool kFine = false>
     __device__ __forceinline__ void prepare(const T* weight, float e, const float2* turn, int lane, bool rotated, int c0,
                                             int c1) {
         norm = weight != nullptr, eps = e, turns = rotated;
@@ -137,7 +139,8 @@ struct Heads {
         for (int i = 0; i < 8; ++i) {
             const float2 t = turns ? turn[8 * lane + i] : make_float2(1.f, 0.f);
             const float gu = g[kInterleaved ? 2 * i : i], gw = g[kInterleaved ? 2 * i + 1 : i + 8];
-            m[i][0] = gu * t.x, m[i][1] = gw * t.y, m[i][2] = gw * t.x, m[i][3] = gu * t.y;
+            if (kFine) m[i][0] = gu, m[i][1] = gw, m[i][2] = t.x, m[i][3] = t.y;
+            else m[i][0] = gu * t.x, m[i][1] = gw * t.y, m[i][2] = gw * t.x, m[i][3] = gu * t.y;
         }
     }
     __device__ __forceinline__ void apply(Vec8<T> (&x)[2]) const {
@@ -146,8 +149,9 @@ struct Heads {
         x[0].set(y[0]);
         x[1].set(y[1]);
     }
-    // the same before it is rounded to T; kFine: with the norm's factor rounded once, and
-    // multiplied to what is turned instead of to both elements before
+    // the same before it is rounded to T; kFine (after prepare<true>): with fewer roundings,
+    // the products of elements and norm weights being exact where T has 8 bits, and the
+    // norm's factor, rounded to nearest, multiplied to what is turned
     template <bool kFine = false>
     __device__ __forceinline__ void turned(const Vec8<T> (&x)[2], float (&y)[2][8]) const {
         float p[16];
@@ -175,10 +179,10 @@ struct Heads {
         const auto products = [&](auto second) {                   // second(): with the second products
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float before = kFine ? 1.f : inv;
-                const float u = p[kInterleaved ? 2 * i : i] * before, w = p[kInterleaved ? 2 * i + 1 : i + 8] * before;
-                float yu = u * m[i][0], yw = w * m[i][2];
-                if (second()) yu -= w * m[i][1], yw += u * m[i][3];
+                const float u = p[kInterleaved ? 2 * i : i] * (kFine ? m[i][0] : inv);
+                const float w = p[kInterleaved ? 2 * i + 1 : i + 8] * (kFine ? m[i][1] : inv);
+                float yu = u * m[i][kFine ? 2 : 0], yw = w * m[i][2];
+                if (second()) yu -= w * m[i][kFine ? 3 : 1], yw += u * m[i][3];
                 if (kFine) yu *= inv, yw *= inv;
                 if (kInterleaved) y[i / 4][i % 4 * 2] = yu, y[i / 4][i % 4 * 2 + 1] = yw;
                 else y[0][i] = yu, y[1][i] = yw;
